@@ -326,3 +326,10 @@ def gemm(a, b, out_dtype=None, cfg: Config | None = None, stream=None):
     c = torch.empty((a.shape[0], b.shape[1]), dtype=out_dtype, device=a.device)
     gemm_into(a, b, c, cfg=cfg, stream=stream)
     return c
+
+
+from .fp8 import (EXPORTED_SYMBOLS_FP8, ExpertOrder, combine, combine_grad, gather_rows, gemm_fp8,  # noqa: E402
+                  gemm_fp8_experts, gemm_fp8_experts_wgrad, quantize_fp8, sort_by_expert)
+
+__all__ += ["quantize_fp8", "gemm_fp8", "gemm_fp8_experts", "gemm_fp8_experts_wgrad", "sort_by_expert", "ExpertOrder",
+            "gather_rows", "combine", "combine_grad", "EXPORTED_SYMBOLS_FP8"]

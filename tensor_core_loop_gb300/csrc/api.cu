@@ -1464,6 +1464,34 @@ int tensor_map_uncached(const void* ptr, CUtensorMapDataType dtype, uint64_t d0,
     return r == CUDA_SUCCESS ? TCL_OK : TCL_ERR_LAUNCH;
 }
 
+int stream_scratch(cudaStream_t stream, size_t need, void** out) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev;
+    DevState* ds;
+    StreamRes* sr;
+    int st = current_device(&dev, &ds);
+    if (st) return st;
+    if ((st = stream_res(ds, stream, &sr))) return st;
+    if ((st = ensure_scratch(ds, sr, need, stream))) return st;
+    *out = sr->scratch;
+    return TCL_OK;
+}
+
+int tensor_map_bytes(const void* ptr, uint64_t k, uint64_t rows, uint64_t mats, uint64_t row_stride, uint64_t mat_stride,
+                     uint32_t box_rows, CUtensorMap* out) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    int st = encode_fn();
+    if (st) return st;
+    const cuuint64_t dims[3] = {k, rows, mats};
+    const cuuint64_t strides[2] = {row_stride, mat_stride};
+    const cuuint32_t box[3] = {128, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? TCL_OK : TCL_ERR_LAUNCH;
+}
+
 }  // namespace tcl
 
 using namespace tcl;

@@ -1,0 +1,338 @@
+// C ABI of the e4m3 products, the quantising and the expert routing (declared in
+// include/tcl_fp8.h): argument checks, the choice of tile, and the launches.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "fp8_launch.cuh"
+#include "tcl_fp8.h"
+
+namespace tcl {
+namespace {
+
+constexpr unsigned long long kTimeoutNs = 1000000000ull;   // bound on every in-kernel wait: 1 s
+
+bool on(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+int elem(int x_type) { return x_type == TCL_X_F32 ? 4 : 2; }
+bool known(int x_type) { return x_type == TCL_X_BF16 || x_type == TCL_X_F32; }
+long long up(long long x, long long m) { return (x + m - 1) / m * m; }
+int groups_of(int k) { return (k + 127) / 128; }
+
+int status_of(cudaError_t err) {
+    if (err == cudaSuccess) return TCL_OK;
+    cudaGetLastError();
+    return err == cudaErrorInvalidValue ? TCL_ERR_DIMS : TCL_ERR_LAUNCH;
+}
+
+int device_check() {
+    int dev, sms;
+    unsigned int* status;
+    return device_context(&dev, &sms, &status);
+}
+
+// An e4m3 operand as its tensor copies read it.
+struct Operand {
+    const uint8_t* p;
+    long long ld, mat;
+    int rows, mats, k;
+    bool copy() const { return !on(p, 16) || ld % 16 || (mats > 1 && mat % 16); }
+    size_t bytes() const { return copy() ? static_cast<size_t>(up(static_cast<long long>(mats) * rows * up(k, 16), 256)) : 0; }
+};
+
+// Copies an operand that is off the tensor copies' grid into `to`.
+int lay_out(Operand& o, uint8_t* to, cudaStream_t stream) {
+    if (!o.copy()) return TCL_OK;
+    if (o.mats > 65535) return TCL_ERR_DIMS;
+    const long long ld = up(o.k, 16);
+    const cudaError_t err = launch_copy_bytes(o.p, o.ld, o.mat, to, ld, o.mats, o.rows, o.k, stream);
+    if (err != cudaSuccess) return status_of(err);
+    o.p = to;
+    o.ld = ld;
+    o.mat = ld * o.rows;
+    return TCL_OK;
+}
+
+// The tile for products with `tokens` rows in all, for `experts` experts. Few rows go to
+// the MMA's N side, many to its M side.
+Fp8Tile choose_tile(long long tokens, int experts) {
+    const long long each = (tokens + experts - 1) / experts;
+    if (each <= 16) return Fp8Tile::FEW16;
+    if (each <= 32) return Fp8Tile::FEW32;
+    return Fp8Tile::ONE;
+}
+
+int product(Operand a, Fp8Side sa, Operand b, Fp8Side sb, Fp8Tile tile, Fp8Params p, long long units, int sms,
+            cudaStream_t stream) {
+    if (const size_t need = a.bytes() + b.bytes()) {
+        void* scratch;
+        int st = stream_scratch(stream, need, &scratch);
+        if (st) return st;
+        uint8_t* at = static_cast<uint8_t*>(scratch);
+        const size_t first = a.bytes();
+        if ((st = lay_out(a, at, stream)) || (st = lay_out(b, at + first, stream))) return st;
+    }
+    const Fp8TileInfo t = fp8_tile_info(tile);
+    // P is the side in the tensor-memory lanes: the tokens, or few tokens' weights
+    const Operand& op = t.swap ? b : a;
+    const Operand& oq = t.swap ? a : b;
+    Fp8Launch l;
+    l.tile = tile;
+    int st;
+    if ((st = tensor_map_bytes(op.p, op.k, op.rows, op.mats, op.ld, op.mats > 1 ? op.mat : up(op.ld * op.rows, 16),
+                               t.box_p, &l.tmP)) ||
+        (st = tensor_map_bytes(oq.p, oq.k, oq.rows, oq.mats, oq.ld, oq.mats > 1 ? oq.mat : up(oq.ld * oq.rows, 16),
+                               t.box_q, &l.tmQ)))
+        return st;
+    p.P = t.swap ? sb : sa;
+    p.Q = t.swap ? sa : sb;
+    p.timeout_ns = kTimeoutNs;
+    l.p = p;
+    l.grid = static_cast<int>(std::max(1ll, std::min<long long>(sms / t.ctas, units))) * t.ctas;
+    l.stream = stream;
+    return status_of(launch_fp8_gemm(l));
+}
+
+// Rows of tokens times the weights of one matrix (offsets NULL) or of each row's expert.
+int rows_product(int rows, int experts, int N, int K, const void* A, int lda, const float* SA, long long sa_row,
+                 long long sa_group, const void* B, int ldb, long long b_expert, const float* SB, int sb_kind,
+                 long long sb_expert, long long sb_row, long long sb_group, const int32_t* offsets, void* C, int ldc,
+                 int out, cudaStream_t stream) {
+    if (rows < 0 || N < 1 || K < 1 || experts < 1) return TCL_ERR_DIMS;
+    if (experts > TCL_MAX_EXPERTS) return TCL_ERR_CONFIG;
+    if (out != TCL_OUT_F32 && out != TCL_OUT_BF16) return TCL_ERR_CONFIG;
+    if (sb_kind != TCL_SCALE_ROWS && sb_kind != TCL_SCALE_BLOCKS) return TCL_ERR_CONFIG;
+    if (!B || !SB || (rows && (!A || !SA || !C))) return TCL_ERR_NULL;
+    if (lda < K || ldb < K || ldc < N) return TCL_ERR_LD;
+    if (experts > 1 && b_expert < static_cast<long long>(N - 1) * ldb + K) return TCL_ERR_LD;
+    const int es = out == TCL_OUT_BF16 ? 2 : 4;
+    if (!on(SA, 4) || !on(SB, 4) || !on(C, es) || !on(offsets, 4)) return TCL_ERR_ALIGN;
+    int dev, sms;
+    unsigned int* status;
+    int st = device_context(&dev, &sms, &status);
+    if (st) return st;
+    if (rows == 0) return TCL_OK;
+    const Fp8Tile tile = choose_tile(rows, experts);
+    const Fp8TileInfo t = fp8_tile_info(tile);
+    const int tt = t.swap ? t.bq : t.bp, tw = t.swap ? t.bp : t.bq;
+    Fp8Params p = {};
+    p.offsets = offsets;
+    p.experts = experts;
+    p.rows = rows;
+    p.wrows = N;
+    p.num_kb = groups_of(K);
+    p.k_tail = K % 16 ? K % 128 : 0;
+    p.C = C;
+    p.ldc = ldc;
+    p.out_bf16 = out == TCL_OUT_BF16;
+    p.vec = on(C, 16) && static_cast<long long>(ldc) * es % 16 == 0;
+    p.status = status;
+    // every expert may end inside a tile, and so may the rows behind the last
+    const long long units = (static_cast<long long>(rows) / tt + 1 + (offsets ? std::min(experts, rows) : 0)) *
+                            ((N + tw - 1) / tw);
+    if (units > 0x3fffffffll) return TCL_ERR_DIMS;
+    return product({static_cast<const uint8_t*>(A), lda, 0, rows, 1, K}, {SA, sa_row, sa_group, 0, 0},
+                   {static_cast<const uint8_t*>(B), ldb, b_expert, N, experts, K},
+                   {SB, sb_row, sb_group, experts > 1 ? sb_expert : 0, sb_kind}, tile, p, units, sms, stream);
+}
+
+}  // namespace
+}  // namespace tcl
+
+using namespace tcl;
+
+extern "C" {
+
+int tcl_quantize_fp8_rows(int x_type, int rows, int cols, const void* X, int ldx, const int32_t* position, int top,
+                          const int32_t* source, int out_rows, void* Q, int ldq, float* scale, long long s_row,
+                          long long s_group, cudaStream_t stream) {
+    if (!known(x_type)) return TCL_ERR_CONFIG;
+    const int made = position ? out_rows : rows;
+    if (rows < 0 || cols < 1 || made < 0 || (position && top < 1)) return TCL_ERR_DIMS;
+    if ((rows && !X) || (made && (!Q || !scale)) || (position && made && !source)) return TCL_ERR_NULL;
+    if (ldx < cols || ldq < cols) return TCL_ERR_LD;
+    if (!on(X, elem(x_type)) || !on(scale, 4) || !on(position, 4) || !on(source, 4)) return TCL_ERR_ALIGN;
+    if (int st = device_check()) return st;
+    if (made == 0) return TCL_OK;
+    return status_of(launch_quant_rows({X, ldx, x_type == TCL_X_F32, rows, cols, position, top, source, out_rows,
+                                        static_cast<uint8_t*>(Q), ldq, scale, s_row, s_group},
+                                       stream));
+}
+
+int tcl_quantize_fp8_columns(int x_type, int rows, int cols, const void* X, int ldx, const int32_t* source, int top,
+                             int out_rows, void* Q, int ldq, float* scale, long long s_row, long long s_group,
+                             cudaStream_t stream) {
+    if (!known(x_type)) return TCL_ERR_CONFIG;
+    const int made = source ? out_rows : rows;
+    if (rows < 0 || cols < 1 || made < 0 || (source && top < 1)) return TCL_ERR_DIMS;
+    if ((rows && !X) || (made && (!Q || !scale))) return TCL_ERR_NULL;
+    if (ldx < cols || ldq < made) return TCL_ERR_LD;
+    if (!on(X, elem(x_type)) || !on(scale, 4) || !on(source, 4)) return TCL_ERR_ALIGN;
+    if (int st = device_check()) return st;
+    if (made == 0) return TCL_OK;
+    return status_of(launch_quant_tiles(QuantTile::COLUMNS,
+                                        {X, ldx, 0, x_type == TCL_X_F32, 1, made, cols, rows, source, top,
+                                         static_cast<uint8_t*>(Q), ldq, 0, scale, s_row, s_group},
+                                        stream));
+}
+
+int tcl_quantize_fp8_blocks(int x_type, int batch, int rows, int cols, const void* X, int ldx, long long x_batch,
+                            int transpose, void* Q, int ldq, long long q_batch, float* scale, cudaStream_t stream) {
+    if (!known(x_type) || (transpose != 0 && transpose != 1)) return TCL_ERR_CONFIG;
+    if (batch < 0 || rows < 0 || cols < 1) return TCL_ERR_DIMS;
+    const bool any = batch > 0 && rows > 0;
+    if (any && (!X || !Q || !scale)) return TCL_ERR_NULL;
+    const int qrows = transpose ? cols : rows, qcols = transpose ? rows : cols;
+    if (ldx < cols || ldq < qcols) return TCL_ERR_LD;
+    if (batch > 1 && any && (x_batch < 0 || q_batch < static_cast<long long>(qrows - 1) * ldq + qcols)) return TCL_ERR_LD;
+    if (!on(X, elem(x_type)) || !on(scale, 4)) return TCL_ERR_ALIGN;
+    if (int st = device_check()) return st;
+    if (!any) return TCL_OK;
+    return status_of(launch_quant_tiles(transpose ? QuantTile::BLOCKS_T : QuantTile::BLOCKS,
+                                        {X, ldx, x_batch, x_type == TCL_X_F32, batch, rows, cols, rows, nullptr, 1,
+                                         static_cast<uint8_t*>(Q), ldq, q_batch, scale, 0, 0},
+                                        stream));
+}
+
+int gemm_fp8(int M, int N, int K, const void* A, int lda, const float* SA, long long sa_row, long long sa_group,
+             const void* B, int ldb, const float* SB, int sb_kind, long long sb_row, long long sb_group, void* C, int ldc,
+             int out, cudaStream_t stream) {
+    return rows_product(M, 1, N, K, A, lda, SA, sa_row, sa_group, B, ldb, 0, SB, sb_kind, 0, sb_row, sb_group, nullptr, C,
+                        ldc, out, stream);
+}
+
+int gemm_fp8_experts(int rows, int experts, int N, int K, const void* A, int lda, const float* SA, long long sa_row,
+                     long long sa_group, const void* B, int ldb, long long b_expert, const float* SB, int sb_kind,
+                     long long sb_expert, long long sb_row, long long sb_group, const int32_t* offsets, void* C, int ldc,
+                     int out, cudaStream_t stream) {
+    if (!offsets) return TCL_ERR_NULL;
+    return rows_product(rows, experts, N, K, A, lda, SA, sa_row, sa_group, B, ldb, b_expert, SB, sb_kind, sb_expert,
+                        sb_row, sb_group, offsets, C, ldc, out, stream);
+}
+
+int gemm_fp8_experts_wgrad(int rows, int experts, int N, int K, const void* A, int lda, const float* SA, long long sa_row,
+                           long long sa_group, const void* B, int ldb, const float* SB, long long sb_row,
+                           long long sb_group, const int32_t* offsets, void* C, int ldc, long long c_expert, int out,
+                           cudaStream_t stream) {
+    if (rows < 0 || N < 1 || K < 1 || experts < 1) return TCL_ERR_DIMS;
+    if (experts > TCL_MAX_EXPERTS) return TCL_ERR_CONFIG;
+    if (out != TCL_OUT_F32 && out != TCL_OUT_BF16) return TCL_ERR_CONFIG;
+    if (!offsets || !C || (rows && (!A || !SA || !B || !SB))) return TCL_ERR_NULL;
+    if (lda < rows || ldb < rows || ldc < K) return TCL_ERR_LD;
+    if (experts > 1 && c_expert < static_cast<long long>(N - 1) * ldc + K) return TCL_ERR_LD;
+    const int es = out == TCL_OUT_BF16 ? 2 : 4;
+    if (!on(SA, 4) || !on(SB, 4) || !on(C, es) || !on(offsets, 4)) return TCL_ERR_ALIGN;
+    int dev, sms;
+    unsigned int* status;
+    int st = device_context(&dev, &sms, &status);
+    if (st) return st;
+    if (rows == 0) {   // no expert has rows: all zeros
+        for (int e = 0; e < experts; ++e)
+            if (cudaMemset2DAsync(static_cast<char*>(C) + e * c_expert * es, static_cast<size_t>(ldc) * es, 0,
+                                  static_cast<size_t>(K) * es, N, stream) != cudaSuccess)
+                return status_of(cudaErrorUnknown);
+        return TCL_OK;
+    }
+    const Fp8Tile tile = Fp8Tile::ONE;
+    const Fp8TileInfo t = fp8_tile_info(tile);
+    Fp8Params p = {};
+    p.offsets = offsets;
+    p.experts = experts;
+    p.rows = rows;
+    p.wrows = N;
+    p.qrows = K;
+    p.wgrad = 1;
+    p.C = C;
+    p.ldc = ldc;
+    p.c_expert = c_expert;
+    p.out_bf16 = out == TCL_OUT_BF16;
+    p.vec = on(C, 16) && static_cast<long long>(ldc) * es % 16 == 0 && (experts == 1 || c_expert * es % 16 == 0);
+    p.status = status;
+    const long long units = static_cast<long long>(experts) * ((N + t.bp - 1) / t.bp) * ((K + t.bq - 1) / t.bq);
+    if (units > 0x3fffffffll) return TCL_ERR_DIMS;
+    return product({static_cast<const uint8_t*>(A), lda, 0, N, 1, rows}, {SA, sa_row, sa_group, 0, 0},
+                   {static_cast<const uint8_t*>(B), ldb, 0, K, 1, rows}, {SB, sb_row, sb_group, 0, 0}, tile, p, units, sms,
+                   stream);
+}
+
+int tcl_sort_by_expert(int tokens, int top, const void* ids, int id_bytes, int experts, int align, int rows,
+                       int32_t* offsets, int32_t* position, int32_t* source, cudaStream_t stream) {
+    if (id_bytes != 4 && id_bytes != 8) return TCL_ERR_CONFIG;
+    if (experts > TCL_MAX_EXPERTS || align < 1 || align > 128) return TCL_ERR_CONFIG;
+    if (tokens < 0 || top < 1 || experts < 1) return TCL_ERR_DIMS;
+    const long long slots = static_cast<long long>(tokens) * top;
+    const long long need = (slots + std::min<long long>(experts, slots) * (align - 1)) / align * align;
+    if (need > 0x7fffffffll || rows < need) return TCL_ERR_DIMS;
+    if (!offsets || (slots && (!ids || !position)) || (rows && !source)) return TCL_ERR_NULL;
+    if (!on(ids, id_bytes) || !on(offsets, 4) || !on(position, 4) || !on(source, 4)) return TCL_ERR_ALIGN;
+    if (int st = device_check()) return st;
+    const long long blocks = (slots + kSortChunk - 1) / kSortChunk;
+    void* counts = nullptr;
+    if (blocks > 1) {
+        if (int st = stream_scratch(stream, static_cast<size_t>(blocks) * experts * sizeof(int), &counts)) return st;
+    }
+    return status_of(launch_sort(slots, ids, id_bytes, experts, align, rows, offsets, position, source,
+                                 static_cast<int*>(counts), stream));
+}
+
+int tcl_gather_rows(int x_type, int tokens, int top, int rows, int cols, const void* X, int ldx, const int32_t* position,
+                    const int32_t* source, void* Y, int ldy, cudaStream_t stream) {
+    if (!known(x_type)) return TCL_ERR_CONFIG;
+    if (tokens < 0 || top < 1 || rows < 0 || cols < 1) return TCL_ERR_DIMS;
+    if ((tokens && (!X || !position)) || (rows && (!Y || !source))) return TCL_ERR_NULL;
+    if (ldx < cols || ldy < cols) return TCL_ERR_LD;
+    if (!on(X, elem(x_type)) || !on(Y, elem(x_type)) || !on(position, 4) || !on(source, 4)) return TCL_ERR_ALIGN;
+    if (int st = device_check()) return st;
+    if (rows == 0) return TCL_OK;
+    RouteRows a = {};
+    a.f32 = x_type == TCL_X_F32;
+    a.tokens = tokens, a.top = top, a.rows = rows, a.cols = cols;
+    a.x = X, a.ldx = ldx;
+    a.position = position, a.source = source;
+    a.out = Y, a.ldo = ldy;
+    return status_of(launch_gather(a, stream));
+}
+
+int tcl_combine(int x_type, int tokens, int top, int rows, int cols, const void* Y, int ldy, const float* weights,
+                const int32_t* position, void* out, int ldo, cudaStream_t stream) {
+    if (!known(x_type)) return TCL_ERR_CONFIG;
+    if (tokens < 0 || top < 1 || rows < 0 || cols < 1) return TCL_ERR_DIMS;
+    if ((tokens && (!out || !position)) || (rows && !Y)) return TCL_ERR_NULL;
+    if (ldy < cols || ldo < cols) return TCL_ERR_LD;
+    if (!on(Y, elem(x_type)) || !on(out, elem(x_type)) || !on(weights, 4) || !on(position, 4)) return TCL_ERR_ALIGN;
+    if (int st = device_check()) return st;
+    RouteRows a = {};
+    a.f32 = x_type == TCL_X_F32;
+    a.tokens = tokens, a.top = top, a.rows = rows, a.cols = cols;
+    a.x = Y, a.ldx = ldy;
+    a.weights = weights;
+    a.position = position;
+    a.out = out, a.ldo = ldo;
+    return status_of(launch_combine(a, stream));
+}
+
+int tcl_combine_grad(int x_type, int tokens, int top, int rows, int cols, const void* G, int ldg, const void* Y, int ldy,
+                     const float* weights, const int32_t* position, const int32_t* source, void* DY, int lddy, float* DW,
+                     cudaStream_t stream) {
+    if (!known(x_type)) return TCL_ERR_CONFIG;
+    if (tokens < 0 || top < 1 || rows < 0 || cols < 1) return TCL_ERR_DIMS;
+    if ((tokens && (!G || !position)) || (DY && rows && !source) || (DW && rows && !Y)) return TCL_ERR_NULL;
+    if (ldg < cols || (DW && ldy < cols) || (DY && lddy < cols)) return TCL_ERR_LD;
+    if (!on(G, elem(x_type)) || !on(Y, elem(x_type)) || !on(DY, elem(x_type)) || !on(DW, 4) || !on(weights, 4) ||
+        !on(position, 4) || !on(source, 4))
+        return TCL_ERR_ALIGN;
+    if (int st = device_check()) return st;
+    if (!DY && !DW) return TCL_OK;
+    RouteRows a = {};
+    a.f32 = x_type == TCL_X_F32;
+    a.tokens = tokens, a.top = top, a.rows = rows, a.cols = cols;
+    a.x = G, a.ldx = ldg;
+    a.y = Y, a.ldy = ldy;
+    a.weights = weights;
+    a.position = position, a.source = source;
+    a.out = DY, a.ldo = lddy;
+    a.dw = DW;
+    return status_of(launch_combine_grad(a, stream));
+}
+
+}  // extern "C"

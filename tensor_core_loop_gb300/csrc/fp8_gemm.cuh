@@ -1,0 +1,550 @@
+// Products of e4m3 matrices that carry one fp32 scale for each 128 values of K.
+//
+// With P_kb the plain product of the operands' k-block kb (128 values of K, or what
+// is left of K in the last block),
+//   out[p][q] = sum over kb of (sp[p][kb] · sq[q][kb]) · P_kb[p][q]
+// where a side's scales belong to its rows or to blocks of 128 rows. A product of two
+// e4m3 values is exact in fp32 and the tensor core adds a block's 128 of them in fp32;
+// the scales differ from block to block, so each P_kb is taken out of tensor memory and
+// added into fp32 registers by one fused multiply-add per element ("promotion").
+//
+// Roles of a CTA (or of each CTA of a pair of SMs):
+//   warp 0      TMA loads of both operands into a ring of 128-byte k-blocks
+//   warp 1      issues the MMAs, four per k-block, into a ring of accumulators
+//   warp 2      copies each k-block's scales into a ring of shared-memory slots (cp.async:
+//               4-byte pieces, so that scales may have any strides)
+//   warps 4..   promotion, and the stores of the finished tile
+//
+// The side in the 128 tensor-memory lanes is P, the one in the columns is Q. Many rows
+// of tokens go to P with the weights' rows in Q; few (SWAP) go to Q, as narrow as the
+// MMA's N allows, with 128 weight rows in P, so that a weight byte is read once for
+// all tokens and no MMA or shared memory is spent on rows that do not exist.
+//
+// Work units are output tiles. Rows sorted by expert come with the experts' offsets on
+// the device: every CTA turns them into a running count of tiles, and walks the tiles
+// blockIdx, blockIdx + grid, ...; tiles past an expert's end read the next expert's rows
+// (harmless: their results are not stored). Rows behind the last expert are written as
+// zeros. In weight-gradient form each expert's k-blocks are its own rows, from an offset
+// that is a multiple of 128, and experts without rows get zeros.
+#pragma once
+
+#include "gemm_kernel_pair.cuh"
+#include "rows8.cuh"
+
+namespace tcl {
+
+enum : unsigned int {
+    DEV_BAD_OFFSETS = 7,   // expert offsets not ascending from 0 within the rows (or, for weight gradients, off 128)
+};
+
+constexpr int kMaxExperts = 1024;
+
+struct Fp8Side {
+    const float* scale;
+    long long s_row, s_group, s_expert;   // strides in elements
+    int block;                            // 1: one scale row for each 128 rows
+};
+
+struct Fp8Params {
+    Fp8Side P, Q;
+    const int* offsets;      // experts + 1 row offsets (NULL: one expert with all rows)
+    int experts;
+    int rows;                // rows of the token side (weight gradient: values of K)
+    int wrows;               // rows of the weight side (weight gradient: rows of P)
+    int qrows;               // weight gradient: rows of Q
+    int num_kb;              // k-blocks of a tile (weight gradient: given by the offsets)
+    int k_tail;              // valid bytes of the last k-block where K is not a multiple of 16, else 0
+    int wgrad;
+    void* C;
+    long long ldc, c_expert;
+    int out_bf16;
+    int vec;                 // rows of C are whole 16-byte pieces
+    unsigned long long timeout_ns;
+    unsigned int* status;
+};
+
+template <int BQ_, bool PAIR_, bool SWAP_>
+struct Fp8Cfg {
+    static constexpr int BQ = BQ_;
+    static constexpr bool PAIR = PAIR_, SWAP = SWAP_;
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int BP = 128 * CTAS;            // rows of P per tile
+    static constexpr int BQL = BQ / CTAS;            // rows of Q that one CTA loads
+    static constexpr int A_BYTES = 128 * 128;
+    static constexpr int B_BYTES = BQL * 128;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = STAGE_BYTES > 40000 ? 4 : STAGE_BYTES > 30000 ? 6 : 8;
+    static constexpr int NB = 512 / BQ < 8 ? 512 / BQ : 8;   // accumulators in tensor memory
+    static constexpr int TMEM_COLS = NB * BQ;
+    static constexpr int PW = BQ >= 64 ? 8 : 4;      // promotion warps, each 32 lanes × CW columns
+    static constexpr int CW = BQ / (PW / 4);
+    static constexpr int CHUNK = CW < 32 ? CW : 32;  // columns per tensor-memory load
+    static constexpr int THREADS = 128 + 32 * PW;
+    static constexpr int SS = 8;                     // scale slots
+    static constexpr int SLOT = 128 + BQ;            // floats: P's scales, then Q's
+    static constexpr int SLOT_Q = 128;
+    static constexpr int TAB = kMaxExperts + 8;
+    static constexpr int NBARS = 2 * STAGES + 2 * SS + 2 * NB + 1;
+    static constexpr int SMEM_BYTES =
+        1024 + STAGES * STAGE_BYTES + SS * SLOT * 4 + 2 * TAB * 4 + (NBARS + 4) * 8;
+    static constexpr uint32_t IDESC = ptx::make_idesc(0, 0, 0, 0, BP, BQ);   // e4m3 both, K-major both
+    static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB per-block shared memory limit");
+    static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TMEM columns");
+    static_assert(BQ % 16 == 0 && CW % CHUNK == 0 && (CHUNK == 16 || CHUNK == 32), "column split");
+};
+
+// One output tile: its first row on either side, the rows that exist, the expert, and
+// the k-blocks [kb0, kb0 + nk).
+struct Fp8Unit {
+    int p0, q0, p_end, q_end, e, kb0, nk;
+};
+
+// The tiles of all experts in one walk. first[e] counts the tiles before expert e;
+// first[experts + 1] is the total (entry `experts` holds the rows behind the last one).
+template <class C>
+__device__ __forceinline__ Fp8Unit fp8_unit(const Fp8Params& p, const int* first, const int* off, int u, int& cur) {
+    Fp8Unit U;
+    if (p.wgrad) {
+        const int tp = (p.wrows + C::BP - 1) / C::BP, tq = (p.qrows + C::BQ - 1) / C::BQ;
+        const int e = u / (tp * tq), r = u - e * (tp * tq);
+        U.e = e;
+        U.p0 = r / tq * C::BP;
+        U.q0 = r % tq * C::BQ;
+        U.p_end = p.wrows;
+        U.q_end = p.qrows;
+        U.kb0 = off[e] >> 7;
+        U.nk = (off[e + 1] >> 7) - U.kb0;
+        return U;
+    }
+    while (u >= first[cur + 1]) ++cur;   // (u only grows along a CTA's walk)
+    constexpr int TT = C::SWAP ? C::BQ : C::BP, TW = C::SWAP ? C::BP : C::BQ;
+    constexpr int G = 8;                 // token tiles that share a pass over the weights
+    const int tw = (p.wrows + TW - 1) / TW;
+    const int t0 = off[cur], t_end = cur < p.experts ? off[cur + 1] : p.rows;
+    const int tt = (t_end - t0 + TT - 1) / TT;
+    const int v = u - first[cur];
+    const int g = v / (G * tw) * G, gn = min(G, tt - g), r = v - g * tw;
+    const int t = t0 + (g + r % gn) * TT, w = r / gn * TW;
+    U.e = cur;
+    U.kb0 = 0;
+    U.nk = cur < p.experts ? p.num_kb : 0;
+    U.p0 = C::SWAP ? w : t;
+    U.q0 = C::SWAP ? t : w;
+    U.p_end = C::SWAP ? p.wrows : t_end;
+    U.q_end = C::SWAP ? t_end : p.wrows;
+    return U;
+}
+
+template <int N>
+__device__ __forceinline__ void fp8_tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
+    if constexpr (N == 32)
+        ptx::tmem_ld_32x32b_x32(addr, r);
+    else
+        ptx::tmem_ld_32x32b_x16(addr, r);
+}
+
+template <int BQ, bool PAIR, bool SWAP>
+__global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP>::THREADS, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                    const Fp8Params p) {
+    using C = Fp8Cfg<BQ, PAIR, SWAP>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = ptx::smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+    float* slots = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(slots + C::SS * C::SLOT);
+    int* first = reinterpret_cast<int*>(bars + C::NBARS + 2);
+    int* off = first + C::TAB;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::NBARS);
+    volatile uint32_t* abort_flag = tmem_holder + 1;
+    volatile uint32_t* bad_offsets = tmem_holder + 2;
+
+    const uint32_t full0 = ptx::smem_u32(bars);
+    const uint32_t empty0 = full0 + 8 * C::STAGES;
+    const uint32_t sfull0 = empty0 + 8 * C::STAGES;
+    const uint32_t sempty0 = sfull0 + 8 * C::SS;
+    const uint32_t accf0 = sempty0 + 8 * C::SS;
+    const uint32_t acce0 = accf0 + 8 * C::NB;
+    const uint32_t drain_bar = acce0 + 8 * C::NB;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            ptx::mbar_init(full0 + 8 * s, 1);     // the (leader's) producer and the bytes
+            ptx::mbar_init(empty0 + 8 * s, 1);    // the MMAs' commit
+        }
+        for (int s = 0; s < C::SS; ++s) {
+            ptx::mbar_init(sfull0 + 8 * s, 32);   // the scale warp's lanes
+            ptx::mbar_init(sempty0 + 8 * s, C::PW);
+        }
+        for (int b = 0; b < C::NB; ++b) {
+            ptx::mbar_init(accf0 + 8 * b, 1);
+            ptx::mbar_init(acce0 + 8 * b, C::CTAS * C::PW);
+        }
+        ptx::mbar_init(drain_bar, 1);
+        *abort_flag = 0u;
+        *bad_offsets = 0u;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&tmP);
+        ptx::prefetch_tensormap(&tmQ);
+    }
+    if (warp == 3) {
+        if constexpr (PAIR) {
+            ptx::tmem_alloc_pair(ptx::smem_u32(tmem_holder), C::TMEM_COLS);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_u32(tmem_holder), C::TMEM_COLS);
+            ptx::tmem_relinquish();
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    if constexpr (PAIR)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    // nothing above touches global memory; the offsets, operands and scales may be the
+    // previous kernel's results
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    // the experts' rows and the running count of their tiles
+    const int E = p.experts;
+    for (int e = threadIdx.x; e <= E; e += C::THREADS) {
+        const int lo = p.offsets ? p.offsets[e] : (e == 0 ? 0 : p.rows);
+        const int hi = e == E ? p.rows : p.offsets ? p.offsets[e + 1] : p.rows;
+        off[e] = lo;
+        if (lo < 0 || lo > hi || hi > p.rows || (e == 0 && lo != 0) || (p.wgrad && (lo & 127))) *bad_offsets = 1u;
+    }
+    __syncthreads();
+    int units = 0;
+    if (*bad_offsets) {
+        if (threadIdx.x == 0) atomicCAS(p.status, 0u, static_cast<unsigned int>(DEV_BAD_OFFSETS));
+    } else if (p.wgrad) {
+        units = E * ((p.wrows + C::BP - 1) / C::BP) * ((p.qrows + BQ - 1) / BQ);
+    } else {
+        constexpr int TT = SWAP ? BQ : C::BP, TW = SWAP ? C::BP : BQ;
+        const int tw = (p.wrows + TW - 1) / TW;
+        if (warp == 0) {
+            int run = 0;
+            for (int e0 = 0; e0 <= E; e0 += 32) {
+                const int e = e0 + lane;
+                int n = 0;
+                if (e <= E) n = ((e < E ? off[e + 1] : p.rows) - off[e] + TT - 1) / TT * tw;
+                int inc = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, inc, d);
+                    if (lane >= d) inc += o;
+                }
+                if (e <= E) first[e + 1] = run + inc;
+                run += __shfl_sync(0xffffffffu, inc, 31);
+            }
+            if (lane == 0) first[0] = 0;
+        }
+        __syncthreads();   // (uniform: every thread takes this branch)
+        units = first[E + 1];
+    }
+    const int u0 = blockIdx.x / C::CTAS, ustep = gridDim.x / C::CTAS;
+    const AbortNet net{ptx::smem_u32(const_cast<uint32_t*>(abort_flag)), C::CTAS};
+    auto wait = [&](uint32_t bar, uint32_t parity, unsigned int code) {
+        if constexpr (PAIR)
+            return wait_warp_pair(bar, parity, abort_flag, net, p.timeout_ns, p.status, code);
+        else
+            return wait_warp(bar, parity, abort_flag, p.timeout_ns, p.status, code);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ operand loads
+        const uint32_t full_leader0 = PAIR ? ptx::mapa_shared(full0, 0u) : full0;
+        uint32_t s = 0, ph = 0;
+        int cur = 0;
+        bool ok = true;
+        for (int u = u0; ok && u < units; u += ustep) {
+            const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+            const int pe = (SWAP && !p.wgrad) ? U.e : 0, qe = (!SWAP && !p.wgrad) ? U.e : 0;
+            const int prow = U.p0 + static_cast<int>(rank) * 128, qrow = U.q0 + static_cast<int>(rank) * C::BQL;
+            for (int kb = 0; kb < U.nk; ++kb) {
+                if (!wait(empty0 + 8 * s, ph ^ 1u, DEV_TIMEOUT_PRODUCER)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sa = ptx::smem_u32(smem) + s * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+                const int x = (U.kb0 + kb) * 128;
+                if (rank == 0) ptx::mbar_arrive_expect_tx_elected(full0 + 8 * s, C::CTAS * C::STAGE_BYTES);
+                if constexpr (PAIR) {
+                    ptx::tma_load_3d_pair_elected(sa, &tmP, full_leader0 + 8 * s, x, prow, pe);
+                    ptx::tma_load_3d_pair_elected(sb, &tmQ, full_leader0 + 8 * s, x, qrow, qe);
+                } else {
+                    ptx::tma_load_3d_elected(sa, &tmP, full0 + 8 * s, x, prow, pe);
+                    ptx::tma_load_3d_elected(sb, &tmQ, full0 + 8 * s, x, qrow, qe);
+                }
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) spin_ns(200000);   // copies issued before the abort land within microseconds
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issue (a pair's leader)
+        if (rank == 0) {
+            const uint32_t stage0 = ptx::smem_u32(smem);
+            const uint64_t adesc0 = ptx::sdesc_sw128(stage0, 16, 1024);
+            const uint64_t bdesc0 = ptx::sdesc_sw128(stage0 + C::A_BYTES, 16, 1024);
+            constexpr uint64_t STEP = C::STAGE_BYTES / 16;
+            uint32_t s = 0, ph = 0, b = 0, bph = 0;
+            int cur = 0;
+            bool ok = true;
+            for (int u = u0; ok && u < units; u += ustep) {
+                const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+                for (int kb = 0; kb < U.nk; ++kb) {
+                    if (!wait(acce0 + 8 * b, bph ^ 1u, DEV_TIMEOUT_MMA_ACC) ||
+                        !wait(full0 + 8 * s, ph, DEV_TIMEOUT_MMA_FULL)) {
+                        ok = false;
+                        break;
+                    }
+                    if constexpr (!PAIR) {
+                        if (p.k_tail && kb + 1 == U.nk) {
+                            // K ends inside a 16-byte piece, of which a tensor copy brings the
+                            // whole: clear what lies behind the end (16-byte units are permuted
+                            // within each 128-byte row by the row's number mod 8)
+                            uint8_t* st = smem + s * C::STAGE_BYTES;
+                            const int unit = p.k_tail >> 4, from = p.k_tail & 15;
+                            for (int r = lane; r < 128 + BQ; r += 32) {
+                                uint8_t* at = st + r * 128 + ((unit ^ (r & 7)) << 4);
+                                for (int i = from; i < 16; ++i) at[i] = 0;
+                            }
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    ptx::tc_fence_after();
+                    const uint64_t ad = adesc0 + s * STEP, bd = bdesc0 + s * STEP;
+                    const uint32_t d = tmem_base + b * BQ;
+                    if constexpr (PAIR) {
+                        ptx::mma_f8_pair_x4_elected(d, ad, bd, ad + 2, bd + 2, ad + 4, bd + 4, ad + 6, bd + 6,
+                                                    C::IDESC, 0u);
+                        ptx::mma_commit_pair_multicast_elected(empty0 + 8 * s, 0x3);
+                        ptx::mma_commit_pair_multicast_elected(accf0 + 8 * b, 0x3);
+                    } else {
+                        ptx::mma_f8_x4_elected(d, ad, bd, ad + 2, bd + 2, ad + 4, bd + 4, ad + 6, bd + 6, C::IDESC,
+                                               0u);
+                        ptx::mma_commit_elected(empty0 + 8 * s);
+                        ptx::mma_commit_elected(accf0 + 8 * b);
+                    }
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    if (++b == C::NB) {
+                        b = 0;
+                        bph ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                if constexpr (PAIR)
+                    ptx::mma_commit_pair_multicast_elected(drain_bar, 0x1);
+                else
+                    ptx::mma_commit_elected(drain_bar);
+                if (lane == 0) wait_drain(drain_bar, 0, p.timeout_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------ scales
+        uint32_t s = 0, ph = 0;
+        int cur = 0;
+        bool ok = true;
+        for (int u = u0; ok && u < units; u += ustep) {
+            const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+            const int prow = U.p0 + static_cast<int>(rank) * 128;
+            const float* ps = p.P.scale + (SWAP ? U.e * p.P.s_expert : 0ll) + U.kb0 * p.P.s_group;
+            const float* qs = p.Q.scale + (SWAP ? 0ll : U.e * p.Q.s_expert) + U.kb0 * p.Q.s_group;
+            for (int kb = 0; kb < U.nk; ++kb) {
+                if (!wait(sempty0 + 8 * s, ph ^ 1u, DEV_TIMEOUT_PRODUCER)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = ptx::smem_u32(slots + s * C::SLOT);
+                const float* pk = ps + kb * p.P.s_group;
+                const float* qk = qs + kb * p.Q.s_group;
+                if (p.P.block) {
+                    if (lane == 0) {
+                        const bool in = prow < U.p_end;
+                        ptx::cp_async_4(dst, in ? pk + (prow >> 7) * p.P.s_row : p.P.scale, in ? 4 : 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = prow + lane + 32 * i;
+                        const bool in = r < U.p_end;
+                        ptx::cp_async_4(dst + 4 * (lane + 32 * i), in ? pk + r * p.P.s_row : p.P.scale, in ? 4 : 0);
+                    }
+                }
+                const uint32_t dq = dst + 4 * C::SLOT_Q;
+                if (p.Q.block) {
+                    if (lane < (BQ + 127) / 128) {
+                        const int r = U.q0 + lane * 128;
+                        const bool in = r < U.q_end;
+                        ptx::cp_async_4(dq + 4 * lane, in ? qk + (r >> 7) * p.Q.s_row : p.Q.scale, in ? 4 : 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < (BQ + 31) / 32; ++i) {
+                        const int c = lane + 32 * i, r = U.q0 + c;
+                        const bool in = r < U.q_end;
+                        if (c < BQ) ptx::cp_async_4(dq + 4 * c, in ? qk + r * p.Q.s_row : p.Q.scale, in ? 4 : 0);
+                    }
+                }
+                ptx::cp_async_arrive_noinc(sfull0 + 8 * s);
+                if (++s == C::SS) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        ptx::cp_async_wait_all();
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------ promotion and stores
+        const int quarter = warp & 3;            // the tensor-memory lanes this warp may read
+        const int h = (warp - 4) >> 2;           // its share of the columns
+        const int prl = quarter * 32 + lane;
+        const uint32_t acce_leader0 = PAIR ? ptx::mapa_shared(acce0, 0u) : acce0;
+        uint32_t s = 0, ph = 0, b = 0, bph = 0;
+        int cur = 0;
+        bool ok = true;
+        for (int u = u0; ok && u < units; u += ustep) {
+            const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+            float acc[C::CW];
+#pragma unroll
+            for (int i = 0; i < C::CW; ++i) acc[i] = 0.0f;
+            for (int kb = 0; kb < U.nk; ++kb) {
+                if (!wait(sfull0 + 8 * s, ph, DEV_TIMEOUT_EPILOGUE) || !wait(accf0 + 8 * b, bph, DEV_TIMEOUT_EPILOGUE)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const float* slot = slots + s * C::SLOT;
+                const float sp = p.P.block ? slot[0] : slot[prl];
+                const float f = p.Q.block ? sp * slot[C::SLOT_Q + ((h * C::CW) >> 7)] : sp;
+                const uint32_t t = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * BQ + h * C::CW;
+#pragma unroll
+                for (int c = 0; c < C::CW; c += C::CHUNK) {
+                    uint32_t r[C::CHUNK];
+                    fp8_tmem_ld<C::CHUNK>(t + c, r);
+                    ptx::tmem_ld_wait(r);
+                    if (c + C::CHUNK == C::CW) {   // the accumulator is read: free for the next k-block
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (PAIR)
+                                ptx::mbar_arrive_cluster_relaxed(acce_leader0 + 8 * b);
+                            else
+                                ptx::mbar_arrive_relaxed(acce0 + 8 * b);
+                        }
+                    }
+                    if (p.Q.block) {
+#pragma unroll
+                        for (int i = 0; i < C::CHUNK; ++i)
+                            acc[c + i] = fmaf(__uint_as_float(r[i]), f, acc[c + i]);
+                    } else {
+                        const float4* q4 = reinterpret_cast<const float4*>(slot + C::SLOT_Q + h * C::CW + c);
+#pragma unroll
+                        for (int i = 0; i < C::CHUNK; i += 4) {
+                            const float4 q = q4[i / 4];
+                            acc[c + i + 0] = fmaf(__uint_as_float(r[i + 0]), f * q.x, acc[c + i + 0]);
+                            acc[c + i + 1] = fmaf(__uint_as_float(r[i + 1]), f * q.y, acc[c + i + 1]);
+                            acc[c + i + 2] = fmaf(__uint_as_float(r[i + 2]), f * q.z, acc[c + i + 2]);
+                            acc[c + i + 3] = fmaf(__uint_as_float(r[i + 3]), f * q.w, acc[c + i + 3]);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sempty0 + 8 * s);
+                if (++s == C::SS) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                if (++b == C::NB) {
+                    b = 0;
+                    bph ^= 1u;
+                }
+            }
+            if (!ok) break;
+            const int pr = U.p0 + static_cast<int>(rank) * 128 + prl;
+            const int qc = U.q0 + h * C::CW;
+            const int n = pr < U.p_end ? min(C::CW, U.q_end - qc) : 0;
+            if constexpr (SWAP) {
+                // consecutive lanes hold consecutive columns of C
+                const long long at = static_cast<long long>(qc) * p.ldc + pr;
+#pragma unroll
+                for (int i = 0; i < C::CW; ++i) {
+                    if (i < n) {
+                        if (p.out_bf16)
+                            static_cast<__nv_bfloat16*>(p.C)[at + i * p.ldc] = __float2bfloat16_rn(acc[i]);
+                        else
+                            static_cast<float*>(p.C)[at + i * p.ldc] = acc[i];
+                    }
+                }
+            } else if (n > 0) {
+                const long long at = (p.wgrad ? U.e * p.c_expert : 0ll) + static_cast<long long>(pr) * p.ldc + qc;
+                if (p.out_bf16) {
+                    __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + at;
+                    if (p.vec && n == C::CW) {
+#pragma unroll
+                        for (int i = 0; i < C::CW; i += 8) {
+                            uint4 v;
+                            v.x = pack_bf16(acc[i + 0], acc[i + 1]);
+                            v.y = pack_bf16(acc[i + 2], acc[i + 3]);
+                            v.z = pack_bf16(acc[i + 4], acc[i + 5]);
+                            v.w = pack_bf16(acc[i + 6], acc[i + 7]);
+                            *reinterpret_cast<uint4*>(c + i) = v;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < C::CW; ++i)
+                            if (i < n) c[i] = __float2bfloat16_rn(acc[i]);
+                    }
+                } else {
+                    float* c = static_cast<float*>(p.C) + at;
+                    if (p.vec && n == C::CW) {
+#pragma unroll
+                        for (int i = 0; i < C::CW; i += 4)
+                            *reinterpret_cast<float4*>(c + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < C::CW; ++i)
+                            if (i < n) c[i] = acc[i];
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        __syncwarp();
+    }
+
+    // ------------------------------------------------ teardown
+    ptx::tc_fence_before();
+    if constexpr (PAIR)
+        ptx::cluster_sync();   // no CTA frees TMEM or exits while its peer may still signal it
+    else
+        __syncthreads();
+    if (warp == 3) {
+        ptx::tc_fence_after();
+        if constexpr (PAIR)
+            ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        else
+            ptx::tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+}
+
+}  // namespace tcl

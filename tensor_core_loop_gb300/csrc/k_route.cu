@@ -1,0 +1,359 @@
+// Tokens sorted by expert and back: the order, the rows laid out in it, the weighted sum of
+// the experts' rows, and its gradients.
+//
+// The order is a counting sort by expert that keeps the slots' order. A block takes 4,096
+// slots, each of its 32 warps 128 consecutive ones. Counts of a warp, then of the warps
+// before it, then of the blocks before it give every slot its row without an atomic whose
+// order could show in the result (the shared-memory atomics below only add counts). One
+// block needs one launch; more need a launch that counts first. Either reads 4 or 8 bytes
+// and writes 4 for each slot and writes 4 for each row: launches, not bytes, take the time.
+//
+// The row kernels are bound by memory: a thread handles eight columns, and a token's row
+// (gather, gradient of combine) is read once for all of its slots.
+#include <algorithm>
+
+#include "fp8_launch.cuh"
+#include "rows8.cuh"
+
+namespace tcl {
+namespace {
+
+constexpr int kSortThreads = 1024, kSortWarps = 32, kPerLane = kSortChunk / kSortThreads;
+
+template <typename ID>
+__device__ __forceinline__ int expert_of(const ID* ids, long long i, long long slots, int experts) {
+    if (i >= slots) return -1;
+    const ID v = ids[i];
+    return v >= 0 && v < experts ? static_cast<int>(v) : -1;
+}
+
+// counts[block][expert]
+template <typename ID>
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const ID* ids, long long slots, int experts,
+                                                                  int* counts) {
+    extern __shared__ int hist[];
+    for (int e = threadIdx.x; e < experts; e += kSortThreads) hist[e] = 0;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    __syncthreads();
+    const long long base = static_cast<long long>(blockIdx.x) * kSortChunk;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+        const int e = expert_of(ids, base + k * kSortThreads + threadIdx.x, slots, experts);
+        if (e >= 0) atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < experts; e += kSortThreads)
+        counts[static_cast<long long>(blockIdx.x) * experts + e] = hist[e];
+}
+
+// counts: NULL for a single block. Shared memory: [warp][expert], then per expert the total,
+// the count of the blocks before this one, the first row, and 32 words for the scan.
+template <typename ID>
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids, long long slots, int experts, int align,
+                                                                  int rows, int* offsets, int* position, int* source,
+                                                                  const int* counts) {
+    extern __shared__ int sm[];
+    int* whist = sm;
+    int* total = whist + kSortWarps * experts;
+    int* before = total + experts;
+    int* firsts = before + experts;   // experts + 1
+    int* part = firsts + experts + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int blocks = gridDim.x;
+    for (int i = threadIdx.x; i < (kSortWarps + 2) * experts; i += kSortThreads) sm[i] = 0;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    __syncthreads();
+
+    // this warp's slots and their counts
+    const long long base = static_cast<long long>(blockIdx.x) * kSortChunk + warp * (kPerLane * 32) + lane;
+    int e[kPerLane], rank[kPerLane];
+    int* mine = whist + warp * experts;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) e[k] = expert_of(ids, base + k * 32, slots, experts);
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+        const unsigned same = __match_any_sync(0xffffffffu, e[k]);
+        const int ahead = __popc(same & ((1u << lane) - 1u));
+        rank[k] = e[k] >= 0 ? mine[e[k]] + ahead : 0;   // among this warp's slots of the expert
+        __syncwarp();
+        if (e[k] >= 0 && ahead == 0) mine[e[k]] += __popc(same);
+        __syncwarp();
+    }
+    if (counts) {
+        const long long n = static_cast<long long>(blocks) * experts;
+        for (long long i = threadIdx.x; i < n; i += kSortThreads) {
+            const int b = static_cast<int>(i / experts), x = static_cast<int>(i - static_cast<long long>(b) * experts);
+            const int c = counts[i];
+            if (c) {
+                atomicAdd(&total[x], c);
+                if (b < static_cast<int>(blockIdx.x)) atomicAdd(&before[x], c);
+            }
+        }
+    }
+    __syncthreads();
+    // (a thread per expert: at most kMaxExperts = 1024) counts of the warps before each warp
+    const int x = threadIdx.x;
+    int length = 0;
+    if (x < experts) {
+        int run = before[x];
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = whist[w * experts + x];
+            whist[w * experts + x] = run;
+            run += c;
+        }
+        if (!counts) total[x] = run;
+        length = (total[x] + align - 1) / align * align;
+    }
+    // first rows: a scan of the rounded lengths
+    int inc = length;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+    }
+    if (lane == 31) part[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        const int own = part[lane];
+        int sum = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        part[lane] = sum - own;
+    }
+    __syncthreads();
+    inc += part[warp];
+    if (x < experts) firsts[x + 1] = inc;
+    if (x == 0) firsts[0] = 0;
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i <= experts; i += kSortThreads) offsets[i] = firsts[i];
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+        const long long i = base + k * 32;
+        if (i >= slots) continue;
+        int r = -1;
+        if (e[k] >= 0) {
+            r = firsts[e[k]] + mine[e[k]] + rank[k];
+            if (r < rows) source[r] = static_cast<int>(i);
+        }
+        position[i] = r;
+    }
+    // rows without a slot: behind each expert's own, and behind the last expert's
+    for (int i = blockIdx.x * kSortWarps + warp; i < experts; i += blocks * kSortWarps)
+        for (int r = firsts[i] + total[i] + lane; r < min(firsts[i + 1], rows); r += 32) source[r] = -1;
+    for (long long r = firsts[experts] + static_cast<long long>(blockIdx.x) * kSortThreads + threadIdx.x; r < rows;
+         r += static_cast<long long>(blocks) * kSortThreads)
+        source[r] = -1;
+}
+
+constexpr int kZeroRows = 64;
+
+// Zeros in the rows that no slot has: rows r0 .. r0+63, this thread's eight columns.
+template <typename T>
+__device__ __forceinline__ void zero_rows(const int* source, int r0, int rows, T* out, long long ldo, int c, int cols,
+                                          bool vec) {
+    const float z[8] = {};
+    for (int r = r0; r < min(r0 + kZeroRows, rows); ++r)
+        if (source[r] < 0 && c < cols) store8(out + r * ldo + c, cols - c, vec, z);
+}
+
+// blockIdx.x: a token, or behind the tokens 64 rows to clear; blockIdx.y: a block's share of
+// the columns.
+template <typename T>
+__global__ void __launch_bounds__(256) gather_kernel(const RouteRows a, bool vec_in, bool vec_out) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+    T* out = static_cast<T*>(a.out);
+    if (blockIdx.x >= static_cast<unsigned>(a.tokens)) {
+        zero_rows(a.source, (blockIdx.x - a.tokens) * kZeroRows, a.rows, out, a.ldo, c, a.cols, vec_out);
+        return;
+    }
+    if (c >= a.cols) return;
+    const long long t = blockIdx.x;
+    float v[8];
+    load8(static_cast<const T*>(a.x) + t * a.ldx + c, a.cols - c, vec_in, v);
+    for (int j = 0; j < a.top; ++j) {
+        const int r = a.position[t * a.top + j];
+        if (r >= 0 && r < a.rows) store8(out + r * a.ldo + c, a.cols - c, vec_out, v);   // (rounding gives v back)
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) combine_kernel(const RouteRows a, bool vec_in, bool vec_out) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+    if (c >= a.cols) return;
+    const long long t = blockIdx.x;
+    const T* y = static_cast<const T*>(a.x);
+    float sum[8] = {};
+    // four slots' loads in flight at a time
+    for (int j0 = 0; j0 < a.top; j0 += 4) {
+        float v[4][8], w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int j = j0 + k;
+            const int r = j < a.top ? a.position[t * a.top + j] : -1;
+            const bool in = r >= 0 && r < a.rows;
+            w[k] = in ? (a.weights ? a.weights[t * a.top + j] : 1.0f) : 0.0f;
+            load8(y + (in ? r * a.ldx + c : 0), in ? a.cols - c : 0, vec_in, v[k]);   // (zeros for a dropped slot)
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[k], v[k][i], sum[i]);
+    }
+    store8(static_cast<T*>(a.out) + t * a.ldo + c, a.cols - c, vec_out, sum);
+}
+
+// A block per token: its gradient row is read for eight slots at a time. blockIdx.x behind the
+// tokens: rows to clear.
+template <typename T>
+__global__ void __launch_bounds__(256) combine_grad_kernel(const RouteRows a, bool vec_g, bool vec_y, bool vec_out) {
+    __shared__ float part[8][8];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    T* dy = static_cast<T*>(a.out);
+    if (blockIdx.x >= static_cast<unsigned>(a.tokens)) {
+        for (int c = threadIdx.x * 8; c < a.cols; c += blockDim.x * 8)
+            zero_rows(a.source, (blockIdx.x - a.tokens) * kZeroRows, a.rows, dy, a.ldo, c, a.cols, vec_out);
+        return;
+    }
+    const long long t = blockIdx.x;
+    const T* g = static_cast<const T*>(a.x) + t * a.ldx;
+    const T* y = static_cast<const T*>(a.y);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    for (int j0 = 0; j0 < a.top; j0 += 8) {
+        int r[8];
+        float w[8], dot[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int j = j0 + k;
+            r[k] = j < a.top ? a.position[t * a.top + j] : -1;
+            if (r[k] >= a.rows) r[k] = -1;
+            w[k] = r[k] >= 0 ? (a.weights ? a.weights[t * a.top + j] : 1.0f) : 0.0f;
+            dot[k] = 0.0f;
+        }
+        for (int c = threadIdx.x * 8; c < a.cols; c += blockDim.x * 8) {
+            float gv[8];
+            load8(g + c, a.cols - c, vec_g, gv);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (r[k] < 0) continue;
+                if (a.dw) {
+                    float yv[8];
+                    load8(y + r[k] * a.ldy + c, a.cols - c, vec_y, yv);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dot[k] = fmaf(gv[i], yv[i], dot[k]);
+                }
+                if (dy) {
+                    float d[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) d[i] = w[k] * gv[i];
+                    store8(dy + r[k] * a.ldo + c, a.cols - c, vec_out, d);
+                }
+            }
+        }
+        if (!a.dw) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], d);
+            if (lane == 0) part[warp][k] = dot[k];
+        }
+        __syncthreads();
+        if (threadIdx.x < 8 && j0 + threadIdx.x < a.top) {
+            float sum = 0.0f;
+            for (int i = 0; i < warps; ++i) sum += part[i][threadIdx.x];
+            a.dw[t * a.top + j0 + threadIdx.x] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T>
+bool vec16(const void* p, long long ld) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<long long>(sizeof(T)) % 16 == 0;
+}
+
+int row_threads(int cols) { return std::min(256, ((cols + 7) / 8 + 31) / 32 * 32); }
+
+template <typename T>
+cudaError_t gather(const RouteRows& a, cudaStream_t stream) {
+    const int th = row_threads(a.cols);
+    const long long x = static_cast<long long>(a.tokens) + (a.rows + kZeroRows - 1) / kZeroRows;
+    if (x == 0) return cudaSuccess;
+    const int by = (a.cols + th * 8 - 1) / (th * 8);
+    if (x > 0x7fffffffll || by > 65535) return cudaErrorInvalidValue;
+    return launch_pdl(gather_kernel<T>, dim3(static_cast<unsigned>(x), by), th, 0, stream, a, vec16<T>(a.x, a.ldx),
+                      vec16<T>(a.out, a.ldo));
+}
+
+template <typename T>
+cudaError_t combine(const RouteRows& a, cudaStream_t stream) {
+    if (a.tokens == 0) return cudaSuccess;
+    const int th = row_threads(a.cols);
+    const int by = (a.cols + th * 8 - 1) / (th * 8);
+    if (by > 65535) return cudaErrorInvalidValue;
+    return launch_pdl(combine_kernel<T>, dim3(a.tokens, by), th, 0, stream, a, vec16<T>(a.x, a.ldx),
+                      vec16<T>(a.out, a.ldo));
+}
+
+template <typename T>
+cudaError_t combine_grad(const RouteRows& a, cudaStream_t stream) {
+    const long long x = static_cast<long long>(a.tokens) + (a.out ? (a.rows + kZeroRows - 1) / kZeroRows : 0);
+    if (x == 0) return cudaSuccess;
+    if (x > 0x7fffffffll) return cudaErrorInvalidValue;
+    return launch_pdl(combine_grad_kernel<T>, dim3(static_cast<unsigned>(x)), row_threads(a.cols), 0, stream, a,
+                      vec16<T>(a.x, a.ldx), vec16<T>(a.y, a.ldy), vec16<T>(a.out, a.ldo));
+}
+
+template <typename ID>
+cudaError_t sort(long long slots, const ID* ids, int experts, int align, int rows, int* offsets, int* position,
+                 int* source, int* counts, cudaStream_t stream) {
+    const int blocks = static_cast<int>(std::max(1ll, (slots + kSortChunk - 1) / kSortChunk));
+    const size_t smem = sizeof(int) * ((kSortWarps + 3) * static_cast<size_t>(experts) + 1 + kSortWarps);
+    if (smem > 48 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(sort_place_kernel<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     static_cast<int>(smem));
+        if (err != cudaSuccess) return err;
+    }
+    if (blocks > 1) {
+        const cudaError_t err = launch_pdl(sort_count_kernel<ID>, dim3(blocks), kSortThreads, sizeof(int) * experts,
+                                           stream, ids, slots, experts, counts);
+        if (err != cudaSuccess) return err;
+    }
+    return launch_pdl(sort_place_kernel<ID>, dim3(blocks), kSortThreads, smem, stream, ids, slots, experts, align, rows,
+                      offsets, position, source, blocks > 1 ? counts : nullptr);
+}
+
+}  // namespace
+
+cudaError_t launch_sort(long long slots, const void* ids, int id_bytes, int experts, int align, int rows, int* offsets,
+                        int* position, int* source, int* counts, cudaStream_t stream) {
+    if (id_bytes == 8)
+        return sort(slots, static_cast<const long long*>(ids), experts, align, rows, offsets, position, source, counts,
+                    stream);
+    return sort(slots, static_cast<const int*>(ids), experts, align, rows, offsets, position, source, counts, stream);
+}
+
+cudaError_t launch_gather(const RouteRows& a, cudaStream_t stream) {
+    return a.f32 ? gather<float>(a, stream) : gather<__nv_bfloat16>(a, stream);
+}
+
+cudaError_t launch_combine(const RouteRows& a, cudaStream_t stream) {
+    return a.f32 ? combine<float>(a, stream) : combine<__nv_bfloat16>(a, stream);
+}
+
+cudaError_t launch_combine_grad(const RouteRows& a, cudaStream_t stream) {
+    return a.f32 ? combine_grad<float>(a, stream) : combine_grad<__nv_bfloat16>(a, stream);
+}
+
+}  // namespace tcl

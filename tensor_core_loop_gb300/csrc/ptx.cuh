@@ -136,6 +136,11 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
                  : "memory");
 }
 
+// The 4-byte form (4-byte aligned addresses; src_bytes 0 writes zeros and reads nothing).
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
 // Arrive on the mbarrier once every cp.async this thread issued so far has
 // landed. `noinc`: the arrival counts against the barrier's expected count.
 __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {
@@ -367,6 +372,40 @@ __device__ __forceinline__ void mma_tf32_pair_x4_elected(uint32_t d, uint64_t a0
         "@el tcgen05.mma.cta_group::2.kind::tf32 [%0], %3, %4, %9, pt;\n\t"
         "@el tcgen05.mma.cta_group::2.kind::tf32 [%0], %5, %6, %9, pt;\n\t"
         "@el tcgen05.mma.cta_group::2.kind::tf32 [%0], %7, %8, %9, pt;\n\t}" ::"r"(d),
+        "l"(a0), "l"(b0), "l"(a1), "l"(b1), "l"(a2), "l"(b2), "l"(a3), "l"(b3), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// One 128-byte k-block of 8-bit floating point operands: four MMAs of 32 values of K each
+// (formats in the instruction descriptor), otherwise as above.
+__device__ __forceinline__ void mma_f8_x4_elected(uint32_t d, uint64_t a0, uint64_t b0, uint64_t a1, uint64_t b1,
+                                                  uint64_t a2, uint64_t b2, uint64_t a3, uint64_t b3,
+                                                  uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred el, p0, pt;\n\t.reg .b32 lane_sel;\n\t"
+        "elect.sync lane_sel|el, 0xffffffff;\n\t"
+        "setp.ne.b32 p0, %10, 0;\n\t"
+        "setp.eq.b32 pt, 0, 0;\n\t"
+        "@el tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %9, p0;\n\t"
+        "@el tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %3, %4, %9, pt;\n\t"
+        "@el tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %5, %6, %9, pt;\n\t"
+        "@el tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %7, %8, %9, pt;\n\t}" ::"r"(d),
+        "l"(a0), "l"(b0), "l"(a1), "l"(b1), "l"(a2), "l"(b2), "l"(a3), "l"(b3), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_f8_pair_x4_elected(uint32_t d, uint64_t a0, uint64_t b0, uint64_t a1,
+                                                       uint64_t b1, uint64_t a2, uint64_t b2, uint64_t a3,
+                                                       uint64_t b3, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred el, p0, pt;\n\t.reg .b32 lane_sel;\n\t"
+        "elect.sync lane_sel|el, 0xffffffff;\n\t"
+        "setp.ne.b32 p0, %10, 0;\n\t"
+        "setp.eq.b32 pt, 0, 0;\n\t"
+        "@el tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %9, p0;\n\t"
+        "@el tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %3, %4, %9, pt;\n\t"
+        "@el tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %5, %6, %9, pt;\n\t"
+        "@el tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %7, %8, %9, pt;\n\t}" ::"r"(d),
         "l"(a0), "l"(b0), "l"(a1), "l"(b1), "l"(a2), "l"(b2), "l"(a3), "l"(b3), "r"(idesc), "r"(acc)
         : "memory");
 }
