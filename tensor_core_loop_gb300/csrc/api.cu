@@ -1477,19 +1477,30 @@ int stream_scratch(cudaStream_t stream, size_t need, void** out) {
     return TCL_OK;
 }
 
-int tensor_map_bytes(const void* ptr, uint64_t k, uint64_t rows, uint64_t mats, uint64_t row_stride, uint64_t mat_stride,
-                     uint32_t box_rows, CUtensorMap* out) {
+static int encode_3d(CUtensorMapDataType type, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
+                     uint64_t stride2, uint32_t b0, uint32_t b1, CUtensorMap* out) {
     std::lock_guard<std::mutex> lock(g_mu);
     int st = encode_fn();
     if (st) return st;
-    const cuuint64_t dims[3] = {k, rows, mats};
-    const cuuint64_t strides[2] = {row_stride, mat_stride};
-    const cuuint32_t box[3] = {128, box_rows, 1};
+    const cuuint64_t dims[3] = {d0, d1, d2};
+    const cuuint64_t strides[2] = {stride1, stride2};
+    const cuuint32_t box[3] = {b0, b1, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+    CUresult r = g_encode(out, type, 3, const_cast<void*>(ptr), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? TCL_OK : TCL_ERR_LAUNCH;
+}
+
+int tensor_map_bytes(const void* ptr, uint64_t k, uint64_t rows, uint64_t mats, uint64_t row_stride, uint64_t mat_stride,
+                     uint32_t box_rows, CUtensorMap* out) {
+    return encode_3d(CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, k, rows, mats, row_stride, mat_stride, 128, box_rows, out);
+}
+
+int tensor_map_result(const void* ptr, int bf16, uint64_t cols, uint64_t rows, uint64_t mats, uint64_t row_stride,
+                      uint64_t mat_stride, CUtensorMap* out) {
+    return encode_3d(bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ptr, cols, rows, mats,
+                     row_stride, mat_stride, bf16 ? 64 : 32, 32, out);
 }
 
 }  // namespace tcl

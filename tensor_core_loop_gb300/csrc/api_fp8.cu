@@ -53,12 +53,14 @@ int lay_out(Operand& o, uint8_t* to, cudaStream_t stream) {
     return TCL_OK;
 }
 
-// The tile for products with `tokens` rows in all, for `experts` experts. Few rows go to
-// the MMA's N side, many to its M side.
-Fp8Tile choose_tile(long long tokens, int experts) {
+// The tile for products of `tokens` rows, for `experts` experts, with N columns. Few rows go
+// to the MMA's N side, many to its M side. (A pair's MMA warp sees only its own SM's shared
+// memory, so it cannot clear a K tail inside a 16-byte piece.)
+Fp8Tile choose_tile(long long tokens, int experts, int N, bool k_tail) {
     const long long each = (tokens + experts - 1) / experts;
     if (each <= 16) return Fp8Tile::FEW16;
     if (each <= 32) return Fp8Tile::FEW32;
+    if (each >= 256 && N >= 256 && !k_tail) return Fp8Tile::PAIR;
     return Fp8Tile::ONE;
 }
 
@@ -84,6 +86,13 @@ int product(Operand a, Fp8Side sa, Operand b, Fp8Side sb, Fp8Tile tile, Fp8Param
         (st = tensor_map_bytes(oq.p, oq.k, oq.rows, oq.mats, oq.ld, oq.mats > 1 ? oq.mat : up(oq.ld * oq.rows, 16),
                                t.box_q, &l.tmQ)))
         return st;
+    if (p.vec && !t.swap) {
+        const int es = p.out_bf16 ? 2 : 4;
+        const long long rows = p.wgrad ? p.wrows : p.rows, cols = p.wgrad ? p.qrows : p.wrows;
+        if ((st = tensor_map_result(p.C, p.out_bf16, cols, rows, p.wgrad ? p.experts : 1, p.ldc * es,
+                                    p.wgrad && p.experts > 1 ? p.c_expert * es : p.ldc * es * rows, &l.tmC)))
+            return st;
+    }
     p.P = t.swap ? sb : sa;
     p.Q = t.swap ? sa : sb;
     p.timeout_ns = kTimeoutNs;
@@ -112,7 +121,7 @@ int rows_product(int rows, int experts, int N, int K, const void* A, int lda, co
     int st = device_context(&dev, &sms, &status);
     if (st) return st;
     if (rows == 0) return TCL_OK;
-    const Fp8Tile tile = choose_tile(rows, experts);
+    const Fp8Tile tile = choose_tile(rows, experts, N, K % 16 != 0);
     const Fp8TileInfo t = fp8_tile_info(tile);
     const int tt = t.swap ? t.bq : t.bp, tw = t.swap ? t.bp : t.bq;
     Fp8Params p = {};
@@ -233,7 +242,7 @@ int gemm_fp8_experts_wgrad(int rows, int experts, int N, int K, const void* A, i
                 return status_of(cudaErrorUnknown);
         return TCL_OK;
     }
-    const Fp8Tile tile = Fp8Tile::ONE;
+    const Fp8Tile tile = choose_tile(N, 1, K, false) == Fp8Tile::PAIR ? Fp8Tile::PAIR : Fp8Tile::ONE;
     const Fp8TileInfo t = fp8_tile_info(tile);
     Fp8Params p = {};
     p.offsets = offsets;

@@ -11,9 +11,14 @@
 // Roles of a CTA (or of each CTA of a pair of SMs):
 //   warp 0      TMA loads of both operands into a ring of 128-byte k-blocks
 //   warp 1      issues the MMAs, four per k-block, into a ring of accumulators
-//   warp 2      copies each k-block's scales into a ring of shared-memory slots (cp.async:
-//               4-byte pieces, so that scales may have any strides)
+//   warps 2, 3  copy each k-block's scales of P and of Q into a ring of shared-memory slots
+//               (cp.async: 4-byte pieces, so that scales may have any strides). One warp for
+//               both, working out addresses for every k-block, paced the whole kernel.
 //   warps 4..   promotion, and the stores of the finished tile
+//
+// The promotion of a k-block has to fit beside its MMAs (256 × 256 tile: 512 cycles): per SM
+// quarter 256 cycles of multiply-adds and as many of tensor-memory loads. With eight warps of
+// 128 sums a thread, what decides is that nothing is spilled to local memory in the loop.
 //
 // The side in the 128 tensor-memory lanes is P, the one in the columns is Q. Many rows
 // of tokens go to P with the weights' rows in Q; few (SWAP) go to Q, as narrow as the
@@ -63,30 +68,38 @@ struct Fp8Params {
     unsigned int* status;
 };
 
-template <int BQ_, bool PAIR_, bool SWAP_>
+template <int BQ_, bool PAIR_, bool SWAP_, bool QVEC_>
 struct Fp8Cfg {
     static constexpr int BQ = BQ_;
-    static constexpr bool PAIR = PAIR_, SWAP = SWAP_;
+    static constexpr bool PAIR = PAIR_, SWAP = SWAP_, QVEC = QVEC_;   // QVEC: a scale for each row of Q
     static constexpr int CTAS = PAIR ? 2 : 1;
     static constexpr int BP = 128 * CTAS;            // rows of P per tile
     static constexpr int BQL = BQ / CTAS;            // rows of Q that one CTA loads
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int B_BYTES = BQL * 128;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = STAGE_BYTES > 40000 ? 4 : STAGE_BYTES > 30000 ? 6 : 8;
+    static constexpr int STAGES = SWAP ? 8 : 4;
     static constexpr int NB = 512 / BQ < 8 ? 512 / BQ : 8;   // accumulators in tensor memory
     static constexpr int TMEM_COLS = NB * BQ;
-    static constexpr int PW = BQ >= 64 ? 8 : 4;      // promotion warps, each 32 lanes × CW columns
+    static constexpr int PW = BQ >= 64 ? 8 : 4;   // promotion warps, each 32 lanes × CW columns
     static constexpr int CW = BQ / (PW / 4);
-    static constexpr int CHUNK = CW < 32 ? CW : 32;  // columns per tensor-memory load
+    static constexpr int CHUNK = CW < 32 || (QVEC && CW > 64) ? 16 : 32;   // columns per tensor-memory load
     static constexpr int THREADS = 128 + 32 * PW;
-    static constexpr int SS = 8;                     // scale slots
-    static constexpr int SLOT = 128 + BQ;            // floats: P's scales, then Q's
-    static constexpr int SLOT_Q = 128;
+    // A finished tile of the unswapped form leaves through slabs of 32 rows × 128 bytes (16-byte
+    // units permuted by the row, as the tensor copies do), SLABS of them per promotion warp
+    static constexpr int SLABS = 2;
+    static constexpr int SLAB_BYTES = 32 * 128;
+    static constexpr int STORE_BYTES = SWAP ? 0 : PW * SLABS * SLAB_BYTES;
+    // 128 sums per thread need more than the 168 registers a thread of 384 starts with: the
+    // roles' warpgroup gives some of its own up (128·56 + 256·224 = 384·168)
+    static constexpr bool SPLIT_REGS = CW > 64;
+    static constexpr int SS = 8;                     // scale slots, a k-block each
+    static constexpr int SLOT_Q = 128;               // a slot: P's scales, then Q's (each, or one per 128 rows)
+    static constexpr int SLOT = SLOT_Q + (QVEC ? BQ : 4);
     static constexpr int TAB = kMaxExperts + 8;
     static constexpr int NBARS = 2 * STAGES + 2 * SS + 2 * NB + 1;
     static constexpr int SMEM_BYTES =
-        1024 + STAGES * STAGE_BYTES + SS * SLOT * 4 + 2 * TAB * 4 + (NBARS + 4) * 8;
+        1024 + STAGES * STAGE_BYTES + STORE_BYTES + SS * SLOT * 4 + 2 * TAB * 4 + (NBARS + 4) * 8;
     static constexpr uint32_t IDESC = ptx::make_idesc(0, 0, 0, 0, BP, BQ);   // e4m3 both, K-major both
     static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB per-block shared memory limit");
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TMEM columns");
@@ -143,15 +156,99 @@ __device__ __forceinline__ void fp8_tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
         ptx::tmem_ld_32x32b_x16(addr, r);
 }
 
-template <int BQ, bool PAIR, bool SWAP>
-__global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP>::THREADS, 1)
+// Promotion of 32 (or 16) columns: sum += r · f, or r · (f · q[column]).
+template <int N>
+__device__ __forceinline__ void fp8_promote(uint64_t* sum, const uint32_t (&r)[N], float f) {
+    const uint64_t ff = ptx::f32x2(f, f);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) sum[i / 2] = ptx::fma_f32x2(ptx::f32x2(r[i], r[i + 1]), ff, sum[i / 2]);
+}
+template <int N>
+__device__ __forceinline__ void fp8_promote(uint64_t* sum, const uint32_t (&r)[N], float f, const float* q) {
+    const uint64_t ff = ptx::f32x2(f, f);
+    const ulonglong2* q4 = reinterpret_cast<const ulonglong2*>(q);
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const ulonglong2 qq = q4[i / 4];
+        sum[i / 2] = ptx::fma_f32x2(ptx::f32x2(r[i], r[i + 1]), ptx::mul_f32x2(ff, qq.x), sum[i / 2]);
+        sum[i / 2 + 1] = ptx::fma_f32x2(ptx::f32x2(r[i + 2], r[i + 3]), ptx::mul_f32x2(ff, qq.y), sum[i / 2 + 1]);
+    }
+}
+
+// Stores a warp's 32 rows × CW columns (lane: row), a slab of 128 bytes of each row at a time.
+// Whole slabs are copied out by the tensor copy engine while the warp goes on with the next
+// tile (a tile's stores take longer than a k-block of its successor: waiting for them cost
+// 12 % of a product with K = 4096 and a sixth of one with K = 2048); the map cuts columns
+// behind the matrix off. A slab that an expert's end cuts, or whose rows do not start and end on
+// whole 16-byte pieces, is read back and stored piece by piece, four rows to an instruction.
+template <class C, typename T>
+__device__ __forceinline__ void fp8_store_rows(const uint64_t (&sum)[C::CW / 2], uint8_t* slabs, int& used,
+                                               const CUtensorMap* map, T* c, long long ldc, int row, int col, int e,
+                                               int rows, int cols, bool vec, int lane) {
+    constexpr int PER = 128 / sizeof(T), UNIT = 16 / sizeof(T);   // columns of a slab, of a 16-byte unit
+    auto place = [](int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); };
+    // (a copy rounds a row's end up to 16 bytes)
+    const bool bulk = vec && rows >= 32, whole = cols % UNIT == 0;
+#pragma unroll
+    for (int c0 = 0; c0 < C::CW; c0 += PER) {
+        uint8_t* slab = slabs + used * C::SLAB_BYTES;
+        used = used + 1 == C::SLABS ? 0 : used + 1;
+        if (lane == 0) ptx::bulk_wait_read<C::SLABS - 1>();   // the copy that last used this slab has read it
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            uint4 v;
+            const uint64_t* s = sum + (c0 + u * UNIT) / 2;
+            if constexpr (sizeof(T) == 2) {
+                const float2 a = ptx::f32x2_get(s[0]), b = ptx::f32x2_get(s[1]), d = ptx::f32x2_get(s[2]),
+                             e4 = ptx::f32x2_get(s[3]);
+                v = make_uint4(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y), pack_bf16(d.x, d.y), pack_bf16(e4.x, e4.y));
+            } else {
+                const float2 a = ptx::f32x2_get(s[0]), b = ptx::f32x2_get(s[1]);
+                v = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+            }
+            *reinterpret_cast<uint4*>(slab + place(lane, u)) = v;
+        }
+        if (bulk && (whole || c0 + PER <= cols)) {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (c0 < cols) ptx::tma_store_3d(map, ptx::smem_u32(slab), col + c0, row, e);
+                ptx::bulk_commit();
+            }
+            continue;
+        }
+        __syncwarp();
+        const int u = lane & 7, n = cols - c0 - u * UNIT;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = k * 4 + (lane >> 3);
+            const T* from = reinterpret_cast<const T*>(slab + place(r, u));
+            T* to = c + r * ldc + c0 + u * UNIT;
+            if (r >= rows) continue;
+            if (vec && n >= UNIT) {
+                *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+            } else {
+#pragma unroll
+                for (int i = 0; i < UNIT; ++i)
+                    if (i < n) to[i] = from[i];
+            }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::bulk_commit();   // (an empty group: every slab used counts as one)
+    }
+}
+
+template <int BQ, bool PAIR, bool SWAP, bool QVEC>
+__global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                    const Fp8Params p) {
-    using C = Fp8Cfg<BQ, PAIR, SWAP>;
+                    const __grid_constant__ CUtensorMap tmC, const Fp8Params p) {
+    using C = Fp8Cfg<BQ, PAIR, SWAP, QVEC>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
-    float* slots = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);
+    uint8_t* slabs = smem + C::STAGES * C::STAGE_BYTES;
+    float* slots = reinterpret_cast<float*>(slabs + C::STORE_BYTES);
     uint64_t* bars = reinterpret_cast<uint64_t*>(slots + C::SS * C::SLOT);
     int* first = reinterpret_cast<int*>(bars + C::NBARS + 2);
     int* off = first + C::TAB;
@@ -177,7 +274,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP>::THREADS, 1)
             ptx::mbar_init(empty0 + 8 * s, 1);    // the MMAs' commit
         }
         for (int s = 0; s < C::SS; ++s) {
-            ptx::mbar_init(sfull0 + 8 * s, 32);   // the scale warp's lanes
+            ptx::mbar_init(sfull0 + 8 * s, 64);   // the scale warps' lanes
             ptx::mbar_init(sempty0 + 8 * s, C::PW);
         }
         for (int b = 0; b < C::NB; ++b) {
@@ -190,6 +287,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP>::THREADS, 1)
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&tmP);
         ptx::prefetch_tensormap(&tmQ);
+        if (!SWAP && p.vec) ptx::prefetch_tensormap(&tmC);
     }
     if (warp == 3) {
         if constexpr (PAIR) {
@@ -251,7 +349,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP>::THREADS, 1)
         units = first[E + 1];
     }
     const int u0 = blockIdx.x / C::CTAS, ustep = gridDim.x / C::CTAS;
-    const AbortNet net{ptx::smem_u32(const_cast<uint32_t*>(abort_flag)), C::CTAS};
+    [[maybe_unused]] const AbortNet net{ptx::smem_u32(const_cast<uint32_t*>(abort_flag)), C::CTAS};
     auto wait = [&](uint32_t bar, uint32_t parity, unsigned int code) {
         if constexpr (PAIR)
             return wait_warp_pair(bar, parity, abort_flag, net, p.timeout_ns, p.status, code);
@@ -259,161 +357,148 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP>::THREADS, 1)
             return wait_warp(bar, parity, abort_flag, p.timeout_ns, p.status, code);
     };
 
-    if (warp == 0) {
-        // ------------------------------------------------ operand loads
-        const uint32_t full_leader0 = PAIR ? ptx::mapa_shared(full0, 0u) : full0;
-        uint32_t s = 0, ph = 0;
-        int cur = 0;
-        bool ok = true;
-        for (int u = u0; ok && u < units; u += ustep) {
-            const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
-            const int pe = (SWAP && !p.wgrad) ? U.e : 0, qe = (!SWAP && !p.wgrad) ? U.e : 0;
-            const int prow = U.p0 + static_cast<int>(rank) * 128, qrow = U.q0 + static_cast<int>(rank) * C::BQL;
-            for (int kb = 0; kb < U.nk; ++kb) {
-                if (!wait(empty0 + 8 * s, ph ^ 1u, DEV_TIMEOUT_PRODUCER)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t sa = ptx::smem_u32(smem) + s * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-                const int x = (U.kb0 + kb) * 128;
-                if (rank == 0) ptx::mbar_arrive_expect_tx_elected(full0 + 8 * s, C::CTAS * C::STAGE_BYTES);
-                if constexpr (PAIR) {
-                    ptx::tma_load_3d_pair_elected(sa, &tmP, full_leader0 + 8 * s, x, prow, pe);
-                    ptx::tma_load_3d_pair_elected(sb, &tmQ, full_leader0 + 8 * s, x, qrow, qe);
-                } else {
-                    ptx::tma_load_3d_elected(sa, &tmP, full0 + 8 * s, x, prow, pe);
-                    ptx::tma_load_3d_elected(sb, &tmQ, full0 + 8 * s, x, qrow, qe);
-                }
-                if (++s == C::STAGES) {
-                    s = 0;
-                    ph ^= 1u;
-                }
-            }
-        }
-        if (!ok && lane == 0) spin_ns(200000);   // copies issued before the abort land within microseconds
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issue (a pair's leader)
-        if (rank == 0) {
-            const uint32_t stage0 = ptx::smem_u32(smem);
-            const uint64_t adesc0 = ptx::sdesc_sw128(stage0, 16, 1024);
-            const uint64_t bdesc0 = ptx::sdesc_sw128(stage0 + C::A_BYTES, 16, 1024);
-            constexpr uint64_t STEP = C::STAGE_BYTES / 16;
-            uint32_t s = 0, ph = 0, b = 0, bph = 0;
+    if (warp < 4) {
+        if constexpr (C::SPLIT_REGS) ptx::setmaxnreg_dec<56>();
+        if (warp == 0) {
+            // ------------------------------------------------ operand loads
+            const uint32_t full_leader0 = PAIR ? ptx::mapa_shared(full0, 0u) : full0;
+            uint32_t s = 0, ph = 0;
             int cur = 0;
             bool ok = true;
             for (int u = u0; ok && u < units; u += ustep) {
                 const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+                const int pe = (SWAP && !p.wgrad) ? U.e : 0, qe = (!SWAP && !p.wgrad) ? U.e : 0;
+                const int prow = U.p0 + static_cast<int>(rank) * 128, qrow = U.q0 + static_cast<int>(rank) * C::BQL;
                 for (int kb = 0; kb < U.nk; ++kb) {
-                    if (!wait(acce0 + 8 * b, bph ^ 1u, DEV_TIMEOUT_MMA_ACC) ||
-                        !wait(full0 + 8 * s, ph, DEV_TIMEOUT_MMA_FULL)) {
+                    if (!wait(empty0 + 8 * s, ph ^ 1u, DEV_TIMEOUT_PRODUCER)) {
                         ok = false;
                         break;
                     }
-                    if constexpr (!PAIR) {
-                        if (p.k_tail && kb + 1 == U.nk) {
-                            // K ends inside a 16-byte piece, of which a tensor copy brings the
-                            // whole: clear what lies behind the end (16-byte units are permuted
-                            // within each 128-byte row by the row's number mod 8)
-                            uint8_t* st = smem + s * C::STAGE_BYTES;
-                            const int unit = p.k_tail >> 4, from = p.k_tail & 15;
-                            for (int r = lane; r < 128 + BQ; r += 32) {
-                                uint8_t* at = st + r * 128 + ((unit ^ (r & 7)) << 4);
-                                for (int i = from; i < 16; ++i) at[i] = 0;
-                            }
-                            ptx::fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
-                    ptx::tc_fence_after();
-                    const uint64_t ad = adesc0 + s * STEP, bd = bdesc0 + s * STEP;
-                    const uint32_t d = tmem_base + b * BQ;
+                    const uint32_t sa = ptx::smem_u32(smem) + s * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+                    const int x = (U.kb0 + kb) * 128;
+                    if (rank == 0) ptx::mbar_arrive_expect_tx_elected(full0 + 8 * s, C::CTAS * C::STAGE_BYTES);
                     if constexpr (PAIR) {
-                        ptx::mma_f8_pair_x4_elected(d, ad, bd, ad + 2, bd + 2, ad + 4, bd + 4, ad + 6, bd + 6,
-                                                    C::IDESC, 0u);
-                        ptx::mma_commit_pair_multicast_elected(empty0 + 8 * s, 0x3);
-                        ptx::mma_commit_pair_multicast_elected(accf0 + 8 * b, 0x3);
+                        ptx::tma_load_3d_pair_elected(sa, &tmP, full_leader0 + 8 * s, x, prow, pe);
+                        ptx::tma_load_3d_pair_elected(sb, &tmQ, full_leader0 + 8 * s, x, qrow, qe);
                     } else {
-                        ptx::mma_f8_x4_elected(d, ad, bd, ad + 2, bd + 2, ad + 4, bd + 4, ad + 6, bd + 6, C::IDESC,
-                                               0u);
-                        ptx::mma_commit_elected(empty0 + 8 * s);
-                        ptx::mma_commit_elected(accf0 + 8 * b);
+                        ptx::tma_load_3d_elected(sa, &tmP, full0 + 8 * s, x, prow, pe);
+                        ptx::tma_load_3d_elected(sb, &tmQ, full0 + 8 * s, x, qrow, qe);
                     }
                     if (++s == C::STAGES) {
                         s = 0;
                         ph ^= 1u;
                     }
-                    if (++b == C::NB) {
-                        b = 0;
-                        bph ^= 1u;
-                    }
                 }
             }
-            if (!ok) {
-                if constexpr (PAIR)
-                    ptx::mma_commit_pair_multicast_elected(drain_bar, 0x1);
-                else
-                    ptx::mma_commit_elected(drain_bar);
-                if (lane == 0) wait_drain(drain_bar, 0, p.timeout_ns);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ------------------------------------------------ scales
-        uint32_t s = 0, ph = 0;
-        int cur = 0;
-        bool ok = true;
-        for (int u = u0; ok && u < units; u += ustep) {
-            const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
-            const int prow = U.p0 + static_cast<int>(rank) * 128;
-            const float* ps = p.P.scale + (SWAP ? U.e * p.P.s_expert : 0ll) + U.kb0 * p.P.s_group;
-            const float* qs = p.Q.scale + (SWAP ? 0ll : U.e * p.Q.s_expert) + U.kb0 * p.Q.s_group;
-            for (int kb = 0; kb < U.nk; ++kb) {
-                if (!wait(sempty0 + 8 * s, ph ^ 1u, DEV_TIMEOUT_PRODUCER)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dst = ptx::smem_u32(slots + s * C::SLOT);
-                const float* pk = ps + kb * p.P.s_group;
-                const float* qk = qs + kb * p.Q.s_group;
-                if (p.P.block) {
-                    if (lane == 0) {
-                        const bool in = prow < U.p_end;
-                        ptx::cp_async_4(dst, in ? pk + (prow >> 7) * p.P.s_row : p.P.scale, in ? 4 : 0);
+            if (!ok && lane == 0) spin_ns(200000);   // copies issued before the abort land within microseconds
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMA issue (a pair's leader)
+            if (rank == 0) {
+                const uint32_t stage0 = ptx::smem_u32(smem);
+                const uint64_t adesc0 = ptx::sdesc_sw128(stage0, 16, 1024);
+                const uint64_t bdesc0 = ptx::sdesc_sw128(stage0 + C::A_BYTES, 16, 1024);
+                constexpr uint64_t STEP = C::STAGE_BYTES / 16;
+                uint32_t s = 0, ph = 0, b = 0, bph = 0;
+                int cur = 0;
+                bool ok = true;
+                for (int u = u0; ok && u < units; u += ustep) {
+                    const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+                    for (int kb = 0; kb < U.nk; ++kb) {
+                        if (!wait(acce0 + 8 * b, bph ^ 1u, DEV_TIMEOUT_MMA_ACC) ||
+                            !wait(full0 + 8 * s, ph, DEV_TIMEOUT_MMA_FULL)) {
+                            ok = false;
+                            break;
+                        }
+                        if constexpr (!PAIR) {
+                            if (p.k_tail && kb + 1 == U.nk) {
+                                // K ends inside a 16-byte piece, of which a tensor copy brings the
+                                // whole: clear what lies behind the end (16-byte units are permuted
+                                // within each 128-byte row by the row's number mod 8)
+                                uint8_t* st = smem + s * C::STAGE_BYTES;
+                                const int unit = p.k_tail >> 4, from = p.k_tail & 15;
+                                for (int r = lane; r < 128 + BQ; r += 32) {
+                                    uint8_t* at = st + r * 128 + ((unit ^ (r & 7)) << 4);
+                                    for (int i = from; i < 16; ++i) at[i] = 0;
+                                }
+                                ptx::fence_proxy_async_smem();
+                                __syncwarp();
+                            }
+                        }
+                        ptx::tc_fence_after();
+                        const uint64_t ad = adesc0 + s * STEP, bd = bdesc0 + s * STEP;
+                        const uint32_t d = tmem_base + b * BQ;
+                        if constexpr (PAIR) {
+                            ptx::mma_f8_pair_x4_elected(d, ad, bd, ad + 2, bd + 2, ad + 4, bd + 4, ad + 6, bd + 6,
+                                                        C::IDESC, 0u);
+                            ptx::mma_commit_pair_multicast_elected(empty0 + 8 * s, 0x3);
+                            ptx::mma_commit_pair_multicast_elected(accf0 + 8 * b, 0x3);
+                        } else {
+                            ptx::mma_f8_x4_elected(d, ad, bd, ad + 2, bd + 2, ad + 4, bd + 4, ad + 6, bd + 6, C::IDESC,
+                                                   0u);
+                            ptx::mma_commit_elected(empty0 + 8 * s);
+                            ptx::mma_commit_elected(accf0 + 8 * b);
+                        }
+                        if (++s == C::STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                        if (++b == C::NB) {
+                            b = 0;
+                            bph ^= 1u;
+                        }
                     }
-                } else {
+                }
+                if (!ok) {
+                    if constexpr (PAIR)
+                        ptx::mma_commit_pair_multicast_elected(drain_bar, 0x1);
+                    else
+                        ptx::mma_commit_elected(drain_bar);
+                    if (lane == 0) wait_drain(drain_bar, 0, p.timeout_ns);
+                }
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------ scales: warp 2 P's, warp 3 Q's
+            constexpr int NI = QVEC && BQ > 128 ? BQ / 32 : 4;
+            const bool of_p = warp == 2;
+            const Fp8Side& side = of_p ? p.P : p.Q;
+            const int per = of_p ? (p.P.block ? 1 : 128) : QVEC ? BQ : (BQ + 127) / 128;   // scales of a k-block
+            const long long step = 32 * side.s_row;
+            const uint32_t dst0 = ptx::smem_u32(slots) + 4 * (lane + (of_p ? 0 : C::SLOT_Q));
+            uint32_t s = 0, ph = 0;
+            int cur = 0;
+            bool ok = true;
+            for (int u = u0; ok && u < units; u += ustep) {
+                const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+                const int row0 = of_p ? U.p0 + static_cast<int>(rank) * 128 : U.q0, end = of_p ? U.p_end : U.q_end;
+                const int r0 = side.block ? row0 >> 7 : row0;
+                const int n = min(per, (side.block ? (end + 127) >> 7 : end) - r0);   // those that exist; zeros behind them
+                const float* at = side.scale + (of_p == SWAP ? U.e * side.s_expert : 0ll) + U.kb0 * side.s_group +
+                                  (r0 + lane) * side.s_row;
+                for (int kb = 0; kb < U.nk; ++kb, at += side.s_group) {
+                    if (!wait(sempty0 + 8 * s, ph ^ 1u, DEV_TIMEOUT_PRODUCER)) {
+                        ok = false;
+                        break;
+                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = prow + lane + 32 * i;
-                        const bool in = r < U.p_end;
-                        ptx::cp_async_4(dst + 4 * (lane + 32 * i), in ? pk + r * p.P.s_row : p.P.scale, in ? 4 : 0);
+                    for (int i = 0; i < NI; ++i) {
+                        const bool in = lane + 32 * i < n;
+                        if (lane + 32 * i < per)
+                            ptx::cp_async_4(dst0 + 4 * (s * C::SLOT + 32 * i), in ? at + i * step : side.scale, in ? 4u : 0u);
                     }
-                }
-                const uint32_t dq = dst + 4 * C::SLOT_Q;
-                if (p.Q.block) {
-                    if (lane < (BQ + 127) / 128) {
-                        const int r = U.q0 + lane * 128;
-                        const bool in = r < U.q_end;
-                        ptx::cp_async_4(dq + 4 * lane, in ? qk + (r >> 7) * p.Q.s_row : p.Q.scale, in ? 4 : 0);
+                    ptx::cp_async_arrive_noinc(sfull0 + 8 * s);
+                    if (++s == C::SS) {
+                        s = 0;
+                        ph ^= 1u;
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < (BQ + 31) / 32; ++i) {
-                        const int c = lane + 32 * i, r = U.q0 + c;
-                        const bool in = r < U.q_end;
-                        if (c < BQ) ptx::cp_async_4(dq + 4 * c, in ? qk + r * p.Q.s_row : p.Q.scale, in ? 4 : 0);
-                    }
-                }
-                ptx::cp_async_arrive_noinc(sfull0 + 8 * s);
-                if (++s == C::SS) {
-                    s = 0;
-                    ph ^= 1u;
                 }
             }
+            ptx::cp_async_wait_all();
+            __syncwarp();
         }
-        ptx::cp_async_wait_all();
-        __syncwarp();
-    } else if (warp >= 4) {
+    } else {
+        if constexpr (C::SPLIT_REGS) ptx::setmaxnreg_inc<224>();
         // ------------------------------------------------ promotion and stores
         const int quarter = warp & 3;            // the tensor-memory lanes this warp may read
         const int h = (warp - 4) >> 2;           // its share of the columns
@@ -421,21 +506,26 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP>::THREADS, 1)
         const uint32_t acce_leader0 = PAIR ? ptx::mapa_shared(acce0, 0u) : acce0;
         uint32_t s = 0, ph = 0, b = 0, bph = 0;
         int cur = 0;
+        [[maybe_unused]] int used = 0;   // the slab whose turn it is
         bool ok = true;
         for (int u = u0; ok && u < units; u += ustep) {
-            const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
-            float acc[C::CW];
+            uint64_t sum[C::CW / 2];   // two columns each
 #pragma unroll
-            for (int i = 0; i < C::CW; ++i) acc[i] = 0.0f;
-            for (int kb = 0; kb < U.nk; ++kb) {
-                if (!wait(sfull0 + 8 * s, ph, DEV_TIMEOUT_EPILOGUE) || !wait(accf0 + 8 * b, bph, DEV_TIMEOUT_EPILOGUE)) {
+            for (int i = 0; i < C::CW / 2; ++i) sum[i] = 0;
+            const int nk = fp8_unit<C>(p, first, off, u, cur).nk;
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!wait(sfull0 + 8 * s, ph, DEV_TIMEOUT_EPILOGUE)) {
+                    ok = false;
+                    break;
+                }
+                const float* slot = slots + s * C::SLOT;
+                float f = slot[p.P.block ? 0 : prl];
+                if constexpr (!QVEC) f *= slot[C::SLOT_Q + ((h * C::CW) >> 7)];
+                if (!wait(accf0 + 8 * b, bph, DEV_TIMEOUT_EPILOGUE)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const float* slot = slots + s * C::SLOT;
-                const float sp = p.P.block ? slot[0] : slot[prl];
-                const float f = p.Q.block ? sp * slot[C::SLOT_Q + ((h * C::CW) >> 7)] : sp;
                 const uint32_t t = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * BQ + h * C::CW;
 #pragma unroll
                 for (int c = 0; c < C::CW; c += C::CHUNK) {
@@ -452,21 +542,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP>::THREADS, 1)
                                 ptx::mbar_arrive_relaxed(acce0 + 8 * b);
                         }
                     }
-                    if (p.Q.block) {
-#pragma unroll
-                        for (int i = 0; i < C::CHUNK; ++i)
-                            acc[c + i] = fmaf(__uint_as_float(r[i]), f, acc[c + i]);
-                    } else {
-                        const float4* q4 = reinterpret_cast<const float4*>(slot + C::SLOT_Q + h * C::CW + c);
-#pragma unroll
-                        for (int i = 0; i < C::CHUNK; i += 4) {
-                            const float4 q = q4[i / 4];
-                            acc[c + i + 0] = fmaf(__uint_as_float(r[i + 0]), f * q.x, acc[c + i + 0]);
-                            acc[c + i + 1] = fmaf(__uint_as_float(r[i + 1]), f * q.y, acc[c + i + 1]);
-                            acc[c + i + 2] = fmaf(__uint_as_float(r[i + 2]), f * q.z, acc[c + i + 2]);
-                            acc[c + i + 3] = fmaf(__uint_as_float(r[i + 3]), f * q.w, acc[c + i + 3]);
-                        }
-                    }
+                    if constexpr (QVEC)
+                        fp8_promote<C::CHUNK>(sum + c / 2, r, f, slot + C::SLOT_Q + h * C::CW + c);
+                    else
+                        fp8_promote<C::CHUNK>(sum + c / 2, r, f);
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(sempty0 + 8 * s);
@@ -480,55 +559,43 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP>::THREADS, 1)
                 }
             }
             if (!ok) break;
-            const int pr = U.p0 + static_cast<int>(rank) * 128 + prl;
+            // (worked out again rather than kept: the sums leave few registers)
+            const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
             const int qc = U.q0 + h * C::CW;
-            const int n = pr < U.p_end ? min(C::CW, U.q_end - qc) : 0;
             if constexpr (SWAP) {
                 // consecutive lanes hold consecutive columns of C
+                const int pr = U.p0 + prl;
+                const int n = pr < U.p_end ? min(C::CW, U.q_end - qc) : 0;
                 const long long at = static_cast<long long>(qc) * p.ldc + pr;
 #pragma unroll
                 for (int i = 0; i < C::CW; ++i) {
+                    const float2 v2 = ptx::f32x2_get(sum[i / 2]);
+                    const float v = i & 1 ? v2.y : v2.x;
                     if (i < n) {
                         if (p.out_bf16)
-                            static_cast<__nv_bfloat16*>(p.C)[at + i * p.ldc] = __float2bfloat16_rn(acc[i]);
+                            static_cast<__nv_bfloat16*>(p.C)[at + i * p.ldc] = __float2bfloat16_rn(v);
                         else
-                            static_cast<float*>(p.C)[at + i * p.ldc] = acc[i];
+                            static_cast<float*>(p.C)[at + i * p.ldc] = v;
                     }
                 }
-            } else if (n > 0) {
-                const long long at = (p.wgrad ? U.e * p.c_expert : 0ll) + static_cast<long long>(pr) * p.ldc + qc;
-                if (p.out_bf16) {
-                    __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + at;
-                    if (p.vec && n == C::CW) {
-#pragma unroll
-                        for (int i = 0; i < C::CW; i += 8) {
-                            uint4 v;
-                            v.x = pack_bf16(acc[i + 0], acc[i + 1]);
-                            v.y = pack_bf16(acc[i + 2], acc[i + 3]);
-                            v.z = pack_bf16(acc[i + 4], acc[i + 5]);
-                            v.w = pack_bf16(acc[i + 6], acc[i + 7]);
-                            *reinterpret_cast<uint4*>(c + i) = v;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < C::CW; ++i)
-                            if (i < n) c[i] = __float2bfloat16_rn(acc[i]);
-                    }
-                } else {
-                    float* c = static_cast<float*>(p.C) + at;
-                    if (p.vec && n == C::CW) {
-#pragma unroll
-                        for (int i = 0; i < C::CW; i += 4)
-                            *reinterpret_cast<float4*>(c + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < C::CW; ++i)
-                            if (i < n) c[i] = acc[i];
-                    }
+            } else {
+                const int pw = U.p0 + static_cast<int>(rank) * 128 + quarter * 32;   // this warp's first row
+                const int rows = U.p_end - pw, cols = U.q_end - qc;
+                const long long at = (p.wgrad ? U.e * p.c_expert : 0ll) + static_cast<long long>(pw) * p.ldc + qc;
+                uint8_t* slab = slabs + (warp - 4) * C::SLABS * C::SLAB_BYTES;
+                if (rows > 0 && cols > 0) {
+                    const int e = p.wgrad ? U.e : 0;
+                    if (p.out_bf16)
+                        fp8_store_rows<C>(sum, slab, used, &tmC, static_cast<__nv_bfloat16*>(p.C) + at, p.ldc, pw, qc, e,
+                                          rows, cols, p.vec != 0, lane);
+                    else
+                        fp8_store_rows<C>(sum, slab, used, &tmC, static_cast<float*>(p.C) + at, p.ldc, pw, qc, e, rows,
+                                          cols, p.vec != 0, lane);
                 }
             }
             __syncwarp();
         }
+        if (!SWAP && lane == 0) ptx::bulk_wait<0>();
         __syncwarp();
     }
 

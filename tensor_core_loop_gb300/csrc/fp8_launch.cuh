@@ -15,16 +15,20 @@ int stream_scratch(cudaStream_t stream, size_t need, void** out);
 // A 3-D map of bytes (K contiguous, rows, matrices), 128-byte swizzle, boxes of 128 bytes × box_rows; not cached.
 int tensor_map_bytes(const void* ptr, uint64_t k, uint64_t rows, uint64_t mats, uint64_t row_stride, uint64_t mat_stride,
                      uint32_t box_rows, CUtensorMap* out);
+// The same for a product's result (fp32 or bf16), boxes of 128 bytes × 32 rows.
+int tensor_map_result(const void* ptr, int bf16, uint64_t cols, uint64_t rows, uint64_t mats, uint64_t row_stride,
+                      uint64_t mat_stride, CUtensorMap* out);
 
 // ---- fp8 products (k_fp8_gemm.cu)
 enum class Fp8Tile : int {
     FEW16,    // 128 weight rows × 16 token rows
     FEW32,    // 128 weight rows × 32 token rows
     ONE,      // 128 × 128 on one SM
+    PAIR,     // 256 × 256 on a pair of SMs
 };
 struct Fp8Launch {
     Fp8Tile tile;
-    CUtensorMap tmP, tmQ;
+    CUtensorMap tmP, tmQ, tmC;
     Fp8Params p;
     int grid;
     cudaStream_t stream;

@@ -4,10 +4,10 @@
 namespace tcl {
 namespace {
 
-template <int BQ, bool PAIR, bool SWAP>
+template <int BQ, bool PAIR, bool SWAP, bool QVEC>
 cudaError_t launch(const Fp8Launch& a) {
-    using C = Fp8Cfg<BQ, PAIR, SWAP>;
-    auto kern = fp8_gemm_kernel<BQ, PAIR, SWAP>;
+    using C = Fp8Cfg<BQ, PAIR, SWAP, QVEC>;
+    auto kern = fp8_gemm_kernel<BQ, PAIR, SWAP, QVEC>;
     // the shared-memory opt-in is per function and device: set once per device
     static bool attr_done[64] = {};
     int dev = 0;
@@ -32,12 +32,12 @@ cudaError_t launch(const Fp8Launch& a) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, a.tmP, a.tmQ, a.p);
+    return cudaLaunchKernelEx(&cfg, kern, a.tmP, a.tmQ, a.tmC, a.p);
 }
 
-template <int BQ, bool PAIR, bool SWAP>
+template <int BQ, bool PAIR, bool SWAP, bool QVEC>
 Fp8TileInfo info() {
-    using C = Fp8Cfg<BQ, PAIR, SWAP>;
+    using C = Fp8Cfg<BQ, PAIR, SWAP, QVEC>;
     return {C::BP, C::BQ, C::CTAS, 128, C::BQL, SWAP ? 1 : 0};
 }
 
@@ -45,17 +45,20 @@ Fp8TileInfo info() {
 
 Fp8TileInfo fp8_tile_info(Fp8Tile t) {
     switch (t) {
-        case Fp8Tile::FEW16: return info<16, false, true>();
-        case Fp8Tile::FEW32: return info<32, false, true>();
-        default: return info<128, false, false>();
+        case Fp8Tile::FEW16: return info<16, false, true, true>();
+        case Fp8Tile::FEW32: return info<32, false, true, true>();
+        case Fp8Tile::PAIR: return info<256, true, false, true>();
+        default: return info<128, false, false, true>();
     }
 }
 
 cudaError_t launch_fp8_gemm(const Fp8Launch& a) {
+    const bool blocks = a.p.Q.block != 0;   // (few tokens: Q is the tokens' side, whose scales belong to rows)
     switch (a.tile) {
-        case Fp8Tile::FEW16: return launch<16, false, true>(a);
-        case Fp8Tile::FEW32: return launch<32, false, true>(a);
-        default: return launch<128, false, false>(a);
+        case Fp8Tile::FEW16: return launch<16, false, true, true>(a);
+        case Fp8Tile::FEW32: return launch<32, false, true, true>(a);
+        case Fp8Tile::PAIR: return blocks ? launch<256, true, false, false>(a) : launch<256, true, false, true>(a);
+        default: return blocks ? launch<128, false, false, false>(a) : launch<128, false, false, true>(a);
     }
 }
 
