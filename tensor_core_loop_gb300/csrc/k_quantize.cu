@@ -51,50 +51,60 @@ __device__ __forceinline__ void put8(uint8_t* p, int n, bool vec, uint2 w) {
         if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
 }
 
-// Groups along the rows: sixteen lanes hold a group, eight values each, eight groups to a
-// block. With an order, a token's row is read and quantised once and written to each of its
-// rows; blocks behind the tokens' write the rows that no token has.
-constexpr int kRowsTeams = 8, kZeroRows = 64;
+// Groups along the rows: sixteen lanes (a team) hold a group, eight values each. A block's
+// eight teams take neighbouring groups, of one row or, where a row has fewer than eight, of
+// several (`row_teams`, a power of two, to a row), and N rows one after another whose loads
+// are all issued first. With an order, a token's row is read and quantised once and written to
+// each of its rows; blocks behind the tokens' write the rows that no token has.
+constexpr int kTeams = 8, kZeroRows = 64;
 
-template <typename T>
-__global__ void __launch_bounds__(16 * kRowsTeams) quant_rows_kernel(const QuantRows a, int groups, int quant_blocks,
-                                                                     int wcols, bool vec_in, bool vec_out) {
+template <typename T, int N>
+__global__ void __launch_bounds__(16 * kTeams) quant_rows_kernel(const QuantRows a, int groups, int row_teams_log2,
+                                                                 int quant_blocks, int wcols, bool vec_in,
+                                                                 bool vec_out) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int team = threadIdx.x >> 4, l = threadIdx.x & 15;
+    const int row_teams = 1 << row_teams_log2, rows_at_once = kTeams >> row_teams_log2;
     if (blockIdx.x >= quant_blocks) {
+        if (blockIdx.y > 0) return;
         const int r0 = (blockIdx.x - quant_blocks) * kZeroRows;
-        for (int r = r0 + team; r < min(r0 + kZeroRows, a.out_rows); r += kRowsTeams) {
+        for (int r = r0 + team; r < min(r0 + kZeroRows, a.out_rows); r += kTeams) {
             if (a.source[r] >= 0) continue;
             for (int c = l * 8; c < wcols; c += 128) put8(a.q + r * a.ldq + c, wcols - c, vec_out, make_uint2(0u, 0u));
             for (int g = l; g < groups; g += 16) a.scale[r * a.s_row + g * a.s_group] = group_scale(0u);
         }
         return;
     }
-    const long long item = static_cast<long long>(blockIdx.x) * kRowsTeams + team;
-    const int row = static_cast<int>(item / groups), g = static_cast<int>(item - static_cast<long long>(row) * groups);
-    const bool on = row < a.rows;
+    const int g = blockIdx.y * row_teams + (team & (row_teams - 1));
+    const int row0 = blockIdx.x * (N * rows_at_once) + (team >> row_teams_log2);
     const int c = g * kG + l * 8;
-    float v[8];
-    load8(static_cast<const T*>(a.x) + (on ? row * a.ldx + c : 0), on ? a.cols - c : 0, vec_in, v);
-    uint32_t top = 0;
+    Raw8<T> raw[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, magnitude(v[i]));
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (!on) return;
-    const float s = group_scale(top);
-    const uint2 w = quant8(v, __frcp_rn(s));
-    if (!a.position) {
-        put8(a.q + row * a.ldq + c, wcols - c, vec_out, w);
-        if (l == 0) a.scale[row * a.s_row + g * a.s_group] = s;
-        return;
+    for (int i = 0; i < N; ++i) {
+        const int row = row0 + i * rows_at_once;
+        const bool in = row < a.rows && g < groups;
+        raw[i].load(static_cast<const T*>(a.x) + (in ? row * a.ldx + c : 0), in ? a.cols - c : 0, vec_in);
     }
-    for (int j = 0; j < a.top; ++j) {
-        const int r = a.position[static_cast<long long>(row) * a.top + j];
-        if (r < 0 || r >= a.out_rows) continue;
-        put8(a.q + r * a.ldq + c, wcols - c, vec_out, w);
-        if (l == 0) a.scale[r * a.s_row + g * a.s_group] = s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int row = row0 + i * rows_at_once;
+        float v[8];
+        raw[i].get(v);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[j]));
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if (row >= a.rows || g >= groups) continue;   // (uniform over the team)
+        const float s = group_scale(top);
+        const uint2 w = quant8(v, __frcp_rn(s));
+        for (int j = 0; j < (a.position ? a.top : 1); ++j) {
+            const int r = a.position ? a.position[static_cast<long long>(row) * a.top + j] : row;
+            if (r < 0 || (a.position && r >= a.out_rows)) continue;
+            put8(a.q + r * a.ldq + c, wcols - c, vec_out, w);
+            if (l == 0) a.scale[r * a.s_row + g * a.s_group] = s;
+        }
     }
 }
 
@@ -113,7 +123,7 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const QuantTiles a, bo
     const int c0 = blockIdx.x * kG, r0 = blockIdx.y * kG;
     const int c = c0 + cg * 8;
     const T* x = static_cast<const T*>(a.x) + blockIdx.z * a.x_batch;
-    float v[8][8];
+    Raw8<T> raw[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         int r = r0 + rg * 8 + i;
@@ -123,14 +133,15 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const QuantTiles a, bo
             r = slot / a.top;
             in = slot >= 0 && r < a.x_rows;
         }
-        load8(x + (in ? r * a.ldx + c : 0), in ? a.cols - c : 0, vec_in, v[i]);
+        raw[i].load(x + (in ? r * a.ldx + c : 0), in ? a.cols - c : 0, vec_in);
     }
-    uint32_t top[8];
+    uint32_t top[8] = {};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        top[j] = 0;
+    for (int i = 0; i < 8; ++i) {
+        float v[8];
+        raw[i].get(v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top[j] = max(top[j], magnitude(v[i][j]));
+        for (int j = 0; j < 8; ++j) top[j] = max(top[j], magnitude(v[j]));
     }
     float inv[8];
     if constexpr (KIND == QuantTile::COLUMNS) {
@@ -175,11 +186,16 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const QuantTiles a, bo
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = r0 + rg * 8 + i;
-            if (r < a.rows && c < wcols) put8(q + r * a.ldq + c, wcols - c, vec_out, quant8(v[i], inv[0]));
+            float v[8];
+            raw[i].get(v);
+            if (r < a.rows && c < wcols) put8(q + r * a.ldq + c, wcols - c, vec_out, quant8(v, inv[0]));
         }
         return;
     }
     if constexpr (TR) {
+        float v[8][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raw[i].get(v[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float w[8];
@@ -213,17 +229,29 @@ bool row_aligned(const void* p, long long ld, int bytes) {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * static_cast<long long>(sizeof(T)) % bytes == 0;
 }
 
+template <typename T, int N>
+cudaError_t quant_rows_n(const QuantRows& a, int groups, int row_teams_log2, cudaStream_t stream) {
+    const int rows_at_once = kTeams >> row_teams_log2;
+    const long long blocks = (static_cast<long long>(a.rows) + N * rows_at_once - 1) / (N * rows_at_once);
+    const long long zero = a.position ? (a.out_rows + kZeroRows - 1) / kZeroRows : 0;
+    const int by = (groups + (1 << row_teams_log2) - 1) >> row_teams_log2;
+    if (blocks + zero > 0x7fffffffll || by > 65535) return cudaErrorInvalidValue;
+    if (blocks + zero == 0) return cudaSuccess;
+    const int wcols = static_cast<int>(std::min<long long>(a.ldq, (a.cols + 15) & ~15));
+    return launch_pdl(quant_rows_kernel<T, N>, dim3(static_cast<unsigned>(blocks + zero), by), 16 * kTeams, 0, stream, a,
+                      groups, row_teams_log2, static_cast<int>(blocks), wcols, row_aligned<T>(a.x, a.ldx, 16),
+                      row_aligned<uint8_t>(a.q, a.ldq, 8));
+}
+
 template <typename T>
 cudaError_t quant_rows(const QuantRows& a, cudaStream_t stream) {
     const int groups = (a.cols + kG - 1) / kG;
-    const long long blocks = (static_cast<long long>(a.rows) * groups + kRowsTeams - 1) / kRowsTeams;
-    const long long zero = a.position ? (a.out_rows + kZeroRows - 1) / kZeroRows : 0;
-    if (blocks + zero > 0x7fffffffll) return cudaErrorInvalidValue;
-    if (blocks + zero == 0) return cudaSuccess;
-    const int wcols = static_cast<int>(std::min<long long>(a.ldq, (a.cols + 15) & ~15));
-    return launch_pdl(quant_rows_kernel<T>, dim3(static_cast<unsigned>(blocks + zero)), 16 * kRowsTeams, 0, stream, a,
-                      groups, static_cast<int>(blocks), wcols, row_aligned<T>(a.x, a.ldx, 16),
-                      row_aligned<uint8_t>(a.q, a.ldq, 8));
+    int log2 = 0;
+    while (log2 < 3 && (1 << log2) < groups) ++log2;
+    // four rows per thread where that leaves enough blocks to fill the GPU several times over
+    if (static_cast<long long>(a.rows) * groups >= 4ll * kTeams * 4096)
+        return quant_rows_n<T, 4>(a, groups, log2, stream);
+    return quant_rows_n<T, 1>(a, groups, log2, stream);
 }
 
 template <typename T, QuantTile KIND>

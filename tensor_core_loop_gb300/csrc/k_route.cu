@@ -194,21 +194,26 @@ __global__ void __launch_bounds__(256) combine_kernel(const RouteRows a, bool ve
     const long long t = blockIdx.x;
     const T* y = static_cast<const T*>(a.x);
     float sum[8] = {};
-    // four slots' loads in flight at a time
-    for (int j0 = 0; j0 < a.top; j0 += 4) {
-        float v[4][8], w[4];
+    // the loads of some slots in flight at a time
+    constexpr int N = sizeof(T) == 2 ? 8 : 4;
+    for (int j0 = 0; j0 < a.top; j0 += N) {
+        Raw8<T> raw[N];
+        float w[N];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < N; ++k) {
             const int j = j0 + k;
             const int r = j < a.top ? a.position[t * a.top + j] : -1;
             const bool in = r >= 0 && r < a.rows;
             w[k] = in ? (a.weights ? a.weights[t * a.top + j] : 1.0f) : 0.0f;
-            load8(y + (in ? r * a.ldx + c : 0), in ? a.cols - c : 0, vec_in, v[k]);   // (zeros for a dropped slot)
+            raw[k].load(y + (in ? r * a.ldx + c : 0), in ? a.cols - c : 0, vec_in);   // (zeros for a dropped slot)
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < N; ++k) {
+            float v[8];
+            raw[k].get(v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[k], v[k][i], sum[i]);
+            for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[k], v[i], sum[i]);
+        }
     }
     store8(static_cast<T*>(a.out) + t * a.ldo + c, a.cols - c, vec_out, sum);
 }
@@ -242,22 +247,24 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RouteRows a, bo
             dot[k] = 0.0f;
         }
         for (int c = threadIdx.x * 8; c < a.cols; c += blockDim.x * 8) {
+            Raw8<T> raw[8];
             float gv[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)   // (nothing is read for a dropped slot: zeros)
+                raw[k].load(y + (a.dw && r[k] >= 0 ? r[k] * a.ldy + c : 0), a.dw && r[k] >= 0 ? a.cols - c : 0, vec_y);
             load8(g + c, a.cols - c, vec_g, gv);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                if (r[k] < 0) continue;
-                if (a.dw) {
-                    float yv[8];
-                    load8(y + r[k] * a.ldy + c, a.cols - c, vec_y, yv);
+                float v[8];
+                raw[k].get(v);
+                if (r[k] >= 0) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dot[k] = fmaf(gv[i], yv[i], dot[k]);
+                    for (int i = 0; i < 8; ++i) dot[k] = fmaf(gv[i], v[i], dot[k]);
                 }
-                if (dy) {
-                    float d[8];
+                if (dy && r[k] >= 0) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] = w[k] * gv[i];
-                    store8(dy + r[k] * a.ldo + c, a.cols - c, vec_out, d);
+                    for (int i = 0; i < 8; ++i) v[i] = w[k] * gv[i];
+                    store8(dy + r[k] * a.ldo + c, a.cols - c, vec_out, v);
                 }
             }
         }

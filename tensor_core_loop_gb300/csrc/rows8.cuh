@@ -22,24 +22,53 @@ __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
     }
 }
 
-// Values p[0..n) (n may be past 8, or below 1), the rest zeros. vec: p is 16-byte aligned.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int n, bool vec, float (&v)[8]) {
-    if (vec && n >= 8) {
-        unpack8(*reinterpret_cast<const uint4*>(p), v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.0f;
-}
+// Eight values as they lie in memory: loaded first, widened where they are used, so that many
+// loads can be in flight without as many fp32 registers.
+template <typename T>
+struct Raw8;
 
-__device__ __forceinline__ void load8(const float* p, int n, bool vec, float (&v)[8]) {
-    if (vec && n >= 8) {
-        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        return;
-    }
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 u;
+    // values p[0..n) (n may be past 8, or below 1), the rest zeros; vec: p is 16-byte aligned
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int n, bool vec) {
+        if (vec && n >= 8) {
+            u = *reinterpret_cast<const uint4*>(p);
+            return;
+        }
+        uint32_t w[4] = {0, 0, 0, 0};
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+        for (int i = 0; i < 8; ++i)
+            if (i < n) w[i / 2] |= static_cast<uint32_t>(h[i]) << (16 * (i & 1));
+        u = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const { unpack8(u, v); }
+};
+
+template <>
+struct Raw8<float> {
+    float f[8];
+    __device__ __forceinline__ void load(const float* p, int n, bool vec) {
+        if (vec && n >= 8) {
+            const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = i < n ? p[i] : 0.0f;
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = f[i];
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
+    Raw8<T> r;
+    r.load(p, n, vec);
+    r.get(v);
 }
 
 // (each value rounded once, to nearest even)

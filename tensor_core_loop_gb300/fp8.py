@@ -18,7 +18,13 @@ and allocate their results on that stream.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from typing import NamedTuple
+
+try:
+    import torch
+except ImportError:   # (the library itself needs no PyTorch; the calls below take its tensors)
+    torch = None
 
 from . import OUT_BF16, OUT_F32, TclError, lib
 
@@ -63,52 +69,37 @@ class ExpertOrder(NamedTuple):
 
 
 def _call(fn, what, device, stream, *args):
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index is None or device.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
+    # (asking for the current stream's handle alone spares the wrapper object: 2 of a small call's microseconds)
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, raw)
     if st:
         raise TclError(st, what)
 
 
-class _on:
+_here = nullcontext()
+
+
+def _on(stream):
     """Allocations inside belong to ``stream`` (None: the current one, nothing to do)."""
-
-    def __init__(self, stream):
-        self.ctx = None
-        if stream is not None:
-            import torch
-            self.ctx = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *err):
-        if self.ctx is not None:
-            self.ctx.__exit__(*err)
+    return _here if stream is None else torch.cuda.stream(stream)
 
 
-def _cuda(**tensors):
-    device = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _device(name, first, *rest):
+    """The GPU that ``first`` (called ``name``) is on; the others that are given have to be there too."""
+    if not first.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    device = first.device
+    for t in rest:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on {device}, where {name} is, not on {t.device}")
     return device
 
 
 def _x_type(t, name):
-    import torch
     if t.dtype == torch.bfloat16:
         return X_BF16
     if t.dtype == torch.float32:
@@ -133,7 +124,6 @@ def _ld(t, name, dim=2):
 
 
 def _int32(t, name, shape=None):
-    import torch
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32")
     if not t.is_contiguous():
@@ -155,7 +145,6 @@ def _order(order, tokens=None):
 
 def _fp8(rows, cols, device, batch=None):
     """e4m3 rows at a pitch of whole 16-byte pieces, as the tensor copies of a product read them."""
-    import torch
     pitch = -(-cols // 16) * 16
     full = torch.empty((rows, pitch) if batch is None else (batch, rows, pitch), dtype=torch.float8_e4m3fn, device=device)
     return full if pitch == cols else full[..., :cols]
@@ -173,7 +162,6 @@ def quantize_fp8(x, along: str = "rows", order: ExpertOrder | None = None, strea
 
     ``order`` (rows and columns): the rows of the sorted layout instead, each token's row in
     the place of each of its slots, zeros in rows without a slot."""
-    import torch
     batched = along in ("blocks", "blocks_t")
     if along not in ("rows", "columns") and not batched:
         raise ValueError("along must be 'rows', 'columns', 'blocks' or 'blocks_t'")
@@ -187,21 +175,21 @@ def quantize_fp8(x, along: str = "rows", order: ExpertOrder | None = None, strea
     if order is not None:
         position, source = _order(order, rows)
         top, made = position.shape[1], source.shape[0]
-    device = _cuda(x=x, position=position, source=source)
+    device = _device("x", x, position, source)
     pos, src = (position.data_ptr(), source.data_ptr()) if order is not None else (None, None)
     with _on(stream):
         if along == "rows":
             data = _fp8(made, cols, device)
-            scale = torch.empty((-(-cols // GROUP), made), dtype=torch.float32, device=device)
+            scale = torch.empty_strided((made, -(-cols // GROUP)), (1, made), dtype=torch.float32, device=device)
             _call(_lib().tcl_quantize_fp8_rows, "quantize_fp8", device, stream, xt, rows, cols, x.data_ptr(), ldx, pos, top,
                   src, made, data.data_ptr(), -(-cols // 16) * 16, scale.data_ptr(), 1, made)
-            return data, scale.t()
+            return data, scale
         if along == "columns":
             data = _fp8(cols, made, device) if made else torch.empty((cols, 0), dtype=torch.float8_e4m3fn, device=device)
-            scale = torch.empty((-(-made // GROUP), cols), dtype=torch.float32, device=device)
+            scale = torch.empty_strided((cols, -(-made // GROUP)), (1, cols), dtype=torch.float32, device=device)
             _call(_lib().tcl_quantize_fp8_columns, "quantize_fp8", device, stream, xt, rows, cols, x.data_ptr(), ldx, src,
                   top, made, data.data_ptr(), -(-made // 16) * 16, scale.data_ptr(), 1, cols)
-            return data, scale.t()
+            return data, scale
         turned = along == "blocks_t"
         batch = x.shape[0] if x.dim() == 3 else None
         qr, qc = (cols, rows) if turned else (rows, cols)
@@ -216,7 +204,6 @@ def quantize_fp8(x, along: str = "rows", order: ExpertOrder | None = None, strea
 
 
 def _operand(data, scale, name, dim=2):
-    import torch
     if data.dtype != torch.float8_e4m3fn:
         raise TypeError(f"{name} must be float8_e4m3fn")
     if scale.dtype != torch.float32:
@@ -240,7 +227,6 @@ def _kind(data, scale, name):
 
 
 def _out(dtype):
-    import torch
     if dtype is None or dtype == torch.bfloat16:
         return torch.bfloat16, OUT_BF16
     if dtype == torch.float32:
@@ -249,7 +235,6 @@ def _out(dtype):
 
 
 def _result(out, shape, dtype, device):
-    import torch
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if tuple(out.shape) != shape or out.dtype != dtype:
@@ -269,7 +254,7 @@ def gemm_fp8(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None):
         raise ValueError(f"a needs scales of shape {(M, -(-K // GROUP))}, not {tuple(a_scale.shape)}")
     kind = _kind(b, b_scale, "b")
     dtype, code = _out(out.dtype if out is not None else out_dtype)
-    device = _cuda(a=a, a_scale=a_scale, b=b, b_scale=b_scale, out=out)
+    device = _device("a", a, a_scale, b, b_scale, out)
     with _on(stream):
         c = _result(out, (M, N), dtype, device)
         _call(_lib().gemm_fp8, "gemm_fp8", device, stream, M, N, K, a.data_ptr(), lda, a_scale.data_ptr(),
@@ -293,7 +278,7 @@ def gemm_fp8_experts(a, a_scale, b, b_scale, offsets, out_dtype=None, out=None, 
     kind = _kind(b, b_scale, "b")
     _int32(offsets, "offsets", (experts + 1,))
     dtype, code = _out(out.dtype if out is not None else out_dtype)
-    device = _cuda(a=a, a_scale=a_scale, b=b, b_scale=b_scale, offsets=offsets, out=out)
+    device = _device("a", a, a_scale, b, b_scale, offsets, out)
     with _on(stream):
         c = _result(out, (rows, N), dtype, device)
         _call(_lib().gemm_fp8_experts, "gemm_fp8_experts", device, stream, rows, experts, N, K, a.data_ptr(), lda,
@@ -308,7 +293,6 @@ def gemm_fp8_experts_wgrad(a, a_scale, b, b_scale, offsets, out_dtype=None, out=
     gradients from ``a`` (N x rows) and ``b`` (K x rows), the result's gradient and the input
     quantised down the sorted rows (``quantize_fp8(..., along="columns")``). ``offsets`` are
     multiples of 128 (``sort_by_expert(..., align=128)``); experts without rows get zeros."""
-    import torch
     for t, s, name in ((a, a_scale, "a"), (b, b_scale, "b")):
         if t.dtype != torch.float8_e4m3fn:
             raise TypeError(f"{name} must be float8_e4m3fn")
@@ -328,7 +312,7 @@ def gemm_fp8_experts_wgrad(a, a_scale, b, b_scale, offsets, out_dtype=None, out=
         raise ValueError("offsets must have one entry more than there are experts")
     _int32(offsets, "offsets", (experts + 1,))
     dtype, code = _out(out.dtype if out is not None else out_dtype)
-    device = _cuda(a=a, a_scale=a_scale, b=b, b_scale=b_scale, offsets=offsets, out=out)
+    device = _device("a", a, a_scale, b, b_scale, offsets, out)
     with _on(stream):
         c = _result(out, (experts, N, K), dtype, device)
         ldc = _ld(c, "out", 3)
@@ -344,7 +328,6 @@ def sort_by_expert(ids, experts: int, align: int = 1, stream=None) -> ExpertOrde
     0 .. experts-1 drops the slot) by expert, and by slot within an expert. Each expert's rows
     are padded to a multiple of ``align``: 1 for a forward pass, 128 where weight gradients are
     to follow."""
-    import torch
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be int32 or int64")
     if ids.dim() != 2 or ids.shape[1] < 1 or not ids.is_contiguous():
@@ -354,22 +337,22 @@ def sort_by_expert(ids, experts: int, align: int = 1, stream=None) -> ExpertOrde
     tokens, top = ids.shape
     slots = tokens * top
     rows = (slots + min(experts, slots) * (align - 1)) // align * align
-    device = _cuda(ids=ids)
+    device = _device("ids", ids)
     with _on(stream):
-        both = torch.empty(experts + 1 + slots + rows, dtype=torch.int32, device=device)
-        offsets, position, source = both.split((experts + 1, slots, rows))
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
+        position = torch.empty((tokens, top), dtype=torch.int32, device=device)
+        source = torch.empty(rows, dtype=torch.int32, device=device)
         _call(_lib().tcl_sort_by_expert, "sort_by_expert", device, stream, tokens, top, ids.data_ptr(), ids.element_size(),
               experts, align, rows, offsets.data_ptr(), position.data_ptr(), source.data_ptr())
-    return ExpertOrder(offsets, position.view(tokens, top), source)
+    return ExpertOrder(offsets, position, source)
 
 
 def gather_rows(x, order: ExpertOrder, stream=None):
     """The tokens' rows of ``x`` (bf16 or fp32) in sorted order, zeros in rows without a slot.
     Its gradient is ``combine(d_rows, None, order)``."""
-    import torch
     xt, ldx = _x_type(x, "x"), _ld(x, "x")
     position, source = _order(order, x.shape[0])
-    device = _cuda(x=x, position=position, source=source)
+    device = _device("x", x, position, source)
     with _on(stream):
         y = torch.empty((source.shape[0], x.shape[1]), dtype=x.dtype, device=device)
         _call(_lib().tcl_gather_rows, "gather_rows", device, stream, xt, x.shape[0], position.shape[1], y.shape[0],
@@ -378,7 +361,6 @@ def gather_rows(x, order: ExpertOrder, stream=None):
 
 
 def _weights(weights, position):
-    import torch
     if weights is None:
         return None
     if weights.dtype != torch.float32 or not weights.is_contiguous() or weights.shape != position.shape:
@@ -389,13 +371,12 @@ def _weights(weights, position):
 def combine(y, weights, order: ExpertOrder, stream=None):
     """out[t] = sum over the token's slots j of weights[t, j]·y[position[t, j]] (None: ones), in
     fp32, rounded once to ``y``'s type. Dropped slots add nothing."""
-    import torch
     xt, ldy = _x_type(y, "y"), _ld(y, "y")
     position, source = _order(order)
     if y.shape[0] != source.shape[0]:
         raise ValueError(f"the order has {source.shape[0]} rows, y {y.shape[0]}")
     w = _weights(weights, position)
-    device = _cuda(y=y, weights=weights, position=position, source=source)
+    device = _device("y", y, weights, position, source)
     tokens, top = position.shape
     with _on(stream):
         out = torch.empty((tokens, y.shape[1]), dtype=y.dtype, device=device)
@@ -407,7 +388,6 @@ def combine(y, weights, order: ExpertOrder, stream=None):
 def combine_grad(grad, y, weights, order: ExpertOrder, stream=None):
     """(gradient of ``y``, gradient of ``weights``) of ``combine`` from the gradient of its output:
     rows weights[t, j]·grad[t] (zeros in rows without a slot), and grad[t]·y[position[t, j]] in fp32."""
-    import torch
     xt, ldg, ldy = _x_type(grad, "grad"), _ld(grad, "grad"), _ld(y, "y")
     if y.dtype != grad.dtype or y.shape[1] != grad.shape[1]:
         raise ValueError("grad and y must have the same type and width")
@@ -415,7 +395,7 @@ def combine_grad(grad, y, weights, order: ExpertOrder, stream=None):
     if y.shape[0] != source.shape[0]:
         raise ValueError(f"the order has {source.shape[0]} rows, y {y.shape[0]}")
     w = _weights(weights, position)
-    device = _cuda(grad=grad, y=y, weights=weights, position=position, source=source)
+    device = _device("grad", grad, y, weights, position, source)
     tokens, top = position.shape
     with _on(stream):
         dy = torch.empty((source.shape[0], y.shape[1]), dtype=y.dtype, device=device)
