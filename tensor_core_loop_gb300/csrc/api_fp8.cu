@@ -96,8 +96,14 @@ int product(Operand a, Fp8Side sa, Operand b, Fp8Side sb, Fp8Tile tile, Fp8Param
     p.P = t.swap ? sb : sa;
     p.Q = t.swap ? sa : sb;
     p.timeout_ns = kTimeoutNs;
+    int ctas = t.ctas;
+    p.split = 1;
+    if (t.swap) {   // few tokens: share tiles while every CTA has an SM and two k-blocks
+        while (p.split < 8 && units * p.split * 2 <= sms && p.num_kb >= p.split * 4) p.split *= 2;
+        ctas = p.split;
+    }
     l.p = p;
-    l.grid = static_cast<int>(std::max(1ll, std::min<long long>(sms / t.ctas, units))) * t.ctas;
+    l.grid = static_cast<int>(std::max(1ll, std::min<long long>(sms / ctas, units))) * ctas;
     l.stream = stream;
     return status_of(launch_fp8_gemm(l));
 }
@@ -136,8 +142,9 @@ int rows_product(int rows, int experts, int N, int K, const void* A, int lda, co
     p.out_bf16 = out == TCL_OUT_BF16;
     p.vec = on(C, 16) && static_cast<long long>(ldc) * es % 16 == 0;
     p.status = status;
-    // every expert may end inside a tile, and so may the rows behind the last
-    const long long units = (static_cast<long long>(rows) / tt + 1 + (offsets ? std::min(experts, rows) : 0)) *
+    // (every expert may end inside a tile, and so may the rows behind the last)
+    const long long units = (offsets ? static_cast<long long>(rows) / tt + 1 + std::min(experts, rows)
+                                     : (static_cast<long long>(rows) + tt - 1) / tt) *
                             ((N + tw - 1) / tw);
     if (units > 0x3fffffffll) return TCL_ERR_DIMS;
     return product({static_cast<const uint8_t*>(A), lda, 0, rows, 1, K}, {SA, sa_row, sa_group, 0, 0},

@@ -25,6 +25,9 @@
 // MMA's N allows, with 128 weight rows in P, so that a weight byte is read once for
 // all tokens and no MMA or shared memory is spent on rows that do not exist.
 //
+// Where few tokens leave most SMs without a tile, the CTAs of a cluster share a tile's
+// k-blocks and one after another's sums are added over distributed shared memory.
+//
 // Work units are output tiles. Rows sorted by expert come with the experts' offsets on
 // the device: every CTA turns them into a running count of tiles, and walks the tiles
 // blockIdx, blockIdx + grid, ...; tiles past an expert's end read the next expert's rows
@@ -58,6 +61,7 @@ struct Fp8Params {
     int wrows;               // rows of the weight side (weight gradient: rows of P)
     int qrows;               // weight gradient: rows of Q
     int num_kb;              // k-blocks of a tile (weight gradient: given by the offsets)
+    int split;               // few tokens: CTAs of a cluster that share a tile's k-blocks (1: no sharing)
     int k_tail;              // valid bytes of the last k-block where K is not a multiple of 16, else 0
     int wgrad;
     void* C;
@@ -348,7 +352,19 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
         __syncthreads();   // (uniform: every thread takes this branch)
         units = first[E + 1];
     }
-    const int u0 = blockIdx.x / C::CTAS, ustep = gridDim.x / C::CTAS;
+    const int share = SWAP ? p.split : C::CTAS;   // CTAs that work on one tile
+    const int u0 = blockIdx.x / share, ustep = gridDim.x / share;
+    // few tokens: this CTA's part of a tile's k-blocks
+    [[maybe_unused]] const int part = SWAP ? static_cast<int>(blockIdx.x) % share : 0;
+    auto unit = [&](int u, int& cur) {
+        Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+        if constexpr (SWAP) {
+            const int n = U.nk;
+            U.kb0 = part * n / share;
+            U.nk = (part + 1) * n / share - U.kb0;
+        }
+        return U;
+    };
     [[maybe_unused]] const AbortNet net{ptx::smem_u32(const_cast<uint32_t*>(abort_flag)), C::CTAS};
     auto wait = [&](uint32_t bar, uint32_t parity, unsigned int code) {
         if constexpr (PAIR)
@@ -366,7 +382,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
             int cur = 0;
             bool ok = true;
             for (int u = u0; ok && u < units; u += ustep) {
-                const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+                const Fp8Unit U = unit(u, cur);
                 const int pe = (SWAP && !p.wgrad) ? U.e : 0, qe = (!SWAP && !p.wgrad) ? U.e : 0;
                 const int prow = U.p0 + static_cast<int>(rank) * 128, qrow = U.q0 + static_cast<int>(rank) * C::BQL;
                 for (int kb = 0; kb < U.nk; ++kb) {
@@ -403,7 +419,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
                 int cur = 0;
                 bool ok = true;
                 for (int u = u0; ok && u < units; u += ustep) {
-                    const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+                    const Fp8Unit U = unit(u, cur);
                     for (int kb = 0; kb < U.nk; ++kb) {
                         if (!wait(acce0 + 8 * b, bph ^ 1u, DEV_TIMEOUT_MMA_ACC) ||
                             !wait(full0 + 8 * s, ph, DEV_TIMEOUT_MMA_FULL)) {
@@ -411,7 +427,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
                             break;
                         }
                         if constexpr (!PAIR) {
-                            if (p.k_tail && kb + 1 == U.nk) {
+                            if (p.k_tail && U.kb0 + kb + 1 == p.num_kb) {
                                 // K ends inside a 16-byte piece, of which a tensor copy brings the
                                 // whole: clear what lies behind the end (16-byte units are permuted
                                 // within each 128-byte row by the row's number mod 8)
@@ -470,7 +486,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
             int cur = 0;
             bool ok = true;
             for (int u = u0; ok && u < units; u += ustep) {
-                const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+                const Fp8Unit U = unit(u, cur);
                 const int row0 = of_p ? U.p0 + static_cast<int>(rank) * 128 : U.q0, end = of_p ? U.p_end : U.q_end;
                 const int r0 = side.block ? row0 >> 7 : row0;
                 const int n = min(per, (side.block ? (end + 127) >> 7 : end) - r0);   // those that exist; zeros behind them
@@ -512,7 +528,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
             uint64_t sum[C::CW / 2];   // two columns each
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) sum[i] = 0;
-            const int nk = fp8_unit<C>(p, first, off, u, cur).nk;
+            const int nk = unit(u, cur).nk;
             for (int kb = 0; kb < nk; ++kb) {
                 if (!wait(sfull0 + 8 * s, ph, DEV_TIMEOUT_EPILOGUE)) {
                     ok = false;
@@ -560,18 +576,22 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
             }
             if (!ok) break;
             // (worked out again rather than kept: the sums leave few registers)
-            const Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
+            const Fp8Unit U = unit(u, cur);
             const int qc = U.q0 + h * C::CW;
             if constexpr (SWAP) {
                 // consecutive lanes hold consecutive columns of C
                 const int pr = U.p0 + prl;
                 const int n = pr < U.p_end ? min(C::CW, U.q_end - qc) : 0;
                 const long long at = static_cast<long long>(qc) * p.ldc + pr;
+                // (the ring is free: a shared tile is this CTA's only one, and all its MMAs are done)
+                float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
                 for (int i = 0; i < C::CW; ++i) {
                     const float2 v2 = ptx::f32x2_get(sum[i / 2]);
                     const float v = i & 1 ? v2.y : v2.x;
-                    if (i < n) {
+                    if (share > 1) {
+                        sums[i * 128 + prl] = v;
+                    } else if (i < n) {
                         if (p.out_bf16)
                             static_cast<__nv_bfloat16*>(p.C)[at + i * p.ldc] = __float2bfloat16_rn(v);
                         else
@@ -597,6 +617,31 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
         }
         if (!SWAP && lane == 0) ptx::bulk_wait<0>();
         __syncwarp();
+    }
+
+    // ------------------------------------------------ shared tiles: the parts' sums, in their order
+    if (SWAP && share > 1) {
+        __syncwarp();
+        ptx::cluster_sync();   // every part's sums are in its shared memory
+        if (warp >= 4 && u0 < units) {
+            int cur = 0;
+            const Fp8Unit U = fp8_unit<C>(p, first, off, u0, cur);
+            const int prl = (warp & 3) * 32 + lane, pr = U.p0 + prl;
+            const uint32_t sums = ptx::smem_u32(smem);
+            for (int i = part; i < C::CW; i += share) {
+                if (pr >= U.p_end || U.q0 + i >= U.q_end) continue;
+                float v = 0.0f;
+                for (int r = 0; r < share; ++r)
+                    v += ptx::ld_cluster_f32(ptx::mapa_shared(sums + 4 * (i * 128 + prl), static_cast<uint32_t>(r)));
+                const long long at = static_cast<long long>(U.q0 + i) * p.ldc + pr;
+                if (p.out_bf16)
+                    static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
+                else
+                    static_cast<float*>(p.C)[at] = v;
+            }
+        }
+        __syncwarp();
+        ptx::cluster_sync();   // no part leaves while another may still read its sums
     }
 
     // ------------------------------------------------ teardown
