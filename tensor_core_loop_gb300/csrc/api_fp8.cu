@@ -53,14 +53,28 @@ int lay_out(Operand& o, uint8_t* to, cudaStream_t stream) {
     return TCL_OK;
 }
 
-// The tile for products of `tokens` rows, for `experts` experts, with N columns. Few rows go
-// to the MMA's N side, many to its M side. (A pair's MMA warp sees only its own SM's shared
-// memory, so it cannot clear a K tail inside a 16-byte piece.)
-Fp8Tile choose_tile(long long tokens, int experts, int N, bool k_tail) {
+// The tile for products of `tokens` rows with N columns, for `experts` experts. Few rows go to
+// the MMA's N side, many to its M side. Measured in CUDA graphs on a GB300, microseconds:
+//   dense, N = K = 4096     M = 16    64   128   256   512  1024  2048
+//     128 × 16 / 32 / 64       8    10.4  13.6  14.8  25.0  46.1  78.0   (the best of the three)
+//     128 × 128               15.7  15.3  15.2  15.6  16.4  27.5  49.7
+//     256 × 256, two SMs        -     -     -   18.8  19.2  19.7  33.7
+//   64 experts, N = 4096, K = 2048: rows each (on average)
+//                                1     2     8    16    32    64   128   256   512
+//     128 × 16                 15.2  53.2  77.3   104   156   275
+//     128 × 32                 16.6  54.1  75.2  93.5   120   195
+//     128 × 64                 19.7  55.4  77.9  89.4   105   140   217
+//     128 × 128                29.6  57.4  82.9  91.1  97.4   113   144   217   382
+//     256 × 256, two SMs                                                  191   287
+// so 128 × 128 tiles while they fit the GPU in one wave, then 256 × 256. (A pair's MMA warp sees
+// only its own SM's shared memory, so it cannot clear a K tail inside a 16-byte piece.)
+Fp8Tile choose_tile(long long tokens, int experts, int N, bool k_tail, int sms) {
     const long long each = (tokens + experts - 1) / experts;
-    if (each <= 16) return Fp8Tile::FEW16;
-    if (each <= 32) return Fp8Tile::FEW32;
-    if (each >= 256 && N >= 256 && !k_tail) return Fp8Tile::PAIR;
+    const long long ones = (each + 127) / 128 * ((N + 127) / 128) * experts;
+    if (each <= (experts == 1 ? 16 : 4)) return Fp8Tile::FEW16;
+    if (each <= (experts == 1 ? 32 : 12)) return Fp8Tile::FEW32;
+    if (each <= (experts == 1 ? 64 : 24) || (each <= 256 && 2 * ones <= sms)) return Fp8Tile::FEW64;
+    if (each > 128 && N > 128 && ones > sms && !k_tail) return Fp8Tile::PAIR;
     return Fp8Tile::ONE;
 }
 
@@ -127,7 +141,7 @@ int rows_product(int rows, int experts, int N, int K, const void* A, int lda, co
     int st = device_context(&dev, &sms, &status);
     if (st) return st;
     if (rows == 0) return TCL_OK;
-    const Fp8Tile tile = choose_tile(rows, experts, N, K % 16 != 0);
+    const Fp8Tile tile = choose_tile(rows, experts, N, K % 16 != 0, sms);
     const Fp8TileInfo t = fp8_tile_info(tile);
     const int tt = t.swap ? t.bq : t.bp, tw = t.swap ? t.bp : t.bq;
     Fp8Params p = {};
@@ -249,7 +263,9 @@ int gemm_fp8_experts_wgrad(int rows, int experts, int N, int K, const void* A, i
                 return status_of(cudaErrorUnknown);
         return TCL_OK;
     }
-    const Fp8Tile tile = choose_tile(N, 1, K, false) == Fp8Tile::PAIR ? Fp8Tile::PAIR : Fp8Tile::ONE;
+    // (as above: 256 × 256 tiles once 128 × 128 ones need a second wave)
+    const long long ones = static_cast<long long>(experts) * ((N + 127) / 128) * ((K + 127) / 128);
+    const Fp8Tile tile = N > 128 && K > 128 && ones > sms ? Fp8Tile::PAIR : Fp8Tile::ONE;
     const Fp8TileInfo t = fp8_tile_info(tile);
     Fp8Params p = {};
     p.offsets = offsets;

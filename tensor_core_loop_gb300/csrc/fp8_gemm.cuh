@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
                     const float2 v2 = ptx::f32x2_get(sum[i / 2]);
                     const float v = i & 1 ? v2.y : v2.x;
                     if (share > 1) {
-                        sums[i * 128 + prl] = v;
+                        sums[(h * C::CW + i) * 128 + prl] = v;
                     } else if (i < n) {
                         if (p.out_bf16)
                             static_cast<__nv_bfloat16*>(p.C)[at + i * p.ldc] = __float2bfloat16_rn(v);
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
             const Fp8Unit U = fp8_unit<C>(p, first, off, u0, cur);
             const int prl = (warp & 3) * 32 + lane, pr = U.p0 + prl;
             const uint32_t sums = ptx::smem_u32(smem);
-            for (int i = part; i < C::CW; i += share) {
+            for (int i = ((warp - 4) >> 2) * share + part; i < BQ; i += share * (C::PW / 4)) {
                 if (pr >= U.p_end || U.q0 + i >= U.q_end) continue;
                 float v = 0.0f;
                 for (int r = 0; r < share; ++r)

@@ -22,7 +22,8 @@ int tensor_map_result(const void* ptr, int bf16, uint64_t cols, uint64_t rows, u
 // ---- fp8 products (k_fp8_gemm.cu)
 enum class Fp8Tile : int {
     FEW16,    // 128 weight rows × 16 token rows
-    FEW32,    // 128 weight rows × 32 token rows
+    FEW32,    // ... × 32
+    FEW64,    // ... × 64
     ONE,      // 128 × 128 on one SM
     PAIR,     // 256 × 256 on a pair of SMs
 };
