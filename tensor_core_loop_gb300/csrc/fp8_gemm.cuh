@@ -46,6 +46,7 @@ enum : unsigned int {
 };
 
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxSorted = 256;   // experts that every CTA can put in order in a microsecond
 
 struct Fp8Side {
     const float* scale;
@@ -101,10 +102,12 @@ struct Fp8Cfg {
     static constexpr int SLOT_Q = 128;               // a slot: P's scales, then Q's (each, or one per 128 rows)
     static constexpr int SLOT = SLOT_Q + (QVEC ? BQ : 4);
     static constexpr int TAB = kMaxExperts + 8;
-    static constexpr int NBARS = 2 * STAGES + 2 * SS + 2 * NB + 1;
+    static constexpr int UR = 2;                     // units published ahead to the promotion warps
+    static constexpr int NBARS = 2 * STAGES + 2 * SS + 2 * NB + 2 * UR + 1;
     static constexpr int SMEM_BYTES =
-        1024 + STAGES * STAGE_BYTES + STORE_BYTES + SS * SLOT * 4 + 2 * TAB * 4 + (NBARS + 4) * 8;
+        1024 + STAGES * STAGE_BYTES + STORE_BYTES + SS * SLOT * 4 + 2 * TAB * 4 + UR * 32 + (NBARS + 4) * 8;
     static constexpr uint32_t IDESC = ptx::make_idesc(0, 0, 0, 0, BP, BQ);   // e4m3 both, K-major both
+    static_assert(STAGE_BYTES % 1024 == 0 && SS * SLOT % 4 == 0, "16-byte aligned tables behind the slots");
     static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB per-block shared memory limit");
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TMEM columns");
     static_assert(BQ % 16 == 0 && CW % CHUNK == 0 && (CHUNK == 16 || CHUNK == 32), "column split");
@@ -118,12 +121,14 @@ struct Fp8Unit {
 
 // The tiles of all experts in one walk. first[e] counts the tiles before expert e;
 // first[experts + 1] is the total (entry `experts` holds the rows behind the last one).
+// For weight gradients first[] lists the experts by falling length instead.
 template <class C>
 __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8Params& p, const int* first, const int* off, int u, int& cur) {
     Fp8Unit U;
     if (p.wgrad) {
         const int tp = (p.wrows + C::BP - 1) / C::BP, tq = (p.qrows + C::BQ - 1) / C::BQ;
-        const int e = u / (tp * tq), r = u - e * (tp * tq);
+        const int i = u / (tp * tq), r = u - i * (tp * tq);
+        const int e = first[i];   // the experts by falling length
         U.e = e;
         U.p0 = r / tq * C::BP;
         U.q0 = r % tq * C::BQ;
@@ -253,7 +258,8 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
     uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
     uint8_t* slabs = smem + C::STAGES * C::STAGE_BYTES;
     float* slots = reinterpret_cast<float*>(slabs + C::STORE_BYTES);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(slots + C::SS * C::SLOT);
+    int* published = reinterpret_cast<int*>(slots + C::SS * C::SLOT);   // UR × 8, 16-byte aligned
+    uint64_t* bars = reinterpret_cast<uint64_t*>(published + C::UR * 8);
     int* first = reinterpret_cast<int*>(bars + C::NBARS + 2);
     int* off = first + C::TAB;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::NBARS);
@@ -266,7 +272,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
     const uint32_t sempty0 = sfull0 + 8 * C::SS;
     const uint32_t accf0 = sempty0 + 8 * C::SS;
     const uint32_t acce0 = accf0 + 8 * C::NB;
-    const uint32_t drain_bar = acce0 + 8 * C::NB;
+    const uint32_t ufull0 = acce0 + 8 * C::NB;
+    const uint32_t uempty0 = ufull0 + 8 * C::UR;
+    const uint32_t drain_bar = uempty0 + 8 * C::UR;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -284,6 +292,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
         for (int b = 0; b < C::NB; ++b) {
             ptx::mbar_init(accf0 + 8 * b, 1);
             ptx::mbar_init(acce0 + 8 * b, C::CTAS * C::PW);
+        }
+        for (int i = 0; i < C::UR; ++i) {
+            ptx::mbar_init(ufull0 + 8 * i, 1);
+            ptx::mbar_init(uempty0 + 8 * i, C::PW);
         }
         ptx::mbar_init(drain_bar, 1);
         *abort_flag = 0u;
@@ -328,7 +340,20 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
     if (*bad_offsets) {
         if (threadIdx.x == 0) atomicCAS(p.status, 0u, static_cast<unsigned int>(DEV_BAD_OFFSETS));
     } else if (p.wgrad) {
+        // a tile takes as long as its expert has rows: long ones first, dealt out back and forth
         units = E * ((p.wrows + C::BP - 1) / C::BP) * ((p.qrows + BQ - 1) / BQ);
+        for (int e = threadIdx.x; e < E; e += C::THREADS) {
+            const int mine = off[e + 1] - off[e];
+            int before = 0;
+            if (E <= kMaxSorted) {
+                for (int o = 0; o < E; ++o) {
+                    const int n = off[o + 1] - off[o];
+                    before += n > mine || (n == mine && o < e);
+                }
+            }
+            first[E <= kMaxSorted ? before : e] = e;
+        }
+        __syncthreads();   // (uniform: every thread takes this branch)
     } else {
         constexpr int TT = SWAP ? BQ : C::BP, TW = SWAP ? C::BP : BQ;
         const int tw = (p.wrows + TW - 1) / TW;
@@ -356,6 +381,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
     const int u0 = blockIdx.x / share, ustep = gridDim.x / share;
     // few tokens: this CTA's part of a tile's k-blocks
     [[maybe_unused]] const int part = SWAP ? static_cast<int>(blockIdx.x) % share : 0;
+    // step j of this CTA's walk
+    auto walk = [&](int j) {
+        if (QVEC && !SWAP && p.wgrad && (j & 1)) return (j + 1) * ustep - 1 - u0;
+        return j * ustep + u0;
+    };
     auto unit = [&](int u, int& cur) {
         Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
         if constexpr (SWAP) {
@@ -381,7 +411,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
             uint32_t s = 0, ph = 0;
             int cur = 0;
             bool ok = true;
-            for (int u = u0; ok && u < units; u += ustep) {
+            for (int j = 0, u = u0; ok && u < units; u = walk(++j)) {
                 const Fp8Unit U = unit(u, cur);
                 const int pe = (SWAP && !p.wgrad) ? U.e : 0, qe = (!SWAP && !p.wgrad) ? U.e : 0;
                 const int prow = U.p0 + static_cast<int>(rank) * 128, qrow = U.q0 + static_cast<int>(rank) * C::BQL;
@@ -418,7 +448,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
                 uint32_t s = 0, ph = 0, b = 0, bph = 0;
                 int cur = 0;
                 bool ok = true;
-                for (int u = u0; ok && u < units; u += ustep) {
+                for (int j = 0, u = u0; ok && u < units; u = walk(++j)) {
                     const Fp8Unit U = unit(u, cur);
                     for (int kb = 0; kb < U.nk; ++kb) {
                         if (!wait(acce0 + 8 * b, bph ^ 1u, DEV_TIMEOUT_MMA_ACC) ||
@@ -485,9 +515,19 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
             uint32_t s = 0, ph = 0;
             int cur = 0;
             bool ok = true;
-            for (int u = u0; ok && u < units; u += ustep) {
+            for (int j = 0, u = u0; ok && u < units; u = walk(++j)) {
                 const Fp8Unit U = unit(u, cur);
-                const int row0 = of_p ? U.p0 + static_cast<int>(rank) * 128 : U.q0, end = of_p ? U.p_end : U.q_end;
+                if (of_p) {   // what the promotion warps need of it (working it out would hold them up between tiles)
+                if (!wait(uempty0 + 8 * (j % C::UR), (j / C::UR & 1) ^ 1u, DEV_TIMEOUT_PRODUCER)) break;
+                if (lane == 0) {
+                    int4* to = reinterpret_cast<int4*>(published + 8 * (j % C::UR));
+                    to[0] = make_int4(U.p0, U.q0, U.p_end, U.q_end);
+                    to[1] = make_int4(U.e, U.nk, 0, 0);
+                    ptx::mbar_arrive(ufull0 + 8 * (j % C::UR));
+                }
+                __syncwarp();
+            }
+            const int row0 = of_p ? U.p0 + static_cast<int>(rank) * 128 : U.q0, end = of_p ? U.p_end : U.q_end;
                 const int r0 = side.block ? row0 >> 7 : row0;
                 const int n = min(per, (side.block ? (end + 127) >> 7 : end) - r0);   // those that exist; zeros behind them
                 const float* at = side.scale + (of_p == SWAP ? U.e * side.s_expert : 0ll) + U.kb0 * side.s_group +
@@ -521,14 +561,15 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
         const int prl = quarter * 32 + lane;
         const uint32_t acce_leader0 = PAIR ? ptx::mapa_shared(acce0, 0u) : acce0;
         uint32_t s = 0, ph = 0, b = 0, bph = 0;
-        int cur = 0;
         [[maybe_unused]] int used = 0;   // the slab whose turn it is
         bool ok = true;
-        for (int u = u0; ok && u < units; u += ustep) {
+        for (int j = 0, u = u0; ok && u < units; u = walk(++j)) {
             uint64_t sum[C::CW / 2];   // two columns each
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) sum[i] = 0;
-            const int nk = unit(u, cur).nk;
+            const int* mine = published + 8 * (j % C::UR);
+            if (!wait(ufull0 + 8 * (j % C::UR), j / C::UR & 1, DEV_TIMEOUT_EPILOGUE)) break;
+            const int nk = mine[5];
             for (int kb = 0; kb < nk; ++kb) {
                 if (!wait(sfull0 + 8 * s, ph, DEV_TIMEOUT_EPILOGUE)) {
                     ok = false;
@@ -575,8 +616,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
                 }
             }
             if (!ok) break;
-            // (worked out again rather than kept: the sums leave few registers)
-            const Fp8Unit U = unit(u, cur);
+            // (read only now: the sums leave few registers)
+            const int4 u4 = *reinterpret_cast<const int4*>(mine);
+            const Fp8Unit U = {u4.x, u4.y, u4.z, u4.w, mine[4], 0, nk};
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(uempty0 + 8 * (j % C::UR));
             const int qc = U.q0 + h * C::CW;
             if constexpr (SWAP) {
                 // consecutive lanes hold consecutive columns of C
