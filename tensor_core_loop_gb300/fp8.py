@@ -36,7 +36,10 @@ EXPORTED_SYMBOLS_FP8 = ("tcl_quantize_fp8_rows", "tcl_quantize_fp8_columns", "tc
                         "tcl_combine", "tcl_combine_grad")
 MAX_EXPERTS = 1024
 GROUP = 128
-X_BF16, X_F32 = 0, 1
+if torch is not None:
+    _F8, _F32, _BF16, _I32 = torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.int32
+    _X_TYPES = {_BF16: 0, _F32: 1}   # X_BF16, X_F32
+    _OUT = {_BF16: OUT_BF16, _F32: OUT_F32}
 SCALE_ROWS, SCALE_BLOCKS = 0, 1
 
 _bound = None
@@ -100,31 +103,31 @@ def _device(name, first, *rest):
 
 
 def _x_type(t, name):
-    if t.dtype == torch.bfloat16:
-        return X_BF16
-    if t.dtype == torch.float32:
-        return X_F32
-    raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+    code = _X_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+    return code
 
 
-def _ld(t, name, dim=2):
-    """Leading dimension of a matrix (or of each of a batch) with contiguous rows."""
-    if t.dim() != dim:
+def _mat(t, name, dim=2):
+    """(rows, columns, leading dimension) of a matrix, or of each of a batch, with contiguous rows."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dim:
         raise ValueError(f"{name} must have {dim} dimensions")
-    rows, cols = t.shape[-2:]
+    rows, cols = shape[-2], shape[-1]
     if cols < 1:
         raise ValueError(f"{name} must have at least one column")
-    if cols > 1 and t.stride(-1) != 1:
+    if cols > 1 and stride[-1] != 1:
         raise ValueError(f"{name}'s rows must be contiguous (stride(-1) == 1)")
-    if rows > 1:
-        if t.stride(-2) < cols:
-            raise ValueError(f"{name}'s rows overlap")
-        return t.stride(-2)
-    return -(-cols // 16) * 16   # a single row never steps to a second one
+    if rows < 2:
+        return rows, cols, (cols + 15) & ~15   # a single row never steps to a second one
+    if stride[-2] < cols:
+        raise ValueError(f"{name}'s rows overlap")
+    return rows, cols, stride[-2]
 
 
 def _int32(t, name, shape=None):
-    if t.dtype != torch.int32:
+    if t.dtype != _I32:
         raise TypeError(f"{name} must be int32")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -133,7 +136,7 @@ def _int32(t, name, shape=None):
 
 
 def _order(order, tokens=None):
-    offsets, position, source = order
+    _, position, source = order
     _int32(position, "position")
     _int32(source, "source")
     if position.dim() != 2 or source.dim() != 1:
@@ -168,15 +171,14 @@ def quantize_fp8(x, along: str = "rows", order: ExpertOrder | None = None, strea
     if order is not None and batched:
         raise ValueError("an order goes with rows or columns")
     xt = _x_type(x, "x")
-    ldx = _ld(x, "x", 3 if batched and x.dim() == 3 else 2)
-    rows, cols = x.shape[-2:]
-    position = source = None
+    rows, cols, ldx = _mat(x, "x", 3 if batched and x.dim() == 3 else 2)
+    position = source = pos = src = None
     top, made = 1, rows
     if order is not None:
         position, source = _order(order, rows)
         top, made = position.shape[1], source.shape[0]
+        pos, src = position.data_ptr(), source.data_ptr()
     device = _device("x", x, position, source)
-    pos, src = (position.data_ptr(), source.data_ptr()) if order is not None else (None, None)
     with _on(stream):
         if along == "rows":
             data = _fp8(made, cols, device)
@@ -204,62 +206,58 @@ def quantize_fp8(x, along: str = "rows", order: ExpertOrder | None = None, strea
 
 
 def _operand(data, scale, name, dim=2):
-    if data.dtype != torch.float8_e4m3fn:
+    """(rows, columns, leading dimension, the scales' shape) of an e4m3 matrix."""
+    if data.dtype != _F8:
         raise TypeError(f"{name} must be float8_e4m3fn")
-    if scale.dtype != torch.float32:
+    if scale.dtype != _F32:
         raise TypeError(f"{name}'s scales must be float32")
-    if scale.dim() != dim:
+    shape = scale.shape
+    if len(shape) != dim:
         raise ValueError(f"{name}'s scales must have {dim} dimensions")
-    return _ld(data, name, dim)
+    return *_mat(data, name, dim), shape
 
 
-def _kind(data, scale, name):
-    """Whether scales belong to the rows of ``data`` or to blocks of 128 of them."""
-    rows, cols = data.shape[-2:]
-    groups = -(-cols // GROUP)
-    if scale.shape[-1] != groups or scale.shape[:-2] != data.shape[:-2]:
-        raise ValueError(f"{name} of shape {tuple(data.shape)} does not go with scales of shape {tuple(scale.shape)}")
-    if scale.shape[-2] == rows:
-        return SCALE_ROWS
-    if scale.shape[-2] == -(-rows // GROUP):
-        return SCALE_BLOCKS
-    raise ValueError(f"{name} of shape {tuple(data.shape)} does not go with scales of shape {tuple(scale.shape)}")
+def _kind(rows, cols, shape, name):
+    """Whether scales of this shape belong to rows of a matrix or to blocks of 128 of them."""
+    if shape[-1] == -(-cols // GROUP):
+        if shape[-2] == rows:
+            return SCALE_ROWS
+        if shape[-2] == -(-rows // GROUP):
+            return SCALE_BLOCKS
+    raise ValueError(f"{name} of {rows} x {cols} does not go with scales of shape {tuple(shape)}")
 
 
-def _out(dtype):
-    if dtype is None or dtype == torch.bfloat16:
-        return torch.bfloat16, OUT_BF16
-    if dtype == torch.float32:
-        return dtype, OUT_F32
-    raise TypeError("the result is bfloat16 or float32")
-
-
-def _result(out, shape, dtype, device):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != shape or out.dtype != dtype:
-        raise ValueError(f"out must be {dtype} of shape {shape}")
-    return out
+def _out_type(out, out_dtype, shape):
+    """(type, its code) of a result: ``out``'s, or ``out_dtype`` (None: bf16)."""
+    if out is not None:
+        if tuple(out.shape) != shape or out_dtype not in (None, out.dtype):
+            raise ValueError(f"out must be {out_dtype or out.dtype} of shape {shape}")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = _BF16
+    code = _OUT.get(out_dtype)
+    if code is None:
+        raise TypeError("the result is bfloat16 or float32")
+    return out_dtype, code
 
 
 def gemm_fp8(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None):
     """C = A·Bᵀ (M x N; bf16 or ``out_dtype=torch.float32``) of e4m3 ``a`` (M x K, a scale for
     each row and 128 of K) and ``b`` (N x K, scales for its rows or for 128 x 128 blocks)."""
-    lda, ldb = _operand(a, a_scale, "a"), _operand(b, b_scale, "b")
-    M, K = a.shape
-    N = b.shape[0]
-    if b.shape[1] != K or N < 1:
+    M, K, lda, sa = _operand(a, a_scale, "a")
+    N, k, ldb, sb = _operand(b, b_scale, "b")
+    if k != K or N < 1:
         raise ValueError(f"shape mismatch: {tuple(a.shape)} and {tuple(b.shape)}")
-    if tuple(a_scale.shape) != (M, -(-K // GROUP)):
-        raise ValueError(f"a needs scales of shape {(M, -(-K // GROUP))}, not {tuple(a_scale.shape)}")
-    kind = _kind(b, b_scale, "b")
-    dtype, code = _out(out.dtype if out is not None else out_dtype)
+    if sa[0] != M or sa[1] != -(-K // GROUP):
+        raise ValueError(f"a needs scales of shape {(M, -(-K // GROUP))}, not {tuple(sa)}")
+    kind = _kind(N, K, sb, "b")
+    dtype, code = _out_type(out, out_dtype, (M, N))
     device = _device("a", a, a_scale, b, b_scale, out)
     with _on(stream):
-        c = _result(out, (M, N), dtype, device)
+        c = torch.empty((M, N), dtype=dtype, device=device) if out is None else out
+        ldc = N if out is None else _mat(c, "out")[2]
         _call(_lib().gemm_fp8, "gemm_fp8", device, stream, M, N, K, a.data_ptr(), lda, a_scale.data_ptr(),
-              a_scale.stride(0), a_scale.stride(1), b.data_ptr(), ldb, b_scale.data_ptr(), kind, b_scale.stride(0),
-              b_scale.stride(1), c.data_ptr(), _ld(c, "out"), code)
+              *a_scale.stride(), b.data_ptr(), ldb, b_scale.data_ptr(), kind, *b_scale.stride(), c.data_ptr(), ldc, code)
     return c
 
 
@@ -268,23 +266,25 @@ def gemm_fp8_experts(a, a_scale, b, b_scale, offsets, out_dtype=None, out=None, 
     ``a`` rows x K sorted by expert, ``b`` experts x N x K, ``offsets`` int32 on the GPU.
     Rows behind the last expert's are zeros. The gradient of ``a`` is the same product of the
     result's gradient with the transposed matrices (``quantize_fp8(w, along="blocks_t")``)."""
-    lda, ldb = _operand(a, a_scale, "a"), _operand(b, b_scale, "b", 3)
-    rows, K = a.shape
-    experts, N = b.shape[:2]
-    if b.shape[2] != K or N < 1 or experts < 1:
+    rows, K, lda, sa = _operand(a, a_scale, "a")
+    N, k, ldb, sb = _operand(b, b_scale, "b", 3)
+    experts = b.shape[0]
+    if k != K or N < 1 or experts < 1:
         raise ValueError(f"shape mismatch: {tuple(a.shape)} and {tuple(b.shape)}")
-    if tuple(a_scale.shape) != (rows, -(-K // GROUP)):
-        raise ValueError(f"a needs scales of shape {(rows, -(-K // GROUP))}, not {tuple(a_scale.shape)}")
-    kind = _kind(b, b_scale, "b")
+    if sa[0] != rows or sa[1] != -(-K // GROUP):
+        raise ValueError(f"a needs scales of shape {(rows, -(-K // GROUP))}, not {tuple(sa)}")
+    if sb[0] != experts:
+        raise ValueError(f"b of {experts} experts does not go with scales of shape {tuple(sb)}")
+    kind = _kind(N, K, sb, "b")
     _int32(offsets, "offsets", (experts + 1,))
-    dtype, code = _out(out.dtype if out is not None else out_dtype)
+    dtype, code = _out_type(out, out_dtype, (rows, N))
     device = _device("a", a, a_scale, b, b_scale, offsets, out)
     with _on(stream):
-        c = _result(out, (rows, N), dtype, device)
+        c = torch.empty((rows, N), dtype=dtype, device=device) if out is None else out
+        ldc = N if out is None else _mat(c, "out")[2]
         _call(_lib().gemm_fp8_experts, "gemm_fp8_experts", device, stream, rows, experts, N, K, a.data_ptr(), lda,
-              a_scale.data_ptr(), a_scale.stride(0), a_scale.stride(1), b.data_ptr(), ldb,
-              b.stride(0) if experts > 1 else N * ldb, b_scale.data_ptr(), kind, b_scale.stride(0), b_scale.stride(1),
-              b_scale.stride(2), offsets.data_ptr(), c.data_ptr(), _ld(c, "out"), code)
+              a_scale.data_ptr(), *a_scale.stride(), b.data_ptr(), ldb, b.stride(0) if experts > 1 else N * ldb,
+              b_scale.data_ptr(), kind, *b_scale.stride(), offsets.data_ptr(), c.data_ptr(), ldc, code)
     return c
 
 
@@ -294,7 +294,7 @@ def gemm_fp8_experts_wgrad(a, a_scale, b, b_scale, offsets, out_dtype=None, out=
     quantised down the sorted rows (``quantize_fp8(..., along="columns")``). ``offsets`` are
     multiples of 128 (``sort_by_expert(..., align=128)``); experts without rows get zeros."""
     for t, s, name in ((a, a_scale, "a"), (b, b_scale, "b")):
-        if t.dtype != torch.float8_e4m3fn:
+        if t.dtype != _F8:
             raise TypeError(f"{name} must be float8_e4m3fn")
         if t.dim() != 2 or s.dim() != 2:
             raise ValueError(f"{name} and its scales must have 2 dimensions")
@@ -306,16 +306,16 @@ def gemm_fp8_experts_wgrad(a, a_scale, b, b_scale, offsets, out_dtype=None, out=
     K = b.shape[0]
     if b.shape[1] != rows or N < 1 or K < 1:
         raise ValueError(f"shape mismatch: {tuple(a.shape)} and {tuple(b.shape)}")
-    lda, ldb = (_ld(a, "a"), _ld(b, "b")) if rows else (0, 0)
+    lda, ldb = (_mat(a, "a")[2], _mat(b, "b")[2]) if rows else (0, 0)
     experts = offsets.numel() - 1
     if experts < 1:
         raise ValueError("offsets must have one entry more than there are experts")
     _int32(offsets, "offsets", (experts + 1,))
-    dtype, code = _out(out.dtype if out is not None else out_dtype)
+    dtype, code = _out_type(out, out_dtype, (experts, N, K))
     device = _device("a", a, a_scale, b, b_scale, offsets, out)
     with _on(stream):
-        c = _result(out, (experts, N, K), dtype, device)
-        ldc = _ld(c, "out", 3)
+        c = torch.empty((experts, N, K), dtype=dtype, device=device) if out is None else out
+        ldc = _mat(c, "out", 3)[2]
         _call(_lib().gemm_fp8_experts_wgrad, "gemm_fp8_experts_wgrad", device, stream, rows, experts, N, K, a.data_ptr(),
               lda, a_scale.data_ptr(), a_scale.stride(0), a_scale.stride(1), b.data_ptr(), ldb, b_scale.data_ptr(),
               b_scale.stride(0), b_scale.stride(1), offsets.data_ptr(), c.data_ptr(), ldc,
@@ -350,20 +350,22 @@ def sort_by_expert(ids, experts: int, align: int = 1, stream=None) -> ExpertOrde
 def gather_rows(x, order: ExpertOrder, stream=None):
     """The tokens' rows of ``x`` (bf16 or fp32) in sorted order, zeros in rows without a slot.
     Its gradient is ``combine(d_rows, None, order)``."""
-    xt, ldx = _x_type(x, "x"), _ld(x, "x")
-    position, source = _order(order, x.shape[0])
+    xt = _x_type(x, "x")
+    tokens, cols, ldx = _mat(x, "x")
+    position, source = _order(order, tokens)
+    rows = source.shape[0]
     device = _device("x", x, position, source)
     with _on(stream):
-        y = torch.empty((source.shape[0], x.shape[1]), dtype=x.dtype, device=device)
-        _call(_lib().tcl_gather_rows, "gather_rows", device, stream, xt, x.shape[0], position.shape[1], y.shape[0],
-              x.shape[1], x.data_ptr(), ldx, position.data_ptr(), source.data_ptr(), y.data_ptr(), x.shape[1])
+        y = torch.empty((rows, cols), dtype=x.dtype, device=device)
+        _call(_lib().tcl_gather_rows, "gather_rows", device, stream, xt, tokens, position.shape[1], rows, cols,
+              x.data_ptr(), ldx, position.data_ptr(), source.data_ptr(), y.data_ptr(), cols)
     return y
 
 
 def _weights(weights, position):
     if weights is None:
         return None
-    if weights.dtype != torch.float32 or not weights.is_contiguous() or weights.shape != position.shape:
+    if weights.dtype != _F32 or not weights.is_contiguous() or weights.shape != position.shape:
         raise ValueError(f"weights must be contiguous float32 of shape {tuple(position.shape)}")
     return weights.data_ptr()
 
@@ -371,36 +373,37 @@ def _weights(weights, position):
 def combine(y, weights, order: ExpertOrder, stream=None):
     """out[t] = sum over the token's slots j of weights[t, j]·y[position[t, j]] (None: ones), in
     fp32, rounded once to ``y``'s type. Dropped slots add nothing."""
-    xt, ldy = _x_type(y, "y"), _ld(y, "y")
+    xt = _x_type(y, "y")
+    rows, cols, ldy = _mat(y, "y")
     position, source = _order(order)
-    if y.shape[0] != source.shape[0]:
-        raise ValueError(f"the order has {source.shape[0]} rows, y {y.shape[0]}")
+    if rows != source.shape[0]:
+        raise ValueError(f"the order has {source.shape[0]} rows, y {rows}")
     w = _weights(weights, position)
     device = _device("y", y, weights, position, source)
     tokens, top = position.shape
     with _on(stream):
-        out = torch.empty((tokens, y.shape[1]), dtype=y.dtype, device=device)
-        _call(_lib().tcl_combine, "combine", device, stream, xt, tokens, top, y.shape[0], y.shape[1], y.data_ptr(), ldy, w,
-              position.data_ptr(), out.data_ptr(), y.shape[1])
+        out = torch.empty((tokens, cols), dtype=y.dtype, device=device)
+        _call(_lib().tcl_combine, "combine", device, stream, xt, tokens, top, rows, cols, y.data_ptr(), ldy, w,
+              position.data_ptr(), out.data_ptr(), cols)
     return out
 
 
 def combine_grad(grad, y, weights, order: ExpertOrder, stream=None):
     """(gradient of ``y``, gradient of ``weights``) of ``combine`` from the gradient of its output:
     rows weights[t, j]·grad[t] (zeros in rows without a slot), and grad[t]·y[position[t, j]] in fp32."""
-    xt, ldg, ldy = _x_type(grad, "grad"), _ld(grad, "grad"), _ld(y, "y")
+    xt, ldg = _x_type(grad, "grad"), _mat(grad, "grad")[2]
+    rows, cols, ldy = _mat(y, "y")
     if y.dtype != grad.dtype or y.shape[1] != grad.shape[1]:
         raise ValueError("grad and y must have the same type and width")
     position, source = _order(order, grad.shape[0])
-    if y.shape[0] != source.shape[0]:
-        raise ValueError(f"the order has {source.shape[0]} rows, y {y.shape[0]}")
+    if rows != source.shape[0]:
+        raise ValueError(f"the order has {source.shape[0]} rows, y {rows}")
     w = _weights(weights, position)
     device = _device("grad", grad, y, weights, position, source)
     tokens, top = position.shape
     with _on(stream):
-        dy = torch.empty((source.shape[0], y.shape[1]), dtype=y.dtype, device=device)
+        dy = torch.empty((rows, cols), dtype=y.dtype, device=device)
         dw = torch.empty((tokens, top), dtype=torch.float32, device=device)
-        _call(_lib().tcl_combine_grad, "combine_grad", device, stream, xt, tokens, top, y.shape[0], y.shape[1],
-              grad.data_ptr(), ldg, y.data_ptr(), ldy, w, position.data_ptr(), source.data_ptr(), dy.data_ptr(),
-              y.shape[1], dw.data_ptr())
+        _call(_lib().tcl_combine_grad, "combine_grad", device, stream, xt, tokens, top, rows, cols, grad.data_ptr(), ldg,
+              y.data_ptr(), ldy, w, position.data_ptr(), source.data_ptr(), dy.data_ptr(), cols, dw.data_ptr())
     return dy, dw
