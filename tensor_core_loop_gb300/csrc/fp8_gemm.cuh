@@ -451,8 +451,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
                 for (int j = 0, u = u0; ok && u < units; u = walk(++j)) {
                     const Fp8Unit U = unit(u, cur);
                     for (int kb = 0; kb < U.nk; ++kb) {
-                        if (!wait(acce0 + 8 * b, bph ^ 1u, DEV_TIMEOUT_MMA_ACC) ||
-                            !wait(full0 + 8 * s, ph, DEV_TIMEOUT_MMA_FULL)) {
+                        // (the operands are there long before the accumulator is free)
+                        if (!wait(full0 + 8 * s, ph, DEV_TIMEOUT_MMA_FULL) ||
+                            !wait(acce0 + 8 * b, bph ^ 1u, DEV_TIMEOUT_MMA_ACC)) {
                             ok = false;
                             break;
                         }
