@@ -66,15 +66,14 @@ int lay_out(Operand& o, uint8_t* to, cudaStream_t stream) {
 //     128 × 64                 19.7  55.4  77.9  89.4   105   140   217
 //     128 × 128                29.6  57.4  82.9  91.1  97.4   113   144   217   382
 //     256 × 256, two SMs                                                  191   287
-// so 128 × 128 tiles while they fit the GPU in one wave, then 256 × 256. (A pair's MMA warp sees
-// only its own SM's shared memory, so it cannot clear a K tail inside a 16-byte piece.)
-Fp8Tile choose_tile(long long tokens, int experts, int N, bool k_tail, int sms) {
+// so 128 × 128 tiles while they fit the GPU in one wave, then 256 × 256.
+Fp8Tile choose_tile(long long tokens, int experts, int N, int sms) {
     const long long each = (tokens + experts - 1) / experts;
     const long long ones = (each + 127) / 128 * ((N + 127) / 128) * experts;
     if (each <= (experts == 1 ? 16 : 4)) return Fp8Tile::FEW16;
     if (each <= (experts == 1 ? 32 : 12)) return Fp8Tile::FEW32;
     if (each <= (experts == 1 ? 64 : 24) || (each <= 256 && 2 * ones <= sms)) return Fp8Tile::FEW64;
-    if (each > 128 && N > 128 && ones > sms && !k_tail) return Fp8Tile::PAIR;
+    if (each > 128 && N > 128 && ones > sms) return Fp8Tile::PAIR;
     return Fp8Tile::ONE;
 }
 
@@ -141,7 +140,7 @@ int rows_product(int rows, int experts, int N, int K, const void* A, int lda, co
     int st = device_context(&dev, &sms, &status);
     if (st) return st;
     if (rows == 0) return TCL_OK;
-    const Fp8Tile tile = choose_tile(rows, experts, N, K % 16 != 0, sms);
+    const Fp8Tile tile = choose_tile(rows, experts, N, sms);
     const Fp8TileInfo t = fp8_tile_info(tile);
     const int tt = t.swap ? t.bq : t.bp, tw = t.swap ? t.bp : t.bq;
     Fp8Params p = {};
@@ -150,7 +149,6 @@ int rows_product(int rows, int experts, int N, int K, const void* A, int lda, co
     p.rows = rows;
     p.wrows = N;
     p.num_kb = groups_of(K);
-    p.k_tail = K % 16 ? K % 128 : 0;
     p.C = C;
     p.ldc = ldc;
     p.out_bf16 = out == TCL_OUT_BF16;

@@ -6,7 +6,8 @@
 // where a side's scales belong to its rows or to blocks of 128 rows. A product of two
 // e4m3 values is exact in fp32 and the tensor core adds a block's 128 of them in fp32;
 // the scales differ from block to block, so each P_kb is taken out of tensor memory and
-// added into fp32 registers by one fused multiply-add per element ("promotion").
+// added into fp32 registers by one fused multiply-add per element ("promotion"). Past the
+// end of K the tensor copies fill in zeros, byte by byte, so K is free.
 //
 // Roles of a CTA (or of each CTA of a pair of SMs):
 //   warp 0      TMA loads of both operands into a ring of 128-byte k-blocks
@@ -63,7 +64,6 @@ struct Fp8Params {
     int qrows;               // weight gradient: rows of Q
     int num_kb;              // k-blocks of a tile (weight gradient: given by the offsets)
     int split;               // few tokens: CTAs of a cluster that share a tile's k-blocks (1: no sharing)
-    int k_tail;              // valid bytes of the last k-block where K is not a multiple of 16, else 0
     int wgrad;
     void* C;
     long long ldc, c_expert;
@@ -456,21 +456,6 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
                             !wait(acce0 + 8 * b, bph ^ 1u, DEV_TIMEOUT_MMA_ACC)) {
                             ok = false;
                             break;
-                        }
-                        if constexpr (!PAIR) {
-                            if (p.k_tail && U.kb0 + kb + 1 == p.num_kb) {
-                                // K ends inside a 16-byte piece, of which a tensor copy brings the
-                                // whole: clear what lies behind the end (16-byte units are permuted
-                                // within each 128-byte row by the row's number mod 8)
-                                uint8_t* st = smem + s * C::STAGE_BYTES;
-                                const int unit = p.k_tail >> 4, from = p.k_tail & 15;
-                                for (int r = lane; r < 128 + BQ; r += 32) {
-                                    uint8_t* at = st + r * 128 + ((unit ^ (r & 7)) << 4);
-                                    for (int i = from; i < 16; ++i) at[i] = 0;
-                                }
-                                ptx::fence_proxy_async_smem();
-                                __syncwarp();
-                            }
                         }
                         ptx::tc_fence_after();
                         const uint64_t ad = adesc0 + s * STEP, bd = bdesc0 + s * STEP;

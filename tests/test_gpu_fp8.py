@@ -144,7 +144,7 @@ def test_quantize_in_expert_order(along, tokens, top, experts, align, cols):
 
 GEMMS = [(1, 1, 1), (1, 128, 128), (1, 4096, 1030), (2, 130, 300), (7, 100, 16), (16, 512, 2048), (17, 257, 129), (32, 640, 384),
          (33, 384, 513), (64, 200, 1000), (100, 776, 130), (128, 128, 128), (129, 129, 2000), (300, 1000, 640),
-         (1000, 776, 1030), (600, 1000, 1024), (1024, 1536, 512)]
+         (1000, 776, 1030), (600, 1000, 1024), (1024, 1536, 512), (1300, 2056, 259), (2000, 1111, 384)]
 
 
 @pytest.mark.parametrize("out", [BF16, F32])
@@ -201,6 +201,19 @@ def test_gemm_non_finite_values_stay_in_their_rows():
         assert torch.equal(c[keep], clean[keep])
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 200, 1), (40, 130, 131), (300, 300, 255), (1500, 1600, 140), (1500, 1600, 1030)])
+def test_gemm_bytes_behind_a_row_do_not_count(M, N, K):
+    pitch = -(-K // 16) * 16
+    a, sa = random_operand(M, K, 3, pitch=pitch)
+    b, sb = random_operand(N, K, 4, per=128, pitch=pitch)
+    clean = tcl.gemm_fp8(a, sa, b, sb, out_dtype=F32)
+    for t in (a, b):
+        t.as_strided((t.shape[0], pitch), (pitch, 1)).view(torch.uint8)[:, K:] = 0x7F       # NaN
+    assert torch.equal(tcl.gemm_fp8(a, sa, b, sb, out_dtype=F32), clean)
+    want, bound = ref.product_bound(ref.values(a, sa), ref.values(b, sb), F32)
+    ref.check(clean, want, bound)
+
+
 def test_gemm_repeats_and_streams():
     a, sa = random_operand(513, 1024, 3)
     b, sb = random_operand(700, 1024, 4, per=128)
@@ -252,10 +265,10 @@ def offsets_of(counts, align=1):
     return o
 
 
-COUNTS = [[1], [0, 1, 0], [3, 0, 5, 1], [16, 17, 0, 15], [40, 1, 0, 33, 64], [130, 0, 127, 1, 256], [0, 0, 700, 0], [300] * 5]
+COUNTS = [[1], [0, 1, 0], [3, 0, 5, 1], [16, 17, 0, 15], [40, 1, 0, 33, 64], [130, 0, 127, 1, 256], [0, 0, 700, 0], [300] * 5, [700, 513, 0, 1025]]
 
 
-@pytest.mark.parametrize("N,K,per,out", [(128, 128, 128, BF16), (300, 513, 128, F32), (257, 640, 1, BF16), (1, 16, 1, F32)])
+@pytest.mark.parametrize("N,K,per,out", [(128, 128, 128, BF16), (300, 513, 128, F32), (257, 640, 1, BF16), (1, 16, 1, F32), (1000, 200, 128, BF16)])
 @pytest.mark.parametrize("counts", COUNTS)
 @pytest.mark.parametrize("behind", [0, 3, 200])
 def test_experts(counts, N, K, per, out, behind):
@@ -308,7 +321,8 @@ def test_bad_offsets_are_reported(o, rows):
     assert tcl.last_device_error() == (0, 0)
 
 
-@pytest.mark.parametrize("N,K,out", [(128, 128, F32), (300, 77, F32), (64, 513, BF16), (1, 1, F32)])
+@pytest.mark.parametrize("N,K,out", [(128, 128, F32), (300, 77, F32), (64, 513, BF16), (1, 1, F32), (1000, 900, F32),
+                                     (1024, 1281, BF16)])
 @pytest.mark.parametrize("counts", [[1], [0, 3], [128, 0, 0, 300], [5, 640, 130, 0, 1]])
 @pytest.mark.parametrize("behind", [0, 128, 40])
 def test_wgrad(counts, N, K, out, behind):
