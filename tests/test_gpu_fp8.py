@@ -227,6 +227,29 @@ def test_gemm_repeats_and_streams():
     assert torch.equal(c, d)
 
 
+def test_streams_have_their_own_scratch():
+    """Operands off the tensor copies' grid go through library scratch: calls on two streams at once."""
+    jobs = []
+    for i, (M, N, K) in enumerate([(900, 700, 1000), (5, 3000, 2000), (300, 300, 3001)]):
+        a, sa = random_operand(M, K, 50 + i, pitch=K + 7)
+        b, sb = random_operand(N, K, 60 + i, per=128, pitch=K + 5)
+        jobs.append((a, sa, b, sb))
+    want = [tcl.gemm_fp8(*job) for job in jobs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(4):
+        for k in range(3):
+            for n, st in enumerate(streams):
+                j = k if n == 0 else 2 - k
+                got.append((j, tcl.gemm_fp8(*jobs[j], stream=st)))
+    torch.cuda.synchronize()
+    for j, c in got:
+        assert torch.equal(c, want[j])
+    for st in streams:
+        tcl.stream_release(st)
+
+
 def test_gemm_in_a_graph():
     x, w = numbers(100, 600, 1).to(DEV), numbers(300, 600, 2).to(DEV)
     wq, ws = tcl.quantize_fp8(w, along="blocks")
