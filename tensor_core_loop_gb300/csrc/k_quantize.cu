@@ -57,7 +57,7 @@ __device__ __forceinline__ void put8(uint8_t* p, int n, bool vec, uint2 w) {
 // several (`row_teams`, a power of two, to a row), and N rows one after another whose loads
 // are all issued first. With an order, a token's row is read and quantised once and written to
 // each of its rows; blocks behind the tokens' write the rows that no token has.
-constexpr int kTeams = 8, kZeroRows = 64;
+constexpr int kTeams = 8, kZeroRows = 32;
 
 template <typename T, int N>
 __global__ void __launch_bounds__(16 * kTeams) quant_rows_kernel(const QuantRows a, int groups, int row_teams_log2,

@@ -64,7 +64,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids,
     int* part = firsts + experts + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int blocks = gridDim.x;
-    for (int i = threadIdx.x; i < (kSortWarps + 2) * experts; i += kSortThreads) sm[i] = 0;
+    // warps of this block that have slots (a few in a serving step: the others' counts are not looked at)
+    const long long left = slots - static_cast<long long>(blockIdx.x) * kSortChunk;
+    const int warps = static_cast<int>(min(static_cast<long long>(kSortWarps), max(0ll, (left + kPerLane * 32 - 1) / (kPerLane * 32))));
+    for (int i = threadIdx.x; i < warps * experts; i += kSortThreads) whist[i] = 0;
+    for (int i = threadIdx.x; i < 2 * experts; i += kSortThreads) total[i] = 0;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     __syncthreads();
@@ -75,14 +79,16 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids,
     int* mine = whist + warp * experts;
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) e[k] = expert_of(ids, base + k * 32, slots, experts);
+    if (warp < warps) {
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-        const unsigned same = __match_any_sync(0xffffffffu, e[k]);
-        const int ahead = __popc(same & ((1u << lane) - 1u));
-        rank[k] = e[k] >= 0 ? mine[e[k]] + ahead : 0;   // among this warp's slots of the expert
-        __syncwarp();
-        if (e[k] >= 0 && ahead == 0) mine[e[k]] += __popc(same);
-        __syncwarp();
+        for (int k = 0; k < kPerLane; ++k) {
+            const unsigned same = __match_any_sync(0xffffffffu, e[k]);
+            const int ahead = __popc(same & ((1u << lane) - 1u));
+            rank[k] = e[k] >= 0 ? mine[e[k]] + ahead : 0;   // among this warp's slots of the expert
+            __syncwarp();
+            if (e[k] >= 0 && ahead == 0) mine[e[k]] += __popc(same);
+            __syncwarp();
+        }
     }
     if (counts) {
         const long long n = static_cast<long long>(blocks) * experts;
@@ -101,8 +107,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids,
     int length = 0;
     if (x < experts) {
         int run = before[x];
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
+#pragma unroll 8
+        for (int w = 0; w < warps; ++w) {
             const int c = whist[w * experts + x];
             whist[w * experts + x] = run;
             run += c;
@@ -155,18 +161,22 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids,
         source[r] = -1;
 }
 
-constexpr int kZeroRows = 64;
+constexpr int kZeroRows = 16;
 
-// Zeros in the rows that no slot has: rows r0 .. r0+63, this thread's eight columns.
+// Zeros in those of the rows r0 .. r0+15 that no slot has, this thread's eight columns.
 template <typename T>
 __device__ __forceinline__ void zero_rows(const int* source, int r0, int rows, T* out, long long ldo, int c, int cols,
                                           bool vec) {
     const float z[8] = {};
-    for (int r = r0; r < min(r0 + kZeroRows, rows); ++r)
-        if (source[r] < 0 && c < cols) store8(out + r * ldo + c, cols - c, vec, z);
+    bool none[kZeroRows];   // (all looked up before the first is used)
+#pragma unroll
+    for (int i = 0; i < kZeroRows; ++i) none[i] = r0 + i < rows && source[r0 + i] < 0;
+#pragma unroll
+    for (int i = 0; i < kZeroRows; ++i)
+        if (none[i] && c < cols) store8(out + (r0 + i) * ldo + c, cols - c, vec, z);
 }
 
-// blockIdx.x: a token, or behind the tokens 64 rows to clear; blockIdx.y: a block's share of
+// blockIdx.x: a token, or behind the tokens 16 rows to clear; blockIdx.y: a block's share of
 // the columns.
 template <typename T>
 __global__ void __launch_bounds__(256) gather_kernel(const RouteRows a, bool vec_in, bool vec_out) {
