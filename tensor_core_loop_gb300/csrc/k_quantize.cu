@@ -112,8 +112,9 @@ __global__ void __launch_bounds__(16 * kTeams) quant_rows_kernel(const QuantRows
 // Tiles of 128 × 128 values, 256 threads with eight rows × eight columns each. Transposed
 // results go through shared memory, column by column of X as 128 bytes, in pieces of 8 bytes
 // whose place is permuted by the column so that neither side has bank conflicts.
+// (fp32 without a bound took 92 registers, two blocks an SM: columns 63 us instead of 53)
 template <typename T, QuantTile KIND>
-__global__ void __launch_bounds__(256) quant_tiles_kernel(const QuantTiles a, bool vec_in, bool vec_out) {
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tiles_kernel(const QuantTiles a, bool vec_in, bool vec_out) {
     constexpr bool TR = KIND != QuantTile::BLOCKS;
     __shared__ uint32_t red[16][kG];
     __shared__ float sc[kG];

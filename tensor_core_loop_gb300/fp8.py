@@ -72,9 +72,9 @@ class ExpertOrder(NamedTuple):
 
 
 def _call(fn, what, device, stream, *args):
-    # (asking for the current stream's handle alone spares the wrapper object: 2 of a small call's microseconds)
+    # (asking for the current stream's handle alone spares its wrapper object: 2 of a small call's microseconds)
     raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
