@@ -110,13 +110,14 @@ int product(Operand a, Fp8Side sa, Operand b, Fp8Side sb, Fp8Tile tile, Fp8Param
     p.Q = t.swap ? sa : sb;
     p.timeout_ns = kTimeoutNs;
     int ctas = t.ctas;
+    const int places = sms * t.per_sm;
     p.split = 1;
-    if (t.swap) {   // few tokens: share tiles while every CTA has an SM and two k-blocks
-        while (p.split < 8 && units * p.split * 2 <= sms && p.num_kb >= p.split * 4) p.split *= 2;
+    if (t.swap) {   // few tokens: share tiles while every CTA has a place and two k-blocks
+        while (p.split < 8 && units * p.split * 2 <= places && p.num_kb >= p.split * 4) p.split *= 2;
         ctas = p.split;
     }
     l.p = p;
-    l.grid = static_cast<int>(std::max(1ll, std::min<long long>(sms / ctas, units))) * ctas;
+    l.grid = static_cast<int>(std::max(1ll, std::min<long long>(places / ctas, units))) * ctas;
     l.stream = stream;
     return status_of(launch_fp8_gemm(l));
 }

@@ -88,7 +88,8 @@ struct Fp8Cfg {
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int B_BYTES = BQL * 128;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = SWAP ? 8 : 4;
+    static constexpr int STAGES = BQ == 64 ? 8 : 4;
+    static constexpr int PER_SM = BQ <= 32 ? 2 : 1;  // CTAs that fit on an SM
     static constexpr int NB = 512 / BQ < 8 ? 512 / BQ : 8;   // accumulators in tensor memory
     static constexpr int TMEM_COLS = NB * BQ;
     static constexpr int PW = BQ >= 64 ? 8 : 4;   // promotion warps, each 32 lanes × CW columns
@@ -113,6 +114,7 @@ struct Fp8Cfg {
         1024 + STAGES * STAGE_BYTES + STORE_BYTES + SS * SLOT * 4 + 2 * TAB * 4 + UR * 32 + (NBARS + 4) * 8;
     static constexpr uint32_t IDESC = ptx::make_idesc(0, 0, 0, 0, BP, BQ);   // e4m3 both, K-major both
     static_assert(STAGE_BYTES % 1024 == 0 && SS * SLOT % 4 == 0, "16-byte aligned tables behind the slots");
+    static_assert(PER_SM * (SMEM_BYTES + 1024) <= 233472 && PER_SM * TMEM_COLS <= 512, "CTAs of an SM");
     static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB per-block shared memory limit");
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TMEM columns");
     static_assert(BQ % 16 == 0 && CW % CHUNK == 0 && (CHUNK == 16 || CHUNK == 32), "column split");
@@ -254,7 +256,7 @@ __device__ __forceinline__ void fp8_store_rows(const uint64_t (&sum)[C::CW / 2],
 }
 
 template <int BQ, bool PAIR, bool SWAP, bool QVEC>
-__global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, 1)
+__global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<BQ, PAIR, SWAP, QVEC>::PER_SM)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmC, const Fp8Params p) {
     using C = Fp8Cfg<BQ, PAIR, SWAP, QVEC>;

@@ -35,7 +35,7 @@ struct Fp8Launch {
     cudaStream_t stream;
 };
 struct Fp8TileInfo {
-    int bp, bq, ctas, box_p, box_q, swap;
+    int bp, bq, ctas, box_p, box_q, swap, per_sm;
 };
 Fp8TileInfo fp8_tile_info(Fp8Tile t);
 cudaError_t launch_fp8_gemm(const Fp8Launch& a);

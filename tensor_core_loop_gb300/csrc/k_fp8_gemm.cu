@@ -39,7 +39,7 @@ cudaError_t launch(const Fp8Launch& a) {
 template <int BQ, bool PAIR, bool SWAP, bool QVEC>
 Fp8TileInfo info() {
     using C = Fp8Cfg<BQ, PAIR, SWAP, QVEC>;
-    return {C::BP, C::BQ, C::CTAS, 128, C::BQL, SWAP ? 1 : 0};
+    return {C::BP, C::BQ, C::CTAS, 128, C::BQL, SWAP ? 1 : 0, C::PER_SM};
 }
 
 }  // namespace
