@@ -55,24 +55,24 @@ int lay_out(Operand& o, uint8_t* to, cudaStream_t stream) {
 
 // The tile for products of `tokens` rows with N columns, for `experts` experts. Few rows go to
 // the MMA's N side, many to its M side. Measured in CUDA graphs on a GB300, microseconds:
-//   dense, N = K = 4096     M = 16    64   128   256   512  1024  2048
-//     128 × 16 / 32 / 64       8    10.4  13.6  14.8  25.0  46.1  78.0   (the best of the three)
-//     128 × 128               15.7  15.3  15.2  15.6  16.4  27.5  49.7
-//     256 × 256, two SMs        -     -     -   18.8  19.2  19.7  33.7
+//   dense, N = K = 4096     M =  8    64   128   256   512  1024  2048
+//     128 × 16                 7.0  12.1  14.0  24.3  42.6
+//     128 × 32                 8.0  10.9  15.1  16.5  28.4
+//     128 × 128               15.6  15.3  15.2  15.5  16.0  27.5  49.7
+//     256 × 256, two SMs                        18.8  19.2  19.4  33.2
 //   64 experts, N = 4096, K = 2048: rows each (on average)
-//                                1     2     8    16    32    64   128   256   512
-//     128 × 16                 15.2  53.2  77.3   104   156   275
-//     128 × 32                 16.6  54.1  75.2  93.5   120   195
-//     128 × 64                 19.7  55.4  77.9  89.4   105   140   217
-//     128 × 128                29.6  57.4  82.9  91.1  97.4   113   144   217   382
-//     256 × 256, two SMs                                                  191   287
-// so 128 × 128 tiles while they fit the GPU in one wave, then 256 × 256.
+//                               1/8     2     8    16    32    64   128   256   512
+//     128 × 16                 11.9  51.6  72.3  85.4   106   173   313
+//     128 × 32                 15.6  52.0  71.8  81.6  92.1   123   210
+//     128 × 128                30.1  57.0  82.4  90.3  96.4   113   143   216   386
+//     256 × 256, two SMs                                                  184   275
+// (128 × 64 tiles were within 5 % of the best of these everywhere.) So 128 × 128 tiles from some
+// dozen rows until they need a second wave of the GPU, then 256 × 256.
 Fp8Tile choose_tile(long long tokens, int experts, int N, int sms) {
     const long long each = (tokens + experts - 1) / experts;
     const long long ones = (each + 127) / 128 * ((N + 127) / 128) * experts;
     if (each <= (experts == 1 ? 16 : 4)) return Fp8Tile::FEW16;
-    if (each <= (experts == 1 ? 32 : 12)) return Fp8Tile::FEW32;
-    if (each <= (experts == 1 ? 64 : 24) || (each <= 256 && 2 * ones <= sms)) return Fp8Tile::FEW64;
+    if (each <= (experts == 1 ? 64 : 40)) return Fp8Tile::FEW32;
     if (each > 128 && N > 128 && ones > sms) return Fp8Tile::PAIR;
     return Fp8Tile::ONE;
 }

@@ -23,7 +23,7 @@
 // 57 % of the time (without promotion 158 us). Eight warps of 128 sums a thread, two to a
 // scheduler, are as many as the registers hold; a few words spilled in the loop cost 30 %.
 // With few rows a weight byte's way from HBM bounds it: 16 tokens on 64 experts of 4096 × 2048
-// read 319 MB in 52 us, 6.1 TB/s. Scales per column (weight gradients) take two fp32
+// read 319 MB in 51 us, 6.2 TB/s. Scales per column (weight gradients) take two fp32
 // operations an element instead of one.
 //
 // The side in the 128 tensor-memory lanes is P, the one in the columns is Q. Many rows
@@ -88,11 +88,11 @@ struct Fp8Cfg {
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int B_BYTES = BQL * 128;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = BQ == 64 ? 8 : 4;
-    static constexpr int PER_SM = BQ <= 32 ? 2 : 1;  // CTAs that fit on an SM
+    static constexpr int STAGES = 4;
+    static constexpr int PER_SM = SWAP ? 2 : 1;      // CTAs that fit on an SM
     static constexpr int NB = 512 / BQ < 8 ? 512 / BQ : 8;   // accumulators in tensor memory
     static constexpr int TMEM_COLS = NB * BQ;
-    static constexpr int PW = BQ >= 64 ? 8 : 4;   // promotion warps, each 32 lanes × CW columns
+    static constexpr int PW = SWAP ? 4 : 8;   // promotion warps, each 32 lanes × CW columns
     static constexpr int CW = BQ / (PW / 4);
     static constexpr int CHUNK = CW < 32 || (QVEC && CW > 64) ? 16 : 32;   // columns per tensor-memory load
     static constexpr int THREADS = 128 + 32 * PW;

@@ -23,7 +23,6 @@ int tensor_map_result(const void* ptr, int bf16, uint64_t cols, uint64_t rows, u
 enum class Fp8Tile : int {
     FEW16,    // 128 weight rows × 16 token rows
     FEW32,    // ... × 32
-    FEW64,    // ... × 64
     ONE,      // 128 × 128 on one SM
     PAIR,     // 256 × 256 on a pair of SMs
 };

@@ -48,7 +48,6 @@ Fp8TileInfo fp8_tile_info(Fp8Tile t) {
     switch (t) {
         case Fp8Tile::FEW16: return info<16, false, true, true>();
         case Fp8Tile::FEW32: return info<32, false, true, true>();
-        case Fp8Tile::FEW64: return info<64, false, true, true>();
         case Fp8Tile::PAIR: return info<256, true, false, true>();
         default: return info<128, false, false, true>();
     }
@@ -59,7 +58,6 @@ cudaError_t launch_fp8_gemm(const Fp8Launch& a) {
     switch (a.tile) {
         case Fp8Tile::FEW16: return launch<16, false, true, true>(a);
         case Fp8Tile::FEW32: return launch<32, false, true, true>(a);
-        case Fp8Tile::FEW64: return launch<64, false, true, true>(a);
         case Fp8Tile::PAIR: return blocks ? launch<256, true, false, false>(a) : launch<256, true, false, true>(a);
         default: return blocks ? launch<128, false, false, false>(a) : launch<128, false, false, true>(a);
     }
