@@ -58,7 +58,8 @@ int lay_out(Operand& o, uint8_t* to, cudaStream_t stream) {
 //   dense, N = K = 4096     M =  8    64   128   256   512  1024  2048
 //     128 × 16                 7.0  12.1  14.0  24.3  42.6
 //     128 × 32                 8.0  10.9  15.1  16.5  28.4
-//     128 × 128               15.6  15.3  15.2  15.5  16.0  27.5  49.7
+//     128 × 128               15.6  15.3  15.2  15.5  16.0  27.5  49.7   (10.4 and 14.0 at M = 128
+//                                                       and 256 since clusters share their k-blocks)
 //     256 × 256, two SMs                        18.8  19.2  19.4  33.2
 //   64 experts, N = 4096, K = 2048: rows each (on average)
 //                               1/8     2     8    16    32    64   128   256   512
@@ -112,8 +113,12 @@ int product(Operand a, Fp8Side sa, Operand b, Fp8Side sb, Fp8Tile tile, Fp8Param
     int ctas = t.ctas;
     const int places = sms * t.per_sm;
     p.split = 1;
-    if (t.swap) {   // few tokens: share tiles while every CTA has a place and two k-blocks
-        while (p.split < 8 && units * p.split * 2 <= places && p.num_kb >= p.split * 4) p.split *= 2;
+    if (t.ctas == 1 && !p.wgrad) {
+        // share tiles while every CTA has a place and enough to do: two k-blocks of a narrow tile,
+        // eight of a 128 × 128 one, whose sums take longer to exchange (1000 × 776 × 1030 with
+        // four or five each 10.8 us, whole 9.2; 128 × 4096 × 4096 with eight each 10.5, whole 15.2)
+        const int least = t.swap ? 2 : 8;
+        while (p.split < 8 && units * p.split * 2 <= places && p.num_kb >= p.split * 2 * least) p.split *= 2;
         ctas = p.split;
     }
     l.p = p;

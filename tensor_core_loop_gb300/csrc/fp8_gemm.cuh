@@ -31,8 +31,8 @@
 // MMA's N allows, with 128 weight rows in P, so that a weight byte is read once for
 // all tokens and no MMA or shared memory is spent on rows that do not exist.
 //
-// Where few tokens leave most SMs without a tile, the CTAs of a cluster share a tile's
-// k-blocks and one after another's sums are added over distributed shared memory.
+// Where one-SM tiles leave most SMs without one, the CTAs of a cluster share a tile's k-blocks
+// and one after another's sums are added over distributed shared memory.
 //
 // Work units are output tiles. Rows sorted by expert come with the experts' offsets on
 // the device: every CTA turns them into a running count of tiles, and walks the tiles
@@ -68,7 +68,7 @@ struct Fp8Params {
     int wrows;               // rows of the weight side (weight gradient: rows of P)
     int qrows;               // weight gradient: rows of Q
     int num_kb;              // k-blocks of a tile (weight gradient: given by the offsets)
-    int split;               // few tokens: CTAs of a cluster that share a tile's k-blocks (1: no sharing)
+    int split;               // one-SM tiles: CTAs of a cluster that share a tile's k-blocks (1: no sharing)
     int wgrad;
     void* C;
     long long ldc, c_expert;
@@ -108,6 +108,7 @@ struct Fp8Cfg {
     static constexpr int SLOT_Q = 128;               // a slot: P's scales, then Q's (each, or one per 128 rows)
     static constexpr int SLOT = SLOT_Q + (QVEC ? BQ : 4);
     static constexpr int TAB = kMaxExperts + 8;
+    static constexpr int SUM_PITCH = BQ + 4;         // floats between rows of a shared tile's sums
     static constexpr int UR = 2;                     // units published ahead to the promotion warps
     static constexpr int NBARS = 2 * STAGES + 2 * SS + 2 * NB + 2 * UR + 1;
     static constexpr int SMEM_BYTES =
@@ -115,6 +116,7 @@ struct Fp8Cfg {
     static constexpr uint32_t IDESC = ptx::make_idesc(0, 0, 0, 0, BP, BQ);   // e4m3 both, K-major both
     static_assert(STAGE_BYTES % 1024 == 0 && SS * SLOT % 4 == 0, "16-byte aligned tables behind the slots");
     static_assert(PER_SM * (SMEM_BYTES + 1024) <= 233472 && PER_SM * TMEM_COLS <= 512, "CTAs of an SM");
+    static_assert(128 * SUM_PITCH * 4 <= STAGES * STAGE_BYTES || PAIR, "a shared tile's sums fit the ring");
     static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB per-block shared memory limit");
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TMEM columns");
     static_assert(BQ % 16 == 0 && CW % CHUNK == 0 && (CHUNK == 16 || CHUNK == 32), "column split");
@@ -384,10 +386,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
         __syncthreads();   // (uniform: every thread takes this branch)
         units = first[E + 1];
     }
-    const int share = SWAP ? p.split : C::CTAS;   // CTAs that work on one tile
+    const int share = PAIR ? C::CTAS : p.split;   // CTAs that work on one tile
     const int u0 = blockIdx.x / share, ustep = gridDim.x / share;
-    // few tokens: this CTA's part of a tile's k-blocks
-    [[maybe_unused]] const int part = SWAP ? static_cast<int>(blockIdx.x) % share : 0;
+    // this CTA's part of a tile's k-blocks
+    [[maybe_unused]] const int part = PAIR ? 0 : static_cast<int>(blockIdx.x) % share;
     // step j of this CTA's walk
     auto walk = [&](int j) {
         if (QVEC && !SWAP && p.wgrad && (j & 1)) return (j + 1) * ustep - 1 - u0;
@@ -395,10 +397,12 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
     };
     auto unit = [&](int u, int& cur) {
         Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
-        if constexpr (SWAP) {
-            const int n = U.nk;
-            U.kb0 = part * n / share;
-            U.nk = (part + 1) * n / share - U.kb0;
+        if constexpr (!PAIR) {
+            if (share > 1) {   // (not for weight gradients: kb0 is 0)
+                const int n = U.nk;
+                U.kb0 = part * n / share;
+                U.nk = (part + 1) * n / share - U.kb0;
+            }
         }
         return U;
     };
@@ -640,7 +644,14 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
                 const int rows = U.p_end - pw, cols = U.q_end - qc;
                 const long long at = (p.wgrad ? U.e * p.c_expert : 0ll) + static_cast<long long>(pw) * p.ldc + qc;
                 uint8_t* slab = slabs + (warp - 4) * C::SLABS * C::SLAB_BYTES;
-                if (rows > 0 && cols > 0) {
+                if (!PAIR && share > 1) {
+                    float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + prl * C::SUM_PITCH + h * C::CW);
+#pragma unroll
+                    for (int i = 0; i < C::CW; i += 4) {
+                        const float2 x = ptx::f32x2_get(sum[i / 2]), y = ptx::f32x2_get(sum[i / 2 + 1]);
+                        to[i / 4] = make_float4(x.x, x.y, y.x, y.y);
+                    }
+                } else if (rows > 0 && cols > 0) {
                     const int e = p.wgrad ? U.e : 0;
                     if (p.out_bf16)
                         fp8_store_rows<C>(sum, slab, used, &tmC, static_cast<__nv_bfloat16*>(p.C) + at, p.ldc, pw, qc, e,
@@ -657,24 +668,61 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
     }
 
     // ------------------------------------------------ shared tiles: the parts' sums, in their order
-    if (SWAP && share > 1) {
+    if (!PAIR && share > 1) {
         __syncwarp();
         ptx::cluster_sync();   // every part's sums are in its shared memory
         if (warp >= 4 && u0 < units) {
             int cur = 0;
             const Fp8Unit U = fp8_unit<C>(p, first, off, u0, cur);
-            const int prl = (warp & 3) * 32 + lane, pr = U.p0 + prl;
             const uint32_t sums = ptx::smem_u32(smem);
-            for (int i = ((warp - 4) >> 2) * share + part; i < BQ; i += share * (C::PW / 4)) {
-                if (pr >= U.p_end || U.q0 + i >= U.q_end) continue;
-                float v = 0.0f;
-                for (int r = 0; r < share; ++r)
-                    v += ptx::ld_cluster_f32(ptx::mapa_shared(sums + 4 * (i * 128 + prl), static_cast<uint32_t>(r)));
-                const long long at = static_cast<long long>(U.q0 + i) * p.ldc + pr;
-                if (p.out_bf16)
-                    static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
-                else
-                    static_cast<float*>(p.C)[at] = v;
+            if constexpr (SWAP) {
+                const int prl = (warp & 3) * 32 + lane, pr = U.p0 + prl;
+                for (int i = part; i < BQ; i += share) {
+                    if (pr >= U.p_end || U.q0 + i >= U.q_end) continue;
+                    float v = 0.0f;
+                    for (int r = 0; r < share; ++r)
+                        v += ptx::ld_cluster_f32(ptx::mapa_shared(sums + 4 * (i * 128 + prl), static_cast<uint32_t>(r)));
+                    const long long at = static_cast<long long>(U.q0 + i) * p.ldc + pr;
+                    if (p.out_bf16)
+                        static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
+                    else
+                        static_cast<float*>(p.C)[at] = v;
+                }
+            } else {
+                // a warp a row, a lane four columns
+                const int n = U.q_end - U.q0 - lane * 4;
+                for (int i = part + share * (warp - 4); i < 128; i += share * C::PW) {
+                    if (U.p0 + i >= U.p_end || n <= 0) continue;
+                    float v[4] = {};
+                    for (int r = 0; r < share; ++r) {
+                        const uint4 x = ptx::ld_cluster_v4(
+                            ptx::mapa_shared(sums + 4 * (i * C::SUM_PITCH + lane * 4), static_cast<uint32_t>(r)));
+                        v[0] += __uint_as_float(x.x);
+                        v[1] += __uint_as_float(x.y);
+                        v[2] += __uint_as_float(x.z);
+                        v[3] += __uint_as_float(x.w);
+                    }
+                    const long long at = static_cast<long long>(U.p0 + i) * p.ldc + U.q0 + lane * 4;
+                    if (p.out_bf16) {
+                        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + at;
+                        if (p.vec && n >= 4) {
+                            *reinterpret_cast<uint2*>(c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k < n) c[k] = __float2bfloat16_rn(v[k]);
+                        }
+                    } else {
+                        float* c = static_cast<float*>(p.C) + at;
+                        if (p.vec && n >= 4) {
+                            *reinterpret_cast<float4*>(c) = make_float4(v[0], v[1], v[2], v[3]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k < n) c[k] = v[k];
+                        }
+                    }
+                }
             }
         }
         __syncwarp();

@@ -27,7 +27,7 @@ cudaError_t launch(const Fp8Launch& a) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    const int cluster = SWAP ? a.p.split : C::CTAS;
+    const int cluster = PAIR ? C::CTAS : a.p.split;
     attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;

@@ -144,7 +144,8 @@ def test_quantize_in_expert_order(along, tokens, top, experts, align, cols):
 
 GEMMS = [(1, 1, 1), (1, 128, 128), (1, 4096, 1030), (2, 130, 300), (7, 100, 16), (16, 512, 2048), (17, 257, 129), (32, 640, 384),
          (33, 384, 513), (64, 200, 1000), (100, 776, 130), (128, 128, 128), (129, 129, 2000), (300, 1000, 640),
-         (1000, 776, 1030), (600, 1000, 1024), (1024, 1536, 512), (1300, 2056, 259), (2000, 1111, 384)]
+         (1000, 776, 1030), (600, 1000, 1024), (1024, 1536, 512), (1300, 2056, 259), (2000, 1111, 384), (70, 500, 4100),
+         (130, 1000, 2050), (255, 300, 8192)]
 
 
 @pytest.mark.parametrize("out", [BF16, F32])
