@@ -113,12 +113,12 @@ int product(Operand a, Fp8Side sa, Operand b, Fp8Side sb, Fp8Tile tile, Fp8Param
     int ctas = t.ctas;
     const int places = sms * t.per_sm;
     p.split = 1;
-    if (t.ctas == 1 && !p.wgrad) {
+    if (t.ctas == 1) {
         // share tiles while every CTA has a place and enough to do: two k-blocks of a narrow tile,
         // eight of a 128 × 128 one, whose sums take longer to exchange (1000 × 776 × 1030 with
         // four or five each 10.8 us, whole 9.2; 128 × 4096 × 4096 with eight each 10.5, whole 15.2)
-        const int least = t.swap ? 2 : 8;
-        while (p.split < 8 && units * p.split * 2 <= places && p.num_kb >= p.split * 2 * least) p.split *= 2;
+        const int least = t.swap ? 2 : 8, kbs = p.wgrad ? p.rows / 128 / p.experts : p.num_kb;
+        while (p.split < 8 && units * p.split * 2 <= places && kbs >= p.split * 2 * least) p.split *= 2;
         ctas = p.split;
     }
     l.p = p;

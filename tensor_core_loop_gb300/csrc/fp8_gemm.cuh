@@ -398,11 +398,9 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
     auto unit = [&](int u, int& cur) {
         Fp8Unit U = fp8_unit<C>(p, first, off, u, cur);
         if constexpr (!PAIR) {
-            if (share > 1) {   // (not for weight gradients: kb0 is 0)
-                const int n = U.nk;
-                U.kb0 = part * n / share;
-                U.nk = (part + 1) * n / share - U.kb0;
-            }
+            const int n = U.nk, lo = part * n / share;
+            U.kb0 += lo;
+            U.nk = (part + 1) * n / share - lo;
         }
         return U;
     };
@@ -702,7 +700,8 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
                         v[2] += __uint_as_float(x.z);
                         v[3] += __uint_as_float(x.w);
                     }
-                    const long long at = static_cast<long long>(U.p0 + i) * p.ldc + U.q0 + lane * 4;
+                    const long long at = (p.wgrad ? U.e * p.c_expert : 0ll) +
+                                         static_cast<long long>(U.p0 + i) * p.ldc + U.q0 + lane * 4;
                     if (p.out_bf16) {
                         __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + at;
                         if (p.vec && n >= 4) {

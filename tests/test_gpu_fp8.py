@@ -363,6 +363,20 @@ def test_wgrad(counts, N, K, out, behind):
         ref.check(c[e], want, bound, f"expert {e}")
 
 
+@pytest.mark.parametrize("counts", [[9000], [5000, 0, 130, 4000]])
+def test_wgrad_of_many_rows_and_few_tiles(counts):
+    """Clusters share the rows of a tile, unevenly long experts and empty ones among them."""
+    o = offsets_of(counts, 128)
+    E, N, K = len(counts), 200, 130
+    a, sa = random_operand(N, o[-1], 1)
+    b, sb = random_operand(K, o[-1], 2)
+    c = tcl.gemm_fp8_experts_wgrad(a, sa, b, sb, torch.tensor(o, dtype=torch.int32, device=DEV), out_dtype=F32)
+    va, vb = ref.values(a, sa), ref.values(b, sb)
+    for e in range(E):
+        want, bound = ref.product_bound(va[:, o[e]:o[e + 1]], vb[:, o[e]:o[e + 1]], F32)
+        ref.check(c[e], want, bound, f"expert {e}")
+
+
 def test_wgrad_refuses_offsets_off_the_groups():
     a, sa = random_operand(64, 256, 1)
     b, sb = random_operand(64, 256, 2)
