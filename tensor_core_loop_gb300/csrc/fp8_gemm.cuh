@@ -198,7 +198,7 @@ __device__ __forceinline__ void fp8_promote(uint64_t* sum, const uint32_t (&r)[N
 // tile (a tile's stores take longer than a k-block of its successor: waiting for them cost
 // 12 % of a product with K = 4096 and a sixth of one with K = 2048); the map cuts columns
 // behind the matrix off. A slab that an expert's end cuts, or whose rows do not start and end on
-// whole 16-byte pieces, is read back and stored piece by piece, four rows to an instruction.
+// whole 16-byte pieces, is read back and stored by the warp.
 template <class C, typename T>
 __device__ __forceinline__ void fp8_store_rows(const uint64_t (&sum)[C::CW / 2], uint8_t* slabs, int& used,
                                                const CUtensorMap* map, T* c, long long ldc, int row, int col, int e,
@@ -237,19 +237,29 @@ __device__ __forceinline__ void fp8_store_rows(const uint64_t (&sum)[C::CW / 2],
             continue;
         }
         __syncwarp();
-        const int u = lane & 7, n = cols - c0 - u * UNIT;
+        if (vec) {   // 16-byte pieces, four rows to an instruction
+            const int u = lane & 7, n = cols - c0 - u * UNIT;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = k * 4 + (lane >> 3);
-            const T* from = reinterpret_cast<const T*>(slab + place(r, u));
-            T* to = c + r * ldc + c0 + u * UNIT;
-            if (r >= rows) continue;
-            if (vec && n >= UNIT) {
-                *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
-            } else {
+            for (int k = 0; k < 8; ++k) {
+                const int r = k * 4 + (lane >> 3);
+                const T* from = reinterpret_cast<const T*>(slab + place(r, u));
+                T* to = c + r * ldc + c0 + u * UNIT;
+                if (r >= rows) continue;
+                if (n >= UNIT) {
+                    *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+                } else {
 #pragma unroll
-                for (int i = 0; i < UNIT; ++i)
-                    if (i < n) to[i] = from[i];
+                    for (int i = 0; i < UNIT; ++i)
+                        if (i < n) to[i] = from[i];
+                }
+            }
+        } else {   // rows at any address: an element a lane, a row at a time
+#pragma unroll 4
+            for (int r = 0; r < min(rows, 32); ++r) {
+#pragma unroll
+                for (int i = lane; i < PER; i += 32)
+                    if (c0 + i < cols)
+                        c[r * ldc + c0 + i] = reinterpret_cast<const T*>(slab + place(r, i / UNIT))[i % UNIT];
             }
         }
         __syncwarp();
