@@ -11,7 +11,7 @@
 //
 // The row kernels are bound by memory: a thread handles eight columns, and a token's row
 // (gather, gradient of combine) is read once for all of its slots. 8191 tokens × 6 slots of
-// 4096 bf16: combine 81 us, 5.8 TB/s, its gradients 151 us, 6.2 TB/s; 16384 × 8 gathered
+// 4096 bf16: combine 81 us, 5.8 TB/s, its gradients 156 us, 6.0 TB/s; 16384 × 8 gathered
 // 209 us, 6.1 TB/s.
 #include <algorithm>
 
@@ -164,45 +164,46 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids,
 constexpr int kZeroRows = 16;
 
 // Zeros in those of the rows r0 .. r0+15 that no slot has, this thread's eight columns.
-template <typename T>
-__device__ __forceinline__ void zero_rows(const int* source, int r0, int rows, T* out, long long ldo, int c, int cols,
-                                          bool vec) {
+template <typename T, bool VEC>
+__device__ __forceinline__ void zero_rows(const int* source, int r0, int rows, T* out, long long ldo, int c, int cols) {
     const float z[8] = {};
     bool none[kZeroRows];   // (all looked up before the first is used)
 #pragma unroll
     for (int i = 0; i < kZeroRows; ++i) none[i] = r0 + i < rows && source[r0 + i] < 0;
 #pragma unroll
     for (int i = 0; i < kZeroRows; ++i)
-        if (none[i] && c < cols) store8(out + (r0 + i) * ldo + c, cols - c, vec, z);
+        if (none[i]) store_columns<VEC>(out + (r0 + i) * ldo, c, cols, z);
 }
 
 // blockIdx.x: a token, or behind the tokens 16 rows to clear; blockIdx.y: a block's share of
 // the columns.
-template <typename T>
-__global__ void __launch_bounds__(256) gather_kernel(const RouteRows a, bool vec_in, bool vec_out) {
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) gather_kernel(const RouteRows a) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+    const int c = first_column<VEC>(blockIdx.y * blockDim.x + threadIdx.x);
+    if (c >= a.cols) return;
     T* out = static_cast<T*>(a.out);
     if (blockIdx.x >= static_cast<unsigned>(a.tokens)) {
-        zero_rows(a.source, (blockIdx.x - a.tokens) * kZeroRows, a.rows, out, a.ldo, c, a.cols, vec_out);
+        zero_rows<T, VEC>(a.source, (blockIdx.x - a.tokens) * kZeroRows, a.rows, out, a.ldo, c, a.cols);
         return;
     }
-    if (c >= a.cols) return;
     const long long t = blockIdx.x;
+    Raw8<T> raw;
     float v[8];
-    load8(static_cast<const T*>(a.x) + t * a.ldx + c, a.cols - c, vec_in, v);
+    load_columns<VEC>(raw, static_cast<const T*>(a.x) + t * a.ldx, c, a.cols);
+    raw.get(v);
     for (int j = 0; j < a.top; ++j) {
         const int r = a.position[t * a.top + j];
-        if (r >= 0 && r < a.rows) store8(out + r * a.ldo + c, a.cols - c, vec_out, v);   // (rounding gives v back)
+        if (r >= 0 && r < a.rows) store_columns<VEC>(out + r * a.ldo, c, a.cols, v);   // (rounding gives v back)
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) combine_kernel(const RouteRows a, bool vec_in, bool vec_out) {
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) combine_kernel(const RouteRows a) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+    const int c = first_column<VEC>(blockIdx.y * blockDim.x + threadIdx.x);
     if (c >= a.cols) return;
     const long long t = blockIdx.x;
     const T* y = static_cast<const T*>(a.x);
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const RouteRows a, bool ve
             const int r = j < a.top ? a.position[t * a.top + j] : -1;
             const bool in = r >= 0 && r < a.rows;
             w[k] = in ? (a.weights ? a.weights[t * a.top + j] : 1.0f) : 0.0f;
-            raw[k].load(y + (in ? r * a.ldx + c : 0), in ? a.cols - c : 0, vec_in);   // (zeros for a dropped slot)
+            load_columns<VEC>(raw[k], y + (in ? r * a.ldx : 0ll), c, in ? a.cols : 0);   // (zeros for a dropped slot)
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -228,20 +229,21 @@ __global__ void __launch_bounds__(256) combine_kernel(const RouteRows a, bool ve
             for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[k], v[i], sum[i]);
         }
     }
-    store8(static_cast<T*>(a.out) + t * a.ldo + c, a.cols - c, vec_out, sum);
+    store_columns<VEC>(static_cast<T*>(a.out) + t * a.ldo, c, a.cols, sum);
 }
 
 // A block per token: its gradient row is read for eight slots at a time. blockIdx.x behind the
 // tokens: rows to clear.
-template <typename T>
-__global__ void __launch_bounds__(256) combine_grad_kernel(const RouteRows a, bool vec_g, bool vec_y, bool vec_out) {
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) combine_grad_kernel(const RouteRows a) {
     __shared__ float part[8][8];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     T* dy = static_cast<T*>(a.out);
+    const int c0 = first_column<VEC>(threadIdx.x);
     if (blockIdx.x >= static_cast<unsigned>(a.tokens)) {
-        for (int c = threadIdx.x * 8; c < a.cols; c += blockDim.x * 8)
-            zero_rows(a.source, (blockIdx.x - a.tokens) * kZeroRows, a.rows, dy, a.ldo, c, a.cols, vec_out);
+        for (int c = c0; c < a.cols; c += blockDim.x * 8)
+            zero_rows<T, VEC>(a.source, (blockIdx.x - a.tokens) * kZeroRows, a.rows, dy, a.ldo, c, a.cols);
         return;
     }
     const long long t = blockIdx.x;
@@ -259,13 +261,16 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RouteRows a, bo
             w[k] = r[k] >= 0 ? (a.weights ? a.weights[t * a.top + j] : 1.0f) : 0.0f;
             dot[k] = 0.0f;
         }
-        for (int c = threadIdx.x * 8; c < a.cols; c += blockDim.x * 8) {
-            Raw8<T> raw[8];
+        for (int c = c0; c < a.cols; c += blockDim.x * 8) {
+            Raw8<T> raw[8], rawg;
             float gv[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)   // (nothing is read for a dropped slot: zeros)
-                raw[k].load(y + (a.dw && r[k] >= 0 ? r[k] * a.ldy + c : 0), a.dw && r[k] >= 0 ? a.cols - c : 0, vec_y);
-            load8(g + c, a.cols - c, vec_g, gv);
+            for (int k = 0; k < 8; ++k) {   // (nothing is read for a dropped slot: zeros)
+                const bool in = a.dw && r[k] >= 0;
+                load_columns<VEC>(raw[k], y + (in ? r[k] * a.ldy : 0ll), c, in ? a.cols : 0);
+            }
+            load_columns<VEC>(rawg, g, c, a.cols);
+            rawg.get(gv);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 float v[8];
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RouteRows a, bo
                 if (dy && r[k] >= 0) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = w[k] * gv[i];
-                    store8(dy + r[k] * a.ldo + c, a.cols - c, vec_out, v);
+                    store_columns<VEC>(dy + r[k] * a.ldo, c, a.cols, v);
                 }
             }
         }
@@ -312,8 +317,9 @@ cudaError_t gather(const RouteRows& a, cudaStream_t stream) {
     if (x == 0) return cudaSuccess;
     const int by = (a.cols + th * 8 - 1) / (th * 8);
     if (x > 0x7fffffffll || by > 65535) return cudaErrorInvalidValue;
-    return launch_pdl(gather_kernel<T>, dim3(static_cast<unsigned>(x), by), th, 0, stream, a, vec16<T>(a.x, a.ldx),
-                      vec16<T>(a.out, a.ldo));
+    const bool vec = vec16<T>(a.x, a.ldx) && vec16<T>(a.out, a.ldo);
+    return launch_pdl(vec ? gather_kernel<T, true> : gather_kernel<T, false>, dim3(static_cast<unsigned>(x), by), th, 0,
+                      stream, a);
 }
 
 template <typename T>
@@ -322,8 +328,8 @@ cudaError_t combine(const RouteRows& a, cudaStream_t stream) {
     const int th = row_threads(a.cols);
     const int by = (a.cols + th * 8 - 1) / (th * 8);
     if (by > 65535) return cudaErrorInvalidValue;
-    return launch_pdl(combine_kernel<T>, dim3(a.tokens, by), th, 0, stream, a, vec16<T>(a.x, a.ldx),
-                      vec16<T>(a.out, a.ldo));
+    const bool vec = vec16<T>(a.x, a.ldx) && vec16<T>(a.out, a.ldo);
+    return launch_pdl(vec ? combine_kernel<T, true> : combine_kernel<T, false>, dim3(a.tokens, by), th, 0, stream, a);
 }
 
 template <typename T>
@@ -331,8 +337,9 @@ cudaError_t combine_grad(const RouteRows& a, cudaStream_t stream) {
     const long long x = static_cast<long long>(a.tokens) + (a.out ? (a.rows + kZeroRows - 1) / kZeroRows : 0);
     if (x == 0) return cudaSuccess;
     if (x > 0x7fffffffll) return cudaErrorInvalidValue;
-    return launch_pdl(combine_grad_kernel<T>, dim3(static_cast<unsigned>(x)), row_threads(a.cols), 0, stream, a,
-                      vec16<T>(a.x, a.ldx), vec16<T>(a.y, a.ldy), vec16<T>(a.out, a.ldo));
+    const bool vec = vec16<T>(a.x, a.ldx) && (!a.dw || vec16<T>(a.y, a.ldy)) && (!a.out || vec16<T>(a.out, a.ldo));
+    return launch_pdl(vec ? combine_grad_kernel<T, true> : combine_grad_kernel<T, false>, dim3(static_cast<unsigned>(x)),
+                      row_threads(a.cols), 0, stream, a);
 }
 
 template <typename ID>

@@ -28,7 +28,7 @@ template <typename T>
 struct Raw8;
 
 template <>
-struct Raw8<__nv_bfloat16> {
+struct __align__(16) Raw8<__nv_bfloat16> {
     uint4 u;
     // values p[0..n) (n may be past 8, or below 1), the rest zeros; vec: p is 16-byte aligned
     __device__ __forceinline__ void load(const __nv_bfloat16* p, int n, bool vec) {
@@ -64,34 +64,48 @@ struct Raw8<float> {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
-    Raw8<T> r;
-    r.load(p, n, vec);
-    r.get(v);
+// A row's columns are dealt out to threads, eight each. Where rows start on 16 bytes (VEC) a
+// thread takes neighbouring ones, its first being first_column; elsewhere every 32nd, so that a
+// warp's single-element accesses are to neighbours (neighbours to a thread there took four times
+// as long).
+template <bool VEC>
+__device__ __forceinline__ int first_column(int thread) {
+    return VEC ? thread * 8 : (thread & ~31) * 8 + (thread & 31);
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void load_columns(Raw8<T>& r, const T* row, int c, int cols) {
+    if constexpr (VEC) {
+        r.load(row + c, cols - c, true);
+    } else {
+        T v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + 32 * i < cols ? row[c + 32 * i] : T(0.0f);
+        r = *reinterpret_cast<const Raw8<T>*>(v);
+    }
 }
 
 // (each value rounded once, to nearest even)
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int n, bool vec, const float (&v)[8]) {
-    if (vec && n >= 8) {
-        *reinterpret_cast<uint4*>(p) =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = __float2bfloat16_rn(v[i]);
-}
+__device__ __forceinline__ __nv_bfloat16 as_type(float v, __nv_bfloat16) { return __float2bfloat16_rn(v); }
+__device__ __forceinline__ float as_type(float v, float) { return v; }
 
-__device__ __forceinline__ void store8(float* p, int n, bool vec, const float (&v)[8]) {
-    if (vec && n >= 8) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_columns(T* row, int c, int cols, const float (&v)[8]) {
+    if (VEC && c + 8 <= cols) {
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(row + c) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                            pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        } else {
+            reinterpret_cast<float4*>(row + c)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(row + c)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = v[i];
+    for (int i = 0; i < 8; ++i) {
+        const int k = c + (VEC ? i : 32 * i);
+        if (k < cols) row[k] = as_type(v[i], T());
+    }
 }
 
 }  // namespace tcl
