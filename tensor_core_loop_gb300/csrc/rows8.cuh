@@ -47,7 +47,7 @@ struct __align__(16) Raw8<__nv_bfloat16> {
 };
 
 template <>
-struct Raw8<float> {
+struct __align__(16) Raw8<float> {
     float f[8];
     __device__ __forceinline__ void load(const float* p, int n, bool vec) {
         if (vec && n >= 8) {
@@ -78,7 +78,7 @@ __device__ __forceinline__ void load_columns(Raw8<T>& r, const T* row, int c, in
     if constexpr (VEC) {
         r.load(row + c, cols - c, true);
     } else {
-        T v[8];
+        alignas(16) T v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = c + 32 * i < cols ? row[c + 32 * i] : T(0.0f);
         r = *reinterpret_cast<const Raw8<T>*>(v);
