@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const RouteRows a) {
     const long long t = blockIdx.x;
     Raw8<T> raw;
     float v[8];
-    load_columns<VEC>(raw, static_cast<const T*>(a.x) + t * a.ldx, c, a.cols);
+    load_columns<VEC>(raw, static_cast<const T*>(a.x), t * a.ldx, c, a.cols, true);
     raw.get(v);
     for (int j = 0; j < a.top; ++j) {
         const int r = a.position[t * a.top + j];
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const RouteRows a) {
             const int r = j < a.top ? a.position[t * a.top + j] : -1;
             const bool in = r >= 0 && r < a.rows;
             w[k] = in ? (a.weights ? a.weights[t * a.top + j] : 1.0f) : 0.0f;
-            load_columns<VEC>(raw[k], y + (in ? r * a.ldx : 0ll), c, in ? a.cols : 0);   // (zeros for a dropped slot)
+            load_columns<VEC>(raw[k], y, r * a.ldx, c, a.cols, in);
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -267,9 +267,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) combine_grad_kern
 #pragma unroll
             for (int k = 0; k < 8; ++k) {   // (nothing is read for a dropped slot: zeros)
                 const bool in = a.dw && r[k] >= 0;
-                load_columns<VEC>(raw[k], y + (in ? r[k] * a.ldy : 0ll), c, in ? a.cols : 0);
+                load_columns<VEC>(raw[k], y, r[k] * a.ldy, c, a.cols, in);
             }
-            load_columns<VEC>(rawg, g, c, a.cols);
+            load_columns<VEC>(rawg, g, 0, c, a.cols, true);
             rawg.get(gv);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {

@@ -73,11 +73,14 @@ __device__ __forceinline__ int first_column(int thread) {
     return VEC ? thread * 8 : (thread & ~31) * 8 + (thread & 31);
 }
 
+// The columns of the row at base + at (in = false: zeros, and nothing is read).
 template <bool VEC, typename T>
-__device__ __forceinline__ void load_columns(Raw8<T>& r, const T* row, int c, int cols) {
+__device__ __forceinline__ void load_columns(Raw8<T>& r, const T* base, long long at, int c, int cols, bool in) {
     if constexpr (VEC) {
-        r.load(row + c, cols - c, true);
+        r.load(base + (in ? at + c : 0ll), in ? cols - c : 0, true);
     } else {
+        const T* row = base + (in ? at : 0ll);
+        if (!in) cols = 0;
         alignas(16) T v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = c + 32 * i < cols ? row[c + 32 * i] : T(0.0f);
