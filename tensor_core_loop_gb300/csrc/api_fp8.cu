@@ -66,15 +66,16 @@ int lay_out(Operand& o, uint8_t* to, cudaStream_t stream) {
 //     128 × 16                 11.9  51.6  72.3  85.4   106   173   313
 //     128 × 32                 15.6  52.0  71.8  81.6  92.1   123   210
 //     128 × 128                30.1  57.0  82.4  90.3  96.4   113   143   216   386
-//     256 × 256, two SMs                                                  184   275
+//     256 × 256, two SMs                               122   123   140   184   275
 // (128 × 64 tiles were within 5 % of the best of these everywhere.) So 128 × 128 tiles from some
-// dozen rows until they need a second wave of the GPU, then 256 × 256.
+// dozen rows until they need a second wave of the GPU, then 256 × 256 (not for experts of about
+// a hundred rows, which leave most of such a tile empty: at 96 rows 132 us against 127).
 Fp8Tile choose_tile(long long tokens, int experts, int N, int sms) {
     const long long each = (tokens + experts - 1) / experts;
     const long long ones = (each + 127) / 128 * ((N + 127) / 128) * experts;
     if (each <= (experts == 1 ? 16 : 4)) return Fp8Tile::FEW16;
     if (each <= (experts == 1 ? 64 : 40)) return Fp8Tile::FEW32;
-    if (each > 128 && N > 128 && ones > sms) return Fp8Tile::PAIR;
+    if (each > 112 && N > 128 && ones > sms) return Fp8Tile::PAIR;
     return Fp8Tile::ONE;
 }
 

@@ -19,7 +19,7 @@
 //
 // What bounds it: with many rows the promotion, which has to fit beside a k-block's MMAs (512
 // cycles of a 256 × 256 tile: per SM quarter 256 cycles of multiply-adds and as many of
-// tensor-memory loads); 8192 × 8192 × 4096 takes 204 us, 2.70 PFLOP/s, the tensor pipe busy
+// tensor-memory loads); 8192 × 8192 × 4096 takes 200 us, 2.75 PFLOP/s, the tensor pipe busy
 // 57 % of the time (without promotion 158 us). Eight warps of 128 sums a thread, two to a
 // scheduler, are as many as the registers hold; a few words spilled in the loop cost 30 %.
 // With few rows a weight byte's way from HBM bounds it: 16 tokens on 64 experts of 4096 × 2048
