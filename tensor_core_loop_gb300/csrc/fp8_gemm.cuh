@@ -106,7 +106,14 @@ struct Fp8Cfg {
     static constexpr bool SPLIT_REGS = CW > 64;
     static constexpr int SS = 8;                     // scale slots, a k-block each
     static constexpr int SLOT_Q = 128;               // a slot: P's scales, then Q's (each, or one per 128 rows)
-    static constexpr int SLOT = SLOT_Q + (QVEC ? BQ : 4);
+    // Scales per column, many rows (QUAD): a thread holds two columns of every eight in four rows,
+    // not all columns of one row, so that it reads a quarter of the columns' scales; those of the
+    // four threads of a row lie QUAD_STEP apart, in four different groups of banks. (A broadcast
+    // of 16 bytes takes shared memory as long as 128 bytes: with all columns to a thread the
+    // scales' reads and the MMAs' own came to more than it gives.)
+    static constexpr bool QUAD = QVEC && !SWAP;
+    static constexpr int QUAD_STEP = CW / 4 + 4;
+    static constexpr int SLOT = SLOT_Q + (QUAD ? 8 * QUAD_STEP : QVEC ? BQ : 4);
     static constexpr int TAB = kMaxExperts + 8;
     static constexpr int SUM_PITCH = BQ + 4;         // floats between rows of a shared tile's sums
     static constexpr int UR = 2;                     // units published ahead to the promotion warps
@@ -213,19 +220,34 @@ __device__ __forceinline__ void fp8_store_rows(const uint64_t (&sum)[C::CW / 2],
         used = used + 1 == C::SLABS ? 0 : used + 1;
         if (lane == 0) ptx::bulk_wait_read<C::SLABS - 1>();   // the copy that last used this slab has read it
         __syncwarp();
+        if constexpr (C::QUAD) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            uint4 v;
-            const uint64_t* s = sum + (c0 + u * UNIT) / 2;
-            if constexpr (sizeof(T) == 2) {
-                const float2 a = ptx::f32x2_get(s[0]), b = ptx::f32x2_get(s[1]), d = ptx::f32x2_get(s[2]),
-                             e4 = ptx::f32x2_get(s[3]);
-                v = make_uint4(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y), pack_bf16(d.x, d.y), pack_bf16(e4.x, e4.y));
-            } else {
-                const float2 a = ptx::f32x2_get(s[0]), b = ptx::f32x2_get(s[1]);
-                v = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+            for (int g = 0; g < PER / 8; ++g)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 8 * k + lane / 4, col = g * 8 + lane % 4 * 2;
+                    const float2 v = ptx::f32x2_get(sum[(c0 / 8 + g) * 4 + k]);
+                    uint8_t* to = slab + place(r, col / UNIT) + col % UNIT * sizeof(T);
+                    if constexpr (sizeof(T) == 2)
+                        *reinterpret_cast<uint32_t*>(to) = pack_bf16(v.x, v.y);
+                    else
+                        *reinterpret_cast<float2*>(to) = v;
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                uint4 v;
+                const uint64_t* s = sum + (c0 + u * UNIT) / 2;
+                if constexpr (sizeof(T) == 2) {
+                    const float2 a = ptx::f32x2_get(s[0]), b = ptx::f32x2_get(s[1]), d = ptx::f32x2_get(s[2]),
+                                 e4 = ptx::f32x2_get(s[3]);
+                    v = make_uint4(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y), pack_bf16(d.x, d.y), pack_bf16(e4.x, e4.y));
+                } else {
+                    const float2 a = ptx::f32x2_get(s[0]), b = ptx::f32x2_get(s[1]);
+                    v = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+                }
+                *reinterpret_cast<uint4*>(slab + place(lane, u)) = v;
             }
-            *reinterpret_cast<uint4*>(slab + place(lane, u)) = v;
         }
         if (bulk && (whole || c0 + PER <= cols)) {
             ptx::fence_proxy_async_smem();
@@ -516,7 +538,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
             const Fp8Side& side = of_p ? p.P : p.Q;
             const int per = of_p ? (p.P.block ? 1 : 128) : QVEC ? BQ : (BQ + 127) / 128;   // scales of a k-block
             const long long step = 32 * side.s_row;
-            const uint32_t dst0 = ptx::smem_u32(slots) + 4 * (lane + (of_p ? 0 : C::SLOT_Q));
+            const bool quad = C::QUAD && !of_p;
+            const int place0 = of_p ? lane
+                               : quad ? C::SLOT_Q + (lane & 7) / 2 * C::QUAD_STEP + (lane >> 3) * 2 + (lane & 1)
+                                      : C::SLOT_Q + lane;
+            const uint32_t dst0 = ptx::smem_u32(slots) + 4 * place0;
             uint32_t s = 0, ph = 0;
             int cur = 0;
             bool ok = true;
@@ -545,8 +571,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
 #pragma unroll
                     for (int i = 0; i < NI; ++i) {
                         const bool in = lane + 32 * i < n;
+                        // (QUAD: 32 columns are four groups of eight, a thread's share of CW columns one run)
+                        const int step_i = quad ? 32 * i / C::CW * 4 * C::QUAD_STEP + 32 * i % C::CW / 4 : 32 * i;
                         if (lane + 32 * i < per)
-                            ptx::cp_async_4(dst0 + 4 * (s * C::SLOT + 32 * i), in ? at + i * step : side.scale, in ? 4u : 0u);
+                            ptx::cp_async_4(dst0 + 4 * (s * C::SLOT + step_i), in ? at + i * step : side.scale, in ? 4u : 0u);
                     }
                     ptx::cp_async_arrive_noinc(sfull0 + 8 * s);
                     if (++s == C::SS) {
@@ -581,33 +609,62 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
                     break;
                 }
                 const float* slot = slots + s * C::SLOT;
-                float f = slot[p.P.block ? 0 : prl];
+                [[maybe_unused]] float f = slot[p.P.block ? 0 : prl];
                 if constexpr (!QVEC) f *= slot[C::SLOT_Q + ((h * C::CW) >> 7)];
                 if (!wait(accf0 + 8 * b, bph, DEV_TIMEOUT_EPILOGUE)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
+                auto release = [&]() {   // the accumulator is read: free for the next k-block
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR)
+                            ptx::mbar_arrive_cluster_relaxed(acce_leader0 + 8 * b);
+                        else
+                            ptx::mbar_arrive_relaxed(acce0 + 8 * b);
+                    }
+                };
                 const uint32_t t = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * BQ + h * C::CW;
+                if constexpr (C::QUAD) {
+                    float rows[4];
 #pragma unroll
-                for (int c = 0; c < C::CW; c += C::CHUNK) {
-                    uint32_t r[C::CHUNK];
-                    fp8_tmem_ld<C::CHUNK>(t + c, r);
-                    ptx::tmem_ld_wait(r);
-                    if (c + C::CHUNK == C::CW) {   // the accumulator is read: free for the next k-block
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if constexpr (PAIR)
-                                ptx::mbar_arrive_cluster_relaxed(acce_leader0 + 8 * b);
-                            else
-                                ptx::mbar_arrive_relaxed(acce0 + 8 * b);
+                    for (int k = 0; k < 4; ++k) rows[k] = slot[quarter * 32 + 8 * k + lane / 4];
+                    const ulonglong2* q2 =
+                        reinterpret_cast<const ulonglong2*>(slot + C::SLOT_Q + (4 * h + lane % 4) * C::QUAD_STEP);
+#pragma unroll
+                    for (int c = 0; c < C::CW; c += 32) {
+                        const ulonglong2 qa = q2[c / 16], qb = q2[c / 16 + 1];
+                        const uint64_t q[4] = {qa.x, qa.y, qb.x, qb.y};
+#pragma unroll
+                        for (int k = 0; k < 4; k += 2) {   // the lower and the upper sixteen lanes
+                            uint32_t r[16];
+                            ptx::tmem_ld_16x256b_x4(t + (static_cast<uint32_t>(k * 8) << 16) + c, r);
+                            ptx::tmem_ld_wait(r);
+                            if (c + 32 == C::CW && k == 2) release();
+                            const uint64_t fa = ptx::f32x2(rows[k], rows[k]), fb = ptx::f32x2(rows[k + 1], rows[k + 1]);
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                uint64_t* to = sum + (c / 8 + g) * 4 + k;
+                                to[0] = ptx::fma_f32x2(ptx::f32x2(r[4 * g], r[4 * g + 1]), ptx::mul_f32x2(fa, q[g]), to[0]);
+                                to[1] = ptx::fma_f32x2(ptx::f32x2(r[4 * g + 2], r[4 * g + 3]), ptx::mul_f32x2(fb, q[g]),
+                                                       to[1]);
+                            }
                         }
                     }
-                    if constexpr (QVEC)
-                        fp8_promote<C::CHUNK>(sum + c / 2, r, f, slot + C::SLOT_Q + h * C::CW + c);
-                    else
-                        fp8_promote<C::CHUNK>(sum + c / 2, r, f);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < C::CW; c += C::CHUNK) {
+                        uint32_t r[C::CHUNK];
+                        fp8_tmem_ld<C::CHUNK>(t + c, r);
+                        ptx::tmem_ld_wait(r);
+                        if (c + C::CHUNK == C::CW) release();
+                        if constexpr (QVEC)
+                            fp8_promote<C::CHUNK>(sum + c / 2, r, f, slot + C::SLOT_Q + c);
+                        else
+                            fp8_promote<C::CHUNK>(sum + c / 2, r, f);
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(sempty0 + 8 * s);
@@ -652,7 +709,13 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
                 const int rows = U.p_end - pw, cols = U.q_end - qc;
                 const long long at = (p.wgrad ? U.e * p.c_expert : 0ll) + static_cast<long long>(pw) * p.ldc + qc;
                 uint8_t* slab = slabs + (warp - 4) * C::SLABS * C::SLAB_BYTES;
-                if (!PAIR && share > 1) {
+                if (C::QUAD && !PAIR && share > 1) {
+                    float* to = reinterpret_cast<float*>(smem) + h * C::CW + lane % 4 * 2;
+#pragma unroll
+                    for (int i = 0; i < C::CW / 2; ++i)
+                        *reinterpret_cast<float2*>(to + (quarter * 32 + i % 4 * 8 + lane / 4) * C::SUM_PITCH + i / 4 * 8) =
+                            ptx::f32x2_get(sum[i]);
+                } else if (!PAIR && share > 1) {
                     float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + prl * C::SUM_PITCH + h * C::CW);
 #pragma unroll
                     for (int i = 0; i < C::CW; i += 4) {
