@@ -41,6 +41,14 @@ __device__ __forceinline__ uint2 quant8(const float (&v)[8], float inv) {
     return make_uint2(w[0], w[1]);
 }
 
+// The bytes of w from the n-th on as zeros: they lie behind the matrix' end (a product of the zeros
+// loaded there with the reciprocal of a NaN's scale is not a zero).
+__device__ __forceinline__ uint2 keep8(uint2 w, int n) {
+    if (n >= 8) return w;
+    const uint64_t v = (static_cast<uint64_t>(w.y) << 32 | w.x) & (n > 0 ? (1ull << (8 * n)) - 1 : 0ull);
+    return make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+}
+
 // n of the 8 bytes (the rest lies behind the row's end)
 __device__ __forceinline__ void put8(uint8_t* p, int n, bool vec, uint2 w) {
     if (vec && n >= 8) {
@@ -99,7 +107,7 @@ __global__ void __launch_bounds__(16 * kTeams) quant_rows_kernel(const QuantRows
         for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         if (row >= a.rows || g >= groups) continue;   // (uniform over the team)
         const float s = group_scale(top);
-        const uint2 w = quant8(v, __frcp_rn(s));
+        const uint2 w = keep8(quant8(v, __frcp_rn(s)), a.cols - c);
         for (int j = 0; j < (a.position ? a.top : 1); ++j) {
             const int r = a.position ? a.position[static_cast<long long>(row) * a.top + j] : row;
             if (r < 0 || (a.position && r >= a.out_rows)) continue;
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tiles_kerne
             const int r = r0 + rg * 8 + i;
             float v[8];
             raw[i].get(v);
-            if (r < a.rows && c < wcols) put8(q + r * a.ldq + c, wcols - c, vec_out, quant8(v, inv[0]));
+            if (r < a.rows && c < wcols) put8(q + r * a.ldq + c, wcols - c, vec_out, keep8(quant8(v, inv[0]), a.cols - c));
         }
         return;
     }
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tiles_kerne
         for (int k = 0; k < 8; ++k) {
             const int cc = k * 16 + rg, r = r0 + cg * 8;   // sixteen threads write a column's 128 bytes
             if (c0 + cc < a.cols && r < wrows)
-                put8(q + (c0 + cc) * a.ldq + r, wrows - r, vec_out, turn[cc * 16 + (cg ^ (cc >> 3))]);
+                put8(q + (c0 + cc) * a.ldq + r, wrows - r, vec_out, keep8(turn[cc * 16 + (cg ^ (cc >> 3))], a.rows - r));
         }
     }
 }
