@@ -7,7 +7,7 @@
  *   Sizes: a count of rows or tokens may be 0 (nothing is launched, or what has
  *     no rows is written as zeros); widths and K are at least 1.
  *   Nothing is kept between calls but library scratch, which only operands that
- *     miss the alignment below and a sort of more than 4,096 slots use.
+ *     miss the alignment below use.
  *   Reported by tcl_last_device_error(): code 7, the experts' offsets do not
  *     ascend from 0 within the rows (or are off the multiples of 128 where
  *     those are asked for); such a launch writes nothing.

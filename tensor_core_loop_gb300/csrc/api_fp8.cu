@@ -303,13 +303,7 @@ int tcl_sort_by_expert(int tokens, int top, const void* ids, int id_bytes, int e
     if (!offsets || (slots && (!ids || !position)) || (rows && !source)) return TCL_ERR_NULL;
     if (!on(ids, id_bytes) || !on(offsets, 4) || !on(position, 4) || !on(source, 4)) return TCL_ERR_ALIGN;
     if (int st = device_check()) return st;
-    const long long blocks = (slots + kSortChunk - 1) / kSortChunk;
-    void* counts = nullptr;
-    if (blocks > 1) {
-        if (int st = stream_scratch(stream, static_cast<size_t>(blocks) * experts * sizeof(int), &counts)) return st;
-    }
-    return status_of(launch_sort(slots, ids, id_bytes, experts, align, rows, offsets, position, source,
-                                 static_cast<int*>(counts), stream));
+    return status_of(launch_sort(slots, ids, id_bytes, experts, align, rows, offsets, position, source, stream));
 }
 
 int tcl_gather_rows(int x_type, int tokens, int top, int rows, int cols, const void* X, int ldx, const int32_t* position,

@@ -94,9 +94,9 @@ cudaError_t launch_copy_bytes(const uint8_t* src, long long ld, long long batch_
                               int batch, int rows, int cols, cudaStream_t stream);
 
 // ---- routing (k_route.cu)
-constexpr int kSortChunk = 4096;   // slots of one block
+constexpr int kSortChunk = 4096;   // most slots of one block
 cudaError_t launch_sort(long long slots, const void* ids, int id_bytes, int experts, int align, int rows, int* offsets,
-                        int* position, int* source, int* counts, cudaStream_t stream);
+                        int* position, int* source, cudaStream_t stream);
 
 struct RouteRows {
     int f32;

@@ -1,13 +1,18 @@
 // Tokens sorted by expert and back: the order, the rows laid out in it, the weighted sum of
 // the experts' rows, and its gradients.
 //
-// The order is a counting sort by expert that keeps the slots' order. A block takes 4,096
+// The order is a counting sort by expert that keeps the slots' order. A block takes up to 4,096
 // slots, each of its 32 warps 128 consecutive ones. Counts of a warp, then of the warps
 // before it, then of the blocks before it give every slot its row without an atomic whose
 // order could show in the result (the shared-memory atomics below only add counts). One
-// block needs one launch; more need a launch that counts first. Either reads 4 or 8 bytes
+// block needs one launch. More need two before it: each block's counts, and for every expert
+// their running sums over the blocks, so that a block reads its own share alone (adding up all
+// blocks' counts in every block took 2.3 ms for 8.4 million slots). What passes between the
+// launches lies in the outputs that the last one fills: the counts in `source`, a block's sums
+// in its own slots of `position`. A sort keeps no memory of its own, so sorts on any streams, from
+// any threads and in graphs that replay beside them stay apart. It reads 4 or 8 bytes
 // and writes 4 for each slot and writes 4 for each row: launches, not bytes, take the time
-// (131,072 slots, 64 experts: 10 us).
+// (131,072 slots, 64 experts: 13 us; 8.4 million, 256 experts: 225).
 //
 // The row kernels are bound by memory: a thread handles eight columns, and a token's row
 // (gather, gradient of combine) is read once for all of its slots. 8191 tokens × 6 slots of
@@ -30,6 +35,11 @@ __device__ __forceinline__ int expert_of(const ID* ids, long long i, long long s
     return v >= 0 && v < experts ? static_cast<int>(v) : -1;
 }
 
+// The slots of block b of `blocks`, dealt out evenly: more than 2,048 of them where there are two
+// blocks or more, so that a block's slots of `position` hold two numbers for every expert.
+__device__ __forceinline__ long long first_slot(long long slots, int b, int blocks) { return slots * b / blocks; }
+static_assert(2 * kMaxExperts <= kSortChunk / 2, "a block's running sums fit its slots");
+
 // counts[block][expert]
 template <typename ID>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const ID* ids, long long slots, int experts,
@@ -39,10 +49,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const ID* ids,
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     __syncthreads();
-    const long long base = static_cast<long long>(blockIdx.x) * kSortChunk;
+    const long long base = first_slot(slots, blockIdx.x, gridDim.x), end = first_slot(slots, blockIdx.x + 1, gridDim.x);
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
-        const int e = expert_of(ids, base + k * kSortThreads + threadIdx.x, slots, experts);
+        const int e = expert_of(ids, base + k * kSortThreads + threadIdx.x, end, experts);
         if (e >= 0) atomicAdd(&hist[e], 1);
     }
     __syncthreads();
@@ -50,12 +60,45 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const ID* ids,
         counts[static_cast<long long>(blockIdx.x) * experts + e] = hist[e];
 }
 
-// counts: NULL for a single block. Shared memory: [warp][expert], then per expert the total,
-// the count of the blocks before this one, the first row, and 32 words for the scan.
+// 32 experts to a block, a lane each; a warp takes a run of the sort's blocks. Into each block's
+// slots of `position`: [expert] the count of the blocks before it, then [experts + expert] of all.
+__global__ void __launch_bounds__(kSortThreads) sort_scan_kernel(const int* counts, long long slots, int experts, int blocks,
+                                                                 int* position) {
+    __shared__ int part[kSortWarps][33];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e = blockIdx.x * 32 + lane;
+    const int lo = static_cast<int>(static_cast<long long>(blocks) * warp / kSortWarps);
+    const int hi = static_cast<int>(static_cast<long long>(blocks) * (warp + 1) / kSortWarps);
+    int sum = 0;
+    if (e < experts) {
+#pragma unroll 8
+        for (int b = lo; b < hi; ++b) sum += counts[static_cast<long long>(b) * experts + e];
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    int run = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        if (w == warp) run = total;
+        total += part[w][lane];
+    }
+    if (e >= experts) return;
+#pragma unroll 4
+    for (int b = lo; b < hi; ++b) {
+        int* to = position + first_slot(slots, b, blocks);
+        to[e] = run;
+        to[experts + e] = total;
+        run += counts[static_cast<long long>(b) * experts + e];
+    }
+}
+
+// Shared memory: [warp][expert], then per expert the total, the count of the blocks before this
+// one, the first row, and 32 words for the scan.
 template <typename ID>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids, long long slots, int experts, int align,
-                                                                  int rows, int* offsets, int* position, int* source,
-                                                                  const int* counts) {
+                                                                  int rows, int* offsets, int* position, int* source) {
     extern __shared__ int sm[];
     int* whist = sm;
     int* total = whist + kSortWarps * experts;
@@ -65,20 +108,27 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int blocks = gridDim.x;
     // warps of this block that have slots (a few in a serving step: the others' counts are not looked at)
-    const long long left = slots - static_cast<long long>(blockIdx.x) * kSortChunk;
-    const int warps = static_cast<int>(min(static_cast<long long>(kSortWarps), max(0ll, (left + kPerLane * 32 - 1) / (kPerLane * 32))));
+    const long long start = first_slot(slots, blockIdx.x, blocks), end = first_slot(slots, blockIdx.x + 1, blocks);
+    const int warps = static_cast<int>((end - start + kPerLane * 32 - 1) / (kPerLane * 32));
     for (int i = threadIdx.x; i < warps * experts; i += kSortThreads) whist[i] = 0;
-    for (int i = threadIdx.x; i < 2 * experts; i += kSortThreads) total[i] = 0;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    if (blocks > 1) {   // (read before this block's positions are written over it)
+        for (int i = threadIdx.x; i < experts; i += kSortThreads) {
+            before[i] = position[start + i];
+            total[i] = position[start + experts + i];
+        }
+    } else {
+        for (int i = threadIdx.x; i < experts; i += kSortThreads) before[i] = 0;
+    }
     __syncthreads();
 
     // this warp's slots and their counts
-    const long long base = static_cast<long long>(blockIdx.x) * kSortChunk + warp * (kPerLane * 32) + lane;
+    const long long base = start + warp * (kPerLane * 32) + lane;
     int e[kPerLane], rank[kPerLane];
     int* mine = whist + warp * experts;
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) e[k] = expert_of(ids, base + k * 32, slots, experts);
+    for (int k = 0; k < kPerLane; ++k) e[k] = expert_of(ids, base + k * 32, end, experts);
     if (warp < warps) {
 #pragma unroll
         for (int k = 0; k < kPerLane; ++k) {
@@ -88,17 +138,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids,
             __syncwarp();
             if (e[k] >= 0 && ahead == 0) mine[e[k]] += __popc(same);
             __syncwarp();
-        }
-    }
-    if (counts) {
-        const long long n = static_cast<long long>(blocks) * experts;
-        for (long long i = threadIdx.x; i < n; i += kSortThreads) {
-            const int b = static_cast<int>(i / experts), x = static_cast<int>(i - static_cast<long long>(b) * experts);
-            const int c = counts[i];
-            if (c) {
-                atomicAdd(&total[x], c);
-                if (b < static_cast<int>(blockIdx.x)) atomicAdd(&before[x], c);
-            }
         }
     }
     __syncthreads();
@@ -113,7 +152,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids,
             whist[w * experts + x] = run;
             run += c;
         }
-        if (!counts) total[x] = run;
+        if (blocks == 1) total[x] = run;
         length = (total[x] + align - 1) / align * align;
     }
     // first rows: a scan of the rounded lengths
@@ -145,7 +184,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const ID* ids,
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
         const long long i = base + k * 32;
-        if (i >= slots) continue;
+        if (i >= end) continue;
         int r = -1;
         if (e[k] >= 0) {
             r = firsts[e[k]] + mine[e[k]] + rank[k];
@@ -342,33 +381,39 @@ cudaError_t combine_grad(const RouteRows& a, cudaStream_t stream) {
                       row_threads(a.cols), 0, stream, a);
 }
 
+// (what a block of the sort needs of shared memory for the most experts)
+constexpr size_t sort_smem(int experts) { return sizeof(int) * ((kSortWarps + 3) * static_cast<size_t>(experts) + 1 + kSortWarps); }
+
 template <typename ID>
 cudaError_t sort(long long slots, const ID* ids, int experts, int align, int rows, int* offsets, int* position,
-                 int* source, int* counts, cudaStream_t stream) {
+                 int* source, cudaStream_t stream) {
     const int blocks = static_cast<int>(std::max(1ll, (slots + kSortChunk - 1) / kSortChunk));
-    const size_t smem = sizeof(int) * ((kSortWarps + 3) * static_cast<size_t>(experts) + 1 + kSortWarps);
-    if (smem > 48 * 1024) {
+    const size_t smem = sort_smem(experts);
+    if (smem > 48 * 1024) {   // (the same limit each time: threads that set it do not get in each other's way)
         const cudaError_t err = cudaFuncSetAttribute(sort_place_kernel<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(smem));
+                                                     static_cast<int>(sort_smem(kMaxExperts)));
         if (err != cudaSuccess) return err;
     }
     if (blocks > 1) {
-        const cudaError_t err = launch_pdl(sort_count_kernel<ID>, dim3(blocks), kSortThreads, sizeof(int) * experts,
-                                           stream, ids, slots, experts, counts);
+        // (blocks * experts counts: at most (slots / 4096 + 1) * 1024, less than the slots and so than the rows)
+        cudaError_t err = launch_pdl(sort_count_kernel<ID>, dim3(blocks), kSortThreads, sizeof(int) * experts, stream, ids,
+                                     slots, experts, source);
+        if (err != cudaSuccess) return err;
+        err = launch_pdl(sort_scan_kernel, dim3((experts + 31) / 32), kSortThreads, 0, stream, source, slots, experts, blocks,
+                         position);
         if (err != cudaSuccess) return err;
     }
     return launch_pdl(sort_place_kernel<ID>, dim3(blocks), kSortThreads, smem, stream, ids, slots, experts, align, rows,
-                      offsets, position, source, blocks > 1 ? counts : nullptr);
+                      offsets, position, source);
 }
 
 }  // namespace
 
 cudaError_t launch_sort(long long slots, const void* ids, int id_bytes, int experts, int align, int rows, int* offsets,
-                        int* position, int* source, int* counts, cudaStream_t stream) {
+                        int* position, int* source, cudaStream_t stream) {
     if (id_bytes == 8)
-        return sort(slots, static_cast<const long long*>(ids), experts, align, rows, offsets, position, source, counts,
-                    stream);
-    return sort(slots, static_cast<const int*>(ids), experts, align, rows, offsets, position, source, counts, stream);
+        return sort(slots, static_cast<const long long*>(ids), experts, align, rows, offsets, position, source, stream);
+    return sort(slots, static_cast<const int*>(ids), experts, align, rows, offsets, position, source, stream);
 }
 
 cudaError_t launch_gather(const RouteRows& a, cudaStream_t stream) {

@@ -46,3 +46,62 @@ def test_padding_is_zero_beside_non_finite_values(along, value, dtype):
     padding = data.as_strided((rows, pitch), (pitch, 1)).view(torch.uint8)[:, cols:]
     assert bool((padding == 0).all())
     assert not bool(torch.isfinite(scale).all())      # (and the groups that hold the value carry it)
+
+
+# ------------------------------------------------------------------------------ sorting
+
+def test_sort_of_many_slots_in_a_graph():
+    """Captured on a stream that the library has not seen, with no scratch in place, and replayed
+    beside sorts on the default stream."""
+    E, shape = 500, (30_000, 4)
+    g = torch.Generator().manual_seed(4)
+    first, second, third = (torch.randint(-1, E, shape, generator=g) for _ in range(3))
+    ids, others = first.to(DEV), third.to(DEV)
+    torch.cuda.synchronize()
+    tcl.lib().tcl_shutdown()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = tcl.sort_by_expert(ids, E, align=16)
+    ids.copy_(second)
+    torch.cuda.synchronize()
+    side, beside = torch.cuda.Stream(), []
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            graph.replay()
+    for _ in range(20):
+        beside.append(tcl.sort_by_expert(others, E, align=16))
+    torch.cuda.synchronize()
+    for order, of in ((got, second), *((b, third) for b in beside[::7])):
+        offsets, position, source = ref.order(of, E, 16, order.source.numel())
+        assert order.offsets.tolist() == offsets
+        assert order.position.reshape(-1).tolist() == position and order.source.tolist() == source
+
+
+@pytest.mark.parametrize("tokens,top,experts,align", [(4097, 1, 1024, 1), (4097, 1, 1024, 128), (1366, 3, 1023, 2), (8193, 1, 33, 128),
+                                                      (2731, 3, 1024, 128), (40_000, 7, 100, 3), (12_289, 1, 1, 128)])
+def test_sort_just_past_a_block(tokens, top, experts, align):
+    g = torch.Generator().manual_seed(tokens)
+    ids = torch.randint(-1, experts, (tokens, top), generator=g)
+    for of in (ids, torch.full_like(ids, -1), torch.full_like(ids, experts - 1)):
+        got = tcl.sort_by_expert(of.to(DEV), experts, align=align)
+        offsets, position, source = ref.order(of, experts, align, got.source.numel())
+        assert got.offsets.tolist() == offsets
+        assert got.position.reshape(-1).tolist() == position and got.source.tolist() == source
+
+
+def test_sort_of_millions_of_slots():
+    tokens, top, E, align = 600_001, 7, 200, 128
+    ids = torch.randint(-1, E, (tokens, top), device=DEV, generator=torch.Generator(device=DEV).manual_seed(6))
+    offsets, position, source = tcl.sort_by_expert(ids, E, align=align)
+    flat = ids.reshape(-1)
+    count = torch.bincount(flat[flat >= 0], minlength=E)
+    length = (count + align - 1) // align * align
+    want = torch.nn.functional.pad(length.cumsum(0), (1, 0))
+    assert torch.equal(offsets.long(), want)
+    slots = torch.argsort(torch.where(flat >= 0, flat, E), stable=True)[:int(count.sum())]
+    e = flat[slots]
+    row = want[e] + torch.arange(len(slots), device=DEV) - torch.nn.functional.pad(count.cumsum(0), (1, 0))[e]
+    assert torch.equal(position.view(-1)[slots].long(), row) and bool((position.view(-1)[flat < 0] == -1).all())
+    full = torch.full_like(source, -1)
+    full[row] = slots.int()
+    assert torch.equal(source, full)
