@@ -1464,8 +1464,9 @@ int tensor_map_uncached(const void* ptr, CUtensorMapDataType dtype, uint64_t d0,
     return r == CUDA_SUCCESS ? TCL_OK : TCL_ERR_LAUNCH;
 }
 
+std::unique_lock<std::mutex> library_lock() { return std::unique_lock<std::mutex>(g_mu); }
+
 int stream_scratch(cudaStream_t stream, size_t need, void** out) {
-    std::lock_guard<std::mutex> lock(g_mu);
     int dev;
     DevState* ds;
     StreamRes* sr;
@@ -1479,7 +1480,6 @@ int stream_scratch(cudaStream_t stream, size_t need, void** out) {
 
 static int encode_3d(CUtensorMapDataType type, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
                      uint64_t stride2, uint32_t b0, uint32_t b1, CUtensorMap* out) {
-    std::lock_guard<std::mutex> lock(g_mu);
     int st = encode_fn();
     if (st) return st;
     const cuuint64_t dims[3] = {d0, d1, d2};

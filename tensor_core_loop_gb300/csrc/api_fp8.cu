@@ -81,6 +81,7 @@ Fp8Tile choose_tile(long long tokens, int experts, int N, int sms) {
 
 int product(Operand a, Fp8Side sa, Operand b, Fp8Side sb, Fp8Tile tile, Fp8Params p, long long units, int sms,
             cudaStream_t stream) {
+    const auto lock = library_lock();   // (to the launch below)
     if (const size_t need = a.bytes() + b.bytes()) {
         void* scratch;
         int st = stream_scratch(stream, need, &scratch);

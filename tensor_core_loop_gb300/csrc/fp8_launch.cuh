@@ -4,12 +4,17 @@
 
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "fp8_gemm.cuh"
 
 namespace tcl {
 
 // ---- services of api.cu
 int device_context(int* dev, int* sms, unsigned int** status);
+// The lock of the library's state. A call holds it from its scratch to the last launch that uses it, so
+// that another thread's call on the stream cannot come in between; what follows is called under it.
+std::unique_lock<std::mutex> library_lock();
 // `need` bytes of the library scratch that belongs to `stream` (grown on demand; TCL_ERR_CAPTURE inside a capture).
 int stream_scratch(cudaStream_t stream, size_t need, void** out);
 // A 3-D map of bytes (K contiguous, rows, matrices), 128-byte swizzle, boxes of 128 bytes × box_rows; not cached.

@@ -25,6 +25,20 @@ def _lib():
     assert tcl.last_device_error() == (0, 0)
 
 
+def random_operand(rows, cols, seed, per=1, pitch=None, batch=None, distance=None):
+    """e4m3 data of any bit pattern but NaN, with scales over a few powers of two; rows `pitch` bytes and
+    matrices `distance` bytes apart."""
+    g = torch.Generator().manual_seed(seed)
+    pitch = pitch or cols
+    distance = distance or rows * pitch
+    bits = torch.randint(0, 254, ((batch or 1) * distance,), generator=g, dtype=torch.uint8)
+    data = torch.where(bits >= 127, bits + 1, bits).view(F8).to(DEV)     # (0x7f and 0xff are NaN)
+    lead = () if batch is None else (batch,)
+    data = data.as_strided(lead + (rows, cols), (distance, pitch, 1)[1 - len(lead):])
+    scale = torch.exp2(3 * torch.randn(lead + (-(-rows // per), ref.groups(cols)), generator=g)).to(DEV)
+    return data, scale
+
+
 # ------------------------------------------------------------------------------ quantising
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -105,3 +119,30 @@ def test_sort_of_millions_of_slots():
     full = torch.full_like(source, -1)
     full[row] = slots.int()
     assert torch.equal(source, full)
+
+
+# ------------------------------------------------------------------------------ streams and threads
+
+def test_threads_on_one_stream():
+    """Calls of several launches from several threads (ctypes lets the others run meanwhile): products whose
+    operands go through library scratch, and sorts."""
+    from concurrent.futures import ThreadPoolExecutor
+    jobs = []
+    for i, (M, N, K) in enumerate([(200, 300, 500), (700, 300, 900), (90, 2000, 1200), (1000, 600, 260)]):
+        a, sa = random_operand(M, K, 70 + i, pitch=K + 7)
+        b, sb = random_operand(N, K, 80 + i, per=128, pitch=K + 5)
+        ids = torch.randint(0, 40 * (i + 1), (2000 * (i + 2), 3), generator=torch.Generator().manual_seed(i)).to(DEV)
+        jobs.append((a, sa, b, sb, ids, 40 * (i + 1)))
+
+    def turn(job):
+        a, sa, b, sb, ids, E = job
+        return tcl.gemm_fp8(a, sa, b, sb), *tcl.sort_by_expert(ids, E, align=8)
+
+    want = [turn(job) for job in jobs]
+    torch.cuda.synchronize()
+    with ThreadPoolExecutor(4) as pool:
+        got = [r for r in pool.map(lambda i: (i % 4, turn(jobs[i % 4])), range(400))]
+    torch.cuda.synchronize()
+    for i, r in got:
+        for u, v in zip(r, want[i]):
+            assert torch.equal(u, v)
