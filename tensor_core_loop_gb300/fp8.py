@@ -13,7 +13,9 @@ expert around them: Python binding of ``include/tcl_fp8.h``.
 An e4m3 matrix is a pair: its data (``torch.float8_e4m3fn``, rows contiguous) and its
 scales (``torch.float32``, one column for each 128 columns of the data, any strides).
 Calls are asynchronous on ``stream`` (default: the current stream of the tensors' device)
-and allocate their results on that stream.
+and allocate their results on that stream. Given another stream than the current one, the
+caller lets it wait for whatever makes the operands (``stream.wait_stream``); the operands
+themselves may be dropped right after the call.
 """
 from __future__ import annotations
 
@@ -91,14 +93,20 @@ def _on(stream):
     return _here if stream is None else torch.cuda.stream(stream)
 
 
-def _device(name, first, *rest):
-    """The GPU that ``first`` (called ``name``) is on; the others that are given have to be there too."""
+def _device(stream, name, first, *rest):
+    """The GPU that ``first`` (called ``name``) is on; the others that are given have to be there too.
+    All of them are recorded on ``stream`` (None: the current one, whose memory they may be): the
+    caching allocator does not hand their memory out again while work on it may still use them."""
     if not first.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     device = first.device
     for t in rest:
         if t is not None and t.device != device:
             raise ValueError(f"all tensors must be on {device}, where {name} is, not on {t.device}")
+    if stream is not None:
+        for t in (first, *rest):
+            if t is not None:
+                t.record_stream(stream)
     return device
 
 
@@ -178,7 +186,7 @@ def quantize_fp8(x, along: str = "rows", order: ExpertOrder | None = None, strea
         position, source = _order(order, rows)
         top, made = position.shape[1], source.shape[0]
         pos, src = position.data_ptr(), source.data_ptr()
-    device = _device("x", x, position, source)
+    device = _device(stream, "x", x, position, source)
     with _on(stream):
         if along == "rows":
             data = _fp8(made, cols, device)
@@ -252,7 +260,7 @@ def gemm_fp8(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None):
         raise ValueError(f"a needs scales of shape {(M, -(-K // GROUP))}, not {tuple(sa)}")
     kind = _kind(N, K, sb, "b")
     dtype, code = _out_type(out, out_dtype, (M, N))
-    device = _device("a", a, a_scale, b, b_scale, out)
+    device = _device(stream, "a", a, a_scale, b, b_scale, out)
     with _on(stream):
         c = torch.empty((M, N), dtype=dtype, device=device) if out is None else out
         ldc = N if out is None else _mat(c, "out")[2]
@@ -278,7 +286,7 @@ def gemm_fp8_experts(a, a_scale, b, b_scale, offsets, out_dtype=None, out=None, 
     kind = _kind(N, K, sb, "b")
     _int32(offsets, "offsets", (experts + 1,))
     dtype, code = _out_type(out, out_dtype, (rows, N))
-    device = _device("a", a, a_scale, b, b_scale, offsets, out)
+    device = _device(stream, "a", a, a_scale, b, b_scale, offsets, out)
     with _on(stream):
         c = torch.empty((rows, N), dtype=dtype, device=device) if out is None else out
         ldc = N if out is None else _mat(c, "out")[2]
@@ -312,7 +320,7 @@ def gemm_fp8_experts_wgrad(a, a_scale, b, b_scale, offsets, out_dtype=None, out=
         raise ValueError("offsets must have one entry more than there are experts")
     _int32(offsets, "offsets", (experts + 1,))
     dtype, code = _out_type(out, out_dtype, (experts, N, K))
-    device = _device("a", a, a_scale, b, b_scale, offsets, out)
+    device = _device(stream, "a", a, a_scale, b, b_scale, offsets, out)
     with _on(stream):
         c = torch.empty((experts, N, K), dtype=dtype, device=device) if out is None else out
         ldc = _mat(c, "out", 3)[2]
@@ -337,7 +345,7 @@ def sort_by_expert(ids, experts: int, align: int = 1, stream=None) -> ExpertOrde
     tokens, top = ids.shape
     slots = tokens * top
     rows = (slots + min(experts, slots) * (align - 1)) // align * align
-    device = _device("ids", ids)
+    device = _device(stream, "ids", ids)
     with _on(stream):
         offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
         position = torch.empty((tokens, top), dtype=torch.int32, device=device)
@@ -354,7 +362,7 @@ def gather_rows(x, order: ExpertOrder, stream=None):
     tokens, cols, ldx = _mat(x, "x")
     position, source = _order(order, tokens)
     rows = source.shape[0]
-    device = _device("x", x, position, source)
+    device = _device(stream, "x", x, position, source)
     with _on(stream):
         y = torch.empty((rows, cols), dtype=x.dtype, device=device)
         _call(_lib().tcl_gather_rows, "gather_rows", device, stream, xt, tokens, position.shape[1], rows, cols,
@@ -379,7 +387,7 @@ def combine(y, weights, order: ExpertOrder, stream=None):
     if rows != source.shape[0]:
         raise ValueError(f"the order has {source.shape[0]} rows, y {rows}")
     w = _weights(weights, position)
-    device = _device("y", y, weights, position, source)
+    device = _device(stream, "y", y, weights, position, source)
     tokens, top = position.shape
     with _on(stream):
         out = torch.empty((tokens, cols), dtype=y.dtype, device=device)
@@ -399,7 +407,7 @@ def combine_grad(grad, y, weights, order: ExpertOrder, stream=None):
     if rows != source.shape[0]:
         raise ValueError(f"the order has {source.shape[0]} rows, y {rows}")
     w = _weights(weights, position)
-    device = _device("grad", grad, y, weights, position, source)
+    device = _device(stream, "grad", grad, y, weights, position, source)
     tokens, top = position.shape
     with _on(stream):
         dy = torch.empty((rows, cols), dtype=y.dtype, device=device)

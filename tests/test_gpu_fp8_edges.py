@@ -123,6 +123,27 @@ def test_sort_of_millions_of_slots():
 
 # ------------------------------------------------------------------------------ streams and threads
 
+def test_operands_of_another_streams_call_are_kept():
+    """Memory of an operand that is dropped right after the call is not handed out while the given
+    stream may still read it."""
+    s = torch.cuda.Stream()
+    x = torch.randn(600, 512, device=DEV).to(BF16)
+    a, sa = tcl.quantize_fp8(x)
+    b, sb = tcl.quantize_fp8(x, along="blocks")
+    want = tcl.gemm_fp8(a, sa, b, sb)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)                  # (a tenth of a second)
+    c = tcl.gemm_fp8(a, sa, b, sb, stream=s)
+    kept = {t.data_ptr() for t in (a, sa, b, sb)}
+    like = [(t.shape, t.stride(), t.dtype) for t in (a, sa, b, sb)]
+    del a, sa, b, sb
+    again = [torch.empty_strided(size, stride, dtype=dtype, device=DEV) for size, stride, dtype in like]
+    assert not kept & {t.data_ptr() for t in again}
+    s.synchronize()
+    assert torch.equal(c, want)
+
+
 def test_threads_on_one_stream():
     """Calls of several launches from several threads (ctypes lets the others run meanwhile): products whose
     operands go through library scratch, and sorts."""
