@@ -230,6 +230,14 @@ def _ld(t) -> int:
     return -(-t.shape[1] // q) * q
 
 
+def _record(stream, *tensors) -> None:
+    """Operands of a call on a given stream (None: the current one): the caching allocator does not
+    hand their memory out again while that stream may still use it."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def gemm_host_into(a, b, c, stream=None) -> None:
     """C = A·B for bf16 CPU tensors (page-locked for overlap) into the CPU tensor ``c``
     (float32 or bfloat16): uploads, GEMMs and downloads pipelined by the library.
@@ -265,6 +273,7 @@ def gemm_simt_into(a, b, c, stream=None) -> None:
     K2, N = b.shape
     if K != K2 or tuple(c.shape) != (M, N):
         raise ValueError(f"shape mismatch: {tuple(a.shape)} x {tuple(b.shape)} -> {tuple(c.shape)}")
+    _record(stream, a, b, c)
     s = stream if stream is not None else torch.cuda.current_stream(a.device)
     with torch.cuda.device(a.device):
         st = lib().gemm_f32_simt(M, N, K, a.data_ptr(), _ld(a), b.data_ptr(), _ld(b), c.data_ptr(), _ld(c),
@@ -284,6 +293,7 @@ def gemm_into(a, b, c, cfg: Config | None = None, stream=None) -> None:
         raise ValueError(f"shape mismatch: {tuple(a.shape)} x {tuple(b.shape)} -> {tuple(c.shape)}")
     if b.dtype != a.dtype:
         raise TypeError("a and b must have the same dtype")
+    _record(stream, a, b, c)
     s = stream if stream is not None else torch.cuda.current_stream(a.device)
     sp = ctypes.c_void_p(s.cuda_stream)
     cp = ctypes.byref(cfg) if cfg is not None else None
