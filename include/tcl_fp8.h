@@ -5,7 +5,8 @@
  * Part of the library that tcl_gemm.h describes: its statuses, memory and
  * ownership, streams and CUDA graphs hold here too, with these differences.
  *   Sizes: a count of rows or tokens may be 0 (nothing is launched, or what has
- *     no rows is written as zeros); widths and K are at least 1.
+ *     no rows is written as zeros); widths and K are at least 1, and either is
+ *     below 2^31 - 2^16 (TCL_ERR_DIMS otherwise).
  *   Nothing is kept between calls but library scratch, which only operands that
  *     miss the alignment below use.
  *   Reported by tcl_last_device_error(): code 7, the experts' offsets do not

@@ -13,6 +13,14 @@ namespace {
 
 constexpr unsigned long long kTimeoutNs = 1000000000ull;   // bound on every in-kernel wait: 1 s
 
+// Counts and widths end here: the kernels round them up to whole tiles, and step past them by up to a
+// block's columns, in 32 bits.
+constexpr int kMostSize = 0x7ffeffff;
+
+bool sizes(int count0, int count1, int width0, int width1) {
+    return count0 >= 0 && count1 >= 0 && width0 >= 1 && width1 >= 1 && std::max(count0, count1) <= kMostSize &&
+           std::max(width0, width1) <= kMostSize;
+}
 bool on(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int elem(int x_type) { return x_type == TCL_X_F32 ? 4 : 2; }
 bool known(int x_type) { return x_type == TCL_X_BF16 || x_type == TCL_X_F32; }
@@ -134,7 +142,7 @@ int rows_product(int rows, int experts, int N, int K, const void* A, int lda, co
                  long long sa_group, const void* B, int ldb, long long b_expert, const float* SB, int sb_kind,
                  long long sb_expert, long long sb_row, long long sb_group, const int32_t* offsets, void* C, int ldc,
                  int out, cudaStream_t stream) {
-    if (rows < 0 || N < 1 || K < 1 || experts < 1) return TCL_ERR_DIMS;
+    if (!sizes(rows, 0, N, K) || experts < 1) return TCL_ERR_DIMS;
     if (experts > TCL_MAX_EXPERTS) return TCL_ERR_CONFIG;
     if (out != TCL_OUT_F32 && out != TCL_OUT_BF16) return TCL_ERR_CONFIG;
     if (sb_kind != TCL_SCALE_ROWS && sb_kind != TCL_SCALE_BLOCKS) return TCL_ERR_CONFIG;
@@ -184,7 +192,7 @@ int tcl_quantize_fp8_rows(int x_type, int rows, int cols, const void* X, int ldx
                           long long s_group, cudaStream_t stream) {
     if (!known(x_type)) return TCL_ERR_CONFIG;
     const int made = position ? out_rows : rows;
-    if (rows < 0 || cols < 1 || made < 0 || (position && top < 1)) return TCL_ERR_DIMS;
+    if (!sizes(rows, made, cols, 1) || (position && top < 1)) return TCL_ERR_DIMS;
     if ((rows && !X) || (made && (!Q || !scale)) || (position && made && !source)) return TCL_ERR_NULL;
     if (ldx < cols || ldq < cols) return TCL_ERR_LD;
     if (!on(X, elem(x_type)) || !on(scale, 4) || !on(position, 4) || !on(source, 4)) return TCL_ERR_ALIGN;
@@ -200,7 +208,7 @@ int tcl_quantize_fp8_columns(int x_type, int rows, int cols, const void* X, int 
                              cudaStream_t stream) {
     if (!known(x_type)) return TCL_ERR_CONFIG;
     const int made = source ? out_rows : rows;
-    if (rows < 0 || cols < 1 || made < 0 || (source && top < 1)) return TCL_ERR_DIMS;
+    if (!sizes(rows, made, cols, 1) || (source && top < 1)) return TCL_ERR_DIMS;
     if ((rows && !X) || (made && (!Q || !scale))) return TCL_ERR_NULL;
     if (ldx < cols || ldq < made) return TCL_ERR_LD;
     if (!on(X, elem(x_type)) || !on(scale, 4) || !on(source, 4)) return TCL_ERR_ALIGN;
@@ -215,7 +223,7 @@ int tcl_quantize_fp8_columns(int x_type, int rows, int cols, const void* X, int 
 int tcl_quantize_fp8_blocks(int x_type, int batch, int rows, int cols, const void* X, int ldx, long long x_batch,
                             int transpose, void* Q, int ldq, long long q_batch, float* scale, cudaStream_t stream) {
     if (!known(x_type) || (transpose != 0 && transpose != 1)) return TCL_ERR_CONFIG;
-    if (batch < 0 || rows < 0 || cols < 1) return TCL_ERR_DIMS;
+    if (!sizes(batch, rows, cols, 1)) return TCL_ERR_DIMS;
     const bool any = batch > 0 && rows > 0;
     if (any && (!X || !Q || !scale)) return TCL_ERR_NULL;
     const int qrows = transpose ? cols : rows, qcols = transpose ? rows : cols;
@@ -250,7 +258,7 @@ int gemm_fp8_experts_wgrad(int rows, int experts, int N, int K, const void* A, i
                            long long sa_group, const void* B, int ldb, const float* SB, long long sb_row,
                            long long sb_group, const int32_t* offsets, void* C, int ldc, long long c_expert, int out,
                            cudaStream_t stream) {
-    if (rows < 0 || N < 1 || K < 1 || experts < 1) return TCL_ERR_DIMS;
+    if (!sizes(rows, 0, N, K) || experts < 1) return TCL_ERR_DIMS;
     if (experts > TCL_MAX_EXPERTS) return TCL_ERR_CONFIG;
     if (out != TCL_OUT_F32 && out != TCL_OUT_BF16) return TCL_ERR_CONFIG;
     if (!offsets || !C || (rows && (!A || !SA || !B || !SB))) return TCL_ERR_NULL;
@@ -297,10 +305,10 @@ int tcl_sort_by_expert(int tokens, int top, const void* ids, int id_bytes, int e
                        int32_t* offsets, int32_t* position, int32_t* source, cudaStream_t stream) {
     if (id_bytes != 4 && id_bytes != 8) return TCL_ERR_CONFIG;
     if (experts > TCL_MAX_EXPERTS || align < 1 || align > 128) return TCL_ERR_CONFIG;
-    if (tokens < 0 || top < 1 || experts < 1) return TCL_ERR_DIMS;
+    if (!sizes(tokens, std::max(rows, 0), top, experts)) return TCL_ERR_DIMS;
     const long long slots = static_cast<long long>(tokens) * top;
     const long long need = (slots + std::min<long long>(experts, slots) * (align - 1)) / align * align;
-    if (need > 0x7fffffffll || rows < need) return TCL_ERR_DIMS;
+    if (need > kMostSize || rows < need) return TCL_ERR_DIMS;
     if (!offsets || (slots && (!ids || !position)) || (rows && !source)) return TCL_ERR_NULL;
     if (!on(ids, id_bytes) || !on(offsets, 4) || !on(position, 4) || !on(source, 4)) return TCL_ERR_ALIGN;
     if (int st = device_check()) return st;
@@ -310,7 +318,7 @@ int tcl_sort_by_expert(int tokens, int top, const void* ids, int id_bytes, int e
 int tcl_gather_rows(int x_type, int tokens, int top, int rows, int cols, const void* X, int ldx, const int32_t* position,
                     const int32_t* source, void* Y, int ldy, cudaStream_t stream) {
     if (!known(x_type)) return TCL_ERR_CONFIG;
-    if (tokens < 0 || top < 1 || rows < 0 || cols < 1) return TCL_ERR_DIMS;
+    if (!sizes(tokens, rows, top, cols)) return TCL_ERR_DIMS;
     if ((tokens && (!X || !position)) || (rows && (!Y || !source))) return TCL_ERR_NULL;
     if (ldx < cols || ldy < cols) return TCL_ERR_LD;
     if (!on(X, elem(x_type)) || !on(Y, elem(x_type)) || !on(position, 4) || !on(source, 4)) return TCL_ERR_ALIGN;
@@ -328,7 +336,7 @@ int tcl_gather_rows(int x_type, int tokens, int top, int rows, int cols, const v
 int tcl_combine(int x_type, int tokens, int top, int rows, int cols, const void* Y, int ldy, const float* weights,
                 const int32_t* position, void* out, int ldo, cudaStream_t stream) {
     if (!known(x_type)) return TCL_ERR_CONFIG;
-    if (tokens < 0 || top < 1 || rows < 0 || cols < 1) return TCL_ERR_DIMS;
+    if (!sizes(tokens, rows, top, cols)) return TCL_ERR_DIMS;
     if ((tokens && (!out || !position)) || (rows && !Y)) return TCL_ERR_NULL;
     if (ldy < cols || ldo < cols) return TCL_ERR_LD;
     if (!on(Y, elem(x_type)) || !on(out, elem(x_type)) || !on(weights, 4) || !on(position, 4)) return TCL_ERR_ALIGN;
@@ -347,7 +355,7 @@ int tcl_combine_grad(int x_type, int tokens, int top, int rows, int cols, const 
                      const float* weights, const int32_t* position, const int32_t* source, void* DY, int lddy, float* DW,
                      cudaStream_t stream) {
     if (!known(x_type)) return TCL_ERR_CONFIG;
-    if (tokens < 0 || top < 1 || rows < 0 || cols < 1) return TCL_ERR_DIMS;
+    if (!sizes(tokens, rows, top, cols)) return TCL_ERR_DIMS;
     if ((tokens && (!G || !position)) || (DY && rows && !source) || (DW && rows && !Y)) return TCL_ERR_NULL;
     if (ldg < cols || (DW && ldy < cols) || (DY && lddy < cols)) return TCL_ERR_LD;
     if (!on(G, elem(x_type)) || !on(Y, elem(x_type)) || !on(DY, elem(x_type)) || !on(DW, 4) || !on(weights, 4) ||

@@ -14,6 +14,37 @@ from test_fp8_host import L, P, experts, gemm, wgrad  # noqa: F401
 TOP = 2 ** 31 - 1
 
 
+@pytest.mark.parametrize("size", [TOP, TOP - 65_535])
+def test_sizes_at_the_end_of_32_bits_are_refused(L, size):  # noqa: F811
+    """Index arithmetic in 32 bits rounds sizes up to whole tiles: it needs room above them."""
+    for kw in (dict(M=size), dict(N=size, ldc=TOP), dict(K=size, lda=TOP, ldb=TOP)):
+        assert gemm(L, **kw) == 2, kw
+    for kw in (dict(rows=size), dict(N=size, ldc=TOP, be=2 ** 40), dict(K=size, lda=TOP, ldb=TOP, be=2 ** 40)):
+        assert experts(L, **kw) == 2, kw
+    for kw in (dict(rows=size, lda=TOP, ldb=TOP), dict(N=size, ce=2 ** 40), dict(K=size, ldc=TOP, ce=2 ** 40)):
+        assert wgrad(L, **kw) == 2, kw
+    big = TOP
+    rows, cols, blocks = L.tcl_quantize_fp8_rows, L.tcl_quantize_fp8_columns, L.tcl_quantize_fp8_blocks
+    assert rows(0, size, 64, P, 64, None, 1, None, 0, P, 64, P, 1, 4, None) == 2
+    assert rows(0, 4, size, P, big, None, 1, None, 0, P, big, P, 1, 4, None) == 2
+    assert rows(0, 4, 64, P, 64, P, 1, P, size, P, 64, P, 1, 4, None) == 2
+    assert cols(0, size, 64, P, 64, None, 1, 0, P, big, P, 1, 64, None) == 2
+    assert cols(0, 4, size, P, big, None, 1, 0, P, 64, P, 1, 64, None) == 2
+    assert cols(0, 4, 64, P, 64, P, 1, size, P, big, P, 1, 64, None) == 2
+    assert blocks(0, 1, size, 64, P, 64, 0, 0, P, 64, 0, P, None) == 2
+    assert blocks(0, 1, 4, size, P, big, 0, 0, P, big, 0, P, None) == 2
+    assert L.tcl_sort_by_expert(size, 1, P, 4, 4, 1, TOP, P, P, P, None) == 2
+    assert L.tcl_sort_by_expert(4, 1, P, 4, 4, 1, size, P, P, P, None) == 2
+    for tokens, n, width in ((size, 8, 64), (4, size, 64), (4, 8, size)):
+        assert L.tcl_gather_rows(0, tokens, 2, n, width, P, big, P, P, P, big, None) == 2
+        assert L.tcl_combine(0, tokens, 2, n, width, P, big, P, P, P, big, None) == 2
+        assert L.tcl_combine_grad(0, tokens, 2, n, width, P, big, P, big, P, P, P, P, big, P, None) == 2
+
+
+def meta(shape, stride, dtype):
+    return torch.empty_strided(shape, stride, dtype=dtype, device="meta")
+
+
 def test_operands_are_recorded_on_the_given_stream(monkeypatch):
     """The caching allocator must know that the given stream reads them (it would hand their memory out
     again once the caller drops them)."""
