@@ -117,6 +117,15 @@ def _x_type(t, name):
     return code
 
 
+_INT = 2 ** 31 - 1
+
+
+def _fits(name, *numbers):
+    """(ctypes would pass on the low 32 bits of a larger one.)"""
+    if max(numbers) > _INT:
+        raise ValueError(f"{name}'s sizes and leading dimension must fit 32 bits")
+
+
 def _mat(t, name, dim=2):
     """(rows, columns, leading dimension) of a matrix, or of each of a batch, with contiguous rows."""
     shape, stride = t.shape, t.stride()
@@ -127,11 +136,11 @@ def _mat(t, name, dim=2):
         raise ValueError(f"{name} must have at least one column")
     if cols > 1 and stride[-1] != 1:
         raise ValueError(f"{name}'s rows must be contiguous (stride(-1) == 1)")
-    if rows < 2:
-        return rows, cols, (cols + 15) & ~15   # a single row never steps to a second one
-    if stride[-2] < cols:
+    ld = stride[-2] if rows > 1 else (cols + 15) & ~15   # (a single row never steps to a second one)
+    if ld < cols:
         raise ValueError(f"{name}'s rows overlap")
-    return rows, cols, stride[-2]
+    _fits(name, shape[0], rows, ld)
+    return rows, cols, ld
 
 
 def _int32(t, name, shape=None):
@@ -149,6 +158,7 @@ def _order(order, tokens=None):
     _int32(source, "source")
     if position.dim() != 2 or source.dim() != 1:
         raise ValueError("position must be tokens x choices and source one row number per row")
+    _fits("the order", *position.shape, source.shape[0])
     if tokens is not None and position.shape[0] != tokens:
         raise ValueError(f"the order is of {position.shape[0]} tokens, not of {tokens}")
     return position, source
@@ -260,10 +270,10 @@ def gemm_fp8(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None):
         raise ValueError(f"a needs scales of shape {(M, -(-K // GROUP))}, not {tuple(sa)}")
     kind = _kind(N, K, sb, "b")
     dtype, code = _out_type(out, out_dtype, (M, N))
+    ldc = N if out is None else _mat(out, "out")[2]
     device = _device(stream, "a", a, a_scale, b, b_scale, out)
     with _on(stream):
         c = torch.empty((M, N), dtype=dtype, device=device) if out is None else out
-        ldc = N if out is None else _mat(c, "out")[2]
         _call(_lib().gemm_fp8, "gemm_fp8", device, stream, M, N, K, a.data_ptr(), lda, a_scale.data_ptr(),
               *a_scale.stride(), b.data_ptr(), ldb, b_scale.data_ptr(), kind, *b_scale.stride(), c.data_ptr(), ldc, code)
     return c
@@ -286,10 +296,10 @@ def gemm_fp8_experts(a, a_scale, b, b_scale, offsets, out_dtype=None, out=None, 
     kind = _kind(N, K, sb, "b")
     _int32(offsets, "offsets", (experts + 1,))
     dtype, code = _out_type(out, out_dtype, (rows, N))
+    ldc = N if out is None else _mat(out, "out")[2]
     device = _device(stream, "a", a, a_scale, b, b_scale, offsets, out)
     with _on(stream):
         c = torch.empty((rows, N), dtype=dtype, device=device) if out is None else out
-        ldc = N if out is None else _mat(c, "out")[2]
         _call(_lib().gemm_fp8_experts, "gemm_fp8_experts", device, stream, rows, experts, N, K, a.data_ptr(), lda,
               a_scale.data_ptr(), *a_scale.stride(), b.data_ptr(), ldb, b.stride(0) if experts > 1 else N * ldb,
               b_scale.data_ptr(), kind, *b_scale.stride(), offsets.data_ptr(), c.data_ptr(), ldc, code)
@@ -320,10 +330,10 @@ def gemm_fp8_experts_wgrad(a, a_scale, b, b_scale, offsets, out_dtype=None, out=
         raise ValueError("offsets must have one entry more than there are experts")
     _int32(offsets, "offsets", (experts + 1,))
     dtype, code = _out_type(out, out_dtype, (experts, N, K))
+    ldc = _mat(out, "out", 3)[2] if out is not None else K if N > 1 else (K + 15) & ~15
     device = _device(stream, "a", a, a_scale, b, b_scale, offsets, out)
     with _on(stream):
         c = torch.empty((experts, N, K), dtype=dtype, device=device) if out is None else out
-        ldc = _mat(c, "out", 3)[2]
         _call(_lib().gemm_fp8_experts_wgrad, "gemm_fp8_experts_wgrad", device, stream, rows, experts, N, K, a.data_ptr(),
               lda, a_scale.data_ptr(), a_scale.stride(0), a_scale.stride(1), b.data_ptr(), ldb, b_scale.data_ptr(),
               b_scale.stride(0), b_scale.stride(1), offsets.data_ptr(), c.data_ptr(), ldc,
@@ -345,6 +355,7 @@ def sort_by_expert(ids, experts: int, align: int = 1, stream=None) -> ExpertOrde
     tokens, top = ids.shape
     slots = tokens * top
     rows = (slots + min(experts, slots) * (align - 1)) // align * align
+    _fits("the order", tokens, top, rows)
     device = _device(stream, "ids", ids)
     with _on(stream):
         offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)

@@ -45,6 +45,43 @@ def meta(shape, stride, dtype):
     return torch.empty_strided(shape, stride, dtype=dtype, device="meta")
 
 
+def test_numbers_past_32_bits_are_refused_not_cut_off():
+    """A leading dimension or a count beyond the C interface's ints (ctypes keeps the low 32 bits)."""
+    far = 2 ** 32 + 64
+    bf16, f8, f32, i32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
+    x, long = meta((2, 64), (far, 1), bf16), meta((far, 64), (64, 1), bf16)
+    a, s = meta((2, 64), (far, 1), f8), meta((2, 1), (1, 2), f32)
+    b, bs = meta((64, 64), (64, 1), f8), meta((64, 1), (1, 64), f32)
+    w, ws, off = meta((3, 64, 64), (4096, 64, 1), f8), meta((3, 64, 1), (64, 1, 64), f32), meta((4,), (1,), i32)
+    out = meta((64, 64), (far, 1), bf16)
+    order = tcl.ExpertOrder(off, meta((2, 1), (1, 1), i32), meta((2,), (1,), i32))
+    wide = tcl.ExpertOrder(off, meta((2, 2 ** 31), (2 ** 31, 1), i32), meta((2,), (1,), i32))
+    many = tcl.ExpertOrder(off, meta((2, 1), (1, 1), i32), meta((far,), (1,), i32))
+    y = meta((2, 64), (64, 1), bf16)
+    for call in (
+        lambda: tcl.quantize_fp8(x),
+        lambda: tcl.quantize_fp8(x, along="columns"),
+        lambda: tcl.quantize_fp8(long, along="blocks"),
+        lambda: tcl.quantize_fp8(meta((far, 2, 64), (128, 64, 1), bf16), along="blocks"),
+        lambda: tcl.quantize_fp8(meta((2, far), (far, 1), bf16)),
+        lambda: tcl.quantize_fp8(y, order=many),
+        lambda: tcl.quantize_fp8(y, order=wide),
+        lambda: tcl.gemm_fp8(a, s, b, bs),
+        lambda: tcl.gemm_fp8(b, bs, b, bs, out=out),
+        lambda: tcl.gemm_fp8_experts(a, s, w, ws, off),
+        lambda: tcl.gemm_fp8_experts(b, bs, meta((far, 64, 64), (4096, 64, 1), f8), meta((far, 64, 1), (64, 1, 64), f32),
+                                     meta((far + 1,), (1,), i32)),
+        lambda: tcl.gemm_fp8_experts_wgrad(a, s, b, bs, off),
+        lambda: tcl.sort_by_expert(meta((far, 1), (1, 1), torch.int64), 4),
+        lambda: tcl.sort_by_expert(meta((4, far), (far, 1), torch.int64), 4),
+        lambda: tcl.gather_rows(x, order),
+        lambda: tcl.combine(x, None, order),
+        lambda: tcl.combine_grad(x, y, None, order),
+    ):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+
+
 def test_operands_are_recorded_on_the_given_stream(monkeypatch):
     """The caching allocator must know that the given stream reads them (it would hand their memory out
     again once the caller drops them)."""
