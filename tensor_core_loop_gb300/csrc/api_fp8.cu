@@ -51,7 +51,6 @@ struct Operand {
 // Copies an operand that is off the tensor copies' grid into `to`.
 int lay_out(Operand& o, uint8_t* to, cudaStream_t stream) {
     if (!o.copy()) return TCL_OK;
-    if (o.mats > 65535) return TCL_ERR_DIMS;
     const long long ld = up(o.k, 16);
     const cudaError_t err = launch_copy_bytes(o.p, o.ld, o.mat, to, ld, o.mats, o.rows, o.k, stream);
     if (err != cudaSuccess) return status_of(err);

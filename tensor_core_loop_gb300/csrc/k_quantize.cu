@@ -41,23 +41,22 @@ __device__ __forceinline__ uint2 quant8(const float (&v)[8], float inv) {
     return make_uint2(w[0], w[1]);
 }
 
-// The bytes of w from the n-th on as zeros: they lie behind the matrix' end (a product of the zeros
-// loaded there with the reciprocal of a NaN's scale is not a zero).
-__device__ __forceinline__ uint2 keep8(uint2 w, int n) {
-    if (n >= 8) return w;
-    const uint64_t v = (static_cast<uint64_t>(w.y) << 32 | w.x) & (n > 0 ? (1ull << (8 * n)) - 1 : 0ull);
-    return make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
-}
-
-// n of the 8 bytes (the rest lies behind the row's end)
-__device__ __forceinline__ void put8(uint8_t* p, int n, bool vec, uint2 w) {
+// The first n of the 8 bytes, and zeros behind them (behind the matrix' end) where the row has room
+// for them. (The zeros are put in here: those loaded there times the reciprocal of a NaN's scale are
+// not zeros. Off the whole pieces' path.)
+__device__ __forceinline__ void put8(uint8_t* p, int n, int room, bool vec, uint2 w) {
     if (vec && n >= 8) {
         *reinterpret_cast<uint2*>(p) = w;
         return;
     }
+    const uint64_t kept = (static_cast<uint64_t>(w.y) << 32 | w.x) & (n >= 8 ? ~0ull : n > 0 ? (1ull << (8 * n)) - 1 : 0ull);
+    if (vec && room >= 8) {
+        *reinterpret_cast<uint64_t*>(p) = kept;
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+        if (i < room) p[i] = static_cast<uint8_t>(kept >> (8 * i));
 }
 
 // Groups along the rows: sixteen lanes (a team) hold a group, eight values each. A block's
@@ -67,10 +66,11 @@ __device__ __forceinline__ void put8(uint8_t* p, int n, bool vec, uint2 w) {
 // each of its rows; blocks behind the tokens' write the rows that no token has.
 constexpr int kTeams = 8, kZeroRows = 32;
 
+// (blocks an SM: with nine of bf16 and N = 4, for three more registers, 16384 × 4096 took 43 us; with
+// seven of fp32 53 instead of 51)
 template <typename T, int N>
-__global__ void __launch_bounds__(16 * kTeams) quant_rows_kernel(const QuantRows a, int groups, int row_teams_log2,
-                                                                 int quant_blocks, int wcols, bool vec_in,
-                                                                 bool vec_out) {
+__global__ void __launch_bounds__(16 * kTeams, N == 1 ? 12 : sizeof(T) == 2 ? 10 : 8)
+    quant_rows_kernel(const QuantRows a, int groups, int row_teams_log2, int quant_blocks, int wcols, bool vec_in, bool vec_out) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int team = threadIdx.x >> 4, l = threadIdx.x & 15;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(16 * kTeams) quant_rows_kernel(const QuantRows
         const int r0 = (blockIdx.x - quant_blocks) * kZeroRows;
         for (int r = r0 + team; r < min(r0 + kZeroRows, a.out_rows); r += kTeams) {
             if (a.source[r] >= 0) continue;
-            for (int c = l * 8; c < wcols; c += 128) put8(a.q + r * a.ldq + c, wcols - c, vec_out, make_uint2(0u, 0u));
+            for (int c = l * 8; c < wcols; c += 128) put8(a.q + r * a.ldq + c, a.cols - c, wcols - c, vec_out, make_uint2(0u, 0u));
             for (int g = l; g < groups; g += 16) a.scale[r * a.s_row + g * a.s_group] = group_scale(0u);
         }
         return;
@@ -107,11 +107,11 @@ __global__ void __launch_bounds__(16 * kTeams) quant_rows_kernel(const QuantRows
         for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         if (row >= a.rows || g >= groups) continue;   // (uniform over the team)
         const float s = group_scale(top);
-        const uint2 w = keep8(quant8(v, __frcp_rn(s)), a.cols - c);
+        const uint2 w = quant8(v, __frcp_rn(s));
         for (int j = 0; j < (a.position ? a.top : 1); ++j) {
             const int r = a.position ? a.position[static_cast<long long>(row) * a.top + j] : row;
             if (r < 0 || (a.position && r >= a.out_rows)) continue;
-            put8(a.q + r * a.ldq + c, wcols - c, vec_out, w);
+            put8(a.q + r * a.ldq + c, a.cols - c, wcols - c, vec_out, w);
             if (l == 0) a.scale[r * a.s_row + g * a.s_group] = s;
         }
     }
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tiles_kerne
             const int r = r0 + rg * 8 + i;
             float v[8];
             raw[i].get(v);
-            if (r < a.rows && c < wcols) put8(q + r * a.ldq + c, wcols - c, vec_out, keep8(quant8(v, inv[0]), a.cols - c));
+            if (r < a.rows && c < wcols) put8(q + r * a.ldq + c, a.cols - c, wcols - c, vec_out, quant8(v, inv[0]));
         }
         return;
     }
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tiles_kerne
         for (int k = 0; k < 8; ++k) {
             const int cc = k * 16 + rg, r = r0 + cg * 8;   // sixteen threads write a column's 128 bytes
             if (c0 + cc < a.cols && r < wrows)
-                put8(q + (c0 + cc) * a.ldq + r, wrows - r, vec_out, keep8(turn[cc * 16 + (cg ^ (cc >> 3))], a.rows - r));
+                put8(q + (c0 + cc) * a.ldq + r, a.rows - r, wrows - r, vec_out, turn[cc * 16 + (cg ^ (cc >> 3))]);
         }
     }
 }
