@@ -215,7 +215,7 @@ int tcl_quantize_fp8_columns(int x_type, int rows, int cols, const void* X, int 
     if (made == 0) return TCL_OK;
     return status_of(launch_quant_tiles(QuantTile::COLUMNS,
                                         {X, ldx, 0, x_type == TCL_X_F32, 1, made, cols, rows, source, top,
-                                         static_cast<uint8_t*>(Q), ldq, 0, scale, s_row, s_group},
+                                         static_cast<uint8_t*>(Q), ldq, 0, scale, 0, s_row, s_group},
                                         stream));
 }
 
@@ -231,9 +231,10 @@ int tcl_quantize_fp8_blocks(int x_type, int batch, int rows, int cols, const voi
     if (!on(X, elem(x_type)) || !on(scale, 4)) return TCL_ERR_ALIGN;
     if (int st = device_check()) return st;
     if (!any) return TCL_OK;
+    const long long groups = groups_of(qcols);   // (the scales lie one matrix after another)
     return status_of(launch_quant_tiles(transpose ? QuantTile::BLOCKS_T : QuantTile::BLOCKS,
                                         {X, ldx, x_batch, x_type == TCL_X_F32, batch, rows, cols, rows, nullptr, 1,
-                                         static_cast<uint8_t*>(Q), ldq, q_batch, scale, 0, 0},
+                                         static_cast<uint8_t*>(Q), ldq, q_batch, scale, groups_of(qrows) * groups, groups, 1},
                                         stream));
 }
 

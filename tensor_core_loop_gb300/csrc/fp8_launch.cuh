@@ -90,7 +90,8 @@ struct QuantTiles {
     uint8_t* q;
     long long ldq, q_batch;
     float* scale;
-    long long s_row, s_group;   // COLUMNS; otherwise contiguous
+    long long s_batch, s_row, s_group;
+    long long room;          // of Q's rows from q on (set by the launch)
 };
 cudaError_t launch_quant_tiles(QuantTile kind, const QuantTiles& a, cudaStream_t stream);
 

@@ -182,17 +182,16 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tiles_kerne
         for (int i = 0; i < 8; ++i) t = max(t, red[0][i]);
         const float s = group_scale(t);
         if (threadIdx.x == 0) {
-            const long long tile = static_cast<long long>(blockIdx.z) * gridDim.x * gridDim.y +
-                                   (KIND == QuantTile::BLOCKS ? blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x
-                                                              : blockIdx.x * static_cast<long long>(gridDim.y) + blockIdx.y);
-            a.scale[tile] = s;
+            const unsigned r = KIND == QuantTile::BLOCKS ? blockIdx.y : blockIdx.x;
+            const unsigned g = KIND == QuantTile::BLOCKS ? blockIdx.x : blockIdx.y;
+            a.scale[blockIdx.z * a.s_batch + r * a.s_row + g * a.s_group] = s;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) inv[j] = __frcp_rn(s);
     }
     uint8_t* q = a.q + blockIdx.z * a.q_batch;
     if constexpr (!TR) {
-        const int wcols = static_cast<int>(min(a.ldq, static_cast<long long>((a.cols + 15) & ~15)));
+        const int wcols = static_cast<int>(min(a.room, static_cast<long long>((a.cols + 15) & ~15)));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = r0 + rg * 8 + i;
@@ -214,7 +213,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tiles_kerne
             turn[(cg * 8 + j) * 16 + (rg ^ cg)] = quant8(w, inv[j]);
         }
         __syncthreads();
-        const int wrows = static_cast<int>(min(a.ldq, static_cast<long long>((a.rows + 15) & ~15)));
+        const int wrows = static_cast<int>(min(a.room, static_cast<long long>((a.rows + 15) & ~15)));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int cc = k * 16 + rg, r = r0 + cg * 8;   // sixteen threads write a column's 128 bytes
@@ -264,14 +263,30 @@ cudaError_t quant_rows(const QuantRows& a, cudaStream_t stream) {
     return quant_rows_n<T, 1>(a, groups, log2, stream);
 }
 
+// One launch for each 65,535 rows of tiles and 65,535 matrices: what the grid's axes hold.
 template <typename T, QuantTile KIND>
 cudaError_t quant_tiles(const QuantTiles& a, cudaStream_t stream) {
-    const dim3 grid((a.cols + kG - 1) / kG, (a.rows + kG - 1) / kG, a.batch);
-    if (grid.y == 0 || grid.z == 0) return cudaSuccess;
-    if (grid.y > 65535 || grid.z > 65535) return cudaErrorInvalidValue;
+    constexpr int kAxis = 65535;
     const bool vec_in = row_aligned<T>(a.x, a.ldx, 16) && (a.batch < 2 || a.x_batch * sizeof(T) % 16 == 0);
     const bool vec_out = row_aligned<uint8_t>(a.q, a.ldq, 8) && (a.batch < 2 || a.q_batch % 8 == 0);
-    return launch_pdl(quant_tiles_kernel<T, KIND>, grid, 256, 0, stream, a, vec_in, vec_out);
+    const long long rows = a.rows;
+    for (long long z = 0; z < a.batch; z += kAxis)
+        for (long long r = 0; r < rows; r += kAxis * kG) {
+            QuantTiles p = a;
+            p.batch = static_cast<int>(std::min<long long>(a.batch - z, kAxis));
+            p.rows = static_cast<int>(std::min<long long>(rows - r, kAxis * kG));
+            p.room = KIND == QuantTile::BLOCKS ? a.ldq : a.ldq - r;
+            p.q += z * a.q_batch + (KIND == QuantTile::BLOCKS ? r * a.ldq : r);
+            p.scale += z * a.s_batch + r / kG * (KIND == QuantTile::BLOCKS ? a.s_row : a.s_group);
+            if (a.source)
+                p.source += r;   // (its rows are X's whichever they are)
+            else
+                p.x = static_cast<const T*>(a.x) + z * a.x_batch + r * a.ldx;
+            const dim3 grid((p.cols + kG - 1) / kG, (p.rows + kG - 1) / kG, p.batch);
+            const cudaError_t err = launch_pdl(quant_tiles_kernel<T, KIND>, grid, 256, 0, stream, p, vec_in, vec_out);
+            if (err != cudaSuccess) return err;
+        }
+    return cudaSuccess;
 }
 
 template <typename T>

@@ -8,6 +8,7 @@ import torch
 
 import fp8_reference as ref
 import tensor_core_loop_gb300 as tcl
+from tensor_core_loop_gb300 import fp8
 
 pytestmark = pytest.mark.gpu
 
@@ -60,6 +61,41 @@ def test_padding_is_zero_beside_non_finite_values(along, value, dtype):
     padding = data.as_strided((rows, pitch), (pitch, 1)).view(torch.uint8)[:, cols:]
     assert bool((padding == 0).all())
     assert not bool(torch.isfinite(scale).all())      # (and the groups that hold the value carry it)
+
+
+@pytest.mark.parametrize("along", ["columns", "blocks", "blocks_t"])
+def test_more_tiles_than_a_grid_axis_holds(along):
+    """65,536 tiles of 128 rows and a piece, and 65,537 matrices of a batch."""
+    cut, rows = 65_535 * 128, 65_536 * 128 + 5
+    x = torch.randn(rows, 3, device=DEV, generator=torch.Generator(device=DEV).manual_seed(2)).to(BF16)
+    data, scale = tcl.quantize_fp8(x, along=along)
+    tail = x[cut:].cpu()
+    want, s = ref.quantize(tail.t() if along == "columns" else tail, 1 if along == "columns" else 128)
+    if along == "blocks":
+        assert torch.equal(data[cut:].cpu().double(), want) and torch.equal(scale[cut // 128:].cpu(), s)
+    else:
+        want, s = (want, s) if along == "columns" else (want.t(), s.t())
+        assert torch.equal(data[:, cut:].cpu().double(), want) and torch.equal(scale[:, cut // 128:].cpu(), s)
+    head = tcl.quantize_fp8(x[:cut], along=along)      # (as many as fit the axis)
+    got = (data[:cut], scale[:cut // 128]) if along == "blocks" else (data[:, :cut], scale[:, :cut // 128])
+    assert torch.equal(got[0].float(), head[0].float()) and torch.equal(got[1], head[1])
+    if along != "blocks":      # rows of the result that leave no room behind them
+        tight, st = torch.empty(3, rows, dtype=F8, device=DEV), torch.empty_like(scale)
+        if along == "columns":
+            status = fp8._lib().tcl_quantize_fp8_columns(0, rows, 3, x.data_ptr(), 3, None, 1, 0, tight.data_ptr(), rows,
+                                                         st.data_ptr(), *st.stride(), torch.cuda.current_stream().cuda_stream)
+        else:
+            status = fp8._lib().tcl_quantize_fp8_blocks(0, 1, rows, 3, x.data_ptr(), 3, 0, 1, tight.data_ptr(), rows, 0,
+                                                        st.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert status == 0 and torch.equal(tight.view(torch.uint8), data.view(torch.uint8)) and torch.equal(st, scale)
+    if along != "columns":
+        w = torch.randn(65_537, 2, 3, device=DEV, generator=torch.Generator(device=DEV).manual_seed(3))
+        data, scale = tcl.quantize_fp8(w, along=along)
+        top = w.abs().amax((1, 2))
+        v = (data.float() * scale).double()
+        v = v.transpose(1, 2) if along == "blocks_t" else v
+        assert bool(((v - w.double()).abs() <= top[:, None, None].double() * 2.0 ** -4).all())
+        assert torch.equal(scale.view(-1), torch.div(top, torch.full_like(top, 448.0)))
 
 
 # ------------------------------------------------------------------------------ sorting
