@@ -229,8 +229,9 @@ __global__ void __launch_bounds__(256) copy_bytes_kernel(const uint8_t* src, lon
     ptx::griddep_launch_dependents();
     src += blockIdx.z * batch_stride;
     dst += static_cast<long long>(blockIdx.z) * rows * ld_dst;
-    for (int r = blockIdx.y; r < rows; r += gridDim.y)
-        for (int c = blockIdx.x * 256 + threadIdx.x; c < cols; c += gridDim.x * 256) dst[r * ld_dst + c] = src[r * ld + c];
+    const int c = blockIdx.x * 256 + threadIdx.x;   // (the grid covers the columns: a step past them could pass 32 bits)
+    if (c >= cols) return;
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) dst[r * ld_dst + c] = src[r * ld + c];
 }
 
 template <typename T>

@@ -203,3 +203,18 @@ def test_threads_on_one_stream():
     for i, r in got:
         for u, v in zip(r, want[i]):
             assert torch.equal(u, v)
+
+
+# ------------------------------------------------------------------------------ products
+
+def test_gemm_of_a_row_past_half_of_32_bits():
+    """More than 2^30 values of K in operands that are copied onto the tensor copies' grid first."""
+    K = 2 ** 30 + 300
+    a, b = (torch.zeros(K + 1, dtype=torch.uint8, device=DEV) for _ in range(2))
+    at = torch.tensor([0, 5, 127, 128, 2 ** 29 + 1, 2 ** 30 - 1, 2 ** 30, 2 ** 30 + 257, K - 1], device=DEV) + 1
+    a[at], b[at] = 0x38, 0x40                            # 1 and 2
+    one = torch.ones(1, device=DEV).expand(1, -(-K // 128))
+    c = tcl.gemm_fp8(a.view(F8)[None, 1:], one, b.view(F8)[None, 1:], one, out_dtype=F32)
+    assert float(c) == 2.0 * len(at)
+    torch.cuda.synchronize()
+    tcl.lib().tcl_shutdown()                             # (2 GB of scratch)
