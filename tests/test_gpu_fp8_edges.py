@@ -218,3 +218,117 @@ def test_gemm_of_a_row_past_half_of_32_bits():
     assert float(c) == 2.0 * len(at)
     torch.cuda.synchronize()
     tcl.lib().tcl_shutdown()                             # (2 GB of scratch)
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def pair_tiles(counts, N, experts):
+    """Tiles of 256 x 256 that rows sorted by expert make, if that is the tile that the library takes for
+    them (from some hundred rows an expert, where tiles of 128 x 128 are more than the SMs)."""
+    rows = sum(counts)
+    each = -(-rows // experts)
+    ones = -(-each // 128) * -(-N // 128) * experts
+    return sum(-(-n // 256) for n in counts) * -(-N // 256) if each > 112 and N > 128 and ones > sms() else 0
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("per", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(3000, 2600, 1300), (3001, 2601, 1153), (2817, 2304, 2048)])
+def test_gemm_pair_tiles_over_several_waves(M, N, K, per, out):
+    """Every pair of SMs walks more than one tile of more than eight k-blocks: the rings' phases, the scales'
+    slots and the slabs of the stores go on from one tile to the next."""
+    assert pair_tiles([M], N, 1) > sms() // 2 and K > 8 * 128
+    pitch = -(-K // 16) * 16
+    a, sa = random_operand(M, K, M + K, pitch=pitch)
+    b, sb = random_operand(N, K, N + 2 * K, per=per, pitch=pitch)
+    c = tcl.gemm_fp8(a, sa, b, sb, out_dtype=out)
+    want, bound = ref.product_bound(ref.values(a, sa), ref.values(b, sb), out)
+    ref.check(c, want, bound, f"{M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("per", [1, 128])
+@pytest.mark.parametrize("N,K", [(1100, 1300), (1111, 1300), (1280, 1153)])
+@pytest.mark.parametrize("behind", [0, 300])
+def test_experts_pair_tiles_over_several_waves(N, K, per, out, behind):
+    counts = [2300, 0, 513, 1, 1700, 0, 260, 1226]
+    assert pair_tiles(counts + [behind], N, len(counts)) > sms() // 2 and K > 8 * 128
+    o = [sum(counts[:i]) for i in range(len(counts) + 1)]
+    rows, E, pitch = o[-1] + behind, len(counts), -(-K // 16) * 16
+    a, sa = random_operand(rows, K, rows + K, pitch=pitch)
+    b, sb = random_operand(N, K, N + K, per=per, pitch=pitch, batch=E)
+    c = tcl.gemm_fp8_experts(a, sa, b, sb, torch.tensor(o, dtype=torch.int32, device=DEV), out_dtype=out)
+    va, vb = ref.values(a, sa), ref.values(b, sb)
+    for e in range(E):
+        want, bound = ref.product_bound(va[o[e]:o[e + 1]], vb[e], out)
+        ref.check(c[o[e]:o[e + 1]], want, bound, f"expert {e}")
+    assert bool((c[o[-1]:] == 0).all())
+
+
+# (rows of operands and results off the tensor copies' grid, matrices at odd distances, strided scales)
+
+def strided(scale):
+    """The same scales, every second column of a larger matrix, NaN between them."""
+    big = torch.full((*scale.shape[:-1], 2 * scale.shape[-1] + 1), float("nan"), device=DEV)
+    big[..., 1::2] = scale
+    return big[..., 1::2]
+
+
+@pytest.mark.parametrize("counts", [[3, 0, 5, 1], [130, 0, 127, 300], [700, 513, 0, 1025]])
+@pytest.mark.parametrize("pitch,distance", [(208, 300 * 208 + 1), (208, 300 * 208 + 8), (207, 300 * 207 + 3), (208, 301 * 208)])
+def test_experts_matrices_at_any_distance(counts, pitch, distance):
+    """An aligned base and leading dimension with the matrices off the grid: all of them are copied."""
+    N, K, E = 300, 200, len(counts)
+    o = [sum(counts[:i]) for i in range(E + 1)]
+    a, sa = random_operand(o[-1], K, 1, pitch=208)
+    b, sb = random_operand(N, K, 2, per=128, pitch=pitch, batch=E, distance=distance)
+    c = tcl.gemm_fp8_experts(a, strided(sa), b, strided(sb), torch.tensor(o, dtype=torch.int32, device=DEV), out_dtype=F32)
+    va, vb = ref.values(a, sa), ref.values(b, sb)
+    for e in range(E):
+        want, bound = ref.product_bound(va[o[e]:o[e + 1]], vb[e], F32)
+        ref.check(c[o[e]:o[e + 1]], want, bound, f"expert {e}")
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("counts", [[2, 1], [60, 33], [3000, 1500, 0, 2001]])
+@pytest.mark.parametrize("off", [0, 1, 8])
+def test_experts_into_a_part_of_a_matrix(counts, off, out):
+    N, K, E = 700, 300, len(counts)
+    o = [sum(counts[:i]) for i in range(E + 1)]
+    rows = o[-1] + 5
+    a, sa = random_operand(rows, K, 1, pitch=304)
+    b, sb = random_operand(N, K, 2, per=128, pitch=304, batch=E)
+    big = torch.full((rows + 2, N + 20), 7.0, dtype=out, device=DEV)
+    c = big[1:rows + 1, off:off + N]
+    assert tcl.gemm_fp8_experts(a, sa, b, sb, torch.tensor(o, dtype=torch.int32, device=DEV), out=c) is c
+    va, vb = ref.values(a, sa), ref.values(b, sb)
+    for e in range(E):
+        want, bound = ref.product_bound(va[o[e]:o[e + 1]], vb[e], out)
+        ref.check(c[o[e]:o[e + 1]], want, bound, f"expert {e}")
+    assert bool((c[o[-1]:] == 0).all())
+    c.fill_(7.0)
+    assert bool((big == 7.0).all())
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("N,K,counts", [(130, 77, [5, 300, 0]), (64, 300, [4000, 1]), (1030, 1100, [256, 0, 900, 130] * 4)])
+@pytest.mark.parametrize("pitches,off", [((None, None), 0), ((3, 16), 1), ((16, 5), 8), ((1, 7), 16)])
+def test_wgrad_strides_and_alignment(N, K, counts, out, pitches, off):
+    """Operands at any pitch, strided scales, the result in the middle of a larger batch."""
+    o = [0]
+    for n in counts:
+        o.append(o[-1] + -(-n // 128) * 128)
+    rows, E = o[-1], len(counts)
+    a, sa = random_operand(N, rows, 1, pitch=rows + pitches[0] if pitches[0] else None)
+    b, sb = random_operand(K, rows, 2, pitch=rows + pitches[1] if pitches[1] else None)
+    big = torch.full((E, N + 2, K + 24), 7.0, dtype=out, device=DEV)
+    c = big[:, 1:N + 1, off:off + K]
+    assert tcl.gemm_fp8_experts_wgrad(a, strided(sa), b, strided(sb), torch.tensor(o, dtype=torch.int32, device=DEV), out=c) is c
+    va, vb = ref.values(a, sa), ref.values(b, sb)
+    for e in range(E):
+        want, bound = ref.product_bound(va[:, o[e]:o[e + 1]], vb[:, o[e]:o[e + 1]], out)
+        ref.check(c[e], want, bound, f"expert {e}")
+    c.fill_(7.0)
+    assert bool((big == 7.0).all())
