@@ -129,7 +129,7 @@ def main():
     layer = ExpertLayer(64, 4096, 2048)
     ids, weights = router(16, 64, 8, "cuda", 3)
     x = torch.randn(16, 4096, device="cuda").to(torch.bfloat16)
-    layer.forward(x, ids, weights)                        # the library's scratch is in place
+    layer.forward(x, ids, weights)                        # kernels are loaded outside the capture
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         layer.forward(x, ids, weights)

@@ -49,3 +49,13 @@ def test_serving_and_training_layouts_agree(example):
     x = torch.randn(200, 256, device="cuda").to(torch.bfloat16)
     out = layer.forward(x, ids, weights)
     assert torch.equal(out, layer.forward(x, ids, weights, train=True)[0])
+
+
+@pytest.mark.parametrize("sizes", [dict(), dict(tokens=7, experts=5, top=3, hidden=130, inner=96),
+                                   dict(tokens=1500, experts=4, top=2, hidden=512, inner=300)])
+def test_each_result_within_its_own_roundings(example, sizes):
+    """The distances of the test above, each held to the rounded operands behind it: 4 for the output (x,
+    W_in, a, W_out), 5 for the router weights' gradients, 7 for the others."""
+    for name, d in example.distances(**sizes).items():
+        n = {"output": 4, "router weights": 5}.get(name, 7)
+        assert d < 2 * 0.026 * n ** 0.5, (name, d)
