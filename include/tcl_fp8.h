@@ -6,12 +6,14 @@
  * ownership, streams and CUDA graphs hold here too, with these differences.
  *   Sizes: a count of rows or tokens may be 0 (nothing is launched, or what has
  *     no rows is written as zeros); widths and K are at least 1, and either is
- *     below 2^31 - 2^16 (TCL_ERR_DIMS otherwise).
+ *     below 2^31 - 2^16 (TCL_ERR_DIMS otherwise; widths of rows that are quantised
+ *     along them, gathered or combined end at 67,107,840).
  *   Nothing is kept between calls but library scratch, which only operands that
  *     miss the alignment below use.
  *   Reported by tcl_last_device_error(): code 7, the experts' offsets do not
  *     ascend from 0 within the rows (or are off the multiples of 128 where
- *     those are asked for); such a launch writes nothing.
+ *     those are asked for); such a launch writes nothing. Waits inside the
+ *     products' kernels end after 1 s (codes 1 to 4 as in tcl_gemm.h).
  *
  * Values: a group of 128 numbers x has the scale s = max(max|x| / 448, 2^-126)
  *   and holds q = e4m3(x · (1/s)), rounded to nearest even; q·s stands for x. A
@@ -30,10 +32,12 @@
  *   overwritten. Leading dimensions are in elements.
  *
  * Alignment: scales 4 bytes, fp32 and bf16 matrices their element size. e4m3
- *   operands whose base is not 16-byte aligned or whose leading dimension is not
- *   a multiple of 16 are copied into library scratch first (one more pass; the
- *   scratch grows on demand, TCL_ERR_CAPTURE if that would be inside a capture).
- *   K itself is free.
+ *   operands whose base is not 16-byte aligned, or whose leading dimension or
+ *   (experts' matrices) distance from one another is not a multiple of 16, are
+ *   copied into library scratch first, every matrix of them, a byte at a time and
+ *   on every call (64 matrices of 4096 × 2048: 2.2 ms before a product of 50 us).
+ *   The scratch grows on demand (TCL_ERR_CAPTURE if that would be inside a
+ *   capture). K itself is free.
  */
 #ifndef TCL_FP8_H
 #define TCL_FP8_H

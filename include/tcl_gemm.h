@@ -94,7 +94,7 @@ extern "C" {
 typedef enum {
     TCL_OK = 0,
     TCL_ERR_NULL = 1,            /* a required pointer is NULL */
-    TCL_ERR_DIMS = 2,            /* M, N or K < 1 */
+    TCL_ERR_DIMS = 2,            /* M, N or K < 1 (tcl_fp8.h: or past a call's sizes) */
     TCL_ERR_LD = 3,              /* lda < K, ldb < N or ldc < N */
     TCL_ERR_ALIGN = 4,           /* a pointer is not aligned to its element size (gemm_s8_static:
                                     the stricter rule given there) */

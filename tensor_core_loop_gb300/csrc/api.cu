@@ -1629,7 +1629,7 @@ const char* tcl_status_string(int status) {
     switch (status) {
         case TCL_OK: return "ok";
         case TCL_ERR_NULL: return "null pointer argument";
-        case TCL_ERR_DIMS: return "M, N and K must be at least 1";
+        case TCL_ERR_DIMS: return "a size is below 1 or past what the call takes";
         case TCL_ERR_LD: return "leading dimension smaller than the row width";
         case TCL_ERR_ALIGN: return "base address or leading dimension not 16-byte aligned";
         case TCL_ERR_K_TOO_LARGE: return "K too large for an exact int32 result";

@@ -24,7 +24,9 @@
 // scheduler, are as many as the registers hold; a few words spilled in the loop cost 30 %.
 // With few rows a weight byte's way from HBM bounds it: 16 tokens on 64 experts of 4096 × 2048
 // read 319 MB in 51 us, 6.2 TB/s. Scales per column (weight gradients) take two fp32
-// operations an element instead of one (32 experts of 2048 × 1024 from 32,700 rows: 109 us).
+// operations an element instead of one. There a tile has few k-blocks (32 experts of 2048 × 1024 from
+// 32,700 rows: eight, 109 us; 8192 × 4096 × 1000 57 us) and its loads, MMAs, promotion and stores follow
+// one another more than they overlap: tensor pipe 26 %, issue slots 41 %, DRAM 35 % busy.
 //
 // The side in the 128 tensor-memory lanes is P, the one in the columns is Q. Many rows
 // of tokens go to P with the weights' rows in Q; few (SWAP) go to Q, as narrow as the
@@ -549,16 +551,16 @@ __global__ void __launch_bounds__(Fp8Cfg<BQ, PAIR, SWAP, QVEC>::THREADS, Fp8Cfg<
             for (int j = 0, u = u0; ok && u < units; u = walk(++j)) {
                 const Fp8Unit U = unit(u, cur);
                 if (of_p) {   // what the promotion warps need of it (working it out would hold them up between tiles)
-                if (!wait(uempty0 + 8 * (j % C::UR), (j / C::UR & 1) ^ 1u, DEV_TIMEOUT_PRODUCER)) break;
-                if (lane == 0) {
-                    int4* to = reinterpret_cast<int4*>(published + 8 * (j % C::UR));
-                    to[0] = make_int4(U.p0, U.q0, U.p_end, U.q_end);
-                    to[1] = make_int4(U.e, U.nk, 0, 0);
-                    ptx::mbar_arrive(ufull0 + 8 * (j % C::UR));
+                    if (!wait(uempty0 + 8 * (j % C::UR), (j / C::UR & 1) ^ 1u, DEV_TIMEOUT_PRODUCER)) break;
+                    if (lane == 0) {
+                        int4* to = reinterpret_cast<int4*>(published + 8 * (j % C::UR));
+                        to[0] = make_int4(U.p0, U.q0, U.p_end, U.q_end);
+                        to[1] = make_int4(U.e, U.nk, 0, 0);
+                        ptx::mbar_arrive(ufull0 + 8 * (j % C::UR));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-            }
-            const int row0 = of_p ? U.p0 + static_cast<int>(rank) * 128 : U.q0, end = of_p ? U.p_end : U.q_end;
+                const int row0 = of_p ? U.p0 + static_cast<int>(rank) * 128 : U.q0, end = of_p ? U.p_end : U.q_end;
                 const int r0 = side.block ? row0 >> 7 : row0;
                 const int n = min(per, (side.block ? (end + 127) >> 7 : end) - r0);   // those that exist; zeros behind them
                 const float* at = side.scale + (of_p == SWAP ? U.e * side.s_expert : 0ll) + U.kb0 * side.s_group +

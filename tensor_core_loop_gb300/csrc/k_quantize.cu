@@ -5,8 +5,11 @@
 // One division for each group and one product for each value. The largest magnitude is
 // taken over the values' bit patterns without their sign, whose order is that of the
 // magnitudes with infinities and NaN above all numbers, so a NaN or an infinity reaches
-// the scale. All three forms are bound by memory: they read X once and write Q once
-// (16384 × 4096 bf16: along rows 41 us, 4.9 TB/s; down columns 39; blocks 34, transposed 36).
+// the scale. They read X once and write Q once and are bound by memory (16384 × 4096 bf16, floor 30 us:
+// down columns 39 us, blocks 34, transposed 36; fp32, floor 50: 53, 51, 51; 64 fp32 matrices of
+// 2048 × 1024, floor 99: 96, some of it still in the L2), but for bf16 along rows: 41 us, 4.9 TB/s, 79 % of
+// the issue slots busy with 38 M warp instructions where blocks take 24 M (addresses, bounds and
+// reductions for each group of 128 values instead of each 128 × 128); fp32 along rows 52.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -120,7 +123,8 @@ __global__ void __launch_bounds__(16 * kTeams, N == 1 ? 12 : sizeof(T) == 2 ? 10
 // Tiles of 128 × 128 values, 256 threads with eight rows × eight columns each. Transposed
 // results go through shared memory, column by column of X as 128 bytes, in pieces of 8 bytes
 // whose place is permuted by the column so that neither side has bank conflicts.
-// (fp32 without a bound took 92 registers, two blocks an SM: columns 63 us instead of 53)
+// (fp32 without a bound took 92 registers, two blocks an SM: columns 63 us instead of 53; with it blocks
+// spill 20 bytes and take 51 us, the floor 50)
 template <typename T, QuantTile KIND>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tiles_kernel(const QuantTiles a, bool vec_in, bool vec_out) {
     constexpr bool TR = KIND != QuantTile::BLOCKS;

@@ -15,7 +15,13 @@ scales (``torch.float32``, one column for each 128 columns of the data, any stri
 Calls are asynchronous on ``stream`` (default: the current stream of the tensors' device)
 and allocate their results on that stream. Given another stream than the current one, the
 caller lets it wait for whatever makes the operands (``stream.wait_stream``); the operands
-themselves may be dropped right after the call.
+themselves may be dropped right after the call. Operands off the 16-byte grid (base, leading
+dimension, distance of experts' matrices) go through scratch of the library, which has to be in
+place before a call is captured into a CUDA graph and which that graph's replays share; nothing
+else here uses any.
+
+The calls compute without a graph of autograd, also for tensors that require gradients: the
+gradients are calls of their own (each docstring says which).
 """
 from __future__ import annotations
 
@@ -261,7 +267,9 @@ def _out_type(out, out_dtype, shape):
 
 def gemm_fp8(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None):
     """C = A·Bᵀ (M x N; bf16 or ``out_dtype=torch.float32``) of e4m3 ``a`` (M x K, a scale for
-    each row and 128 of K) and ``b`` (N x K, scales for its rows or for 128 x 128 blocks)."""
+    each row and 128 of K) and ``b`` (N x K, scales for its rows or for 128 x 128 blocks). Gradients are
+    products of the same form: of ``a`` with ``b`` transposed (``quantize_fp8(b, along="blocks_t")``), of
+    ``b`` with both operands quantised down the rows (``along="columns"``)."""
     M, K, lda, sa = _operand(a, a_scale, "a")
     N, k, ldb, sb = _operand(b, b_scale, "b")
     if k != K or N < 1:
@@ -282,7 +290,8 @@ def gemm_fp8(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None):
 def gemm_fp8_experts(a, a_scale, b, b_scale, offsets, out_dtype=None, out=None, stream=None):
     """C[r] = A[r]·B[e]ᵀ for the rows r of each expert e, ``offsets[e] <= r < offsets[e+1]``:
     ``a`` rows x K sorted by expert, ``b`` experts x N x K, ``offsets`` int32 on the GPU.
-    Rows behind the last expert's are zeros. The gradient of ``a`` is the same product of the
+    Rows behind the last expert's are zeros. Offsets that do not ascend from 0 within the rows write
+    nothing and are reported by ``last_device_error``. The gradient of ``a`` is the same product of the
     result's gradient with the transposed matrices (``quantize_fp8(w, along="blocks_t")``)."""
     rows, K, lda, sa = _operand(a, a_scale, "a")
     N, k, ldb, sb = _operand(b, b_scale, "b", 3)
@@ -310,7 +319,8 @@ def gemm_fp8_experts_wgrad(a, a_scale, b, b_scale, offsets, out_dtype=None, out=
     """C[e] = sum over expert e's rows r of A[:, r]·B[:, r]ᵀ (experts x N x K): the weights'
     gradients from ``a`` (N x rows) and ``b`` (K x rows), the result's gradient and the input
     quantised down the sorted rows (``quantize_fp8(..., along="columns")``). ``offsets`` are
-    multiples of 128 (``sort_by_expert(..., align=128)``); experts without rows get zeros."""
+    multiples of 128 (``sort_by_expert(..., align=128)``), reported as above where they are not;
+    experts without rows get zeros."""
     for t, s, name in ((a, a_scale, "a"), (b, b_scale, "b")):
         if t.dtype != _F8:
             raise TypeError(f"{name} must be float8_e4m3fn")
@@ -391,7 +401,7 @@ def _weights(weights, position):
 
 def combine(y, weights, order: ExpertOrder, stream=None):
     """out[t] = sum over the token's slots j of weights[t, j]·y[position[t, j]] (None: ones), in
-    fp32, rounded once to ``y``'s type. Dropped slots add nothing."""
+    fp32, rounded once to ``y``'s type. Dropped slots add nothing. Gradients: ``combine_grad``."""
     xt = _x_type(y, "y")
     rows, cols, ldy = _mat(y, "y")
     position, source = _order(order)
