@@ -27,8 +27,8 @@
  *   weights as they are stored, outputs × inputs),
  *     C[i][j] = sum over groups g of (SA[i][g] · SB[j][g]) · sum over k in g of
  *               A[i][k] · B[j][k],
- *   a group's sum on the tensor cores in fp32, scales and the sum over groups in
- *   fp32, C rounded once. C is fp32 (TCL_OUT_F32) or bf16 (TCL_OUT_BF16) and is
+ *   a group's sum on the tensor cores in fp32, scales (their product too, which
+ *   over- and underflows as one) and the sum over groups in fp32, C rounded once. C is fp32 (TCL_OUT_F32) or bf16 (TCL_OUT_BF16) and is
  *   overwritten. Leading dimensions are in elements.
  *
  * Alignment: scales 4 bytes, fp32 and bf16 matrices their element size. e4m3

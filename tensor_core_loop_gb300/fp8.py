@@ -126,10 +126,9 @@ def _x_type(t, name):
 _INT = 2 ** 31 - 1
 
 
-def _fits(name, *numbers):
-    """(ctypes would pass on the low 32 bits of a larger one.)"""
-    if max(numbers) > _INT:
-        raise ValueError(f"{name}'s sizes and leading dimension must fit 32 bits")
+def _too_large(name):
+    """For numbers past _INT, of which ctypes would pass on the low 32 bits."""
+    raise ValueError(f"{name}'s sizes and leading dimension must fit 32 bits")
 
 
 def _mat(t, name, dim=2):
@@ -145,7 +144,8 @@ def _mat(t, name, dim=2):
     ld = stride[-2] if rows > 1 else (cols + 15) & ~15   # (a single row never steps to a second one)
     if ld < cols:
         raise ValueError(f"{name}'s rows overlap")
-    _fits(name, shape[0], rows, ld)
+    if ld > _INT or rows > _INT or shape[0] > _INT:
+        _too_large(name)
     return rows, cols, ld
 
 
@@ -164,7 +164,8 @@ def _order(order, tokens=None):
     _int32(source, "source")
     if position.dim() != 2 or source.dim() != 1:
         raise ValueError("position must be tokens x choices and source one row number per row")
-    _fits("the order", *position.shape, source.shape[0])
+    if position.shape[0] > _INT or position.shape[1] > _INT or source.shape[0] > _INT:
+        _too_large("the order")
     if tokens is not None and position.shape[0] != tokens:
         raise ValueError(f"the order is of {position.shape[0]} tokens, not of {tokens}")
     return position, source
@@ -365,7 +366,8 @@ def sort_by_expert(ids, experts: int, align: int = 1, stream=None) -> ExpertOrde
     tokens, top = ids.shape
     slots = tokens * top
     rows = (slots + min(experts, slots) * (align - 1)) // align * align
-    _fits("the order", tokens, top, rows)
+    if tokens > _INT or top > _INT or rows > _INT:
+        _too_large("the order")
     device = _device(stream, "ids", ids)
     with _on(stream):
         offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
