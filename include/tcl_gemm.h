@@ -106,9 +106,10 @@ typedef enum {
     TCL_ERR_DEVICE = 10,         /* current device is not an sm_103 GPU */
     TCL_ERR_STATIC_LIMIT = 11,   /* gemm_s8_static: the problem needs more scratch than the fixed
                                     TCL_S8_STATIC_SCRATCH_BYTES buffer holds */
-    TCL_ERR_CAPTURE = 12         /* the call needs more library scratch than is allocated while its
+    TCL_ERR_CAPTURE = 12,        /* the call needs more library scratch than is allocated while its
                                     stream is being captured into a CUDA graph: run it (or a larger
                                     one) once outside capture first */
+    TCL_ERR_WORKSPACE = 13       /* tcl_dense.h: the call needs a larger workspace than it was given */
 } tcl_status;
 
 typedef enum { TCL_OUT_F32 = 0, TCL_OUT_BF16 = 1 } tcl_out_t;

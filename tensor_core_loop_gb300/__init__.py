@@ -26,6 +26,7 @@ STATUS = {
     0: "TCL_OK", 1: "TCL_ERR_NULL", 2: "TCL_ERR_DIMS", 3: "TCL_ERR_LD", 4: "TCL_ERR_ALIGN",
     5: "TCL_ERR_K_TOO_LARGE", 6: "TCL_ERR_LAUNCH", 7: "TCL_ERR_DEVICE_TIMEOUT", 8: "TCL_ERR_CONFIG",
     9: "TCL_ERR_NO_MEMORY", 10: "TCL_ERR_DEVICE", 11: "TCL_ERR_STATIC_LIMIT", 12: "TCL_ERR_CAPTURE",
+    13: "TCL_ERR_WORKSPACE",
 }
 OUT_F32, OUT_BF16 = 0, 1
 PRODUCER_TMA, PRODUCER_SYNC, PRODUCER_CPASYNC = 0, 1, 2
@@ -343,3 +344,9 @@ from .fp8 import (EXPORTED_SYMBOLS_FP8, ExpertOrder, combine, combine_grad, gath
 
 __all__ += ["quantize_fp8", "gemm_fp8", "gemm_fp8_experts", "gemm_fp8_experts_wgrad", "sort_by_expert", "ExpertOrder",
             "gather_rows", "combine", "combine_grad", "EXPORTED_SYMBOLS_FP8"]
+
+from .dense import (EXPORTED_SYMBOLS_DENSE, GatedFfnKept, clip_grads, cross_entropy, cross_entropy_grad,  # noqa: E402
+                    gated_ffn, gated_ffn_grad, grad_norm)
+
+__all__ += ["gated_ffn", "gated_ffn_grad", "GatedFfnKept", "cross_entropy", "cross_entropy_grad", "grad_norm", "clip_grads",
+            "EXPORTED_SYMBOLS_DENSE"]

@@ -1497,6 +1497,19 @@ int tensor_map_bytes(const void* ptr, uint64_t k, uint64_t rows, uint64_t mats, 
     return encode_3d(CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, k, rows, mats, row_stride, mat_stride, 128, box_rows, out);
 }
 
+int tensor_map_bf16(const void* ptr, uint64_t cols, uint64_t rows, uint64_t row_bytes, uint32_t box_rows, CUtensorMap* out) {
+    int st = encode_fn();
+    if (st) return st;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? TCL_OK : TCL_ERR_LAUNCH;
+}
+
 int tensor_map_result(const void* ptr, int bf16, uint64_t cols, uint64_t rows, uint64_t mats, uint64_t row_stride,
                       uint64_t mat_stride, CUtensorMap* out) {
     return encode_3d(bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ptr, cols, rows, mats,
@@ -1640,6 +1653,7 @@ const char* tcl_status_string(int status) {
         case TCL_ERR_DEVICE: return "current device is not an sm_103 GPU";
         case TCL_ERR_STATIC_LIMIT: return "problem needs more scratch than the fixed static buffer holds";
         case TCL_ERR_CAPTURE: return "scratch would have to grow while the stream is being captured";
+        case TCL_ERR_WORKSPACE: return "the call needs a larger workspace";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,693 @@
+// C ABI of the gated feed-forward block, of the cross entropy over a vocabulary and of the
+// gradients' norm and clipping (declared in include/tcl_dense.h): argument checks, the workspace's
+// layout, the choice of kernels, and the launches.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "clip_launch.cuh"
+#include "dense_launch.cuh"
+#include "tcl_dense.h"
+
+namespace tcl {
+namespace {
+
+typedef __nv_bfloat16 bf16;
+
+constexpr unsigned long long kTimeoutNs = 1000000000ull;   // bound on every in-kernel wait: 1 s
+constexpr int kMostSize = 0x7ffeffff;                       // sizes are rounded up to whole tiles in 32 bits
+constexpr int kMostFew = 64;                                // tokens of the kernel for few of them
+constexpr long long kExpBytes = 1ll << 31;                  // exponentials kept at a time
+
+bool width(int n) { return n >= 1 && n <= kMostSize; }
+bool on(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+long long up(long long x, long long m) { return (x + m - 1) / m * m; }
+int tiles_of(int n, int tile) { return static_cast<int>((static_cast<long long>(n) + tile - 1) / tile); }
+long long blocks64(long long k) { return (k + 63) / 64; }
+
+int status_of(cudaError_t err) {
+    if (err == cudaSuccess) return TCL_OK;
+    cudaGetLastError();
+    return err == cudaErrorInvalidValue ? TCL_ERR_DIMS : TCL_ERR_LAUNCH;
+}
+
+// A stored matrix: rows of cols values.
+struct Mat {
+    const bf16* p;
+    long long ld;
+    int rows, cols;
+    bool copy() const { return !on(p, 16) || (rows > 1 && ld % 8); }
+};
+
+// The workspace, dealt out in 256-byte steps. Planning goes past its end; nothing is launched then.
+struct Room {
+    uint8_t* base;
+    size_t have, used = 0;
+    DenseCopies copies = {};
+    template <typename T>
+    T* take(long long n) {
+        T* p = reinterpret_cast<T*>(base + used);
+        used += static_cast<size_t>(up(n * static_cast<long long>(sizeof(T)), 256));
+        return p;
+    }
+    // An operand as the tensor copies can read it.
+    Mat operand(const void* p, long long ld, int rows, int cols) {
+        Mat m = {static_cast<const bf16*>(p), rows > 1 ? ld : up(cols, 8), rows, cols};
+        if (!m.copy()) return m;
+        const long long pitch = up(cols, 8);
+        bf16* to = take<bf16>(pitch * rows);
+        copies.job[copies.n++] = {m.p, ld, rows, cols, to};
+        return {to, pitch, rows, cols};
+    }
+};
+
+int enough(const Room& room, size_t* workspace_bytes) {
+    if (room.used <= room.have) return TCL_OK;
+    *workspace_bytes = room.used;
+    return TCL_ERR_WORKSPACE;
+}
+
+struct Gpu {
+    int sms;
+    unsigned int* status;
+    cudaStream_t stream;
+};
+
+int gpu_of(cudaStream_t stream, Gpu* g) {
+    int dev;
+    g->stream = stream;
+    return device_context(&dev, &g->sms, &g->status);
+}
+
+// K ranges of a product of `tiles` 256 × 256 tiles with kb k-blocks: as many as make the GPU's pairs
+// of SMs finish together, if what the ranges' sums cost in memory is less than the time that saves.
+// Microseconds, measured on a GB300: 0.28 a k-block, 3 a tile, 5 TB/s and 3 us for joining the sums.
+int choose_splits(long long tiles, long long kb, int M, int N, int sms) {
+    const long long pairs = sms / 2;
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= 32 && s <= kb; ++s) {
+        const double waves = static_cast<double>((tiles * s + pairs - 1) / pairs);
+        double us = waves * (0.28 * static_cast<double>((kb + s - 1) / s) + 3.0);
+        if (s > 1) us += 3.0 + 8.0 * s * M * static_cast<double>(N) / 5e6;
+        if (s == 1 || us < 0.97 * least) {
+            best = s;
+            least = us;
+        }
+    }
+    return best;
+}
+
+// D = A·B^T over one operand pair or two; `mn`: the operand's rows (not K) are contiguous in memory.
+struct Product {
+    Mat a, b, a1, b1;
+    bool a_mn, b_mn, two;
+    int M, N, f32;
+    void* out;
+    long long ldo;
+    const float* factor;
+    const float* plus;
+    long long ld_plus;
+    int splits;
+    float* parts;
+};
+
+long long k_of(const Mat& m, bool mn) { return mn ? m.rows : m.cols; }
+
+void plan(Room& room, Product& q, const Gpu& g) {
+    const long long kb = blocks64(k_of(q.a, q.a_mn)) + (q.two ? blocks64(k_of(q.a1, q.a_mn)) : 0);
+    q.splits = choose_splits(static_cast<long long>(tiles_of(q.M, 256)) * tiles_of(q.N, 256), kb, q.M, q.N, g.sms);
+    q.parts = q.splits > 1 ? room.take<float>(static_cast<long long>(q.splits) * q.M * up(q.N, 4)) : nullptr;
+}
+
+int map_of(const Mat& m, bool mn, CUtensorMap* out) {
+    return tensor_map_bf16(m.p, m.cols, m.rows, m.ld * 2, mn ? 64 : 128, out);
+}
+
+int map_out(const DenseOut& o, int f32, int rows, int mats, CUtensorMap* out) {
+    if (!o.tma) return TCL_OK;
+    const long long row = up(o.ld * (f32 ? 4 : 2), 16);   // (a single row never steps to a second one)
+    return tensor_map_result(o.p, !f32, o.cols, rows, mats, row, row * rows, out);
+}
+
+DenseOut result(void* p, long long ld, int cols, int rows, int f32) {
+    return {p, ld, cols, on(p, 16) && (rows == 1 || ld * (f32 ? 4 : 2) % 16 == 0)};
+}
+
+int launch_pairs(DenseLaunch& l, const Gpu& g) {
+    DenseParams& p = l.p;
+    p.group = 8;
+    p.timeout_ns = kTimeoutNs;
+    p.status = g.status;
+    const long long units = static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits;
+    if (units > 0x3fffffffll) return TCL_ERR_DIMS;
+    l.grid = static_cast<int>(std::min<long long>(g.sms / 2, units)) * 2;
+    l.stream = g.stream;
+    return status_of(launch_dense_pair(l));
+}
+
+int run(const Product& q, const Gpu& g) {
+    DenseLaunch l = {};
+    l.end = DenseEnd::STORE;
+    l.a_mn = q.a_mn;
+    l.b_mn = q.b_mn;
+    int st;
+    if ((st = map_of(q.a, q.a_mn, &l.a[0])) || (st = map_of(q.b, q.b_mn, &l.b[0]))) return st;
+    if (q.two && ((st = map_of(q.a1, q.a_mn, &l.a[1])) || (st = map_of(q.b1, q.b_mn, &l.b[1])))) return st;
+    DenseParams& p = l.p;
+    p.M = q.M;
+    p.N = q.N;
+    p.kb0 = static_cast<int>(blocks64(k_of(q.a, q.a_mn)));
+    p.kb1 = q.two ? static_cast<int>(blocks64(k_of(q.a1, q.a_mn))) : 0;
+    p.tiles_m = tiles_of(q.M, 256);
+    p.tiles_n = tiles_of(q.N, 256);
+    p.splits = q.splits;
+    const long long pitch = up(q.N, 4);
+    if (q.splits > 1) {
+        p.f32 = 1;
+        p.out[0] = {q.parts, pitch, static_cast<int>(pitch), 1};
+    } else {
+        p.f32 = q.f32;
+        p.out[0] = result(q.out, q.ldo, q.N, q.M, q.f32);
+        p.factor = q.factor;
+        p.plus = q.plus;
+        p.ld_plus = q.ld_plus;
+    }
+    if ((st = map_out(p.out[0], p.f32, q.M, q.splits, &l.c[0]))) return st;
+    if ((st = launch_pairs(l, g)) || q.splits == 1) return st;
+    return status_of(launch_dense_join({q.parts, pitch, pitch * q.M, q.splits, q.M, q.N, q.f32, q.factor, q.plus, q.ld_plus,
+                                        q.out, q.ldo},
+                                       g.stream));
+}
+
+// ------------------------------------------------------------------ few tokens
+
+int launch_few(DenseEnd end, const Mat& x, const Mat& w0, const Mat* w1, DenseFewParams p, const Gpu& g) {
+    DenseFewLaunch l = {};
+    l.end = end;
+    l.bq = p.T <= 16 ? 16 : p.T <= 32 ? 32 : 64;
+    int st;
+    if ((st = tensor_map_bf16(x.p, x.cols, x.rows, x.ld * 2, l.bq, &l.x)) || (st = map_of(w0, false, &l.w[0]))) return st;
+    if (w1 && (st = map_of(*w1, false, &l.w[1]))) return st;
+    p.N = w0.rows;
+    p.num_kb = static_cast<int>(blocks64(w0.cols));
+    p.tiles = tiles_of(w0.rows, 128);
+    p.timeout_ns = kTimeoutNs;
+    p.status = g.status;
+    // share tiles while every CTA has a place and two k-blocks or more
+    const int places = g.sms * dense_few_per_sm(l.bq);
+    p.split = 1;
+    while (p.split < 8 && static_cast<long long>(p.tiles) * p.split * 2 <= places && p.num_kb >= p.split * 4) p.split *= 2;
+    l.p = p;
+    l.grid = std::min(places / p.split, p.tiles) * p.split;
+    l.stream = g.stream;
+    return status_of(launch_dense_few(l));
+}
+
+// ------------------------------------------------------------------ the feed-forward block
+
+struct Ffn {
+    int T, H, F, act;
+    Mat x, wg, wu, wd;
+};
+
+int ffn_sizes(int tokens, int hidden, int inner, int act) {
+    if (tokens < 0 || tokens > kMostSize || !width(hidden) || !width(inner)) return TCL_ERR_DIMS;
+    return act < 0 || act > 2 ? TCL_ERR_CONFIG : TCL_OK;
+}
+
+int gate_pairs(const Ffn& f, bf16* gate, bf16* upp, bf16* h, long long ldk, const Gpu& g) {
+    DenseLaunch l = {};
+    l.end = DenseEnd::GATE;
+    int st;
+    if ((st = map_of(f.x, false, &l.a[0])) || (st = map_of(f.wg, false, &l.b[0])) || (st = map_of(f.wu, false, &l.b[1]))) return st;
+    DenseParams& p = l.p;
+    p.M = f.T;
+    p.N = f.F;
+    p.kb0 = static_cast<int>(blocks64(f.H));
+    p.tiles_m = tiles_of(f.T, 256);
+    p.tiles_n = tiles_of(f.F, 128);
+    p.splits = 1;
+    p.act = f.act;
+    void* const to[3] = {h, gate, upp};
+    for (int i = 0; i < (gate ? 3 : 1); ++i) {
+        p.out[i] = {to[i], ldk, static_cast<int>(up(f.F, 8)), 1};
+        if ((st = map_out(p.out[i], 0, f.T, 1, &l.c[i]))) return st;
+    }
+    return launch_pairs(l, g);
+}
+
+int gate_grad(const Ffn& f, const Mat& grad, const bf16* gate, const bf16* upp, long long ldk, bf16* dg, bf16* du,
+              long long ldd, const Gpu& g) {
+    DenseLaunch l = {};
+    l.end = DenseEnd::GATE_GRAD;
+    l.b_mn = 1;
+    int st;
+    if ((st = map_of(grad, false, &l.a[0])) || (st = map_of(f.wd, true, &l.b[0]))) return st;
+    DenseParams& p = l.p;
+    p.M = f.T;
+    p.N = f.F;
+    p.kb0 = static_cast<int>(blocks64(f.H));
+    p.tiles_m = tiles_of(f.T, 256);
+    p.tiles_n = tiles_of(f.F, 256);
+    p.splits = 1;
+    p.act = f.act;
+    p.gate = gate;
+    p.up = upp;
+    p.ld_kept = ldk;
+    bf16* const to[2] = {dg, du};
+    for (int i = 0; i < 2; ++i) {
+        p.out[i] = {to[i], ldd, static_cast<int>(up(f.F, 8)), 1};
+        if ((st = map_out(p.out[i], 0, f.T, 1, &l.c[i]))) return st;
+    }
+    return launch_pairs(l, g);
+}
+
+int zeros(void* p, long long ld, int rows, int cols, int f32, cudaStream_t stream) {
+    const size_t es = f32 ? 4 : 2;
+    return status_of(cudaMemset2DAsync(p, ld * es, 0, cols * es, rows, stream));
+}
+
+// ------------------------------------------------------------------ the cross entropy
+
+struct Entropy {
+    int T, H, V;
+    Mat x, w;
+    const void* targets;
+    int target_bytes;
+    float *loss, *lse;
+};
+
+int entropy_checks(int tokens, int hidden, int vocab, const void* X, int ldx, const void* W, int ldw, const void* targets,
+                   int target_bytes, const float* loss, const float* lse) {
+    if (tokens < 0 || tokens > kMostSize || !width(hidden) || !width(vocab)) return TCL_ERR_DIMS;
+    if (target_bytes != 4 && target_bytes != 8) return TCL_ERR_CONFIG;
+    if (tokens && (!X || !W || !targets || !loss || !lse)) return TCL_ERR_NULL;
+    if (ldx < hidden || ldw < hidden) return TCL_ERR_LD;
+    if (!on(X, 2) || !on(W, 2) || !on(targets, target_bytes) || !on(loss, 4) || !on(lse, 4)) return TCL_ERR_ALIGN;
+    return TCL_OK;
+}
+
+// The logits of rows [t0, t0 + rows) and what is kept of them; e NULL: sums alone.
+int entropy_pairs(const Entropy& n, int t0, int rows, bf16* e, long long lde, float2* parts, float* target_logit, const Gpu& g) {
+    DenseLaunch l = {};
+    l.end = DenseEnd::ENTROPY;
+    const Mat x = {n.x.p + t0 * n.x.ld, n.x.ld, rows, n.H};
+    int st;
+    if ((st = map_of(x, false, &l.a[0])) || (st = map_of(n.w, false, &l.b[0]))) return st;
+    DenseParams& p = l.p;
+    p.M = rows;
+    p.N = n.V;
+    p.kb0 = static_cast<int>(blocks64(n.H));
+    p.tiles_m = tiles_of(rows, 256);
+    p.tiles_n = tiles_of(n.V, 256);
+    p.splits = 1;
+    p.targets = static_cast<const uint8_t*>(n.targets) + static_cast<long long>(t0) * n.target_bytes;
+    p.wide_targets = n.target_bytes == 8;
+    p.parts = parts;
+    p.target_logit = target_logit;
+    p.exps = e != nullptr;
+    if (e) {
+        p.out[0] = {e, lde, static_cast<int>(up(n.V, 8)), 1};
+        if ((st = map_out(p.out[0], 0, rows, 1, &l.c[0]))) return st;
+    }
+    return launch_pairs(l, g);
+}
+
+EntropyRows entropy_rows(const Entropy& n, int t0, int rows, int chunks, const float2* parts, const float* target_logit) {
+    EntropyRows r = {};
+    r.parts = parts;
+    r.chunks = chunks;
+    r.rows = rows;
+    r.vocab = n.V;
+    r.target_logit = target_logit;
+    r.targets = static_cast<const uint8_t*>(n.targets) + static_cast<long long>(t0) * n.target_bytes;
+    r.wide_targets = n.target_bytes == 8;
+    r.loss = n.loss + t0;
+    r.lse = n.lse + t0;
+    return r;
+}
+
+// ------------------------------------------------------------------ clipping
+
+int clip_checks(int count, const void* const* from, const long long* lengths, const int* types, const float* norm) {
+    if (count < 0) return TCL_ERR_DIMS;
+    if (!norm || (count && (!from || !lengths || !types))) return TCL_ERR_NULL;
+    if (!on(norm, 4)) return TCL_ERR_ALIGN;
+    for (int i = 0; i < count; ++i) {
+        if (types[i] != TCL_OUT_F32 && types[i] != TCL_OUT_BF16) return TCL_ERR_CONFIG;
+        if (lengths[i] < 0 || lengths[i] > (1ll << 48)) return TCL_ERR_DIMS;
+        if (lengths[i] && !from[i]) return TCL_ERR_NULL;
+        if (!on(from[i], types[i] == TCL_OUT_F32 ? 4 : 2)) return TCL_ERR_ALIGN;
+    }
+    return TCL_OK;
+}
+
+// Calls f with one launch's tensors after another's: those of one type, kClipTensors at most.
+template <class F>
+int each_launch(int count, const void* const* from, void* const* to, const long long* lengths, const int* types, F f) {
+    long long total = 0;
+    for (int i = 0; i < count; ++i) total += lengths[i];
+    // pieces that give every block several, but at least 4096 elements
+    const long long piece = std::min(65536ll, std::max(4096ll, total / (4 * kClipBlocks) / 4096 * 4096));
+    for (int f32 = 0; f32 < 2; ++f32) {
+        ClipTensors a;
+        a.n = 0;
+        a.f32 = f32;
+        a.piece = static_cast<int>(piece);
+        a.pieces = 0;
+        for (int i = 0; i <= count; ++i) {
+            if (a.n == kClipTensors || (i == count && a.n)) {
+                if (const int st = f(a)) return st;
+                a.n = 0;
+                a.pieces = 0;
+            }
+            if (i == count || (types[i] == TCL_OUT_F32) != f32 || lengths[i] == 0) continue;
+            a.t[a.n++] = {from[i], to ? to[i] : nullptr, lengths[i], a.pieces};
+            a.pieces += (lengths[i] + piece - 1) / piece;
+        }
+    }
+    return TCL_OK;
+}
+
+}  // namespace
+}  // namespace tcl
+
+using namespace tcl;
+
+extern "C" {
+
+int tcl_gated_ffn(int tokens, int hidden, int inner, const void* X, int ldx, const void* Wgate, int ld_gate, const void* Wup,
+                  int ld_up, const void* Wdown, int ld_down, int act, void* gate, void* upp, void* h, int ld_kept, void* out,
+                  int ldo, void* workspace, size_t* workspace_bytes, cudaStream_t stream) {
+    if (const int st = ffn_sizes(tokens, hidden, inner, act)) return st;
+    if (!workspace_bytes || (*workspace_bytes && !workspace)) return TCL_ERR_NULL;
+    if (tokens && (!X || !Wgate || !Wup || !Wdown || !h || !out || !gate != !upp)) return TCL_ERR_NULL;
+    if (ldx < hidden || ld_gate < hidden || ld_up < hidden || ld_down < inner || ldo < hidden || ld_kept < inner || ld_kept % 8)
+        return TCL_ERR_LD;
+    if (!on(X, 2) || !on(Wgate, 2) || !on(Wup, 2) || !on(Wdown, 2) || !on(out, 2) || !on(gate, 16) || !on(upp, 16) ||
+        !on(h, 16) || !on(workspace, 256))
+        return TCL_ERR_ALIGN;
+    Gpu g;
+    if (const int st = gpu_of(stream, &g)) return st;
+    if (tokens == 0) return TCL_OK;
+    Room room{static_cast<uint8_t*>(workspace), *workspace_bytes};
+    Ffn f = {tokens, hidden, inner, act, room.operand(X, ldx, tokens, hidden), room.operand(Wgate, ld_gate, inner, hidden),
+             room.operand(Wup, ld_up, inner, hidden), room.operand(Wdown, ld_down, hidden, inner)};
+    const Mat kept = {static_cast<const bf16*>(h), ld_kept, tokens, inner};
+    Product q = {};
+    q.a = kept;
+    q.b = f.wd;
+    q.M = tokens;
+    q.N = hidden;
+    q.out = out;
+    q.ldo = ldo;
+    if (tokens > kMostFew) plan(room, q, g);
+    if (const int st = enough(room, workspace_bytes)) return st;
+    const auto lock = library_lock();
+    int st;
+    if (room.copies.n && (st = status_of(launch_dense_copies(room.copies, stream)))) return st;
+    if (tokens > kMostFew) {
+        if ((st = gate_pairs(f, static_cast<bf16*>(gate), static_cast<bf16*>(upp), static_cast<bf16*>(h), ld_kept, g))) return st;
+        return run(q, g);
+    }
+    DenseFewParams p = {};
+    p.T = tokens;
+    p.act = act;
+    p.out[0] = {h, ld_kept, 0, 0};
+    p.out[1] = {gate, ld_kept, 0, 0};
+    p.out[2] = {upp, ld_kept, 0, 0};
+    if ((st = launch_few(DenseEnd::GATE, f.x, f.wg, &f.wu, p, g))) return st;
+    p.out[0] = {out, ldo, 0, 0};
+    return launch_few(DenseEnd::STORE, kept, f.wd, nullptr, p, g);
+}
+
+int tcl_gated_ffn_grad(int tokens, int hidden, int inner, const void* grad, int ld_grad, const void* X, int ldx,
+                       const void* Wgate, int ld_gate, const void* Wup, int ld_up, const void* Wdown, int ld_down, int act,
+                       const void* gate, const void* upp, const void* h, int ld_kept, void* dX, int ld_dx, void* dWgate,
+                       int ld_dgate, void* dWup, int ld_dup, void* dWdown, int ld_ddown, int w_type, void* workspace,
+                       size_t* workspace_bytes, cudaStream_t stream) {
+    if (const int st = ffn_sizes(tokens, hidden, inner, act)) return st;
+    if (w_type != TCL_OUT_F32 && w_type != TCL_OUT_BF16) return TCL_ERR_CONFIG;
+    if (!workspace_bytes || (*workspace_bytes && !workspace) || !dWgate || !dWup || !dWdown) return TCL_ERR_NULL;
+    if (tokens && (!grad || !X || !Wgate || !Wup || !Wdown || !gate || !upp || !h || !dX)) return TCL_ERR_NULL;
+    if (ldx < hidden || ld_grad < hidden || ld_gate < hidden || ld_up < hidden || ld_down < inner || ld_dx < hidden ||
+        ld_dgate < hidden || ld_dup < hidden || ld_ddown < inner || ld_kept < inner || ld_kept % 8)
+        return TCL_ERR_LD;
+    const int f32 = w_type == TCL_OUT_F32, es = f32 ? 4 : 2;
+    if (!on(grad, 2) || !on(X, 2) || !on(Wgate, 2) || !on(Wup, 2) || !on(Wdown, 2) || !on(dX, 2) || !on(dWgate, es) ||
+        !on(dWup, es) || !on(dWdown, es) || !on(gate, 16) || !on(upp, 16) || !on(h, 16) || !on(workspace, 256))
+        return TCL_ERR_ALIGN;
+    Gpu g;
+    int st;
+    if ((st = gpu_of(stream, &g))) return st;
+    if (tokens == 0) {
+        if ((st = zeros(dWgate, ld_dgate, inner, hidden, f32, stream)) || (st = zeros(dWup, ld_dup, inner, hidden, f32, stream)))
+            return st;
+        return zeros(dWdown, ld_ddown, hidden, inner, f32, stream);
+    }
+    Room room{static_cast<uint8_t*>(workspace), *workspace_bytes};
+    Ffn f = {tokens, hidden, inner, act, room.operand(X, ldx, tokens, hidden), room.operand(Wgate, ld_gate, inner, hidden),
+             room.operand(Wup, ld_up, inner, hidden), room.operand(Wdown, ld_down, hidden, inner)};
+    const Mat gr = room.operand(grad, ld_grad, tokens, hidden);
+    const Mat kept = {static_cast<const bf16*>(h), ld_kept, tokens, inner};
+    const long long ldd = up(inner, 8);
+    bf16* dg = room.take<bf16>(ldd * tokens);
+    bf16* du = room.take<bf16>(ldd * tokens);
+    const Mat mg = {dg, ldd, tokens, inner}, mu = {du, ldd, tokens, inner};
+    Product q[4] = {};
+    // dX = dgate·Wgate + dup·Wup: one product over both
+    q[0].a = mg;
+    q[0].b = f.wg;
+    q[0].a1 = mu;
+    q[0].b1 = f.wu;
+    q[0].two = q[0].b_mn = true;
+    q[0].M = tokens;
+    q[0].N = hidden;
+    q[0].out = dX;
+    q[0].ldo = ld_dx;
+    const Mat left[3] = {mg, mu, gr}, right[3] = {f.x, f.x, kept};
+    void* const to[3] = {dWgate, dWup, dWdown};
+    const int ld[3] = {ld_dgate, ld_dup, ld_ddown};
+    for (int i = 0; i < 3; ++i) {
+        Product& w = q[i + 1];
+        w.a = left[i];
+        w.b = right[i];
+        w.a_mn = w.b_mn = true;
+        w.M = left[i].cols;
+        w.N = right[i].cols;
+        w.f32 = f32;
+        w.out = to[i];
+        w.ldo = ld[i];
+    }
+    // (the products follow one another: they share the room for their sums)
+    size_t most = room.used;
+    for (Product& w : q) {
+        const size_t at = room.used;
+        plan(room, w, g);
+        most = std::max(most, room.used);
+        room.used = at;
+    }
+    room.used = most;
+    if ((st = enough(room, workspace_bytes))) return st;
+    const auto lock = library_lock();
+    if (room.copies.n && (st = status_of(launch_dense_copies(room.copies, stream)))) return st;
+    if ((st = gate_grad(f, gr, static_cast<const bf16*>(gate), static_cast<const bf16*>(upp), ld_kept, dg, du, ldd, g))) return st;
+    for (const Product& w : q)
+        if ((st = run(w, g))) return st;
+    return TCL_OK;
+}
+
+int tcl_cross_entropy(int tokens, int hidden, int vocab, const void* X, int ldx, const void* W, int ldw, const void* targets,
+                      int target_bytes, float* loss, float* lse, void* workspace, size_t* workspace_bytes,
+                      cudaStream_t stream) {
+    if (const int st = entropy_checks(tokens, hidden, vocab, X, ldx, W, ldw, targets, target_bytes, loss, lse)) return st;
+    if (!workspace_bytes || (*workspace_bytes && !workspace)) return TCL_ERR_NULL;
+    if (!on(workspace, 256)) return TCL_ERR_ALIGN;
+    Gpu g;
+    int st;
+    if ((st = gpu_of(stream, &g))) return st;
+    if (tokens == 0) return TCL_OK;
+    Room room{static_cast<uint8_t*>(workspace), *workspace_bytes};
+    const Entropy n = {tokens, hidden, vocab, room.operand(X, ldx, tokens, hidden), room.operand(W, ldw, vocab, hidden), targets,
+                       target_bytes, loss, lse};
+    const bool few = tokens <= kMostFew;
+    const int chunks = tiles_of(vocab, few ? 32 : 128);
+    float2* parts = room.take<float2>(static_cast<long long>(chunks) * tokens);
+    float* target_logit = room.take<float>(tokens);
+    if ((st = enough(room, workspace_bytes))) return st;
+    const auto lock = library_lock();
+    if (room.copies.n && (st = status_of(launch_dense_copies(room.copies, stream)))) return st;
+    if (few) {
+        DenseFewParams p = {};
+        p.T = tokens;
+        p.targets = targets;
+        p.wide_targets = target_bytes == 8;
+        p.parts = parts;
+        p.target_logit = target_logit;
+        st = launch_few(DenseEnd::ENTROPY, n.x, n.w, nullptr, p, g);
+    } else {
+        st = entropy_pairs(n, 0, tokens, nullptr, 0, parts, target_logit, g);
+    }
+    if (st) return st;
+    return status_of(launch_entropy_rows(entropy_rows(n, 0, tokens, chunks, parts, target_logit), stream));
+}
+
+int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int ldx, const void* W, int ldw,
+                           const void* targets, int target_bytes, const float* grad, float* loss, float* lse, void* dX,
+                           int ld_dx, void* dW, int ld_dw, int w_type, void* workspace, size_t* workspace_bytes,
+                           cudaStream_t stream) {
+    if (const int st = entropy_checks(tokens, hidden, vocab, X, ldx, W, ldw, targets, target_bytes, loss, lse)) return st;
+    if (w_type != TCL_OUT_F32 && w_type != TCL_OUT_BF16) return TCL_ERR_CONFIG;
+    if (!workspace_bytes || (*workspace_bytes && !workspace) || !dW || (tokens && (!grad || !dX))) return TCL_ERR_NULL;
+    if (ld_dx < hidden || ld_dw < hidden) return TCL_ERR_LD;
+    const int f32 = w_type == TCL_OUT_F32;
+    if (!on(grad, 4) || !on(dX, 2) || !on(dW, f32 ? 4 : 2) || !on(workspace, 256)) return TCL_ERR_ALIGN;
+    Gpu g;
+    int st;
+    if ((st = gpu_of(stream, &g))) return st;
+    if (tokens == 0) return zeros(dW, ld_dw, vocab, hidden, f32, stream);
+    Room room{static_cast<uint8_t*>(workspace), *workspace_bytes};
+    const Entropy n = {tokens, hidden, vocab, room.operand(X, ldx, tokens, hidden), room.operand(W, ldw, vocab, hidden), targets,
+                       target_bytes, loss, lse};
+    // tokens of a piece: whole tiles, pieces of one size
+    const long long lde = up(vocab, 8), most = std::max(256ll, kExpBytes / (2 * lde) / 256 * 256);
+    const int pieces = static_cast<int>((tokens + most - 1) / most);
+    const int piece = static_cast<int>(std::min<long long>(tokens, up((tokens + pieces - 1) / pieces, 256)));
+    const int chunks = tiles_of(vocab, 128);
+    const long long ldh = up(hidden, 8);
+    bf16* e = room.take<bf16>(lde * piece);
+    float2* parts = room.take<float2>(static_cast<long long>(chunks) * piece);
+    float* target_logit = room.take<float>(piece);
+    float* factor = room.take<float>(piece);
+    bf16* scaled = room.take<bf16>(ldh * piece);
+    const long long ld_sum = up(hidden, 4);
+    float* sum = piece < tokens ? room.take<float>(ld_sum * vocab) : nullptr;   // of the pieces' dW
+    auto products = [&](int t0, int rows, Product (&q)[2]) {
+        q[0] = {};
+        q[0].a = {e, lde, rows, vocab};
+        q[0].b = n.w;
+        q[0].b_mn = true;
+        q[0].M = rows;
+        q[0].N = hidden;
+        q[0].out = static_cast<bf16*>(dX) + static_cast<long long>(t0) * ld_dx;
+        q[0].ldo = ld_dx;
+        q[0].factor = factor;
+        const bool last = t0 + rows == tokens;
+        q[1] = {};
+        q[1].a = {e, lde, rows, vocab};
+        q[1].b = {scaled, ldh, rows, hidden};
+        q[1].a_mn = q[1].b_mn = true;
+        q[1].M = vocab;
+        q[1].N = hidden;
+        q[1].f32 = last ? f32 : 1;
+        q[1].out = last ? dW : sum;
+        q[1].ldo = last ? ld_dw : ld_sum;
+        q[1].plus = t0 ? sum : nullptr;
+        q[1].ld_plus = ld_sum;
+    };
+    // room for the products' sums: one piece's product after another's, the last piece may be the shorter one
+    const size_t at = room.used;
+    size_t end = at;
+    for (int i = 0; i < 2; ++i) {
+        const int t0 = i ? tokens - 1 - (tokens - 1) % piece : 0;
+        Product q[2];
+        products(t0, std::min(piece, tokens - t0), q);
+        for (Product& w : q) {
+            plan(room, w, g);
+            end = std::max(end, room.used);
+            room.used = at;
+        }
+    }
+    room.used = end;
+    if ((st = enough(room, workspace_bytes))) return st;
+    const auto lock = library_lock();
+    if (room.copies.n && (st = status_of(launch_dense_copies(room.copies, stream)))) return st;
+    for (int t0 = 0; t0 < tokens; t0 += piece) {
+        const int rows = std::min(piece, tokens - t0);
+        if ((st = entropy_pairs(n, t0, rows, e, lde, parts, target_logit, g))) return st;
+        EntropyRows r = entropy_rows(n, t0, rows, chunks, parts, target_logit);
+        r.grad = grad + t0;
+        r.e = e;
+        r.ld_e = lde;
+        r.factor = factor;
+        r.x = n.x.p + t0 * n.x.ld;
+        r.ld_x = n.x.ld;
+        r.scaled = scaled;
+        r.ld_scaled = ldh;
+        r.hidden = hidden;
+        if ((st = status_of(launch_entropy_rows(r, stream)))) return st;
+        Product q[2];
+        products(t0, rows, q);
+        for (Product& w : q) {
+            room.used = at;
+            plan(room, w, g);
+            if ((st = run(w, g))) return st;
+        }
+    }
+    return TCL_OK;
+}
+
+int tcl_grad_norm(int count, const void* const* tensors, const long long* lengths, const int* types, float* norm,
+                  void* workspace, size_t* workspace_bytes, cudaStream_t stream) {
+    if (const int st = clip_checks(count, tensors, lengths, types, norm)) return st;
+    if (!workspace_bytes || (*workspace_bytes && !workspace)) return TCL_ERR_NULL;
+    if (!on(workspace, 256)) return TCL_ERR_ALIGN;
+    Gpu g;
+    if (const int st = gpu_of(stream, &g)) return st;
+    int blocks = 0;
+    each_launch(count, tensors, nullptr, lengths, types, [&](const ClipTensors& a) {
+        blocks += clip_blocks(a.pieces);
+        return TCL_OK;
+    });
+    Room room{static_cast<uint8_t*>(workspace), *workspace_bytes};
+    double* parts = room.take<double>(blocks);
+    if (const int st = enough(room, workspace_bytes)) return st;
+    int at = 0;
+    const int st = each_launch(count, tensors, nullptr, lengths, types, [&](const ClipTensors& a) {
+        const int mine = at;
+        at += clip_blocks(a.pieces);
+        return status_of(launch_square_sums(a, parts + mine, stream));
+    });
+    return st ? st : status_of(launch_norm(parts, blocks, norm, stream));
+}
+
+int tcl_clip_gradients(int count, const void* const* from, void* const* to, const long long* lengths, const int* types,
+                       float bound, float* norm, void* workspace, size_t* workspace_bytes, cudaStream_t stream) {
+    if (const int st = clip_checks(count, from, lengths, types, norm)) return st;
+    if (!(bound >= 0.0f)) return TCL_ERR_CONFIG;
+    if (!workspace_bytes || (*workspace_bytes && !workspace) || (count && !to)) return TCL_ERR_NULL;
+    if (!on(workspace, 256)) return TCL_ERR_ALIGN;
+    for (int i = 0; i < count; ++i) {
+        if (lengths[i] && !to[i]) return TCL_ERR_NULL;
+        if (!on(to[i], types[i] == TCL_OUT_F32 ? 4 : 2)) return TCL_ERR_ALIGN;
+    }
+    Gpu g;
+    if (const int st = gpu_of(stream, &g)) return st;
+    int blocks = 0;
+    each_launch(count, from, to, lengths, types, [&](const ClipTensors& a) {
+        blocks += clip_blocks(a.pieces);
+        return TCL_OK;
+    });
+    Room room{static_cast<uint8_t*>(workspace), *workspace_bytes};
+    double* parts = room.take<double>(blocks);
+    if (const int st = enough(room, workspace_bytes)) return st;
+    int at = 0;
+    int st = each_launch(count, from, to, lengths, types, [&](const ClipTensors& a) {
+        const int mine = at;
+        at += clip_blocks(a.pieces);
+        return status_of(launch_square_sums(a, parts + mine, stream));
+    });
+    if (st) return st;
+    if (!blocks) return status_of(launch_norm(parts, 0, norm, stream));
+    float* told = norm;   // (the first launch's)
+    return each_launch(count, from, to, lengths, types, [&](const ClipTensors& a) {
+        float* const mine = told;
+        told = nullptr;
+        return status_of(launch_clip(a, parts, blocks, bound, mine, stream));
+    });
+}
+
+}  // extern "C"

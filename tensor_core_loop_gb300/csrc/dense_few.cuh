@@ -1,0 +1,275 @@
+// Products of few rows of tokens with bf16 weight matrices: D = x·W^T, x T × K with T <= 64.
+//
+// What bounds them is the weights' way from HBM, once: 128 weight rows are the MMA's M side
+// (tensor-memory lanes), the tokens its N side, so that no shared memory and no MMA is spent on
+// tokens that do not exist and a thread holds one output column of every token. The loads run
+// through a ring of 64-value k-blocks that keeps some 100 KB in flight on each SM; where
+// tiles leave places on the GPU free, the CTAs of a cluster share a tile's k-blocks and one
+// after another's sums are added over distributed shared memory.
+//
+// The ends are those of dense_product.cuh, for the forward direction: STORE, GATE (two weight
+// tiles to a CTA: 128 rows of either matrix), ENTROPY (sums over a warp's 32 vocabulary rows).
+#pragma once
+
+#include "dense_product.cuh"
+
+namespace tcl {
+
+struct DenseFewParams {
+    int T, N, num_kb, tiles, split;
+    int act, f32;
+    DenseOut out[3];
+    const void* targets;
+    int wide_targets;
+    float2* parts;         // ENTROPY: [32-row chunk of W][token]
+    float* target_logit;
+    unsigned long long timeout_ns;
+    unsigned int* status;
+};
+
+template <int BQ_, DenseEnd E_>
+struct DenseFewCfg {
+    static constexpr int BQ = BQ_;                       // tokens
+    static constexpr int MATS = E_ == DenseEnd::GATE ? 2 : 1;
+    static constexpr int A_BYTES = 128 * 128, Q_BYTES = BQ * 128;
+    static constexpr int STAGE_BYTES = MATS * A_BYTES + Q_BYTES;
+    static constexpr int PER_SM = BQ <= 32 ? 2 : 1;
+    static constexpr int STAGES = (PER_SM == 2 ? 112640 : 204800) / STAGE_BYTES;
+    static constexpr int COLS = MATS * BQ;               // tensor-memory columns of a tile
+    static constexpr int TMEM_COLS = 2 * COLS < 32 ? 32 : 2 * COLS;
+    static constexpr int THREADS = 64 + 128;
+    static constexpr int NBARS = 2 * STAGES + 5;
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + (NBARS + 2) * 8;
+    static_assert(PER_SM * (SMEM_BYTES + 1024) <= 233472 && PER_SM * TMEM_COLS <= 512, "CTAs of an SM");
+    static_assert(COLS * 128 * 4 <= STAGES * STAGE_BYTES, "a shared tile's sums fit the ring");
+    static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor-memory columns");
+};
+
+// k-blocks of 64 values: four MMAs each, one or two weight tiles.
+template <int BQ, DenseEnd E>
+__global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E>::PER_SM)
+    dense_few_kernel(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1,
+                     const __grid_constant__ CUtensorMap tmX, const DenseFewParams p) {
+    using C = DenseFewCfg<BQ, E>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = ptx::smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::NBARS);
+    volatile uint32_t* abort_flag = tmem_holder + 1;
+
+    const uint32_t full0 = ptx::smem_u32(bars);
+    const uint32_t empty0 = full0 + 8 * C::STAGES;
+    const uint32_t accf0 = empty0 + 8 * C::STAGES;
+    const uint32_t acce0 = accf0 + 16;
+    const uint32_t drain_bar = acce0 + 16;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            ptx::mbar_init(full0 + 8 * s, 1);
+            ptx::mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(accf0 + 8 * b, 1);
+            ptx::mbar_init(acce0 + 8 * b, 4);
+        }
+        ptx::mbar_init(drain_bar, 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&tmW0);
+        ptx::prefetch_tensormap(&tmX);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_holder), C::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    const int share = p.split;
+    const int u0 = blockIdx.x / share, ustep = gridDim.x / share, part = static_cast<int>(blockIdx.x) % share;
+    const int lo = static_cast<int>(static_cast<long long>(p.num_kb) * part / share);
+    const int hi = static_cast<int>(static_cast<long long>(p.num_kb) * (part + 1) / share);
+    auto wait = [&](uint32_t bar, uint32_t parity, unsigned int code) {
+        return wait_warp(bar, parity, abort_flag, p.timeout_ns, p.status, code);
+    };
+    // D of weight row `row` and token i, as this lane's (GATE: gate and up)
+    auto finish = [&](int row0, int i, float v, float v1) {
+        const int row = row0 + lane;
+        if constexpr (E == DenseEnd::ENTROPY) {
+            if (i >= p.T || row0 >= p.N) return;   // (the same for all lanes)
+            const long long target =
+                p.wide_targets ? static_cast<const long long*>(p.targets)[i] : static_cast<const int*>(p.targets)[i];
+            if (row == target && row < p.N) p.target_logit[i] = v;
+            const float l2 = row < p.N ? v * 1.4426950408889634f : __int_as_float(0xff800000);
+            auto total = [](float x) {
+#pragma unroll
+                for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                return x;
+            };
+            float ref = 0.0f, sum = total(ptx::exp2_approx(l2));
+            if (!dense_plain_sum(sum)) {
+                float top = row < p.N ? v : __int_as_float(0xff800000);
+#pragma unroll
+                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                ref = dense_exponent(top);
+                sum = total(ptx::exp2_approx(row < p.N ? fmaf(v, 1.4426950408889634f, -ref) : __int_as_float(0xff800000)));
+            }
+            if (lane == 0) p.parts[static_cast<long long>(row0 / 32) * p.T + i] = make_float2(ref, sum);
+        } else {
+            if (i >= p.T || row >= p.N) return;
+            auto put = [&](const DenseOut& o, float x) {
+                if (E == DenseEnd::STORE && p.f32)
+                    static_cast<float*>(o.p)[i * o.ld + row] = x;
+                else
+                    static_cast<__nv_bfloat16*>(o.p)[i * o.ld + row] = __float2bfloat16_rn(x);
+            };
+            if constexpr (E == DenseEnd::GATE) {
+                float unused;
+                put(p.out[0], dense_act<false>(p.act, v, unused) * v1);
+                if (p.out[1].p) {
+                    put(p.out[1], v);
+                    put(p.out[2], v1);
+                }
+            } else {
+                put(p.out[0], v);
+            }
+        }
+    };
+
+    if (warp == 0) {
+        uint32_t s = 0, ph = 0;
+        bool ok = true;
+        for (int u = u0; ok && u < p.tiles; u += ustep) {
+            for (int kb = lo; kb < hi; ++kb) {
+                if (!wait(empty0 + 8 * s, ph ^ 1u, DEV_TIMEOUT_PRODUCER)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sa = ptx::smem_u32(smem) + s * C::STAGE_BYTES, fb = full0 + 8 * s;
+                ptx::mbar_arrive_expect_tx_elected(fb, C::STAGE_BYTES);
+                ptx::tma_load_2d_elected(sa, &tmW0, fb, kb * 64, u * 128);
+                if constexpr (C::MATS == 2) ptx::tma_load_2d_elected(sa + C::A_BYTES, &tmW1, fb, kb * 64, u * 128);
+                ptx::tma_load_2d_elected(sa + C::MATS * C::A_BYTES, &tmX, fb, kb * 64, 0);
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) spin_ns(200000);   // copies issued before the abort land within microseconds
+        __syncwarp();
+    } else if (warp == 1) {
+        constexpr uint32_t IDESC = ptx::make_idesc(1, 1, 0, 0, 128, BQ);
+        constexpr uint64_t STEP = C::STAGE_BYTES / 16;
+        const uint32_t stage0 = ptx::smem_u32(smem);
+        const uint64_t adesc0 = ptx::sdesc_sw128(stage0, 16, 1024);
+        const uint64_t qdesc0 = ptx::sdesc_sw128(stage0 + C::MATS * C::A_BYTES, 16, 1024);
+        uint32_t s = 0, ph = 0;
+        bool ok = true;
+        for (int u = u0, j = 0; ok && u < p.tiles; u += ustep, ++j) {
+            const uint32_t b = j & 1;
+            if (!wait(acce0 + 8 * b, ((j >> 1) & 1) ^ 1u, DEV_TIMEOUT_MMA_ACC)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            for (int kb = lo; kb < hi; ++kb) {
+                if (!wait(full0 + 8 * s, ph, DEV_TIMEOUT_MMA_FULL)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint64_t qd = qdesc0 + s * STEP;
+#pragma unroll
+                for (int m = 0; m < C::MATS; ++m) {
+                    const uint64_t ad = adesc0 + s * STEP + m * (C::A_BYTES / 16);
+                    ptx::mma_f16_x4_elected(tmem_base + b * C::COLS + m * BQ, ad, qd, ad + 2, qd + 2, ad + 4, qd + 4, ad + 6,
+                                            qd + 6, IDESC, kb > lo ? 1u : 0u);
+                }
+                ptx::mma_commit_elected(empty0 + 8 * s);
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (ok) ptx::mma_commit_elected(accf0 + 8 * b);
+        }
+        if (!ok) {
+            ptx::mma_commit_elected(drain_bar);
+            if (lane == 0) wait_drain(drain_bar, 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3;
+        for (int u = u0, j = 0; u < p.tiles; u += ustep, ++j) {
+            const uint32_t b = j & 1;
+            if (!wait(accf0 + 8 * b, (j >> 1) & 1, DEV_TIMEOUT_EPILOGUE)) break;
+            ptx::tc_fence_after();
+            const uint32_t t = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * C::COLS;
+            // (the ring is free: a shared tile is this CTA's only one, and all its MMAs are done)
+            float* sums = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+#pragma unroll
+            for (int c = 0; c < BQ; c += 16) {
+                uint32_t r[16], r1[16];
+                ptx::tmem_ld_32x32b_x16(t + c, r);
+                if constexpr (C::MATS == 2) ptx::tmem_ld_32x32b_x16(t + BQ + c, r1);
+                ptx::tmem_ld_wait(r);
+                if constexpr (C::MATS == 2) ptx::tmem_ld_wait(r1);
+                if (c + 16 == BQ) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_relaxed(acce0 + 8 * b);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (share > 1) {
+                        sums[(c + i) * 128] = __uint_as_float(r[i]);
+                        if constexpr (C::MATS == 2) sums[(BQ + c + i) * 128] = __uint_as_float(r1[i]);
+                    } else {
+                        finish(u * 128 + quarter * 32, c + i, __uint_as_float(r[i]),
+                               C::MATS == 2 ? __uint_as_float(r1[i]) : 0.0f);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    }
+
+    // ------------------------------------------------ shared tiles: the parts' sums, in their order
+    if (share > 1) {
+        __syncwarp();
+        ptx::cluster_sync();   // every part's sums are in its shared memory
+        if (warp >= 2 && u0 < p.tiles) {
+            const int quarter = warp & 3;
+            const uint32_t sums = ptx::smem_u32(smem) + 4 * (quarter * 32 + lane);
+            for (int i = part; i < min(BQ, p.T); i += share) {
+                float v = 0.0f, v1 = 0.0f;
+                for (int r = 0; r < share; ++r) {
+                    const uint32_t at = ptx::mapa_shared(sums, static_cast<uint32_t>(r));
+                    v += ptx::ld_cluster_f32(at + 4 * (i * 128));
+                    if constexpr (C::MATS == 2) v1 += ptx::ld_cluster_f32(at + 4 * ((BQ + i) * 128));
+                }
+                finish(u0 * 128 + quarter * 32, i, v, v1);
+            }
+        }
+        __syncwarp();
+        ptx::cluster_sync();   // no part leaves while another may still read its sums
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+}
+
+}  // namespace tcl

@@ -1,0 +1,84 @@
+// Internal launch interface of the dense bf16 products with fused ends and of the passes around
+// them: what api_dense.cu needs of the translation units that hold the kernels, and of api.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "dense_few.cuh"
+#include "fp8_launch.cuh"
+
+namespace tcl {
+
+// ---- services of api.cu (under the library's lock)
+// A 2-D map of a stored bf16 matrix (cols contiguous), 128-byte swizzle, boxes of 64 columns × box_rows.
+int tensor_map_bf16(const void* ptr, uint64_t cols, uint64_t rows, uint64_t row_bytes, uint32_t box_rows, CUtensorMap* out);
+
+// ---- products (k_dense.cu, k_dense_few.cu)
+struct DenseLaunch {
+    DenseEnd end;
+    int a_mn, b_mn;
+    CUtensorMap a[2], b[2], c[3];
+    DenseParams p;
+    int grid;
+    cudaStream_t stream;
+};
+cudaError_t launch_dense_pair(const DenseLaunch& a);
+
+struct DenseFewLaunch {
+    DenseEnd end;
+    int bq;              // 16, 32 or 64
+    CUtensorMap w[2], x;
+    DenseFewParams p;
+    int grid;
+    cudaStream_t stream;
+};
+int dense_few_per_sm(int bq);
+cudaError_t launch_dense_few(const DenseFewLaunch& a);
+
+// ---- passes (k_dense_rows.cu)
+struct DenseCopy {       // rows × cols of bf16 to a pitch of whole 16-byte pieces
+    const __nv_bfloat16* from;
+    long long ld;
+    int rows, cols;
+    __nv_bfloat16* to;
+};
+constexpr int kDenseCopies = 6;
+struct DenseCopies {
+    DenseCopy job[kDenseCopies];
+    int n;
+};
+cudaError_t launch_dense_copies(const DenseCopies& a, cudaStream_t stream);
+
+struct DenseJoin {       // the sums of K ranges, added in their order
+    const float* parts;
+    long long ld, part;  // elements between rows, between ranges
+    int splits, rows, cols, f32;
+    const float* factor;
+    const float* plus;
+    long long ld_plus;
+    void* out;
+    long long ld_out;
+};
+cudaError_t launch_dense_join(const DenseJoin& a, cudaStream_t stream);
+
+struct EntropyRows {
+    const float2* parts;   // [chunk][row]
+    int chunks, rows, vocab;
+    const float* target_logit;
+    const void* targets;
+    int wide_targets;
+    float *loss, *lse;
+    // in training:
+    const float* grad;     // NULL: no gradients
+    __nv_bfloat16* e;      // exponentials, chunks of 128 columns
+    long long ld_e;
+    float* factor;
+    const __nv_bfloat16* x;
+    long long ld_x;
+    __nv_bfloat16* scaled;
+    long long ld_scaled;
+    int hidden;
+};
+cudaError_t launch_entropy_rows(const EntropyRows& a, cudaStream_t stream);
+
+}  // namespace tcl

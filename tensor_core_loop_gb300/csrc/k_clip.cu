@@ -1,0 +1,197 @@
+// The norm over many tensors of gradients, and their scaling down to a bound on it.
+//
+// What bounds both is the memory: one pass reads every gradient, another reads and writes it. The
+// tensors' addresses travel in the launch's parameters (no copy to the GPU, so that a captured
+// launch replays on its own), their elements are dealt out in pieces over all
+// tensors, and a block finds a piece's tensor by bisection. The second pass walks the pieces
+// backwards: what the first one read last is still in L2.
+//
+// Squares are added in fp32 within a thread's 32 elements and in fp64 from there on, in an order
+// that depends on the sizes alone, so that equal gradients give equal norms. Where 32 squares leave
+// fp32's range (elements beyond 2^63 or all below 2^-50), they are added again in fp64.
+#include <cuda_bf16.h>
+
+#include "clip_launch.cuh"
+#include "fp8_launch.cuh"
+
+namespace tcl {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int tensor_of(const ClipTensors& a, long long piece) {
+    int lo = 0, hi = a.n - 1;   // the last tensor that starts at or before the piece (empty ones have none)
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.t[mid].before <= piece)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+template <typename T>
+__device__ __forceinline__ float value(T x);
+template <>
+__device__ __forceinline__ float value(float x) { return x; }
+template <>
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+__device__ __forceinline__ void unpack(uint4 v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+
+// The sum over a block of 256, the same for all of its threads; its order is fixed.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double sh[kThreads / 32];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) s += sh[i];
+    return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) square_sums_kernel(const __grid_constant__ ClipTensors a, double* parts) {
+    constexpr int U = 16 / sizeof(T), Q = 32 / U;   // elements of a 16-byte unit, units of a thread's 32 elements
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    double sum = 0.0;
+    for (long long piece = blockIdx.x; piece < a.pieces; piece += gridDim.x) {
+        const ClipTensor& t = a.t[tensor_of(a, piece)];
+        const long long at = (piece - t.before) * a.piece;
+        const T* x = static_cast<const T*>(t.from) + at;
+        const int n = static_cast<int>(t.n - at < a.piece ? t.n - at : a.piece);
+        int done = 0;
+        if (reinterpret_cast<uintptr_t>(x) % 16 == 0) {
+            constexpr int STEP = kThreads * 32;
+            for (; done + STEP <= n; done += STEP) {
+                uint4 v[Q];
+#pragma unroll
+                for (int q = 0; q < Q; ++q) v[q] = reinterpret_cast<const uint4*>(x + done)[q * kThreads + threadIdx.x];
+                float s = 0.0f;
+                uint32_t any = 0;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    float f[U];
+                    unpack(v[q], f);
+#pragma unroll
+                    for (int i = 0; i < U; ++i) s = fmaf(f[i], f[i], s);
+                    any |= v[q].x | v[q].y | v[q].z | v[q].w;
+                }
+                if (s >= 7.9e-31f && s < __int_as_float(0x7f800000)) {   // 2^-100, infinity
+                    sum += static_cast<double>(s);
+                } else if (any) {
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        float f[U];
+                        unpack(v[q], f);
+#pragma unroll
+                        for (int i = 0; i < U; ++i) sum += static_cast<double>(f[i]) * f[i];
+                    }
+                }
+            }
+        }
+        for (int i = done + threadIdx.x; i < n; i += kThreads) {
+            const double f = value(x[i]);
+            sum += f * f;
+        }
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) parts[blockIdx.x] = sum;
+}
+
+__device__ __forceinline__ double norm_of(const double* parts, int n) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += kThreads) s += parts[i];
+    return sqrt(block_sum(s));
+}
+
+__global__ void __launch_bounds__(kThreads) norm_kernel(const double* parts, int n, float* norm) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const double v = norm_of(parts, n);
+    if (threadIdx.x == 0) *norm = static_cast<float>(v);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ ClipTensors a, const double* parts, int nparts,
+                                                        float bound, float* norm) {
+    constexpr int U = 16 / sizeof(T), Q = 4;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const double length = norm_of(parts, nparts);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(length);
+    // (a norm that is NaN or infinite scales nothing: the caller, who is told of it, drops the step)
+    const bool scaled = length > bound && length < __longlong_as_double(0x7ff0000000000000ll);
+    const float f = scaled ? static_cast<float>(static_cast<double>(bound) / length) : 1.0f;
+    for (long long back = blockIdx.x; back < a.pieces; back += gridDim.x) {
+        const long long piece = a.pieces - 1 - back;
+        const ClipTensor& t = a.t[tensor_of(a, piece)];
+        if (!scaled && t.from == t.to) continue;
+        const long long at = (piece - t.before) * a.piece;
+        const T* x = static_cast<const T*>(t.from) + at;
+        T* y = static_cast<T*>(t.to) + at;
+        const int n = static_cast<int>(t.n - at < a.piece ? t.n - at : a.piece);
+        int done = 0;
+        if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % 16 == 0) {
+            constexpr int STEP = kThreads * Q * U;
+            for (; done + STEP <= n; done += STEP) {
+                uint4 v[Q];
+#pragma unroll
+                for (int q = 0; q < Q; ++q) v[q] = reinterpret_cast<const uint4*>(x + done)[q * kThreads + threadIdx.x];
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    float e[U];
+                    unpack(v[q], e);
+#pragma unroll
+                    for (int i = 0; i < U; ++i) e[i] *= f;
+                    reinterpret_cast<uint4*>(y + done)[q * kThreads + threadIdx.x] = scaled ? pack(e) : v[q];
+                }
+            }
+        }
+        for (int i = done + threadIdx.x; i < n; i += kThreads) y[i] = scaled ? static_cast<T>(value(x[i]) * f) : x[i];
+    }
+}
+
+}  // namespace
+
+int clip_blocks(long long pieces) { return static_cast<int>(pieces < 1 ? 1 : pieces > kClipBlocks ? kClipBlocks : pieces); }
+
+cudaError_t launch_square_sums(const ClipTensors& a, double* parts, cudaStream_t stream) {
+    return launch_pdl(a.f32 ? square_sums_kernel<float> : square_sums_kernel<__nv_bfloat16>, dim3(clip_blocks(a.pieces)),
+                      kThreads, 0, stream, a, parts);
+}
+
+cudaError_t launch_norm(const double* parts, int n, float* norm, cudaStream_t stream) {
+    return launch_pdl(norm_kernel, dim3(1), kThreads, 0, stream, parts, n, norm);
+}
+
+cudaError_t launch_clip(const ClipTensors& a, const double* parts, int n, float bound, float* norm, cudaStream_t stream) {
+    return launch_pdl(a.f32 ? clip_kernel<float> : clip_kernel<__nv_bfloat16>, dim3(clip_blocks(a.pieces)), kThreads, 0,
+                      stream, a, parts, n, bound, norm);
+}
+
+}  // namespace tcl

@@ -1,0 +1,203 @@
+// The passes around the dense products: operands brought onto the tensor copies' grid, the sums of
+// K ranges joined, and the rows of the cross entropy.
+#include "dense_launch.cuh"
+
+namespace tcl {
+namespace {
+
+// ------------------------------------------------------------------ operands onto the grid
+// A thread builds one 16-byte piece from eight elements at any address; a row's last piece is
+// filled up with zeros.
+__global__ void dense_copy_kernel(const DenseCopies a) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const DenseCopy& c = a.job[blockIdx.y];
+    const int pieces = (c.cols + 7) / 8;
+    const long long n = static_cast<long long>(c.rows) * pieces, step = static_cast<long long>(gridDim.x) * blockDim.x;
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
+        const long long row = i / pieces;
+        const int col = static_cast<int>(i - row * pieces) * 8;
+        const unsigned short* from = reinterpret_cast<const unsigned short*>(c.from) + row * c.ld + col;
+        unsigned short v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = col + k < c.cols ? from[k] : static_cast<unsigned short>(0);
+        reinterpret_cast<uint4*>(c.to)[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+}
+
+// ------------------------------------------------------------------ K ranges joined
+__global__ void dense_join_kernel(const DenseJoin a) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int quads = (a.cols + 3) / 4;
+    const long long n = static_cast<long long>(a.rows) * quads, step = static_cast<long long>(gridDim.x) * blockDim.x;
+    const bool vec = reinterpret_cast<uintptr_t>(a.out) % (a.f32 ? 16 : 8) == 0 && a.ld_out % 4 == 0;
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
+        const long long row = i / quads;
+        const int col = static_cast<int>(i - row * quads) * 4;
+        const float* from = a.parts + row * a.ld + col;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int z = 0; z < a.splits; ++z) {
+            const float4 v = *reinterpret_cast<const float4*>(from + z * a.part);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        if (a.factor) {
+            const float f = a.factor[row];
+            s = f == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
+        }
+        if (a.plus) {
+            const float4 v = *reinterpret_cast<const float4*>(a.plus + row * a.ld_plus + col);
+            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        const float e[4] = {s.x, s.y, s.z, s.w};
+        const long long at = row * a.ld_out + col;
+        if (a.f32) {
+            float* to = static_cast<float*>(a.out) + at;
+            if (vec && col + 4 <= a.cols) {
+                *reinterpret_cast<float4*>(to) = s;
+            } else {
+                for (int k = 0; k < 4 && col + k < a.cols; ++k) to[k] = e[k];
+            }
+        } else {
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at;
+            if (vec && col + 4 <= a.cols) {
+                *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+            } else {
+                for (int k = 0; k < 4 && col + k < a.cols; ++k) to[k] = __float2bfloat16_rn(e[k]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ rows of the cross entropy
+// Row t's logits l[v] left chunk sums s_i of 2^(l log2 e - ref_i). With c the largest ref_i of a
+// chunk that has a sum, S = sum_i s_i 2^(ref_i - c):
+//   lse = c ln 2 + ln S,  loss = lse - l[target]
+// and in training, with the exponentials e[v] = 2^(l[v] log2 e - ref_i) in bf16,
+//   d loss / d l[v] = e[v] 2^(ref_i - c) / S - [v = target]
+// The factor grad/S of a row goes into the rows of x for the product with e^T, and into the end of
+// the product e·W; the one at the target, e - S = S (exp(l[target] - lse) - 1), is worked out in
+// fp32, so that a row that is nearly certain of its target keeps the small difference, and replaces
+// e there. Chunks relative to another power of two (a row's chunks differ only where logits leave
+// +-44 or so) are brought to c in place.
+//
+// A block takes 8 rows, 32 threads to a row; both the sums (64 bytes of a chunk's row at a time)
+// and the rows of x are read once.
+constexpr int kRowThreads = 32, kRowsBlock = 8;
+
+__global__ void __launch_bounds__(kRowThreads * kRowsBlock) entropy_rows_kernel(const EntropyRows a) {
+    __shared__ float sh[kRowThreads][kRowsBlock + 1];
+    __shared__ float factor[kRowsBlock];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int r = threadIdx.x % kRowsBlock, k = threadIdx.x / kRowsBlock;   // the sums: neighbouring threads, neighbouring rows
+    const long long row = static_cast<long long>(blockIdx.x) * kRowsBlock + r;
+    const bool in = row < a.rows;
+    auto over_slices = [&](float v, auto op) {   // the same for all threads of a row
+        sh[k][r] = v;
+        __syncthreads();
+        float all = sh[0][r];
+        for (int i = 1; i < kRowThreads; ++i) all = op(all, sh[i][r]);
+        __syncthreads();
+        return all;
+    };
+    const float none = __int_as_float(0xff800000);
+    float c = none;
+    if (in) {
+#pragma unroll 8
+        for (int i = k; i < a.chunks; i += kRowThreads) {
+            const float2 p = a.parts[static_cast<long long>(i) * a.rows + row];
+            if (p.y != 0.0f) c = fmaxf(c, p.x);
+        }
+    }
+    c = over_slices(c, [](float x, float y) { return fmaxf(x, y); });
+    if (c == none) c = 0.0f;
+    float s = 0.0f;
+    bool other = false;   // a chunk of this thread's is relative to another power of two
+    if (in) {
+#pragma unroll 8
+        for (int i = k; i < a.chunks; i += kRowThreads) {
+            const float2 p = a.parts[static_cast<long long>(i) * a.rows + row];
+            other |= p.x != c;
+            s += p.x == c ? p.y : p.y * exp2f(p.x - c);
+        }
+    }
+    s = over_slices(s, [](float x, float y) { return x + y; });
+    long long target = -1;
+    if (in) target = a.wide_targets ? static_cast<const long long*>(a.targets)[row] : static_cast<const int*>(a.targets)[row];
+    const bool kept = target >= 0 && target < a.vocab;
+    const float lse = fmaf(c, 0.69314718055994531f, logf(s));
+    if (in && k == 0) {
+        a.loss[row] = kept ? lse - a.target_logit[row] : 0.0f;
+        a.lse[row] = lse;
+    }
+    if (!a.grad) return;   // (the same for all threads)
+
+    if (kept && other) {
+        for (int i = k; i < a.chunks; i += kRowThreads) {
+            const float ref = a.parts[static_cast<long long>(i) * a.rows + row].x;
+            if (ref == c) continue;
+            const float f = exp2f(ref - c);
+            for (int v = i * 128; v < min(i * 128 + 128, a.vocab); ++v) {
+                __nv_bfloat16* e = a.e + row * a.ld_e + v;
+                *e = __float2bfloat16_rn(__bfloat162float(*e) * f);
+            }
+        }
+    }
+    if (k == 0) {
+        const float f = kept ? a.grad[row] / s : 0.0f;
+        factor[r] = f;
+        if (in) a.factor[row] = f;
+    }
+    __syncthreads();
+    if (kept && k == 0) a.e[row * a.ld_e + target] = __float2bfloat16_rn(expm1f(a.target_logit[row] - lse) * s);
+    // the rows of x, a warp each
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const long long mine = static_cast<long long>(blockIdx.x) * kRowsBlock + warp;
+    if (mine >= a.rows) return;
+    const float f = factor[warp];
+    const __nv_bfloat16* x = a.x + mine * a.ld_x;
+    uint4* to = reinterpret_cast<uint4*>(a.scaled + mine * a.ld_scaled);
+    auto scale = [f](uint32_t w) {   // (a dropped token's row may hold anything)
+        return f == 0.0f ? 0u : pack_bf16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+    };
+#pragma unroll 4
+    for (int i = lane; i < a.hidden / 8; i += 32) {
+        const uint4 v = reinterpret_cast<const uint4*>(x)[i];
+        to[i] = make_uint4(scale(v.x), scale(v.y), scale(v.z), scale(v.w));
+    }
+    const int rest = a.hidden / 8 * 8 + lane;   // (the row may end with the buffer)
+    if (rest < a.hidden)
+        a.scaled[mine * a.ld_scaled + rest] = __float2bfloat16_rn(f == 0.0f ? 0.0f : __bfloat162float(x[rest]) * f);
+}
+
+int blocks_for(long long n, int per) {
+    const long long b = (n + per - 1) / per;
+    return static_cast<int>(b < 1 ? 1 : b > 152 * 16 ? 152 * 16 : b);
+}
+
+}  // namespace
+
+cudaError_t launch_dense_copies(const DenseCopies& a, cudaStream_t stream) {
+    long long most = 0;
+    for (int i = 0; i < a.n; ++i) {
+        const long long n = static_cast<long long>(a.job[i].rows) * ((a.job[i].cols + 7) / 8);
+        if (n > most) most = n;
+    }
+    return launch_pdl(dense_copy_kernel, dim3(blocks_for(most, 256), a.n), 256, 0, stream, a);
+}
+
+cudaError_t launch_dense_join(const DenseJoin& a, cudaStream_t stream) {
+    return launch_pdl(dense_join_kernel, dim3(blocks_for(static_cast<long long>(a.rows) * ((a.cols + 3) / 4), 256)), 256, 0,
+                      stream, a);
+}
+
+cudaError_t launch_entropy_rows(const EntropyRows& a, cudaStream_t stream) {
+    return launch_pdl(entropy_rows_kernel, dim3((a.rows + kRowsBlock - 1) / kRowsBlock), kRowThreads * kRowsBlock, 0, stream, a);
+}
+
+}  // namespace tcl

@@ -1,0 +1,278 @@
+"""A language model's dense path on bf16 matrices, and its gradients: Python binding of
+``include/tcl_dense.h``.
+
+    out = gated_ffn(x, w_gate, w_up, w_down)                            # serving: prompts, single tokens
+    out, kept = gated_ffn(x, w_gate, w_up, w_down, keep=True)           # training
+    dx, dw_gate, dw_up, dw_down = gated_ffn_grad(grad, x, w_gate, w_up, w_down, kept)
+
+    loss, lse = cross_entropy(x, w, targets)                            # logits x · wᵀ, never stored
+    loss, lse, dx, dw = cross_entropy_grad(x, w, targets, grad)         # grad: each token's weight in the sum
+
+    norm = clip_grads([dw_gate, dw_up, dw_down, dw], 1.0)               # in place
+
+Weights are outputs × inputs, as a layer stores them. Matrices have contiguous rows, with any
+distance between them; rows that start on 16-byte pieces are read in place, others are copied first.
+Calls are asynchronous on ``stream`` (default: the current stream of the tensors' device) and
+allocate their results and workspaces on that stream; nothing is kept between calls, so any of
+them may be captured into a CUDA graph. Given another stream than the current one, the caller lets it
+wait for whatever makes the operands (``stream.wait_stream``); the operands themselves may be
+dropped right after the call.
+
+The calls compute without a graph of autograd, also for tensors that require gradients: the
+gradients are calls of their own.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+try:
+    import torch
+except ImportError:   # (the library itself needs no PyTorch; the calls below take its tensors)
+    torch = None
+
+from . import OUT_BF16, OUT_F32, TclError, lib
+from .fp8 import _INT, _device, _mat, _on, _too_large
+
+__all__ = ["gated_ffn", "gated_ffn_grad", "GatedFfnKept", "cross_entropy", "cross_entropy_grad", "grad_norm", "clip_grads",
+           "EXPORTED_SYMBOLS_DENSE"]
+
+EXPORTED_SYMBOLS_DENSE = ("tcl_gated_ffn", "tcl_gated_ffn_grad", "tcl_cross_entropy", "tcl_cross_entropy_grad",
+                          "tcl_grad_norm", "tcl_clip_gradients")
+_ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+_WORKSPACE = 13   # TCL_ERR_WORKSPACE
+if torch is not None:
+    _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+    _TYPES = {_BF16: OUT_BF16, _F32: OUT_F32}
+
+_bound = None
+
+
+def _lib():
+    global _bound
+    if _bound is None:
+        L = lib()
+        I, P, F, Z = ctypes.c_int, ctypes.c_void_p, ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
+        L.tcl_gated_ffn.argtypes = [I, I, I, P, I, P, I, P, I, P, I, I, P, P, P, I, P, I, P, Z, P]
+        L.tcl_gated_ffn_grad.argtypes = [I, I, I, P, I, P, I, P, I, P, I, P, I, I, P, P, P, I, P, I, P, I, P, I, P, I, I, P, Z, P]
+        L.tcl_cross_entropy.argtypes = [I, I, I, P, I, P, I, P, I, P, P, P, Z, P]
+        L.tcl_cross_entropy_grad.argtypes = [I, I, I, P, I, P, I, P, I, P, P, P, P, I, P, I, I, P, Z, P]
+        L.tcl_grad_norm.argtypes = [I, P, P, P, P, P, Z, P]
+        L.tcl_clip_gradients.argtypes = [I, P, P, P, P, F, P, P, Z, P]
+        _bound = L
+    return _bound
+
+
+class GatedFfnKept(NamedTuple):
+    """What ``gated_ffn`` keeps for its gradients; tokens × inner, bf16, rows on 16-byte pieces."""
+    gate: "torch.Tensor"     # x · w_gateᵀ  # noqa: F821
+    up: "torch.Tensor"       # x · w_upᵀ  # noqa: F821
+    hidden: "torch.Tensor"   # act(gate) · up  # noqa: F821
+
+
+def _call(fn, what, device, stream, *args):
+    """Calls fn(*args, workspace, its size, stream), with a workspace where it asks for one."""
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    size = ctypes.c_size_t(0)
+
+    def once(workspace):
+        if device.index == torch._C._cuda_getDevice():
+            return fn(*args, workspace, size, raw)
+        with torch.cuda.device(device):
+            return fn(*args, workspace, size, raw)
+
+    st = once(None)
+    if st == _WORKSPACE:
+        room = torch.empty(size.value, dtype=torch.uint8, device=device)
+        st = once(room.data_ptr())
+    if st:
+        raise TclError(st, what)
+
+
+def _bf16(t, name):
+    """(rows, columns, leading dimension) of a bf16 matrix."""
+    if t.dtype != _BF16:
+        raise TypeError(f"{name} must be bfloat16, not {t.dtype}")
+    return _mat(t, name)
+
+
+def _shape(rows, cols, want, name):
+    if (rows, cols) != want:
+        raise ValueError(f"{name} must be {want[0]} x {want[1]}, not {rows} x {cols}")
+
+
+def _w_type(out_dtype):
+    if out_dtype is None:
+        out_dtype = _BF16
+    code = _TYPES.get(out_dtype)
+    if code is None:
+        raise TypeError("weights' gradients are bfloat16 or float32")
+    return out_dtype, code
+
+
+def _ffn(x, w_gate, w_up, w_down, activation):
+    """Checks of the block's operands: (tokens, hidden, inner, act), each one's leading dimension."""
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    tokens, hidden, ldx = _bf16(x, "x")
+    inner, h, ldg = _bf16(w_gate, "w_gate")
+    _shape(inner, h, (inner, hidden), "w_gate")
+    r, h, ldu = _bf16(w_up, "w_up")
+    _shape(r, h, (inner, hidden), "w_up")
+    r, h, ldd = _bf16(w_down, "w_down")
+    _shape(r, h, (hidden, inner), "w_down")
+    if inner < 1:
+        raise ValueError("the weights must have at least one row")
+    return (tokens, hidden, inner, act), (ldx, ldg, ldu, ldd)
+
+
+def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", keep: bool = False, stream=None):
+    """out = (act(x · w_gateᵀ) * (x · w_upᵀ)) · w_downᵀ: tokens × hidden, bf16. ``w_gate`` and
+    ``w_up`` are inner × hidden, ``w_down`` hidden × inner. ``activation``: "silu", "gelu" (with the
+    normal distribution) or "gelu_tanh". The product in the middle is rounded to bf16.
+
+    ``keep=True``: (out, kept) with what ``gated_ffn_grad`` needs."""
+    (tokens, hidden, inner, act), (ldx, ldg, ldu, ldd) = _ffn(x, w_gate, w_up, w_down, activation)
+    device = _device(stream, "x", x, w_gate, w_up, w_down)
+    with _on(stream):
+        pitch = (inner + 7) & ~7
+        mid = torch.empty((3 if keep else 1, tokens, pitch), dtype=_BF16, device=device)
+        out = torch.empty((tokens, hidden), dtype=_BF16, device=device)
+        h = mid.data_ptr()
+        part = 2 * tokens * pitch
+        _call(_lib().tcl_gated_ffn, "gated_ffn", device, stream, tokens, hidden, inner, x.data_ptr(), ldx, w_gate.data_ptr(),
+              ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd, act, h + part if keep else None,
+              h + 2 * part if keep else None, h, pitch, out.data_ptr(), hidden)
+        if not keep:
+            return out
+        mid = mid[..., :inner]
+        return out, GatedFfnKept(mid[1], mid[2], mid[0])
+
+
+def gated_ffn_grad(grad, x, w_gate, w_up, w_down, kept: GatedFfnKept, activation: str = "silu", out_dtype=None, stream=None):
+    """(dx, dw_gate, dw_up, dw_down) of ``gated_ffn`` from the gradient of its result and what it
+    kept. ``dx`` is bf16, the weights' gradients are bf16 or ``out_dtype=torch.float32``. The gradients
+    of the two products in the middle are rounded to bf16."""
+    (tokens, hidden, inner, act), (ldx, ldg, ldu, ldd) = _ffn(x, w_gate, w_up, w_down, activation)
+    r, c, ld_grad = _bf16(grad, "grad")
+    _shape(r, c, (tokens, hidden), "grad")
+    dtype, code = _w_type(out_dtype)
+    ldk = None
+    for t, name in zip(kept, ("kept.gate", "kept.up", "kept.hidden")):
+        r, c, _ = _bf16(t, name)
+        _shape(r, c, (tokens, inner), name)
+        if ldk is None:
+            ldk = t.stride(0) if tokens > 1 else (inner + 7) & ~7
+        if (tokens > 1 and t.stride(0) != ldk) or ldk % 8 or t.data_ptr() % 16:
+            raise ValueError("kept must be as gated_ffn returned it: rows on 16-byte pieces, one distance between them")
+    device = _device(stream, "grad", grad, x, w_gate, w_up, w_down, *kept)
+    with _on(stream):
+        dx = torch.empty((tokens, hidden), dtype=_BF16, device=device)
+        dw = [torch.empty(w.shape, dtype=dtype, device=device) for w in (w_gate, w_up, w_down)]
+        _call(_lib().tcl_gated_ffn_grad, "gated_ffn_grad", device, stream, tokens, hidden, inner, grad.data_ptr(), ld_grad,
+              x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd, act,
+              *(t.data_ptr() for t in kept), ldk, dx.data_ptr(), hidden, dw[0].data_ptr(), hidden, dw[1].data_ptr(), hidden,
+              dw[2].data_ptr(), inner, code)
+    return dx, *dw
+
+
+def _entropy(x, w, targets):
+    tokens, hidden, ldx = _bf16(x, "x")
+    vocab, h, ldw = _bf16(w, "w")
+    _shape(vocab, h, (vocab, hidden), "w")
+    if vocab < 1:
+        raise ValueError("w must have at least one row")
+    if targets.dtype not in (_I32, _I64):
+        raise TypeError("targets must be int32 or int64")
+    if tuple(targets.shape) != (tokens,) or not targets.is_contiguous():
+        raise ValueError(f"targets must be contiguous of shape {(tokens,)}")
+    return tokens, hidden, vocab, ldx, ldw
+
+
+def cross_entropy(x, w, targets, stream=None):
+    """(loss, lse) of the logits l = x · wᵀ (tokens × vocabulary), which are never stored: for each
+    token lse = log Σ exp(l) and loss = lse - l[target], fp32. ``targets`` (int32 or int64) outside the
+    vocabulary drop their token: its loss is 0."""
+    tokens, hidden, vocab, ldx, ldw = _entropy(x, w, targets)
+    device = _device(stream, "x", x, w, targets)
+    with _on(stream):
+        loss, lse = torch.empty((2, tokens), dtype=_F32, device=device)
+        _call(_lib().tcl_cross_entropy, "cross_entropy", device, stream, tokens, hidden, vocab, x.data_ptr(), ldx, w.data_ptr(),
+              ldw, targets.data_ptr(), targets.element_size(), loss.data_ptr(), lse.data_ptr())
+    return loss, lse
+
+
+def cross_entropy_grad(x, w, targets, grad, out_dtype=None, stream=None):
+    """(loss, lse, dx, dw): ``cross_entropy`` and the gradients of Σ grad · loss, ``grad`` a float32
+    weight for each token (1/tokens for a mean). Dropped tokens add nothing and get zeros. ``dx`` is
+    bf16, ``dw`` bf16 or ``out_dtype=torch.float32``. The exponentials of the logits, computed once for
+    both, are kept in bf16 for 2 GiB of them at a time."""
+    tokens, hidden, vocab, ldx, ldw = _entropy(x, w, targets)
+    if grad.dtype != _F32:
+        raise TypeError("grad must be float32")
+    if tuple(grad.shape) != (tokens,) or not grad.is_contiguous():
+        raise ValueError(f"grad must be contiguous of shape {(tokens,)}")
+    dtype, code = _w_type(out_dtype)
+    device = _device(stream, "x", x, w, targets, grad)
+    with _on(stream):
+        loss, lse = torch.empty((2, tokens), dtype=_F32, device=device)
+        dx = torch.empty((tokens, hidden), dtype=_BF16, device=device)
+        dw = torch.empty((vocab, hidden), dtype=dtype, device=device)
+        _call(_lib().tcl_cross_entropy_grad, "cross_entropy_grad", device, stream, tokens, hidden, vocab, x.data_ptr(), ldx,
+              w.data_ptr(), ldw, targets.data_ptr(), targets.element_size(), grad.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+              dx.data_ptr(), hidden, dw.data_ptr(), hidden, code)
+    return loss, lse, dx, dw
+
+
+def _tensors(tensors, name):
+    """(host arrays of addresses, lengths and types) of contiguous bf16 and fp32 tensors."""
+    n = len(tensors)
+    if n > _INT:
+        _too_large(name)
+    ptr, length, types = (ctypes.c_void_p * n)(), (ctypes.c_longlong * n)(), (ctypes.c_int * n)()
+    for i, t in enumerate(tensors):
+        code = _TYPES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        ptr[i], length[i], types[i] = t.data_ptr(), t.numel(), code
+    return ptr, length, types
+
+
+def grad_norm(tensors, stream=None):
+    """The square root of the sum of all elements' squares over bf16 and fp32 tensors: an fp32 scalar
+    on the GPU. The same tensors give the same bits."""
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError("at least one tensor")
+    ptr, length, types = _tensors(tensors, "tensors")
+    device = _device(stream, "tensors", *tensors)
+    with _on(stream):
+        norm = torch.empty((), dtype=_F32, device=device)
+        _call(_lib().tcl_grad_norm, "grad_norm", device, stream, len(tensors), ptr, length, types, norm.data_ptr())
+    return norm
+
+
+def clip_grads(tensors, max_norm: float, out=None, stream=None):
+    """Scales the tensors, in place or into ``out`` (a list of the same shapes and types), by
+    max_norm / norm where their ``grad_norm`` is larger than ``max_norm``; a norm that is infinite or
+    NaN scales nothing. Returns the norm before, an fp32 scalar on the GPU."""
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError("at least one tensor")
+    max_norm = float(max_norm)
+    if not max_norm >= 0:
+        raise ValueError("max_norm must not be negative")
+    ptr, length, types = _tensors(tensors, "tensors")
+    to = tensors if out is None else list(out)
+    if out is not None and [(t.shape, t.dtype) for t in to] != [(t.shape, t.dtype) for t in tensors]:
+        raise ValueError("out must hold a tensor of the same shape and type for each one")
+    to_ptr = ptr if out is None else _tensors(to, "out")[0]
+    device = _device(stream, "tensors", *tensors, *(() if out is None else to))
+    with _on(stream):
+        norm = torch.empty((), dtype=_F32, device=device)
+        _call(_lib().tcl_clip_gradients, "clip_grads", device, stream, len(tensors), ptr, to_ptr, length, types, max_norm,
+              norm.data_ptr())
+    return norm
