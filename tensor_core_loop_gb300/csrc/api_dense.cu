@@ -81,25 +81,6 @@ int gpu_of(cudaStream_t stream, Gpu* g) {
     return device_context(&dev, &g->sms, &g->status);
 }
 
-// K ranges of a product of `tiles` 256 × 256 tiles with kb k-blocks: as many as make the GPU's pairs
-// of SMs finish together, if what the ranges' sums cost in memory is less than the time that saves.
-// Microseconds, measured on a GB300: 0.28 a k-block, 3 a tile, 5 TB/s and 3 us for joining the sums.
-int choose_splits(long long tiles, long long kb, int M, int N, int sms) {
-    const long long pairs = sms / 2;
-    int best = 1;
-    double least = 0.0;
-    for (int s = 1; s <= 32 && s <= kb; ++s) {
-        const double waves = static_cast<double>((tiles * s + pairs - 1) / pairs);
-        double us = waves * (0.28 * static_cast<double>((kb + s - 1) / s) + 3.0);
-        if (s > 1) us += 3.0 + 8.0 * s * M * static_cast<double>(N) / 5e6;
-        if (s == 1 || us < 0.97 * least) {
-            best = s;
-            least = us;
-        }
-    }
-    return best;
-}
-
 // D = A·B^T over one operand pair or two; `mn`: the operand's rows (not K) are contiguous in memory.
 struct Product {
     Mat a, b, a1, b1;
@@ -115,15 +96,86 @@ struct Product {
 };
 
 long long k_of(const Mat& m, bool mn) { return mn ? m.rows : m.cols; }
-
-void plan(Room& room, Product& q, const Gpu& g) {
-    const long long kb = blocks64(k_of(q.a, q.a_mn)) + (q.two ? blocks64(k_of(q.a1, q.a_mn)) : 0);
-    q.splits = choose_splits(static_cast<long long>(tiles_of(q.M, 256)) * tiles_of(q.N, 256), kb, q.M, q.N, g.sms);
-    q.parts = q.splits > 1 ? room.take<float>(static_cast<long long>(q.splits) * q.M * up(q.N, 4)) : nullptr;
+long long blocks_of(const Product& q) {
+    return blocks64(k_of(q.a, q.a_mn)) + (q.two ? blocks64(k_of(q.a1, q.a_mn)) : 0);
 }
 
-int map_of(const Mat& m, bool mn, CUtensorMap* out) {
-    return tensor_map_bf16(m.p, m.cols, m.rows, m.ld * 2, mn ? 64 : 128, out);
+// What a launch costs, in microseconds, measured on a GB300: a k-block of a tile, a tile's end (where it does
+// not hide behind the next tile's k-blocks), a launch, and the joining of K ranges.
+double block_us(int bn) { return bn == 256 ? 0.27 : 0.16; }
+double tile_us(int bn) { return bn == 256 ? 3.0 : 2.0; }
+constexpr double kLaunchUs = 5.0;
+
+// A launch of up to kDenseProblems products: the tiles' width, K ranges of the first one (the longest),
+// and its units' way to the pairs of SMs (dense_walk).
+struct Group {
+    Product* q;
+    int n, bn;
+    int units, long_units, extra, pairs;
+};
+
+// Deals the units out; the time that takes.
+double deal(Group& g, int sms) {
+    long long units = 0, first = 0;
+    double each[2] = {0.0, 0.0}, work = 0.0;   // a unit of the first product, the longest of the others
+    for (int i = 0; i < g.n; ++i) {
+        const Product& q = g.q[i];
+        const long long n = static_cast<long long>(tiles_of(q.M, 256)) * tiles_of(q.N, g.bn) * q.splits;
+        const double us = block_us(g.bn) * std::ceil(static_cast<double>(blocks_of(q)) / q.splits) + 0.3;
+        units += n;
+        work += us * static_cast<double>(n);
+        if (i == 0) first = n;
+        each[i > 0] = std::max(each[i > 0], us);
+    }
+    g.units = static_cast<int>(std::min(units, 0x40000000ll));
+    g.pairs = static_cast<int>(std::min<long long>(sms / 2, units));
+    g.long_units = static_cast<int>(std::min(first, 0x40000000ll));
+    const int r0 = g.long_units % g.pairs;
+    g.extra = g.n > 1 && r0 ? static_cast<int>(each[0] / each[1] + 0.5) : 0;
+    // the pair that ends last: of those with one more of the long units, or of the others
+    const long long rest = units - first, late = static_cast<long long>(g.extra) * (g.pairs - r0);
+    const long long rounds = rest > late ? (rest - late + g.pairs - 1) / g.pairs : 0;
+    const double most = each[0] * static_cast<double>(first / g.pairs + (r0 > 0)) + each[1] * static_cast<double>(rounds);
+    const double others = each[0] * static_cast<double>(first / g.pairs) +
+                          each[1] * static_cast<double>(rounds + std::min<long long>(g.extra, (rest + g.pairs - r0 - 1) / (g.pairs - r0)));
+    return std::max(std::max(most, r0 < g.pairs ? others : 0.0), work / g.pairs) + tile_us(g.bn) + kLaunchUs;
+}
+
+// Chooses width and K ranges by the costs above; the time.
+double choose(Group& g, int sms) {
+    double least = 0.0;
+    int bn = 0, splits = 1;
+    const long long kb = blocks_of(g.q[0]);
+    for (int i = 1; i < g.n; ++i) g.q[i].splits = 1;
+    for (g.bn = 256; g.bn >= 128; g.bn /= 2) {
+        for (int s = 1; s <= 64 && s * 4 <= std::max(kb, 4ll); s += s < 8 ? 1 : s / 4) {
+            g.q[0].splits = s;
+            double us = deal(g, sms);
+            // the ranges' sums are written and read again, at 5 TB/s
+            if (s > 1) us += kLaunchUs + 8.0 * s * g.q[0].M * static_cast<double>(g.q[0].N) / 5e6;
+            if (!bn || us < 0.98 * least) {
+                bn = g.bn;
+                splits = s;
+                least = us;
+            }
+        }
+    }
+    g.bn = bn;
+    g.q[0].splits = splits;
+    deal(g, sms);
+    return least;
+}
+
+// Room for the sums of K ranges.
+void reserve(Room& room, Group& g) {
+    for (int i = 0; i < g.n; ++i) {
+        Product& q = g.q[i];
+        q.parts = q.splits > 1 ? room.take<float>(static_cast<long long>(q.splits) * q.M * up(q.N, 4)) : nullptr;
+    }
+}
+
+int map_of(const Mat& m, bool mn, int rows, CUtensorMap* out) {
+    return tensor_map_bf16(m.p, m.cols, m.rows, m.ld * 2, mn ? 64 : rows, out);
 }
 
 int map_out(const DenseOut& o, int f32, int rows, int mats, CUtensorMap* out) {
@@ -137,60 +189,100 @@ DenseOut result(void* p, long long ld, int cols, int rows, int f32) {
 }
 
 int launch_pairs(DenseLaunch& l, const Gpu& g) {
-    DenseParams& p = l.p;
-    p.group = 8;
-    p.timeout_ns = kTimeoutNs;
-    p.status = g.status;
-    const long long units = static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits;
-    if (units > 0x3fffffffll) return TCL_ERR_DIMS;
-    l.grid = static_cast<int>(std::min<long long>(g.sms / 2, units)) * 2;
+    l.p.timeout_ns = kTimeoutNs;
+    l.p.status = g.status;
     l.stream = g.stream;
+    if (l.p.units > 0x3fffffff) return TCL_ERR_DIMS;
     return status_of(launch_dense_pair(l));
 }
 
-int run(const Product& q, const Gpu& g) {
+int run(const Group& g, const Gpu& gpu) {
     DenseLaunch l = {};
     l.end = DenseEnd::STORE;
-    l.a_mn = q.a_mn;
-    l.b_mn = q.b_mn;
-    int st;
-    if ((st = map_of(q.a, q.a_mn, &l.a[0])) || (st = map_of(q.b, q.b_mn, &l.b[0]))) return st;
-    if (q.two && ((st = map_of(q.a1, q.a_mn, &l.a[1])) || (st = map_of(q.b1, q.b_mn, &l.b[1])))) return st;
+    l.bn = g.bn;
+    l.pairs = g.pairs;
     DenseParams& p = l.p;
-    p.M = q.M;
-    p.N = q.N;
-    p.kb0 = static_cast<int>(blocks64(k_of(q.a, q.a_mn)));
-    p.kb1 = q.two ? static_cast<int>(blocks64(k_of(q.a1, q.a_mn))) : 0;
-    p.tiles_m = tiles_of(q.M, 256);
-    p.tiles_n = tiles_of(q.N, 256);
-    p.splits = q.splits;
-    const long long pitch = up(q.N, 4);
-    if (q.splits > 1) {
-        p.f32 = 1;
-        p.out[0] = {q.parts, pitch, static_cast<int>(pitch), 1};
-    } else {
-        p.f32 = q.f32;
-        p.out[0] = result(q.out, q.ldo, q.N, q.M, q.f32);
-        p.factor = q.factor;
-        p.plus = q.plus;
-        p.ld_plus = q.ld_plus;
+    p.n = g.n;
+    p.units = g.units;
+    p.long_units = g.long_units;
+    p.extra = g.extra;
+    int st, first = 0;
+    for (int i = 0; i < g.n; ++i) {
+        const Product& q = g.q[i];
+        DenseProblem& d = p.q[i];
+        if ((st = map_of(q.a, q.a_mn, 128, &l.maps.a[i][0])) || (st = map_of(q.b, q.b_mn, g.bn / 2, &l.maps.b[i][0]))) return st;
+        if (q.two && ((st = map_of(q.a1, q.a_mn, 128, &l.maps.a[i][1])) || (st = map_of(q.b1, q.b_mn, g.bn / 2, &l.maps.b[i][1]))))
+            return st;
+        d.M = q.M;
+        d.N = q.N;
+        d.kb0 = static_cast<int>(blocks64(k_of(q.a, q.a_mn)));
+        d.kb1 = static_cast<int>(blocks_of(q)) - d.kb0;
+        d.tiles_m = tiles_of(q.M, 256);
+        d.tiles_n = tiles_of(q.N, g.bn);
+        d.splits = q.splits;
+        d.first = first;
+        d.a_mn = q.a_mn;
+        d.b_mn = q.b_mn;
+        const long long pitch = up(q.N, 4);
+        if (q.splits > 1) {
+            d.f32 = 1;
+            d.out = {q.parts, pitch, static_cast<int>(pitch), 1};
+        } else {
+            d.f32 = q.f32;
+            d.out = result(q.out, q.ldo, q.N, q.M, q.f32);
+            d.factor = q.factor;
+            d.plus = q.plus;
+            d.ld_plus = q.ld_plus;
+        }
+        if ((st = map_out(d.out, d.f32, q.M, q.splits, &l.maps.c[i]))) return st;
+        if (g.units < 0x40000000) first += d.tiles_m * d.tiles_n * d.splits;
     }
-    if ((st = map_out(p.out[0], p.f32, q.M, q.splits, &l.c[0]))) return st;
-    if ((st = launch_pairs(l, g)) || q.splits == 1) return st;
-    return status_of(launch_dense_join({q.parts, pitch, pitch * q.M, q.splits, q.M, q.N, q.f32, q.factor, q.plus, q.ld_plus,
-                                        q.out, q.ldo},
-                                       g.stream));
+    if ((st = launch_pairs(l, gpu))) return st;
+    for (int i = 0; i < g.n; ++i) {
+        const Product& q = g.q[i];
+        const long long pitch = up(q.N, 4);
+        if (q.splits > 1 && (st = status_of(launch_dense_join({q.parts, pitch, pitch * q.M, q.splits, q.M, q.N, q.f32, q.factor,
+                                                               q.plus, q.ld_plus, q.out, q.ldo},
+                                                              gpu.stream))))
+            return st;
+    }
+    return TCL_OK;
+}
+
+// The launch of one M × N result with an end of its own, K contiguous in A.
+DenseLaunch ended(DenseEnd end, int M, int N, long long k, int cols256, const Gpu& g) {
+    DenseLaunch l = {};
+    l.end = end;
+    // narrow tiles where wide ones leave SMs without a tile and the tiles' ends show
+    const long long wide = static_cast<long long>(tiles_of(M, 256)) * tiles_of(N, cols256);
+    const long long narrow = static_cast<long long>(tiles_of(M, 256)) * tiles_of(N, cols256 / 2);
+    const long long pairs = g.sms / 2;
+    auto us = [&](long long tiles, int bn) {
+        return static_cast<double>((tiles + pairs - 1) / pairs) * (block_us(bn) * static_cast<double>(blocks64(k)) + 0.3) + tile_us(bn);
+    };
+    l.bn = us(narrow, 128) < us(wide, 256) ? 128 : 256;
+    DenseProblem& d = l.p.q[0];
+    d.M = M;
+    d.N = N;
+    d.kb0 = static_cast<int>(blocks64(k));
+    d.tiles_m = tiles_of(M, 256);
+    d.tiles_n = tiles_of(N, l.bn == 256 ? cols256 : cols256 / 2);
+    d.splits = 1;
+    l.p.n = 1;
+    l.p.units = l.p.long_units = static_cast<int>(std::min(l.bn == 256 ? wide : narrow, 0x40000000ll));
+    l.pairs = static_cast<int>(std::min<long long>(pairs, l.p.units));
+    return l;
 }
 
 // ------------------------------------------------------------------ few tokens
 
-int launch_few(DenseEnd end, const Mat& x, const Mat& w0, const Mat* w1, DenseFewParams p, const Gpu& g) {
+int launch_few(DenseEnd end, const Mat& x, const Mat& w0, const Mat* w1, DenseFewParams p, const Gpu& g, int* ctas = nullptr) {
     DenseFewLaunch l = {};
     l.end = end;
     l.bq = p.T <= 16 ? 16 : p.T <= 32 ? 32 : 64;
     int st;
-    if ((st = tensor_map_bf16(x.p, x.cols, x.rows, x.ld * 2, l.bq, &l.x)) || (st = map_of(w0, false, &l.w[0]))) return st;
-    if (w1 && (st = map_of(*w1, false, &l.w[1]))) return st;
+    if ((st = tensor_map_bf16(x.p, x.cols, x.rows, x.ld * 2, l.bq, &l.x)) || (st = map_of(w0, false, 128, &l.w[0]))) return st;
+    if (w1 && (st = map_of(*w1, false, 128, &l.w[1]))) return st;
     p.N = w0.rows;
     p.num_kb = static_cast<int>(blocks64(w0.cols));
     p.tiles = tiles_of(w0.rows, 128);
@@ -203,6 +295,7 @@ int launch_few(DenseEnd end, const Mat& x, const Mat& w0, const Mat* w1, DenseFe
     l.p = p;
     l.grid = std::min(places / p.split, p.tiles) * p.split;
     l.stream = g.stream;
+    if (ctas) *ctas = l.grid;
     return status_of(launch_dense_few(l));
 }
 
@@ -219,49 +312,33 @@ int ffn_sizes(int tokens, int hidden, int inner, int act) {
 }
 
 int gate_pairs(const Ffn& f, bf16* gate, bf16* upp, bf16* h, long long ldk, const Gpu& g) {
-    DenseLaunch l = {};
-    l.end = DenseEnd::GATE;
+    DenseLaunch l = ended(DenseEnd::GATE, f.T, f.F, f.H, 128, g);
     int st;
-    if ((st = map_of(f.x, false, &l.a[0])) || (st = map_of(f.wg, false, &l.b[0])) || (st = map_of(f.wu, false, &l.b[1]))) return st;
-    DenseParams& p = l.p;
-    p.M = f.T;
-    p.N = f.F;
-    p.kb0 = static_cast<int>(blocks64(f.H));
-    p.tiles_m = tiles_of(f.T, 256);
-    p.tiles_n = tiles_of(f.F, 128);
-    p.splits = 1;
-    p.act = f.act;
+    if ((st = map_of(f.x, false, 128, &l.maps.a[0][0])) || (st = map_of(f.wg, false, l.bn / 2, &l.maps.b[0][0])) ||
+        (st = map_of(f.wu, false, l.bn / 2, &l.maps.b[0][1])))
+        return st;
+    l.p.act = f.act;
     void* const to[3] = {h, gate, upp};
     for (int i = 0; i < (gate ? 3 : 1); ++i) {
-        p.out[i] = {to[i], ldk, static_cast<int>(up(f.F, 8)), 1};
-        if ((st = map_out(p.out[i], 0, f.T, 1, &l.c[i]))) return st;
+        DenseOut& o = i ? l.p.more[i - 1] : l.p.q[0].out;
+        o = {to[i], ldk, static_cast<int>(up(f.F, 8)), 1};
+        if ((st = map_out(o, 0, f.T, 1, &l.maps.c[i]))) return st;
     }
     return launch_pairs(l, g);
 }
 
 int gate_grad(const Ffn& f, const Mat& grad, const bf16* gate, const bf16* upp, long long ldk, bf16* dg, bf16* du,
               long long ldd, const Gpu& g) {
-    DenseLaunch l = {};
-    l.end = DenseEnd::GATE_GRAD;
-    l.b_mn = 1;
+    DenseLaunch l = ended(DenseEnd::GATE_GRAD, f.T, f.F, f.H, 256, g);
     int st;
-    if ((st = map_of(grad, false, &l.a[0])) || (st = map_of(f.wd, true, &l.b[0]))) return st;
-    DenseParams& p = l.p;
-    p.M = f.T;
-    p.N = f.F;
-    p.kb0 = static_cast<int>(blocks64(f.H));
-    p.tiles_m = tiles_of(f.T, 256);
-    p.tiles_n = tiles_of(f.F, 256);
-    p.splits = 1;
-    p.act = f.act;
-    p.gate = gate;
-    p.up = upp;
-    p.ld_kept = ldk;
-    bf16* const to[2] = {dg, du};
-    for (int i = 0; i < 2; ++i) {
-        p.out[i] = {to[i], ldd, static_cast<int>(up(f.F, 8)), 1};
-        if ((st = map_out(p.out[i], 0, f.T, 1, &l.c[i]))) return st;
-    }
+    if ((st = map_of(grad, false, 128, &l.maps.a[0][0])) || (st = map_of(f.wd, true, 0, &l.maps.b[0][0]))) return st;
+    l.p.act = f.act;
+    l.p.gate = gate;
+    l.p.up = upp;
+    l.p.ld_kept = ldk;
+    l.p.q[0].out = {dg, ldd, static_cast<int>(up(f.F, 8)), 1};
+    l.p.more[0] = {du, ldd, static_cast<int>(up(f.F, 8)), 1};
+    if ((st = map_out(l.p.q[0].out, 0, f.T, 1, &l.maps.c[0])) || (st = map_out(l.p.more[0], 0, f.T, 1, &l.maps.c[1]))) return st;
     return launch_pairs(l, g);
 }
 
@@ -290,36 +367,32 @@ int entropy_checks(int tokens, int hidden, int vocab, const void* X, int ldx, co
     return TCL_OK;
 }
 
-// The logits of rows [t0, t0 + rows) and what is kept of them; e NULL: sums alone.
-int entropy_pairs(const Entropy& n, int t0, int rows, bf16* e, long long lde, float2* parts, float* target_logit, const Gpu& g) {
-    DenseLaunch l = {};
-    l.end = DenseEnd::ENTROPY;
+// The logits of rows [t0, t0 + rows) and what is kept of them; e NULL: sums alone. `chunk`: columns of a sum.
+int entropy_pairs(const Entropy& n, int t0, int rows, bf16* e, long long lde, float2* parts, float* target_logit, int* chunk,
+                  const Gpu& g) {
+    DenseLaunch l = ended(DenseEnd::ENTROPY, rows, n.V, n.H, 256, g);
     const Mat x = {n.x.p + t0 * n.x.ld, n.x.ld, rows, n.H};
     int st;
-    if ((st = map_of(x, false, &l.a[0])) || (st = map_of(n.w, false, &l.b[0]))) return st;
+    if ((st = map_of(x, false, 128, &l.maps.a[0][0])) || (st = map_of(n.w, false, l.bn / 2, &l.maps.b[0][0]))) return st;
     DenseParams& p = l.p;
-    p.M = rows;
-    p.N = n.V;
-    p.kb0 = static_cast<int>(blocks64(n.H));
-    p.tiles_m = tiles_of(rows, 256);
-    p.tiles_n = tiles_of(n.V, 256);
-    p.splits = 1;
     p.targets = static_cast<const uint8_t*>(n.targets) + static_cast<long long>(t0) * n.target_bytes;
     p.wide_targets = n.target_bytes == 8;
     p.parts = parts;
     p.target_logit = target_logit;
     p.exps = e != nullptr;
     if (e) {
-        p.out[0] = {e, lde, static_cast<int>(up(n.V, 8)), 1};
-        if ((st = map_out(p.out[0], 0, rows, 1, &l.c[0]))) return st;
+        p.q[0].out = {e, lde, static_cast<int>(up(n.V, 8)), 1};
+        if ((st = map_out(p.q[0].out, 0, rows, 1, &l.maps.c[0]))) return st;
     }
+    *chunk = l.bn / 2;
     return launch_pairs(l, g);
 }
 
-EntropyRows entropy_rows(const Entropy& n, int t0, int rows, int chunks, const float2* parts, const float* target_logit) {
+EntropyRows entropy_rows(const Entropy& n, int t0, int rows, int chunks, int chunk, const float2* parts, const float* target_logit) {
     EntropyRows r = {};
     r.parts = parts;
     r.chunks = chunks;
+    r.chunk = chunk;
     r.rows = rows;
     r.vocab = n.V;
     r.target_logit = target_logit;
@@ -350,8 +423,8 @@ template <class F>
 int each_launch(int count, const void* const* from, void* const* to, const long long* lengths, const int* types, F f) {
     long long total = 0;
     for (int i = 0; i < count; ++i) total += lengths[i];
-    // pieces that give every block several, but at least 4096 elements
-    const long long piece = std::min(65536ll, std::max(4096ll, total / (4 * kClipBlocks) / 4096 * 4096));
+    // pieces that give every block several, of whole steps of the kernels' loops
+    const long long piece = std::min(65536ll, std::max(8192ll, total / (4 * kClipBlocks) / 8192 * 8192));
     for (int f32 = 0; f32 < 2; ++f32) {
         ClipTensors a;
         a.n = 0;
@@ -404,14 +477,18 @@ int tcl_gated_ffn(int tokens, int hidden, int inner, const void* X, int ldx, con
     q.N = hidden;
     q.out = out;
     q.ldo = ldo;
-    if (tokens > kMostFew) plan(room, q, g);
+    Group down = {&q, 1};
+    if (tokens > kMostFew) {
+        choose(down, g.sms);
+        reserve(room, down);
+    }
     if (const int st = enough(room, workspace_bytes)) return st;
     const auto lock = library_lock();
     int st;
     if (room.copies.n && (st = status_of(launch_dense_copies(room.copies, stream)))) return st;
     if (tokens > kMostFew) {
         if ((st = gate_pairs(f, static_cast<bf16*>(gate), static_cast<bf16*>(upp), static_cast<bf16*>(h), ld_kept, g))) return st;
-        return run(q, g);
+        return run(down, g);
     }
     DenseFewParams p = {};
     p.T = tokens;
@@ -421,6 +498,7 @@ int tcl_gated_ffn(int tokens, int hidden, int inner, const void* X, int ldx, con
     p.out[2] = {upp, ld_kept, 0, 0};
     if ((st = launch_few(DenseEnd::GATE, f.x, f.wg, &f.wu, p, g))) return st;
     p.out[0] = {out, ldo, 0, 0};
+    p.early = 1;
     return launch_few(DenseEnd::STORE, kept, f.wd, nullptr, p, g);
 }
 
@@ -482,22 +560,14 @@ int tcl_gated_ffn_grad(int tokens, int hidden, int inner, const void* grad, int 
         w.out = to[i];
         w.ldo = ld[i];
     }
-    // (the products follow one another: they share the room for their sums)
-    size_t most = room.used;
-    for (Product& w : q) {
-        const size_t at = room.used;
-        plan(room, w, g);
-        most = std::max(most, room.used);
-        room.used = at;
-    }
-    room.used = most;
+    Group all = {q, 4};
+    choose(all, g.sms);
+    reserve(room, all);
     if ((st = enough(room, workspace_bytes))) return st;
     const auto lock = library_lock();
     if (room.copies.n && (st = status_of(launch_dense_copies(room.copies, stream)))) return st;
     if ((st = gate_grad(f, gr, static_cast<const bf16*>(gate), static_cast<const bf16*>(upp), ld_kept, dg, du, ldd, g))) return st;
-    for (const Product& w : q)
-        if ((st = run(w, g))) return st;
-    return TCL_OK;
+    return run(all, g);
 }
 
 int tcl_cross_entropy(int tokens, int hidden, int vocab, const void* X, int ldx, const void* W, int ldw, const void* targets,
@@ -514,7 +584,7 @@ int tcl_cross_entropy(int tokens, int hidden, int vocab, const void* X, int ldx,
     const Entropy n = {tokens, hidden, vocab, room.operand(X, ldx, tokens, hidden), room.operand(W, ldw, vocab, hidden), targets,
                        target_bytes, loss, lse};
     const bool few = tokens <= kMostFew;
-    const int chunks = tiles_of(vocab, few ? 32 : 128);
+    int chunks = few ? 4 * 2 * g.sms : tiles_of(vocab, 64), chunk = 0;
     float2* parts = room.take<float2>(static_cast<long long>(chunks) * tokens);
     float* target_logit = room.take<float>(tokens);
     if ((st = enough(room, workspace_bytes))) return st;
@@ -527,12 +597,15 @@ int tcl_cross_entropy(int tokens, int hidden, int vocab, const void* X, int ldx,
         p.wide_targets = target_bytes == 8;
         p.parts = parts;
         p.target_logit = target_logit;
-        st = launch_few(DenseEnd::ENTROPY, n.x, n.w, nullptr, p, g);
+        int ctas = 0;
+        st = launch_few(DenseEnd::ENTROPY, n.x, n.w, nullptr, p, g, &ctas);
+        chunks = 4 * ctas;
     } else {
-        st = entropy_pairs(n, 0, tokens, nullptr, 0, parts, target_logit, g);
+        st = entropy_pairs(n, 0, tokens, nullptr, 0, parts, target_logit, &chunk, g);
+        chunks = tiles_of(vocab, chunk);
     }
     if (st) return st;
-    return status_of(launch_entropy_rows(entropy_rows(n, 0, tokens, chunks, parts, target_logit), stream));
+    return status_of(launch_entropy_rows(entropy_rows(n, 0, tokens, chunks, chunk, parts, target_logit), stream));
 }
 
 int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int ldx, const void* W, int ldw,
@@ -556,10 +629,10 @@ int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int
     const long long lde = up(vocab, 8), most = std::max(256ll, kExpBytes / (2 * lde) / 256 * 256);
     const int pieces = static_cast<int>((tokens + most - 1) / most);
     const int piece = static_cast<int>(std::min<long long>(tokens, up((tokens + pieces - 1) / pieces, 256)));
-    const int chunks = tiles_of(vocab, 128);
+    const int most_chunks = tiles_of(vocab, 64);
     const long long ldh = up(hidden, 8);
     bf16* e = room.take<bf16>(lde * piece);
-    float2* parts = room.take<float2>(static_cast<long long>(chunks) * piece);
+    float2* parts = room.take<float2>(static_cast<long long>(most_chunks) * piece);
     float* target_logit = room.take<float>(piece);
     float* factor = room.take<float>(piece);
     bf16* scaled = room.take<bf16>(ldh * piece);
@@ -595,11 +668,11 @@ int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int
         const int t0 = i ? tokens - 1 - (tokens - 1) % piece : 0;
         Product q[2];
         products(t0, std::min(piece, tokens - t0), q);
-        for (Product& w : q) {
-            plan(room, w, g);
-            end = std::max(end, room.used);
-            room.used = at;
-        }
+        Group both = {q, 2};
+        choose(both, g.sms);
+        reserve(room, both);
+        end = std::max(end, room.used);
+        room.used = at;
     }
     room.used = end;
     if ((st = enough(room, workspace_bytes))) return st;
@@ -607,8 +680,9 @@ int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int
     if (room.copies.n && (st = status_of(launch_dense_copies(room.copies, stream)))) return st;
     for (int t0 = 0; t0 < tokens; t0 += piece) {
         const int rows = std::min(piece, tokens - t0);
-        if ((st = entropy_pairs(n, t0, rows, e, lde, parts, target_logit, g))) return st;
-        EntropyRows r = entropy_rows(n, t0, rows, chunks, parts, target_logit);
+        int chunk;
+        if ((st = entropy_pairs(n, t0, rows, e, lde, parts, target_logit, &chunk, g))) return st;
+        EntropyRows r = entropy_rows(n, t0, rows, tiles_of(vocab, chunk), chunk, parts, target_logit);
         r.grad = grad + t0;
         r.e = e;
         r.ld_e = lde;
@@ -621,11 +695,11 @@ int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int
         if ((st = status_of(launch_entropy_rows(r, stream)))) return st;
         Product q[2];
         products(t0, rows, q);
-        for (Product& w : q) {
-            room.used = at;
-            plan(room, w, g);
-            if ((st = run(w, g))) return st;
-        }
+        room.used = at;
+        Group both = {q, 2};
+        choose(both, g.sms);
+        reserve(room, both);
+        if ((st = run(both, g))) return st;
     }
     return TCL_OK;
 }

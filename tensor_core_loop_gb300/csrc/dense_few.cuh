@@ -8,7 +8,7 @@
 // after another's sums are added over distributed shared memory.
 //
 // The ends are those of dense_product.cuh, for the forward direction: STORE, GATE (two weight
-// tiles to a CTA: 128 rows of either matrix), ENTROPY (sums over a warp's 32 vocabulary rows).
+// tiles to a CTA: 128 rows of either matrix), ENTROPY (sums over all vocabulary rows that a warp saw).
 #pragma once
 
 #include "dense_product.cuh"
@@ -18,10 +18,11 @@ namespace tcl {
 struct DenseFewParams {
     int T, N, num_kb, tiles, split;
     int act, f32;
+    int early;             // the weights are not what the kernel before this one in the stream writes
     DenseOut out[3];
     const void* targets;
     int wide_targets;
-    float2* parts;         // ENTROPY: [32-row chunk of W][token]
+    float2* parts;         // ENTROPY: [warp, four to a CTA][token]
     float* target_logit;
     unsigned long long timeout_ns;
     unsigned int* status;
@@ -90,16 +91,35 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
 
     const int share = p.split;
     const int u0 = blockIdx.x / share, ustep = gridDim.x / share, part = static_cast<int>(blockIdx.x) % share;
     const int lo = static_cast<int>(static_cast<long long>(p.num_kb) * part / share);
     const int hi = static_cast<int>(static_cast<long long>(p.num_kb) * (part + 1) / share);
+    // The weights of the first k-blocks, up to a ring of them, are on their way before the kernel before this
+    // one has ended, where that kernel does not write them.
+    const int ahead = p.early && u0 < p.tiles ? min(hi - lo, C::STAGES) : 0;
+    auto load_weights = [&](uint32_t s, int kb, int tile) {
+        const uint32_t sa = ptx::smem_u32(smem) + s * C::STAGE_BYTES, fb = full0 + 8 * s;
+        ptx::mbar_arrive_expect_tx_elected(fb, C::STAGE_BYTES);
+        ptx::tma_load_2d_elected(sa, &tmW0, fb, kb * 64, tile * 128);
+        if constexpr (C::MATS == 2) ptx::tma_load_2d_elected(sa + C::A_BYTES, &tmW1, fb, kb * 64, tile * 128);
+    };
+    if (warp == 0)
+        for (int i = 0; i < ahead; ++i) load_weights(i, lo + i, u0);
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     auto wait = [&](uint32_t bar, uint32_t parity, unsigned int code) {
         return wait_warp(bar, parity, abort_flag, p.timeout_ns, p.status, code);
     };
+    auto act_of = [&](float g) {
+        float unused;
+        return p.act == DENSE_SILU   ? dense_act<DENSE_SILU, false>(g, unused)
+               : p.act == DENSE_GELU ? dense_act<DENSE_GELU, false>(g, unused)
+                                     : dense_act<DENSE_GELU_TANH, false>(g, unused);
+    };
+    // ENTROPY: what this warp has summed up over its tiles; lane i % 32 holds token i's
+    [[maybe_unused]] float run_ref[(BQ + 31) / 32] = {}, run_sum[(BQ + 31) / 32] = {};
     // D of weight row `row` and token i, as this lane's (GATE: gate and up)
     auto finish = [&](int row0, int i, float v, float v1) {
         const int row = row0 + lane;
@@ -122,7 +142,9 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E
                 ref = dense_exponent(top);
                 sum = total(ptx::exp2_approx(row < p.N ? fmaf(v, 1.4426950408889634f, -ref) : __int_as_float(0xff800000)));
             }
-            if (lane == 0) p.parts[static_cast<long long>(row0 / 32) * p.T + i] = make_float2(ref, sum);
+#pragma unroll
+            for (int k = 0; k < (BQ + 31) / 32; ++k)
+                if (i == lane + 32 * k) dense_merge(run_ref[k], run_sum[k], ref, sum);
         } else {
             if (i >= p.T || row >= p.N) return;
             auto put = [&](const DenseOut& o, float x) {
@@ -132,8 +154,7 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E
                     static_cast<__nv_bfloat16*>(o.p)[i * o.ld + row] = __float2bfloat16_rn(x);
             };
             if constexpr (E == DenseEnd::GATE) {
-                float unused;
-                put(p.out[0], dense_act<false>(p.act, v, unused) * v1);
+                put(p.out[0], act_of(v) * v1);
                 if (p.out[1].p) {
                     put(p.out[1], v);
                     put(p.out[2], v1);
@@ -146,6 +167,7 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E
 
     if (warp == 0) {
         uint32_t s = 0, ph = 0;
+        int there = ahead;
         bool ok = true;
         for (int u = u0; ok && u < p.tiles; u += ustep) {
             for (int kb = lo; kb < hi; ++kb) {
@@ -153,11 +175,12 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E
                     ok = false;
                     break;
                 }
-                const uint32_t sa = ptx::smem_u32(smem) + s * C::STAGE_BYTES, fb = full0 + 8 * s;
-                ptx::mbar_arrive_expect_tx_elected(fb, C::STAGE_BYTES);
-                ptx::tma_load_2d_elected(sa, &tmW0, fb, kb * 64, u * 128);
-                if constexpr (C::MATS == 2) ptx::tma_load_2d_elected(sa + C::A_BYTES, &tmW1, fb, kb * 64, u * 128);
-                ptx::tma_load_2d_elected(sa + C::MATS * C::A_BYTES, &tmX, fb, kb * 64, 0);
+                if (there > 0)
+                    --there;
+                else
+                    load_weights(s, kb, u);
+                ptx::tma_load_2d_elected(ptx::smem_u32(smem) + s * C::STAGE_BYTES + C::MATS * C::A_BYTES, &tmX, full0 + 8 * s,
+                                         kb * 64, 0);
                 if (++s == C::STAGES) {
                     s = 0;
                     ph ^= 1u;
@@ -264,6 +287,13 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E
         ptx::cluster_sync();   // no part leaves while another may still read its sums
     }
 
+    if (E == DenseEnd::ENTROPY && warp >= 2) {
+#pragma unroll
+        for (int k = 0; k < (BQ + 31) / 32; ++k)
+            if (lane + 32 * k < p.T)
+                p.parts[static_cast<long long>(blockIdx.x * 4 + (warp & 3)) * p.T + lane + 32 * k] =
+                    make_float2(run_ref[k], run_sum[k]);
+    }
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 1) {

@@ -16,10 +16,10 @@ int tensor_map_bf16(const void* ptr, uint64_t cols, uint64_t rows, uint64_t row_
 // ---- products (k_dense.cu, k_dense_few.cu)
 struct DenseLaunch {
     DenseEnd end;
-    int a_mn, b_mn;
-    CUtensorMap a[2], b[2], c[3];
+    int bn;              // 256 or 128: columns of a tile
+    DenseMaps maps;
     DenseParams p;
-    int grid;
+    int pairs;
     cudaStream_t stream;
 };
 cudaError_t launch_dense_pair(const DenseLaunch& a);
@@ -63,14 +63,14 @@ cudaError_t launch_dense_join(const DenseJoin& a, cudaStream_t stream);
 
 struct EntropyRows {
     const float2* parts;   // [chunk][row]
-    int chunks, rows, vocab;
+    int chunks, chunk, rows, vocab;   // chunk: columns of e of one sum (in training)
     const float* target_logit;
     const void* targets;
     int wide_targets;
     float *loss, *lse;
     // in training:
     const float* grad;     // NULL: no gradients
-    __nv_bfloat16* e;      // exponentials, chunks of 128 columns
+    __nv_bfloat16* e;      // exponentials
     long long ld_e;
     float* factor;
     const __nv_bfloat16* x;

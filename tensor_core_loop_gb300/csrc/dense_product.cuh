@@ -27,6 +27,8 @@
 // Every wait is bounded; a role that gives up raises the pair's abort flag.
 #pragma once
 
+#include <type_traits>
+
 #include "gemm_kernel_pair.cuh"
 #include "rows8.cuh"
 
@@ -34,6 +36,7 @@ namespace tcl {
 
 enum class DenseEnd : int { STORE, GATE, GATE_GRAD, ENTROPY };
 enum : int { DENSE_SILU = 0, DENSE_GELU = 1, DENSE_GELU_TANH = 2 };
+constexpr int kDenseProblems = 4;   // of one launch
 
 struct DenseOut {
     void* p;
@@ -42,78 +45,143 @@ struct DenseOut {
     int tma;          // rows start on 16-byte pieces: there is a tensor map
 };
 
-struct DenseParams {
+// One D = A·B^T of a launch.
+struct DenseProblem {
     int M, N;              // rows and columns of D (GATE: N columns of h)
     int kb0, kb1;          // k-blocks of the first and of the second operand pair (0: one pair)
-    int tiles_m, tiles_n, splits, group;
+    int tiles_m, tiles_n, splits;
+    int first;             // its first unit
+    int a_mn, b_mn;        // STORE: rows (not K) contiguous; the other ends: both K, GATE_GRAD B's rows
     int f32;               // STORE: fp32 result
-    int act;
-    DenseOut out[3];       // D, h or dgate or the exponentials; gate or dup; up
+    DenseOut out;          // D, h or dgate or the exponentials
     const float* factor;   // STORE: of each row (NULL: ones); a row whose factor is zero is zeros
-    const float* plus;     // STORE: added to the result (NULL: nothing)
+    const float* plus;     // STORE: added to the result (NULL: nothing); rows of whole 16-byte pieces
     long long ld_plus;
+};
+
+struct DenseMaps {
+    CUtensorMap a[kDenseProblems][2], b[kDenseProblems][2], c[kDenseProblems];   // (one problem: c for each result)
+};
+
+struct DenseParams {
+    DenseProblem q[kDenseProblems];
+    int n, units;
+    // How units are dealt out to the pairs of SMs: the first long_units of them (of one problem, those with the
+    // longest K ranges) in turn; `extra` units of the rest to each pair that got one fewer; then
+    // the others in turn. Everyone ends within about one unit of the others.
+    int long_units, extra;
+    int act;
+    DenseOut more[2];      // GATE: gate, up (no address: not asked for); GATE_GRAD: dup
     const __nv_bfloat16 *gate, *up;   // GATE_GRAD; rows on 16-byte pieces
     long long ld_kept;
     const void* targets;   // ENTROPY: M of them, int32 or int64
     int wide_targets;
-    float2* parts;         // ENTROPY: [128-column chunk][row of D]: exponent taken out, sum
+    float2* parts;         // ENTROPY: [chunk of BN/2 columns][row of D]: exponent taken out, sum
     float* target_logit;   // ENTROPY: [row of D]
     int exps;              // ENTROPY: store the exponentials
     unsigned long long timeout_ns;
     unsigned int* status;
 };
 
-// act(g), and its derivative where it is asked for.
-template <bool SLOPE>
-__device__ __forceinline__ float dense_act(int act, float g, float& slope) {
-    if (act == DENSE_GELU) {
-        const float p = 0.5f * erfcf(-0.70710678118654752f * g);   // (no cancellation for g < 0)
-        if (SLOPE) slope = p + g * 0.39894228040143268f * __expf(-0.5f * g * g);
-        return g * p;
-    }
-    float z = g;
-    if (act == DENSE_GELU_TANH) z = 1.5957691216057308f * g * (1.0f + 0.044715f * g * g);   // (1 + tanh(z/2))/2 is the sigmoid of z
-    const float s = __fdividef(1.0f, 1.0f + __expf(-z));
-    if (SLOPE) {
-        if (act == DENSE_GELU_TANH) {
-            const float c = fminf(fmaxf(g, -1e4f), 1e4f);   // (s(1 - s) is zero long before that)
-            slope = s + c * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 3.0f * 0.044715f * c * c);
-        } else {
-            slope = s * (1.0f + g * (1.0f - s));
-        }
-    }
-    return g * s;
+// Phi(-a) for a >= 0, with ex = exp(-a^2/2): ex·t·P(t), t = 1/(1 + 0.33 a), P fitted to
+// exp(a^2/2)·Phi(-a)/t over all a >= 0 (least largest relative error: 1e-6).
+__device__ __forceinline__ float dense_normal_tail(float a, float ex) {
+    const float t = __fdividef(1.0f, fmaf(0.33f, a, 1.0f));
+    float v = 0.033285726f;
+    v = fmaf(v, t, -0.10566493f);
+    v = fmaf(v, t, 0.067431189f);
+    v = fmaf(v, t, 0.033428829f);
+    v = fmaf(v, t, 0.091004848f);
+    v = fmaf(v, t, 0.11721677f);
+    v = fmaf(v, t, 0.13164698f);
+    v = fmaf(v, t, 0.13165107f);
+    return ex * t * v;
 }
 
+// act(g), and its derivative where it is asked for.
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ float dense_act(float g, float& slope) {
+    if constexpr (ACT == DENSE_GELU) {
+        const float ex = ptx::exp2_approx(-0.72134752044448170f * g * g);
+        const float q = dense_normal_tail(fabsf(g), ex), p = g > 0.0f ? 1.0f - q : q;
+        if (SLOPE) slope = fmaf(g * 0.39894228040143268f, ex, p);
+        return g * p;
+    } else {
+        float z = -1.4426950408889634f * g;
+        if constexpr (ACT == DENSE_GELU_TANH) z *= 1.5957691216057308f * fmaf(0.044715f * g, g, 1.0f);   // (1 + tanh(y))/2 = 1/(1 + exp(-2y))
+        const float s = __fdividef(1.0f, 1.0f + ptx::exp2_approx(z));
+        if constexpr (SLOPE && ACT == DENSE_GELU_TANH) {
+            const float c = fminf(fmaxf(g, -1e4f), 1e4f);   // (s(1 - s) is zero long before that)
+            slope = fmaf(c * s * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * c, c, 1.0f), s);
+        } else if constexpr (SLOPE) {
+            slope = s * fmaf(g, 1.0f - s, 1.0f);
+        }
+        return g * s;
+    }
+}
+
+// f with the activation as a compile-time number: the loops over a tile's values must stay short, since
+// what does not fit the instruction cache is fetched again by every warp (all three activations
+// in one unrolled loop of 64 values: 35 us a tile instead of 5).
+template <class F>
+__device__ __forceinline__ void dense_with_act(int act, F f) {
+    if (act == DENSE_SILU)
+        f(std::integral_constant<int, DENSE_SILU>());
+    else if (act == DENSE_GELU)
+        f(std::integral_constant<int, DENSE_GELU>());
+    else
+        f(std::integral_constant<int, DENSE_GELU_TANH>());
+}
+
+template <int BN_>
 struct DenseCfg {
-    static constexpr int BM = 256, BN = 256, BK = 64;
-    static constexpr int STAGES = 5;
-    static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;   // a CTA's share of a k-block
+    static constexpr int BM = 256, BN = BN_, BK = 64;
+    static constexpr int CW = BN / 2;               // columns of an epilogue warp
+    static constexpr int STAGES = BN == 256 ? 5 : 6;
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128;   // a CTA's share of a k-block
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EW = 8;                    // epilogue warps
     static constexpr int SLABS = 2, SLAB_BYTES = 32 * 128;
     static constexpr int NBARS = 2 * STAGES + 5;
     static constexpr int THREADS = 64 + 32 * EW;
+    static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EW * SLABS * SLAB_BYTES + (NBARS + 2) * 8;
     static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB per-block shared memory limit");
 };
 
 struct DenseUnit {
-    int m0, n, z, lo, hi;   // first row, tile column, K range's number and k-blocks
+    int q, m0, n, z, lo, hi;   // problem, first row, tile column, K range's number and k-blocks
 };
 
+// The unit at step j of pair r of `pairs`; p.units or more: none is left.
+__device__ __forceinline__ int dense_walk(const DenseParams& p, int r, int pairs, int j) {
+    const int r0 = p.long_units % pairs, mine = p.long_units / pairs + (r < r0 ? 1 : 0);
+    if (j < mine) return j * pairs + r;
+    j -= mine;
+    if (r < r0) return p.long_units + p.extra * (pairs - r0) + j * pairs + r;
+    if (j < p.extra) return p.long_units + j * (pairs - r0) + r - r0;
+    return p.long_units + p.extra * (pairs - r0) + (j - p.extra) * pairs + r;
+}
+
+template <DenseEnd E>
 __device__ __forceinline__ DenseUnit dense_unit(const DenseParams& p, int u) {
-    // `group` tile rows share a pass over the tile columns, so that a wave of the GPU reads few
+    // eight tile rows share a pass over the tile columns, so that a wave of the GPU reads few
     // operand rows of either side
-    const int tiles = p.tiles_m * p.tiles_n, z = u / tiles, t = u - z * tiles;
-    const int g = t / (p.group * p.tiles_n) * p.group, gn = min(p.group, p.tiles_m - g), r = t - g * p.tiles_n;
-    const long long kb = p.kb0 + p.kb1;
+    constexpr int G = 8;
     DenseUnit U;
-    U.m0 = (g + r % gn) * DenseCfg::BM;
+    U.q = 0;
+    if constexpr (E == DenseEnd::STORE)
+        while (U.q + 1 < p.n && u >= p.q[U.q + 1].first) ++U.q;
+    const DenseProblem& q = p.q[U.q];
+    u -= q.first;
+    const int tiles = q.tiles_m * q.tiles_n, z = u / tiles, t = u - z * tiles;
+    const int g = t / (G * q.tiles_n) * G, gn = min(G, q.tiles_m - g), r = t - g * q.tiles_n;
+    const long long kb = q.kb0 + q.kb1;
+    U.m0 = (g + r % gn) * 256;
     U.n = r / gn;
     U.z = z;
-    U.lo = static_cast<int>(kb * z / p.splits);
-    U.hi = static_cast<int>(kb * (z + 1) / p.splits);
+    U.lo = static_cast<int>(kb * z / q.splits);
+    U.hi = static_cast<int>(kb * (z + 1) / q.splits);
     return U;
 }
 
@@ -123,17 +191,26 @@ struct DenseSlabs {
     uint8_t* base;
     int used, lane;
     __device__ __forceinline__ uint8_t* take() {
-        uint8_t* s = base + used * DenseCfg::SLAB_BYTES;
+        uint8_t* s = base + used * DenseCfg<256>::SLAB_BYTES;
         used ^= 1;
-        if (lane == 0) ptx::bulk_wait_read<DenseCfg::SLABS - 1>();   // the copy that last used this slab has read it
+        if (lane == 0) ptx::bulk_wait_read<DenseCfg<256>::SLABS - 1>();   // the copy that last used this slab has read it
+        __syncwarp();
+        return s;
+    }
+    // The other slab too, right after take().
+    __device__ __forceinline__ uint8_t* take_other() {
+        uint8_t* s = base + used * DenseCfg<256>::SLAB_BYTES;
+        used ^= 1;
+        if (lane == 0) ptx::bulk_wait_read<0>();
         __syncwarp();
         return s;
     }
     static __device__ __forceinline__ int place(int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); }
-    // units [u0, u0 + 4) of this lane's row
-    __device__ __forceinline__ void put4(uint8_t* slab, int u0, const uint32_t* w) const {
+    // N units of this lane's row from u0 on
+    template <int N>
+    __device__ __forceinline__ void put(uint8_t* slab, int u0, const uint32_t* w) const {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < N; ++u)
             *reinterpret_cast<uint4*>(slab + place(lane, u0 + u)) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
     }
     // The slab's rows to rows row.. and columns col.. of `o` (T: its element); M rows exist.
@@ -153,18 +230,29 @@ struct DenseSlabs {
         }
         __syncwarp();
         T* c = static_cast<T*>(o.p) + z * z_stride + static_cast<long long>(row) * o.ld + col;
+        if (sizeof(T) == 2 && o.ld % 2 == 0 && reinterpret_cast<uintptr_t>(o.p) % 4 == 0) {   // two elements a lane
 #pragma unroll 4
-        for (int r = 0; r < min(rows, 32); ++r) {
+            for (int r = 0; r < min(rows, 32); ++r) {
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(slab + place(r, lane / 4) + lane % 4 * 4);
+                if (2 * lane + 1 < cols)
+                    *reinterpret_cast<uint32_t*>(c + r * o.ld + 2 * lane) = v;
+                else if (2 * lane < cols)
+                    *reinterpret_cast<uint16_t*>(c + r * o.ld + 2 * lane) = static_cast<uint16_t>(v);
+            }
+        } else {
+#pragma unroll 4
+            for (int r = 0; r < min(rows, 32); ++r) {
 #pragma unroll
-            for (int i = lane; i < PER; i += 32)
-                if (i < cols) c[r * o.ld + i] = reinterpret_cast<const T*>(slab + place(r, i / UNIT))[i % UNIT];
+                for (int i = lane; i < PER; i += 32)
+                    if (i < cols) c[r * o.ld + i] = reinterpret_cast<const T*>(slab + place(r, i / UNIT))[i % UNIT];
+            }
         }
         __syncwarp();
         if (lane == 0) ptx::bulk_commit();   // (an empty group: every slab used counts as one)
     }
 };
 
-// e and the sum of 32 logits of a row, relative to 2^ref; columns from `cols` on do not exist.
+// The exponentials of 32 logits of a row, relative to 2^ref, and their sum; columns from `cols` on do not exist.
 __device__ __forceinline__ float dense_exps(uint32_t (&r)[32], float ref, int cols) {
     float s0 = 0.0f, s1 = 0.0f;
     if (cols < 32) {
@@ -194,13 +282,24 @@ __device__ __forceinline__ float dense_exponent(float top) {
     return fabsf(top) < __int_as_float(0x7f800000) ? ceilf(top * 1.4426950408889634f) : 0.0f;
 }
 
-template <bool A_MN, bool B_MN, DenseEnd E>
-__global__ void __launch_bounds__(DenseCfg::THREADS, 1)
-    dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
-                      const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
-                      const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmC1,
-                      const __grid_constant__ CUtensorMap tmC2, const DenseParams p) {
-    using C = DenseCfg;
+// Adds a chunk's sum, relative to 2^ref, to a row's.
+__device__ __forceinline__ void dense_merge(float& to_ref, float& to_sum, float ref, float sum) {
+    if (sum == 0.0f) return;
+    if (to_sum == 0.0f) {
+        to_ref = ref;
+        to_sum = sum;
+    } else if (ref <= to_ref) {
+        to_sum += ref == to_ref ? sum : sum * exp2f(ref - to_ref);
+    } else {
+        to_sum = to_sum * exp2f(to_ref - ref) + sum;
+        to_ref = ref;
+    }
+}
+
+template <int BN, DenseEnd E>
+__global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
+    dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__ DenseParams p) {
+    using C = DenseCfg<BN>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -231,11 +330,11 @@ __global__ void __launch_bounds__(DenseCfg::THREADS, 1)
         ptx::mbar_init(drain_bar, 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
-        ptx::prefetch_tensormap(&tmA0);
-        ptx::prefetch_tensormap(&tmB0);
+        ptx::prefetch_tensormap(&maps.a[0][0]);
+        ptx::prefetch_tensormap(&maps.b[0][0]);
     }
     if (warp == 1) {
-        ptx::tmem_alloc_pair(ptx::smem_u32(tmem_holder), 512);
+        ptx::tmem_alloc_pair(ptx::smem_u32(tmem_holder), C::TMEM_COLS);
         ptx::tmem_relinquish_pair();
     }
     __syncwarp();
@@ -247,8 +346,7 @@ __global__ void __launch_bounds__(DenseCfg::THREADS, 1)
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
-    const int units = p.tiles_m * p.tiles_n * p.splits;
-    const int u0 = blockIdx.x / 2, ustep = gridDim.x / 2;
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const AbortNet net{ptx::smem_u32(const_cast<uint32_t*>(abort_flag)), 2};
     auto wait = [&](uint32_t bar, uint32_t parity, unsigned int code) {
         return wait_warp_pair(bar, parity, abort_flag, net, p.timeout_ns, p.status, code);
@@ -259,31 +357,34 @@ __global__ void __launch_bounds__(DenseCfg::THREADS, 1)
         const uint32_t full_leader0 = ptx::mapa_shared(full0, 0u);
         uint32_t s = 0, ph = 0;
         bool ok = true;
-        for (int u = u0; ok && u < units; u += ustep) {
-            const DenseUnit U = dense_unit(p, u);
+        for (int j = 0, u; ok && (u = dense_walk(p, pair, pairs, j)) < p.units; ++j) {
+            const DenseUnit U = dense_unit<E>(p, u);
+            const DenseProblem& q = p.q[U.q];
+            const bool a_mn = E == DenseEnd::STORE && q.a_mn;
+            const bool b_mn = E == DenseEnd::GATE_GRAD || (E == DenseEnd::STORE && q.b_mn);
             const int row = U.m0 + static_cast<int>(rank) * 128;
-            const int col = E == DenseEnd::GATE ? U.n * 128 : U.n * C::BN + static_cast<int>(rank) * 128;
+            const int col = E == DenseEnd::GATE ? U.n * C::CW : U.n * BN + static_cast<int>(rank) * C::CW;
             for (int kb = U.lo; kb < U.hi; ++kb) {
                 if (!wait(empty0 + 8 * s, ph ^ 1u, DEV_TIMEOUT_PRODUCER)) {
                     ok = false;
                     break;
                 }
-                const bool second = E == DenseEnd::STORE && kb >= p.kb0;
-                const int k = (second ? kb - p.kb0 : kb) * C::BK;
-                const CUtensorMap* ma = second ? &tmA1 : &tmA0;
-                const CUtensorMap* mb = second || (E == DenseEnd::GATE && rank) ? &tmB1 : &tmB0;
+                const int second = E == DenseEnd::STORE && kb >= q.kb0;
+                const int k = (second ? kb - q.kb0 : kb) * C::BK;
+                const CUtensorMap* ma = &maps.a[U.q][second];
+                const CUtensorMap* mb = &maps.b[U.q][E == DenseEnd::GATE ? static_cast<int>(rank) : second];
                 const uint32_t sa = ptx::smem_u32(smem) + s * C::STAGE_BYTES, sb = sa + C::A_BYTES;
                 const uint32_t fb = full_leader0 + 8 * s;
                 if (rank == 0) ptx::mbar_arrive_expect_tx_elected(full0 + 8 * s, 2 * C::STAGE_BYTES);
-                if constexpr (A_MN) {   // boxes of 64 rows of M × 64 of K
+                if (a_mn) {   // boxes of 64 rows of M × 64 of K
                     ptx::tma_load_2d_pair_elected(sa, ma, fb, row, k);
                     ptx::tma_load_2d_pair_elected(sa + 8192, ma, fb, row + 64, k);
                 } else {
                     ptx::tma_load_2d_pair_elected(sa, ma, fb, k, row);
                 }
-                if constexpr (B_MN) {
+                if (b_mn) {
                     ptx::tma_load_2d_pair_elected(sb, mb, fb, col, k);
-                    ptx::tma_load_2d_pair_elected(sb + 8192, mb, fb, col + 64, k);
+                    if constexpr (BN == 256) ptx::tma_load_2d_pair_elected(sb + 8192, mb, fb, col + 64, k);
                 } else {
                     ptx::tma_load_2d_pair_elected(sb, mb, fb, k, col);
                 }
@@ -298,17 +399,21 @@ __global__ void __launch_bounds__(DenseCfg::THREADS, 1)
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issue (the pair's leader)
         if (rank == 0) {
-            constexpr uint32_t IDESC = ptx::make_idesc(1, 1, A_MN, B_MN, C::BM, C::BN);
-            // K contiguous: a k-slice of 16 values is 32 bytes further in the row. Rows contiguous:
-            // boxes of 64 rows 8192 bytes apart, a k-slice 16 rows of 128 bytes further.
-            constexpr uint64_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2, STEP = C::STAGE_BYTES / 16;
+            constexpr uint64_t STEP = C::STAGE_BYTES / 16;
             const uint32_t stage0 = ptx::smem_u32(smem);
-            const uint64_t adesc0 = ptx::sdesc_sw128(stage0, A_MN ? 8192 : 16, 1024);
-            const uint64_t bdesc0 = ptx::sdesc_sw128(stage0 + C::A_BYTES, B_MN ? 8192 : 16, 1024);
             uint32_t s = 0, ph = 0;
             bool ok = true;
-            for (int u = u0, j = 0; ok && u < units; u += ustep, ++j) {
-                const DenseUnit U = dense_unit(p, u);
+            for (int j = 0, u; ok && (u = dense_walk(p, pair, pairs, j)) < p.units; ++j) {
+                const DenseUnit U = dense_unit<E>(p, u);
+                const DenseProblem& q = p.q[U.q];
+                const bool a_mn = E == DenseEnd::STORE && q.a_mn;
+                const bool b_mn = E == DenseEnd::GATE_GRAD || (E == DenseEnd::STORE && q.b_mn);
+                const uint32_t idesc = ptx::make_idesc(1, 1, a_mn, b_mn, C::BM, BN);
+                // K contiguous: a k-slice of 16 values is 32 bytes further in the row. Rows contiguous:
+                // boxes of 64 rows 8192 bytes apart, a k-slice 16 rows of 128 bytes further.
+                const uint64_t as = a_mn ? 128 : 2, bs = b_mn ? 128 : 2;
+                const uint64_t adesc0 = ptx::sdesc_sw128(stage0, a_mn ? 8192 : 16, 1024);
+                const uint64_t bdesc0 = ptx::sdesc_sw128(stage0 + C::A_BYTES, b_mn ? 8192 : 16, 1024);
                 const uint32_t b = j & 1;
                 if (!wait(acce0 + 8 * b, ((j >> 1) & 1) ^ 1u, DEV_TIMEOUT_MMA_ACC)) {
                     ok = false;
@@ -322,9 +427,8 @@ __global__ void __launch_bounds__(DenseCfg::THREADS, 1)
                     }
                     ptx::tc_fence_after();
                     const uint64_t ad = adesc0 + s * STEP, bd = bdesc0 + s * STEP;
-                    ptx::mma_f16_pair_x4_elected(tmem_base + b * C::BN, ad, bd, ad + A_STEP, bd + B_STEP, ad + 2 * A_STEP,
-                                                 bd + 2 * B_STEP, ad + 3 * A_STEP, bd + 3 * B_STEP, IDESC,
-                                                 kb > U.lo ? 1u : 0u);
+                    ptx::mma_f16_pair_x4_elected(tmem_base + b * BN, ad, bd, ad + as, bd + bs, ad + 2 * as, bd + 2 * bs,
+                                                 ad + 3 * as, bd + 3 * bs, idesc, kb > U.lo ? 1u : 0u);
                     ptx::mma_commit_pair_multicast_elected(empty0 + 8 * s, 0x3);
                     if (++s == C::STAGES) {
                         s = 0;
@@ -345,37 +449,38 @@ __global__ void __launch_bounds__(DenseCfg::THREADS, 1)
         const int h = (warp - 2) >> 2;        // its share of the columns
         const uint32_t acce_leader0 = ptx::mapa_shared(acce0, 0u);
         DenseSlabs out{slabs + (warp - 2) * C::SLABS * C::SLAB_BYTES, 0, lane};
-        for (int u = u0, j = 0; u < units; u += ustep, ++j) {
-            const DenseUnit U = dense_unit(p, u);
+        for (int j = 0, u; (u = dense_walk(p, pair, pairs, j)) < p.units; ++j) {
+            const DenseUnit U = dense_unit<E>(p, u);
+            const DenseProblem& q = p.q[U.q];
             const uint32_t b = j & 1;
             const int row0 = U.m0 + static_cast<int>(rank) * 128 + quarter * 32, row = row0 + lane;
-            if (!wait(accf0 + 8 * b, (j >> 1) & 1, DEV_TIMEOUT_EPILOGUE)) break;
-            ptx::tc_fence_after();
+            const int col0 = U.n * BN + h * C::CW;                            // (GATE: of the two tiles side by side)
+            const uint32_t t = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * BN;
+            const uint32_t th = t + h * C::CW;
             auto release = [&]() {   // the accumulator is read: free for the tile after the next
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_cluster_relaxed(acce_leader0 + 8 * b);
             };
-            const uint32_t t = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * C::BN;
             if constexpr (E == DenseEnd::STORE) {
-                const uint32_t th = t + h * 128;
-                const int col0 = U.n * C::BN + h * 128;
-                const float f = p.factor && row < p.M ? p.factor[row] : 1.0f;
-                const float* plus = p.plus && row < p.M ? p.plus + static_cast<long long>(row) * p.ld_plus : nullptr;
-                const long long z_stride = static_cast<long long>(p.M) * p.out[0].ld;
+                const float f = q.factor && row < q.M ? q.factor[row] : 1.0f;
+                if (!wait(accf0 + 8 * b, (j >> 1) & 1, DEV_TIMEOUT_EPILOGUE)) break;
+                ptx::tc_fence_after();
+                const float* plus = q.plus && row < q.M ? q.plus + static_cast<long long>(row) * q.ld_plus : nullptr;
+                const long long z_stride = static_cast<long long>(q.M) * q.out.ld;
                 auto values = [&](uint32_t (&r)[32], int c) {
                     ptx::tmem_ld_32x32b_x32(th + c, r);
                     ptx::tmem_ld_wait(r);
-                    if (c == 96) release();
-                    if (p.factor) {
+                    if (c + 32 == C::CW) release();
+                    if (q.factor) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             r[i] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(r[i]) * f);
                     }
-                    if (plus) {   // (rows of whole 16-byte pieces, in a workspace)
+                    if (plus) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
-                            if (col0 + c + i >= p.N) continue;
+                            if (col0 + c + i >= q.N) continue;
                             const float4 x = *reinterpret_cast<const float4*>(plus + col0 + c + i);
                             r[i] = __float_as_uint(__uint_as_float(r[i]) + x.x);
                             r[i + 1] = __float_as_uint(__uint_as_float(r[i + 1]) + x.y);
@@ -384,128 +489,143 @@ __global__ void __launch_bounds__(DenseCfg::THREADS, 1)
                         }
                     }
                 };
-                if (p.f32) {
+                if (q.f32) {
 #pragma unroll 1
-                    for (int c = 0; c < 128; c += 32) {
+                    for (int c = 0; c < C::CW; c += 32) {
                         uint32_t r[32];
                         values(r, c);
                         uint8_t* slab = out.take();
-                        out.put4(slab, 0, r);
-                        out.put4(slab, 4, r + 16);
-                        out.out<float>(slab, &tmC0, p.out[0], row0, col0 + c, U.z, p.M, z_stride);
+                        out.put<8>(slab, 0, r);
+                        out.out<float>(slab, &maps.c[U.q], q.out, row0, col0 + c, U.z, q.M, z_stride);
                     }
                 } else {
 #pragma unroll 1
-                    for (int c = 0; c < 128; c += 64) {
-                        uint32_t w[32];
+                    for (int c = 0; c < C::CW; c += 64) {
+                        uint8_t* slab = out.take();
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             uint32_t r[32];
                             values(r, c + 32 * k);
+                            uint32_t w[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                w[16 * k + i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                                w[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                            out.put<4>(slab, 4 * k, w);
                         }
-                        uint8_t* slab = out.take();
-                        out.put4(slab, 0, w);
-                        out.put4(slab, 4, w + 16);
-                        out.out<__nv_bfloat16>(slab, &tmC0, p.out[0], row0, col0 + c, U.z, p.M, z_stride);
+                        out.out<__nv_bfloat16>(slab, &maps.c[U.q], q.out, row0, col0 + c, U.z, q.M, z_stride);
                     }
                 }
             } else if constexpr (E == DenseEnd::GATE) {
-                const uint32_t th = t + h * 64;
-                const int col0 = U.n * 128 + h * 64;
-                uint8_t* slab = out.take();
+                // half of the tile's CW columns of h to a warp; in a narrow tile the warps of the second
+                // half have nothing to do (a slab is 64 columns wide)
+                constexpr int W = 64;
+                if (!wait(accf0 + 8 * b, (j >> 1) & 1, DEV_TIMEOUT_EPILOGUE)) break;
+                ptx::tc_fence_after();
+                if (BN == 256 || h == 0) {
+                    const uint32_t tg = t + h * W;
+                    const int hc = U.n * C::CW + h * W;
+                    uint8_t* slab = out.take();
+                    dense_with_act(p.act, [&](auto a) {
 #pragma unroll 1
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t g[32], x[32], w[16];
-                    ptx::tmem_ld_32x32b_x32(th + c, g);
-                    ptx::tmem_ld_32x32b_x32(th + 128 + c, x);
-                    ptx::tmem_ld_wait(g);
-                    ptx::tmem_ld_wait(x);
-                    float unused;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = pack_bf16(dense_act<false>(p.act, __uint_as_float(g[2 * i]), unused) * __uint_as_float(x[2 * i]),
-                                         dense_act<false>(p.act, __uint_as_float(g[2 * i + 1]), unused) *
-                                             __uint_as_float(x[2 * i + 1]));
-                    out.put4(slab, c / 8, w);
-                }
-                out.out<__nv_bfloat16>(slab, &tmC0, p.out[0], row0, col0, 0, p.M, 0);
-                if (p.out[1].p) {
-#pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {
-                        slab = out.take();
-#pragma unroll
-                        for (int c = 0; c < 64; c += 32) {
-                            uint32_t g[32], w[16];
-                            ptx::tmem_ld_32x32b_x32(th + 128 * k + c, g);
+                        for (int c = 0; c < W; c += 16) {
+                            uint32_t g[16], x[16], w[8];
+                            ptx::tmem_ld_32x32b_x16(tg + c, g);
+                            ptx::tmem_ld_32x32b_x16(tg + C::CW + c, x);
                             ptx::tmem_ld_wait(g);
+                            ptx::tmem_ld_wait(x);
+                            float unused;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                w[i] = pack_bf16(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
-                            out.put4(slab, c / 8, w);
+                            for (int i = 0; i < 8; ++i)
+                                w[i] = pack_bf16(
+                                    dense_act<decltype(a)::value, false>(__uint_as_float(g[2 * i]), unused) *
+                                        __uint_as_float(x[2 * i]),
+                                    dense_act<decltype(a)::value, false>(__uint_as_float(g[2 * i + 1]), unused) *
+                                        __uint_as_float(x[2 * i + 1]));
+                            out.put<2>(slab, c / 8, w);
                         }
-                        out.out<__nv_bfloat16>(slab, k ? &tmC2 : &tmC1, k ? p.out[2] : p.out[1], row0, col0, 0, p.M, 0);
+                    });
+                    out.out<__nv_bfloat16>(slab, &maps.c[0], q.out, row0, hc, 0, q.M, 0);
+                    if (p.more[0].p) {
+#pragma unroll 1
+                        for (int k = 0; k < 2; ++k) {
+                            slab = out.take();
+#pragma unroll
+                            for (int c = 0; c < W; c += 32) {
+                                uint32_t g[32], w[16];
+                                ptx::tmem_ld_32x32b_x32(tg + C::CW * k + c, g);
+                                ptx::tmem_ld_wait(g);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    w[i] = pack_bf16(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
+                                out.put<4>(slab, c / 8, w);
+                            }
+                            out.out<__nv_bfloat16>(slab, &maps.c[1 + k], p.more[k], row0, hc, 0, q.M, 0);
+                        }
                     }
                 }
                 release();
             } else if constexpr (E == DenseEnd::GATE_GRAD) {
-                const uint32_t th = t + h * 128;
-                const int col0 = U.n * C::BN + h * 128;
-                const long long at = static_cast<long long>(row) * p.ld_kept;
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
-                    uint32_t wg[32], wu[32];
+                // 16 columns at a time; what was kept of them is on its way while the 16 before are worked on
+                const __nv_bfloat16* gp = p.gate + static_cast<long long>(row) * p.ld_kept + col0;
+                const __nv_bfloat16* up = p.up + static_cast<long long>(row) * p.ld_kept + col0;
+                const int there = row < q.M ? q.N - col0 : 0;   // (the buffers' rows are whole pieces)
+                uint4 g4[2], u4[2];
+                auto fetch = [&](int c) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int col = col0 + c + 32 * k;
-                        uint4 g4[4], u4[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool in = row < p.M && col + 8 * i < p.N;   // (the buffers' rows are whole pieces)
-                            g4[i] = in ? *reinterpret_cast<const uint4*>(p.gate + at + col + 8 * i) : make_uint4(0, 0, 0, 0);
-                            u4[i] = in ? *reinterpret_cast<const uint4*>(p.up + at + col + 8 * i) : make_uint4(0, 0, 0, 0);
-                        }
-                        uint32_t r[32];
-                        ptx::tmem_ld_32x32b_x32(th + c + 32 * k, r);
-                        ptx::tmem_ld_wait(r);
-                        if (c + 32 * k == 96) release();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint32_t g2 = (&g4[i / 4].x)[i % 4], x2 = (&u4[i / 4].x)[i % 4];
-                            float dg[2], du[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float g = __uint_as_float(e ? g2 & 0xffff0000u : g2 << 16);
-                                const float x = __uint_as_float(e ? x2 & 0xffff0000u : x2 << 16);
-                                const float d = __uint_as_float(r[2 * i + e]);
-                                float slope;
-                                const float a = dense_act<true>(p.act, g, slope);
-                                dg[e] = d * x * slope;
-                                du[e] = d * a;
-                            }
-                            wg[16 * k + i] = pack_bf16(dg[0], dg[1]);
-                            wu[16 * k + i] = pack_bf16(du[0], du[1]);
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        const bool in = c + 8 * i < there && c < C::CW;
+                        g4[i] = in ? *reinterpret_cast<const uint4*>(gp + c + 8 * i) : make_uint4(0, 0, 0, 0);
+                        u4[i] = in ? *reinterpret_cast<const uint4*>(up + c + 8 * i) : make_uint4(0, 0, 0, 0);
                     }
-                    uint8_t* slab = out.take();
-                    out.put4(slab, 0, wg);
-                    out.put4(slab, 4, wg + 16);
-                    out.out<__nv_bfloat16>(slab, &tmC0, p.out[0], row0, col0 + c, 0, p.M, 0);
-                    slab = out.take();
-                    out.put4(slab, 0, wu);
-                    out.put4(slab, 4, wu + 16);
-                    out.out<__nv_bfloat16>(slab, &tmC1, p.out[1], row0, col0 + c, 0, p.M, 0);
-                }
+                };
+                fetch(0);
+                if (!wait(accf0 + 8 * b, (j >> 1) & 1, DEV_TIMEOUT_EPILOGUE)) break;
+                ptx::tc_fence_after();
+                dense_with_act(p.act, [&](auto act) {
+#pragma unroll 1
+                    for (int c = 0; c < C::CW; c += 64) {
+                        uint8_t* sg = out.take();   // both slabs: this warp's copies have read them
+                        uint8_t* su = out.take_other();
+#pragma unroll 1
+                        for (int k = 0; k < 64; k += 16) {
+                            uint32_t r[16], wg[8], wu[8];
+                            ptx::tmem_ld_32x32b_x16(th + c + k, r);
+                            const uint32_t gw[8] = {g4[0].x, g4[0].y, g4[0].z, g4[0].w, g4[1].x, g4[1].y, g4[1].z, g4[1].w};
+                            const uint32_t uw[8] = {u4[0].x, u4[0].y, u4[0].z, u4[0].w, u4[1].x, u4[1].y, u4[1].z, u4[1].w};
+                            fetch(c + k + 16);
+                            ptx::tmem_ld_wait(r);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                float dg[2], du[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float g = __uint_as_float(e ? gw[i] & 0xffff0000u : gw[i] << 16);
+                                    const float x = __uint_as_float(e ? uw[i] & 0xffff0000u : uw[i] << 16);
+                                    const float d = __uint_as_float(r[2 * i + e]);
+                                    float slope;
+                                    const float a = dense_act<decltype(act)::value, true>(g, slope);
+                                    dg[e] = d * x * slope;
+                                    du[e] = d * a;
+                                }
+                                wg[i] = pack_bf16(dg[0], dg[1]);
+                                wu[i] = pack_bf16(du[0], du[1]);
+                            }
+                            out.put<2>(sg, k / 8, wg);
+                            out.put<2>(su, k / 8, wu);
+                        }
+                        if (c + 64 == C::CW) release();
+                        out.out<__nv_bfloat16>(sg, &maps.c[0], q.out, row0, col0 + c, 0, q.M, 0);
+                        out.out<__nv_bfloat16>(su, &maps.c[1], p.more[0], row0, col0 + c, 0, q.M, 0);
+                    }
+                });
             } else {
-                const uint32_t th = t + h * 128;
-                const int col0 = U.n * C::BN + h * 128;
                 long long target = -1;
-                if (row < p.M)
+                if (row < q.M)
                     target = p.wide_targets ? static_cast<const long long*>(p.targets)[row]
                                             : static_cast<const int*>(p.targets)[row];
-                const bool kept = target >= 0 && target < p.N;
+                if (!wait(accf0 + 8 * b, (j >> 1) & 1, DEV_TIMEOUT_EPILOGUE)) break;
+                ptx::tc_fence_after();
+                const bool kept = target >= 0 && target < q.N;
                 const int mine = kept ? static_cast<int>(target) - col0 : -1;   // the target's column in this warp's
                 uint8_t *slab = nullptr, *slab1 = nullptr;   // the first and the second 64 columns
                 float sum = 0.0f, ref = 0.0f;
@@ -514,7 +634,7 @@ __global__ void __launch_bounds__(DenseCfg::THREADS, 1)
                 auto exps = [&](bool first) {
                     sum = 0.0f;
 #pragma unroll 1
-                    for (int c = 0; c < 128; c += 32) {
+                    for (int c = 0; c < C::CW; c += 32) {
                         uint32_t r[32];
                         ptx::tmem_ld_32x32b_x32(th + c, r);
                         ptx::tmem_ld_wait(r);
@@ -525,44 +645,41 @@ __global__ void __launch_bounds__(DenseCfg::THREADS, 1)
                                 if (mine == c + i) v = __uint_as_float(r[i]);
                             if (mine >= c && mine < c + 32) p.target_logit[row] = v;
                         }
-                        sum += dense_exps(r, ref, p.N - col0 - c);
+                        sum += dense_exps(r, ref, q.N - col0 - c);
                         if (p.exps) {
                             uint32_t w[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 w[i] = kept ? pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0u;
-                            out.put4(c < 64 ? slab : slab1, c % 64 / 8, w);
+                            out.put<4>(c < 64 ? slab : slab1, c % 64 / 8, w);
                         }
                     }
                 };
                 if (p.exps) {
                     slab = out.take();
-                    slab1 = out.base + out.used * C::SLAB_BYTES;
-                    if (lane == 0) ptx::bulk_wait_read<0>();
-                    __syncwarp();
-                    out.used ^= 1;
+                    if constexpr (BN == 256) slab1 = out.take_other();
                 }
                 exps(true);
-                const bool exists = col0 < p.N && row < p.M;
+                const bool exists = col0 < q.N && row < q.M;
                 if (__any_sync(0xffffffffu, exists && !dense_plain_sum(sum))) {
                     float top = __int_as_float(0xff800000);
 #pragma unroll 1
-                    for (int c = 0; c < 128; c += 32) {
+                    for (int c = 0; c < C::CW; c += 32) {
                         uint32_t r[32];
                         ptx::tmem_ld_32x32b_x32(th + c, r);
                         ptx::tmem_ld_wait(r);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (col0 + c + i < p.N) top = fmaxf(top, __uint_as_float(r[i]));
+                            if (col0 + c + i < q.N) top = fmaxf(top, __uint_as_float(r[i]));
                     }
                     if (!dense_plain_sum(sum)) ref = dense_exponent(top);
                     exps(false);
                 }
                 release();
-                if (exists) p.parts[static_cast<long long>(col0 / 128) * p.M + row] = make_float2(ref, sum);
+                if (exists) p.parts[static_cast<long long>(col0 / C::CW) * q.M + row] = make_float2(ref, sum);
                 if (p.exps) {
-                    out.out<__nv_bfloat16>(slab, &tmC0, p.out[0], row0, col0, 0, p.M, 0);
-                    out.out<__nv_bfloat16>(slab1, &tmC0, p.out[0], row0, col0 + 64, 0, p.M, 0);
+                    out.out<__nv_bfloat16>(slab, &maps.c[0], q.out, row0, col0, 0, q.M, 0);
+                    if constexpr (BN == 256) out.out<__nv_bfloat16>(slab1, &maps.c[0], q.out, row0, col0 + 64, 0, q.M, 0);
                 }
             }
             __syncwarp();
@@ -576,7 +693,7 @@ __global__ void __launch_bounds__(DenseCfg::THREADS, 1)
     ptx::cluster_sync();   // no CTA frees TMEM or exits while its peer may still signal it
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc_pair(tmem_base, 512);
+        ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
     }
 }
 

@@ -79,6 +79,29 @@ __global__ void __launch_bounds__(kThreads) square_sums_kernel(const __grid_cons
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     double sum = 0.0;
+    auto squares = [&](auto& v) {   // of some units
+        float s = 0.0f;
+        uint32_t any = 0;
+#pragma unroll
+        for (auto& w : v) {
+            float f[U];
+            unpack(w, f);
+#pragma unroll
+            for (int i = 0; i < U; ++i) s = fmaf(f[i], f[i], s);
+            any |= w.x | w.y | w.z | w.w;
+        }
+        if (s >= 7.9e-31f && s < __int_as_float(0x7f800000)) {   // 2^-100, infinity
+            sum += static_cast<double>(s);
+        } else if (any) {
+#pragma unroll
+            for (auto& w : v) {
+                float f[U];
+                unpack(w, f);
+#pragma unroll
+                for (int i = 0; i < U; ++i) sum += static_cast<double>(f[i]) * f[i];
+            }
+        }
+    };
     for (long long piece = blockIdx.x; piece < a.pieces; piece += gridDim.x) {
         const ClipTensor& t = a.t[tensor_of(a, piece)];
         const long long at = (piece - t.before) * a.piece;
@@ -87,32 +110,18 @@ __global__ void __launch_bounds__(kThreads) square_sums_kernel(const __grid_cons
         int done = 0;
         if (reinterpret_cast<uintptr_t>(x) % 16 == 0) {
             constexpr int STEP = kThreads * 32;
+            const uint4* x4 = reinterpret_cast<const uint4*>(x);
             for (; done + STEP <= n; done += STEP) {
                 uint4 v[Q];
 #pragma unroll
-                for (int q = 0; q < Q; ++q) v[q] = reinterpret_cast<const uint4*>(x + done)[q * kThreads + threadIdx.x];
-                float s = 0.0f;
-                uint32_t any = 0;
-#pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    float f[U];
-                    unpack(v[q], f);
-#pragma unroll
-                    for (int i = 0; i < U; ++i) s = fmaf(f[i], f[i], s);
-                    any |= v[q].x | v[q].y | v[q].z | v[q].w;
-                }
-                if (s >= 7.9e-31f && s < __int_as_float(0x7f800000)) {   // 2^-100, infinity
-                    sum += static_cast<double>(s);
-                } else if (any) {
-#pragma unroll
-                    for (int q = 0; q < Q; ++q) {
-                        float f[U];
-                        unpack(v[q], f);
-#pragma unroll
-                        for (int i = 0; i < U; ++i) sum += static_cast<double>(f[i]) * f[i];
-                    }
-                }
+                for (int q = 0; q < Q; ++q) v[q] = x4[done / U + q * kThreads + threadIdx.x];
+                squares(v);
             }
+            for (int i = done / U + threadIdx.x; i < n / U; i += kThreads) {
+                const uint4 v[1] = {x4[i]};
+                squares(v);
+            }
+            done = n / U * U;
         }
         for (int i = done + threadIdx.x; i < n; i += kThreads) {
             const double f = value(x[i]);
@@ -158,19 +167,24 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
         int done = 0;
         if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % 16 == 0) {
             constexpr int STEP = kThreads * Q * U;
+            const uint4* x4 = reinterpret_cast<const uint4*>(x);
+            uint4* y4 = reinterpret_cast<uint4*>(y);
+            auto times = [&](uint4 v) {
+                float e[U];
+                unpack(v, e);
+#pragma unroll
+                for (int i = 0; i < U; ++i) e[i] *= f;
+                return scaled ? pack(e) : v;
+            };
             for (; done + STEP <= n; done += STEP) {
                 uint4 v[Q];
 #pragma unroll
-                for (int q = 0; q < Q; ++q) v[q] = reinterpret_cast<const uint4*>(x + done)[q * kThreads + threadIdx.x];
+                for (int q = 0; q < Q; ++q) v[q] = x4[done / U + q * kThreads + threadIdx.x];
 #pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    float e[U];
-                    unpack(v[q], e);
-#pragma unroll
-                    for (int i = 0; i < U; ++i) e[i] *= f;
-                    reinterpret_cast<uint4*>(y + done)[q * kThreads + threadIdx.x] = scaled ? pack(e) : v[q];
-                }
+                for (int q = 0; q < Q; ++q) y4[done / U + q * kThreads + threadIdx.x] = times(v[q]);
             }
+            for (int i = done / U + threadIdx.x; i < n / U; i += kThreads) y4[i] = times(x4[i]);
+            done = n / U * U;
         }
         for (int i = done + threadIdx.x; i < n; i += kThreads) y[i] = scaled ? static_cast<T>(value(x[i]) * f) : x[i];
     }

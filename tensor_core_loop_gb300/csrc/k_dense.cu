@@ -4,23 +4,24 @@
 namespace tcl {
 namespace {
 
-template <bool A_MN, bool B_MN, DenseEnd E>
+template <int BN, DenseEnd E>
 cudaError_t launch(const DenseLaunch& a) {
-    auto kern = dense_pair_kernel<A_MN, B_MN, E>;
+    using C = DenseCfg<BN>;
+    auto kern = dense_pair_kernel<BN, E>;
     // the shared-memory opt-in is per function and device: set once per device
     static bool attr_done[64] = {};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DenseCfg::SMEM_BYTES);
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
         if (err != cudaSuccess) return err;
         if (dev >= 0 && dev < 64) attr_done[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.grid);
-    cfg.blockDim = dim3(DenseCfg::THREADS);
-    cfg.dynamicSmemBytes = DenseCfg::SMEM_BYTES;
+    cfg.gridDim = dim3(2 * a.pairs);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -31,20 +32,21 @@ cudaError_t launch(const DenseLaunch& a) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, a.a[0], a.a[1], a.b[0], a.b[1], a.c[0], a.c[1], a.c[2], a.p);
+    return cudaLaunchKernelEx(&cfg, kern, a.maps, a.p);
+}
+
+template <int BN>
+cudaError_t launch(const DenseLaunch& a) {
+    switch (a.end) {
+        case DenseEnd::GATE: return launch<BN, DenseEnd::GATE>(a);
+        case DenseEnd::GATE_GRAD: return launch<BN, DenseEnd::GATE_GRAD>(a);
+        case DenseEnd::ENTROPY: return launch<BN, DenseEnd::ENTROPY>(a);
+        default: return launch<BN, DenseEnd::STORE>(a);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_dense_pair(const DenseLaunch& a) {
-    switch (a.end) {
-        case DenseEnd::GATE: return launch<false, false, DenseEnd::GATE>(a);
-        case DenseEnd::GATE_GRAD: return launch<false, true, DenseEnd::GATE_GRAD>(a);
-        case DenseEnd::ENTROPY: return launch<false, false, DenseEnd::ENTROPY>(a);
-        default:
-            if (a.a_mn) return launch<true, true, DenseEnd::STORE>(a);
-            return a.b_mn ? launch<false, true, DenseEnd::STORE>(a) : launch<false, false, DenseEnd::STORE>(a);
-    }
-}
+cudaError_t launch_dense_pair(const DenseLaunch& a) { return a.bn == 256 ? launch<256>(a) : launch<128>(a); }
 
 }  // namespace tcl

@@ -85,88 +85,85 @@ __global__ void dense_join_kernel(const DenseJoin a) {
 // e there. Chunks relative to another power of two (a row's chunks differ only where logits leave
 // +-44 or so) are brought to c in place.
 //
-// A block takes 8 rows, 32 threads to a row; both the sums (64 bytes of a chunk's row at a time)
-// and the rows of x are read once.
-constexpr int kRowThreads = 32, kRowsBlock = 8;
+// A block of 256 threads takes ROWS rows: eight where there are thousands of them (64 bytes of a chunk's
+// row at a time), one where that leaves too few blocks.
+constexpr int kRowThreads = 256;
 
-__global__ void __launch_bounds__(kRowThreads * kRowsBlock) entropy_rows_kernel(const EntropyRows a) {
-    __shared__ float sh[kRowThreads][kRowsBlock + 1];
-    __shared__ float factor[kRowsBlock];
+template <int ROWS>
+__global__ void __launch_bounds__(kRowThreads) entropy_rows_kernel(const EntropyRows a) {
+    constexpr int KT = kRowThreads / ROWS;   // threads of a row's sums
+    __shared__ float2 sh[KT][ROWS + 1];
+    __shared__ float factor[ROWS];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int r = threadIdx.x % kRowsBlock, k = threadIdx.x / kRowsBlock;   // the sums: neighbouring threads, neighbouring rows
-    const long long row = static_cast<long long>(blockIdx.x) * kRowsBlock + r;
+    const int r = threadIdx.x % ROWS, k = threadIdx.x / ROWS;   // the sums: neighbouring threads, neighbouring rows
+    const long long row = static_cast<long long>(blockIdx.x) * ROWS + r;
     const bool in = row < a.rows;
-    auto over_slices = [&](float v, auto op) {   // the same for all threads of a row
-        sh[k][r] = v;
-        __syncthreads();
-        float all = sh[0][r];
-        for (int i = 1; i < kRowThreads; ++i) all = op(all, sh[i][r]);
-        __syncthreads();
-        return all;
-    };
-    const float none = __int_as_float(0xff800000);
-    float c = none;
-    if (in) {
-#pragma unroll 8
-        for (int i = k; i < a.chunks; i += kRowThreads) {
-            const float2 p = a.parts[static_cast<long long>(i) * a.rows + row];
-            if (p.y != 0.0f) c = fmaxf(c, p.x);
-        }
-    }
-    c = over_slices(c, [](float x, float y) { return fmaxf(x, y); });
-    if (c == none) c = 0.0f;
-    float s = 0.0f;
-    bool other = false;   // a chunk of this thread's is relative to another power of two
-    if (in) {
-#pragma unroll 8
-        for (int i = k; i < a.chunks; i += kRowThreads) {
-            const float2 p = a.parts[static_cast<long long>(i) * a.rows + row];
-            other |= p.x != c;
-            s += p.x == c ? p.y : p.y * exp2f(p.x - c);
-        }
-    }
-    s = over_slices(s, [](float x, float y) { return x + y; });
     long long target = -1;
-    if (in) target = a.wide_targets ? static_cast<const long long*>(a.targets)[row] : static_cast<const int*>(a.targets)[row];
+    float logit = 0.0f, weight = 0.0f;
+    if (in) {
+        target = a.wide_targets ? static_cast<const long long*>(a.targets)[row] : static_cast<const int*>(a.targets)[row];
+        logit = a.target_logit[row];
+        if (a.grad) weight = a.grad[row];
+    }
+    float c = 0.0f, s = 0.0f;
+    bool other = false;   // a chunk of this thread's is relative to something else than 1
+    if (in) {
+#pragma unroll 8
+        for (int i = k; i < a.chunks; i += KT) {
+            const float2 p = a.parts[static_cast<long long>(i) * a.rows + row];
+            other |= p.x != 0.0f;
+            dense_merge(c, s, p.x, p.y);
+        }
+    }
+    sh[k][r] = make_float2(c, s);
+    __syncthreads();
+    if (KT > 32 && k < 32) {   // (in a fixed order)
+        for (int i = k + 32; i < KT; i += 32) dense_merge(c, s, sh[i][r].x, sh[i][r].y);
+        sh[k][r] = make_float2(c, s);
+    }
+    if (KT > 32) __syncthreads();
+    c = s = 0.0f;
+    for (int i = 0; i < (KT < 32 ? KT : 32); ++i) dense_merge(c, s, sh[i][r].x, sh[i][r].y);
     const bool kept = target >= 0 && target < a.vocab;
     const float lse = fmaf(c, 0.69314718055994531f, logf(s));
     if (in && k == 0) {
-        a.loss[row] = kept ? lse - a.target_logit[row] : 0.0f;
+        a.loss[row] = kept ? lse - logit : 0.0f;
         a.lse[row] = lse;
     }
     if (!a.grad) return;   // (the same for all threads)
 
-    if (kept && other) {
-        for (int i = k; i < a.chunks; i += kRowThreads) {
+    if (kept && (other || c != 0.0f)) {
+        for (int i = k; i < a.chunks; i += KT) {
             const float ref = a.parts[static_cast<long long>(i) * a.rows + row].x;
             if (ref == c) continue;
             const float f = exp2f(ref - c);
-            for (int v = i * 128; v < min(i * 128 + 128, a.vocab); ++v) {
+            for (int v = i * a.chunk; v < min(i * a.chunk + a.chunk, a.vocab); ++v) {
                 __nv_bfloat16* e = a.e + row * a.ld_e + v;
                 *e = __float2bfloat16_rn(__bfloat162float(*e) * f);
             }
         }
     }
     if (k == 0) {
-        const float f = kept ? a.grad[row] / s : 0.0f;
+        const float f = kept ? weight / s : 0.0f;
         factor[r] = f;
         if (in) a.factor[row] = f;
     }
     __syncthreads();
-    if (kept && k == 0) a.e[row * a.ld_e + target] = __float2bfloat16_rn(expm1f(a.target_logit[row] - lse) * s);
-    // the rows of x, a warp each
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const long long mine = static_cast<long long>(blockIdx.x) * kRowsBlock + warp;
+    if (kept && k == 0) a.e[row * a.ld_e + target] = __float2bfloat16_rn(expm1f(logit - lse) * s);
+    // the rows of x: a warp each, or the block its one
+    constexpr int XT = ROWS == 1 ? kRowThreads : 32;
+    const int mine_of = threadIdx.x / XT, lane = threadIdx.x % XT;
+    const long long mine = static_cast<long long>(blockIdx.x) * ROWS + mine_of;
     if (mine >= a.rows) return;
-    const float f = factor[warp];
+    const float f = factor[mine_of];
     const __nv_bfloat16* x = a.x + mine * a.ld_x;
     uint4* to = reinterpret_cast<uint4*>(a.scaled + mine * a.ld_scaled);
     auto scale = [f](uint32_t w) {   // (a dropped token's row may hold anything)
         return f == 0.0f ? 0u : pack_bf16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
     };
 #pragma unroll 4
-    for (int i = lane; i < a.hidden / 8; i += 32) {
+    for (int i = lane; i < a.hidden / 8; i += XT) {
         const uint4 v = reinterpret_cast<const uint4*>(x)[i];
         to[i] = make_uint4(scale(v.x), scale(v.y), scale(v.z), scale(v.w));
     }
@@ -197,7 +194,8 @@ cudaError_t launch_dense_join(const DenseJoin& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_entropy_rows(const EntropyRows& a, cudaStream_t stream) {
-    return launch_pdl(entropy_rows_kernel, dim3((a.rows + kRowsBlock - 1) / kRowsBlock), kRowThreads * kRowsBlock, 0, stream, a);
+    if (a.rows > 2048) return launch_pdl(entropy_rows_kernel<8>, dim3((a.rows + 7) / 8), kRowThreads, 0, stream, a);
+    return launch_pdl(entropy_rows_kernel<1>, dim3(a.rows), kRowThreads, 0, stream, a);
 }
 
 }  // namespace tcl

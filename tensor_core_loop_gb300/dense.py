@@ -24,6 +24,7 @@ gradients are calls of their own.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import NamedTuple
 
 try:
@@ -83,7 +84,7 @@ def _call(fn, what, device, stream, *args):
 
     st = once(None)
     if st == _WORKSPACE:
-        room = torch.empty(size.value, dtype=torch.uint8, device=device)
+        room = torch.empty(size.value, dtype=torch.uint8, device=device)   # (on the stream: the caller is inside _on)
         st = once(room.data_ptr())
     if st:
         raise TclError(st, what)
@@ -230,15 +231,17 @@ def _tensors(tensors, name):
     n = len(tensors)
     if n > _INT:
         _too_large(name)
-    ptr, length, types = (ctypes.c_void_p * n)(), (ctypes.c_longlong * n)(), (ctypes.c_int * n)()
-    for i, t in enumerate(tensors):
-        code = _TYPES.get(t.dtype)
-        if code is None:
-            raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        ptr[i], length[i], types[i] = t.data_ptr(), t.numel(), code
-    return ptr, length, types
+    types = [_TYPES.get(t.dtype) for t in tensors]
+    if None in types:
+        raise TypeError(f"{name} must be bfloat16 or float32, not {tensors[types.index(None)].dtype}")
+    if not all([t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{name} must be contiguous")
+    return (array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]), array("i", types))
+
+
+def _at(a):
+    """The address of an array's first element."""
+    return a.buffer_info()[0]
 
 
 def grad_norm(tensors, stream=None):
@@ -251,7 +254,7 @@ def grad_norm(tensors, stream=None):
     device = _device(stream, "tensors", *tensors)
     with _on(stream):
         norm = torch.empty((), dtype=_F32, device=device)
-        _call(_lib().tcl_grad_norm, "grad_norm", device, stream, len(tensors), ptr, length, types, norm.data_ptr())
+        _call(_lib().tcl_grad_norm, "grad_norm", device, stream, len(tensors), *map(_at, (ptr, length, types)), norm.data_ptr())
     return norm
 
 
@@ -267,12 +270,14 @@ def clip_grads(tensors, max_norm: float, out=None, stream=None):
         raise ValueError("max_norm must not be negative")
     ptr, length, types = _tensors(tensors, "tensors")
     to = tensors if out is None else list(out)
-    if out is not None and [(t.shape, t.dtype) for t in to] != [(t.shape, t.dtype) for t in tensors]:
+    if out is not None and ([t.shape for t in to] != [t.shape for t in tensors] or
+                            [t.dtype for t in to] != [t.dtype for t in tensors]):
         raise ValueError("out must hold a tensor of the same shape and type for each one")
     to_ptr = ptr if out is None else _tensors(to, "out")[0]
+    host = [_at(a) for a in (ptr, to_ptr, length, types)]
     device = _device(stream, "tensors", *tensors, *(() if out is None else to))
     with _on(stream):
         norm = torch.empty((), dtype=_F32, device=device)
-        _call(_lib().tcl_clip_gradients, "clip_grads", device, stream, len(tensors), ptr, to_ptr, length, types, max_norm,
+        _call(_lib().tcl_clip_gradients, "clip_grads", device, stream, len(tensors), *host, max_norm,
               norm.data_ptr())
     return norm
