@@ -41,6 +41,11 @@ struct Mat {
     bool copy() const { return !on(p, 16) || (rows > 1 && ld % 8); }
 };
 
+// Rows of this library's own buffers start on whole lines of 128 bytes: a box of a tensor copy whose rows
+// straddle two lines each costs the L2 twice the requests (logits of 1023 tokens, hidden
+// 1030, at a pitch of 1032: a k-block every 665 cycles instead of 512).
+long long pitch_of(int cols) { return up(cols, 64); }
+
 // The workspace, dealt out in 256-byte steps. Planning goes past its end; nothing is launched then.
 struct Room {
     uint8_t* base;
@@ -56,9 +61,9 @@ struct Room {
     Mat operand(const void* p, long long ld, int rows, int cols) {
         Mat m = {static_cast<const bf16*>(p), rows > 1 ? ld : up(cols, 8), rows, cols};
         if (!m.copy()) return m;
-        const long long pitch = up(cols, 8);
+        const long long pitch = pitch_of(cols);
         bf16* to = take<bf16>(pitch * rows);
-        copies.job[copies.n++] = {m.p, ld, rows, cols, to};
+        copies.job[copies.n++] = {m.p, ld, rows, cols, to, pitch};
         return {to, pitch, rows, cols};
     }
 };
@@ -102,7 +107,9 @@ long long blocks_of(const Product& q) {
 
 // What a launch costs, in microseconds, measured on a GB300: a k-block of a tile, a tile's end (where it does
 // not hide behind the next tile's k-blocks), a launch, and the joining of K ranges.
-double block_us(int bn) { return bn == 256 ? 0.27 : 0.16; }
+// (A narrow tile has 2/3 of a wide one's operand bytes and half of its MMAs: the way from the L2, 64 bytes a cycle
+// and SM, bounds it.)
+double block_us(int bn) { return bn == 256 ? 0.27 : 0.23; }
 double tile_us(int bn) { return bn == 256 ? 3.0 : 2.0; }
 constexpr double kLaunchUs = 5.0;
 
@@ -531,7 +538,7 @@ int tcl_gated_ffn_grad(int tokens, int hidden, int inner, const void* grad, int 
              room.operand(Wup, ld_up, inner, hidden), room.operand(Wdown, ld_down, hidden, inner)};
     const Mat gr = room.operand(grad, ld_grad, tokens, hidden);
     const Mat kept = {static_cast<const bf16*>(h), ld_kept, tokens, inner};
-    const long long ldd = up(inner, 8);
+    const long long ldd = pitch_of(inner);
     bf16* dg = room.take<bf16>(ldd * tokens);
     bf16* du = room.take<bf16>(ldd * tokens);
     const Mat mg = {dg, ldd, tokens, inner}, mu = {du, ldd, tokens, inner};
@@ -626,11 +633,11 @@ int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int
     const Entropy n = {tokens, hidden, vocab, room.operand(X, ldx, tokens, hidden), room.operand(W, ldw, vocab, hidden), targets,
                        target_bytes, loss, lse};
     // tokens of a piece: whole tiles, pieces of one size
-    const long long lde = up(vocab, 8), most = std::max(256ll, kExpBytes / (2 * lde) / 256 * 256);
+    const long long lde = pitch_of(vocab), most = std::max(256ll, kExpBytes / (2 * lde) / 256 * 256);
     const int pieces = static_cast<int>((tokens + most - 1) / most);
     const int piece = static_cast<int>(std::min<long long>(tokens, up((tokens + pieces - 1) / pieces, 256)));
     const int most_chunks = tiles_of(vocab, 64);
-    const long long ldh = up(hidden, 8);
+    const long long ldh = pitch_of(hidden);
     bf16* e = room.take<bf16>(lde * piece);
     float2* parts = room.take<float2>(static_cast<long long>(most_chunks) * piece);
     float* target_logit = room.take<float>(piece);

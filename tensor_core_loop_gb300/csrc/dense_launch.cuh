@@ -36,11 +36,12 @@ int dense_few_per_sm(int bq);
 cudaError_t launch_dense_few(const DenseFewLaunch& a);
 
 // ---- passes (k_dense_rows.cu)
-struct DenseCopy {       // rows × cols of bf16 to a pitch of whole 16-byte pieces
+struct DenseCopy {       // rows × cols of bf16 to rows of whole 16-byte pieces
     const __nv_bfloat16* from;
     long long ld;
     int rows, cols;
     __nv_bfloat16* to;
+    long long ld_to;
 };
 constexpr int kDenseCopies = 6;
 struct DenseCopies {

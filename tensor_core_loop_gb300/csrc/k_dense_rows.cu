@@ -21,7 +21,8 @@ __global__ void dense_copy_kernel(const DenseCopies a) {
         unsigned short v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = col + k < c.cols ? from[k] : static_cast<unsigned short>(0);
-        reinterpret_cast<uint4*>(c.to)[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        *reinterpret_cast<uint4*>(c.to + row * c.ld_to + col) =
+            make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
 }
 

@@ -137,7 +137,7 @@ def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", keep: bool = Fa
     (tokens, hidden, inner, act), (ldx, ldg, ldu, ldd) = _ffn(x, w_gate, w_up, w_down, activation)
     device = _device(stream, "x", x, w_gate, w_up, w_down)
     with _on(stream):
-        pitch = (inner + 7) & ~7
+        pitch = (inner + 63) & ~63   # (rows on whole lines of 128 bytes)
         mid = torch.empty((3 if keep else 1, tokens, pitch), dtype=_BF16, device=device)
         out = torch.empty((tokens, hidden), dtype=_BF16, device=device)
         h = mid.data_ptr()
