@@ -1510,6 +1510,20 @@ int tensor_map_bf16(const void* ptr, uint64_t cols, uint64_t rows, uint64_t row_
     return r == CUDA_SUCCESS ? TCL_OK : TCL_ERR_LAUNCH;
 }
 
+int tensor_map_bf16_chunks(const void* ptr, uint64_t chunks, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
+                           uint32_t box_chunks, CUtensorMap* out) {
+    int st = encode_fn();
+    if (st) return st;
+    const cuuint64_t dims[3] = {64, rows, chunks};
+    const cuuint64_t strides[2] = {row_bytes, 128};
+    const cuuint32_t box[3] = {64, box_rows, box_chunks};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? TCL_OK : TCL_ERR_LAUNCH;
+}
+
 int tensor_map_result(const void* ptr, int bf16, uint64_t cols, uint64_t rows, uint64_t mats, uint64_t row_stride,
                       uint64_t mat_stride, CUtensorMap* out) {
     return encode_3d(bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ptr, cols, rows, mats,

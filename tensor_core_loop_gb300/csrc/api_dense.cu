@@ -38,6 +38,8 @@ struct Mat {
     const bf16* p;
     long long ld;
     int rows, cols;
+    bool whole = false;   // a buffer of this library's own: chunks of 64 columns are whole
+    bool chunks() const { return whole || cols % 64 == 0; }
     bool copy() const { return !on(p, 16) || (rows > 1 && ld % 8); }
 };
 
@@ -64,7 +66,7 @@ struct Room {
         const long long pitch = pitch_of(cols);
         bf16* to = take<bf16>(pitch * rows);
         copies.job[copies.n++] = {m.p, ld, rows, cols, to, pitch};
-        return {to, pitch, rows, cols};
+        return {to, pitch, rows, cols, true};
     }
 };
 
@@ -181,7 +183,11 @@ void reserve(Room& room, Group& g) {
     }
 }
 
-int map_of(const Mat& m, bool mn, int rows, CUtensorMap* out) {
+// Boxes of 64 columns × `rows` rows of a K-contiguous operand; of 64 rows × `rows` columns of the other
+// kind (two copies of 64 columns where the matrix has no whole chunks of them).
+int map_of(const Mat& m, bool mn, int rows, CUtensorMap* out, bool chunks = false) {
+    if (mn && chunks)
+        return tensor_map_bf16_chunks(m.p, blocks64(m.cols), m.rows, m.ld * 2, 64, rows / 64, out);
     return tensor_map_bf16(m.p, m.cols, m.rows, m.ld * 2, mn ? 64 : rows, out);
 }
 
@@ -217,8 +223,13 @@ int run(const Group& g, const Gpu& gpu) {
     for (int i = 0; i < g.n; ++i) {
         const Product& q = g.q[i];
         DenseProblem& d = p.q[i];
-        if ((st = map_of(q.a, q.a_mn, 128, &l.maps.a[i][0])) || (st = map_of(q.b, q.b_mn, g.bn / 2, &l.maps.b[i][0]))) return st;
-        if (q.two && ((st = map_of(q.a1, q.a_mn, 128, &l.maps.a[i][1])) || (st = map_of(q.b1, q.b_mn, g.bn / 2, &l.maps.b[i][1]))))
+        d.a_3d = q.a.chunks() && (!q.two || q.a1.chunks());
+        d.b_3d = q.b.chunks() && (!q.two || q.b1.chunks());
+        const int br = g.bn / 2;
+        if ((st = map_of(q.a, q.a_mn, 128, &l.maps.a[i][0], d.a_3d)) || (st = map_of(q.b, q.b_mn, br, &l.maps.b[i][0], d.b_3d)))
+            return st;
+        if (q.two && ((st = map_of(q.a1, q.a_mn, 128, &l.maps.a[i][1], d.a_3d)) ||
+                      (st = map_of(q.b1, q.b_mn, br, &l.maps.b[i][1], d.b_3d))))
             return st;
         d.M = q.M;
         d.N = q.N;
@@ -338,7 +349,8 @@ int gate_grad(const Ffn& f, const Mat& grad, const bf16* gate, const bf16* upp, 
               long long ldd, const Gpu& g) {
     DenseLaunch l = ended(DenseEnd::GATE_GRAD, f.T, f.F, f.H, 256, g);
     int st;
-    if ((st = map_of(grad, false, 128, &l.maps.a[0][0])) || (st = map_of(f.wd, true, 0, &l.maps.b[0][0]))) return st;
+    if ((st = map_of(grad, false, 128, &l.maps.a[0][0])) || (st = map_of(f.wd, true, l.bn / 2, &l.maps.b[0][0], f.wd.chunks()))) return st;
+    l.p.q[0].b_3d = f.wd.chunks();
     l.p.act = f.act;
     l.p.gate = gate;
     l.p.up = upp;
@@ -541,7 +553,7 @@ int tcl_gated_ffn_grad(int tokens, int hidden, int inner, const void* grad, int 
     const long long ldd = pitch_of(inner);
     bf16* dg = room.take<bf16>(ldd * tokens);
     bf16* du = room.take<bf16>(ldd * tokens);
-    const Mat mg = {dg, ldd, tokens, inner}, mu = {du, ldd, tokens, inner};
+    const Mat mg = {dg, ldd, tokens, inner, true}, mu = {du, ldd, tokens, inner, true};
     Product q[4] = {};
     // dX = dgate·Wgate + dup·Wup: one product over both
     q[0].a = mg;
@@ -657,8 +669,8 @@ int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int
         q[0].factor = factor;
         const bool last = t0 + rows == tokens;
         q[1] = {};
-        q[1].a = {e, lde, rows, vocab};
-        q[1].b = {scaled, ldh, rows, hidden};
+        q[1].a = {e, lde, rows, vocab, true};
+        q[1].b = {scaled, ldh, rows, hidden, true};
         q[1].a_mn = q[1].b_mn = true;
         q[1].M = vocab;
         q[1].N = hidden;

@@ -12,6 +12,9 @@ namespace tcl {
 // ---- services of api.cu (under the library's lock)
 // A 2-D map of a stored bf16 matrix (cols contiguous), 128-byte swizzle, boxes of 64 columns × box_rows.
 int tensor_map_bf16(const void* ptr, uint64_t cols, uint64_t rows, uint64_t row_bytes, uint32_t box_rows, CUtensorMap* out);
+// The same matrix as chunks of 64 columns: a 3-D map (64 columns, rows, chunks), boxes of 64 × box_rows × box_chunks.
+int tensor_map_bf16_chunks(const void* ptr, uint64_t chunks, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
+                           uint32_t box_chunks, CUtensorMap* out);
 
 // ---- products (k_dense.cu, k_dense_few.cu)
 struct DenseLaunch {

@@ -52,6 +52,7 @@ struct DenseProblem {
     int tiles_m, tiles_n, splits;
     int first;             // its first unit
     int a_mn, b_mn;        // STORE: rows (not K) contiguous; the other ends: both K, GATE_GRAD B's rows
+    int a_3d, b_3d;        // rows contiguous: both boxes of 64 rows in one copy (3-D maps of whole chunks of 64 rows)
     int f32;               // STORE: fp32 result
     DenseOut out;          // D, h or dgate or the exponentials
     const float* factor;   // STORE: of each row (NULL: ones); a row whose factor is zero is zeros
@@ -380,13 +381,17 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
                 const uint32_t sa = ptx::smem_u32(smem) + s * C::STAGE_BYTES, sb = sa + C::A_BYTES;
                 const uint32_t fb = full_leader0 + 8 * s;
                 if (rank == 0) ptx::mbar_arrive_expect_tx_elected(full0 + 8 * s, 2 * C::STAGE_BYTES);
-                if (a_mn) {   // boxes of 64 rows of M × 64 of K
+                if (a_mn && q.a_3d) {   // boxes of 64 rows of M × 64 of K
+                    ptx::tma_load_3d_pair_elected(sa, ma, fb, 0, k, row / 64);
+                } else if (a_mn) {
                     ptx::tma_load_2d_pair_elected(sa, ma, fb, row, k);
                     ptx::tma_load_2d_pair_elected(sa + 8192, ma, fb, row + 64, k);
                 } else {
                     ptx::tma_load_2d_pair_elected(sa, ma, fb, k, row);
                 }
-                if (b_mn) {
+                if (b_mn && q.b_3d) {
+                    ptx::tma_load_3d_pair_elected(sb, mb, fb, 0, k, col / 64);
+                } else if (b_mn) {
                     ptx::tma_load_2d_pair_elected(sb, mb, fb, col, k);
                     if constexpr (BN == 256) ptx::tma_load_2d_pair_elected(sb + 8192, mb, fb, col + 64, k);
                 } else {
