@@ -61,7 +61,8 @@ struct DenseProblem {
 };
 
 struct DenseMaps {
-    CUtensorMap a[kDenseProblems][2], b[kDenseProblems][2], c[kDenseProblems];   // (one problem: c for each result)
+    // (STORE: for each problem; the other ends: c for each result, GATE_GRAD a[1] gate and up)
+    CUtensorMap a[kDenseProblems][2], b[kDenseProblems][2], c[kDenseProblems];
 };
 
 struct DenseParams {
@@ -73,8 +74,6 @@ struct DenseParams {
     int long_units, extra;
     int act;
     DenseOut more[2];      // GATE: gate, up (no address: not asked for); GATE_GRAD: dup
-    const __nv_bfloat16 *gate, *up;   // GATE_GRAD; rows on 16-byte pieces
-    long long ld_kept;
     const void* targets;   // ENTROPY: M of them, int32 or int64
     int wide_targets;
     float2* parts;         // ENTROPY: [chunk of BN/2 columns][row of D]: exponent taken out, sum
@@ -143,7 +142,7 @@ struct DenseCfg {
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EW = 8;                    // epilogue warps
     static constexpr int SLABS = 2, SLAB_BYTES = 32 * 128;
-    static constexpr int NBARS = 2 * STAGES + 5;
+    static constexpr int NBARS = 2 * STAGES + 5 + EW;   // (a warp's own: GATE_GRAD)
     static constexpr int THREADS = 64 + 32 * EW;
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EW * SLABS * SLAB_BYTES + (NBARS + 2) * 8;
@@ -213,6 +212,17 @@ struct DenseSlabs {
 #pragma unroll
         for (int u = 0; u < N; ++u)
             *reinterpret_cast<uint4*>(slab + place(lane, u0 + u)) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+    }
+    template <int N>
+    __device__ __forceinline__ void get(const uint8_t* slab, int u0, uint32_t* w) const {
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const uint4 v = *reinterpret_cast<const uint4*>(slab + place(lane, u0 + u));
+            w[4 * u] = v.x;
+            w[4 * u + 1] = v.y;
+            w[4 * u + 2] = v.z;
+            w[4 * u + 3] = v.w;
+        }
     }
     // The slab's rows to rows row.. and columns col.. of `o` (T: its element); M rows exist.
     template <typename T>
@@ -333,6 +343,7 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
             ptx::mbar_init(acce0 + 8 * b, 2 * C::EW);
         }
         ptx::mbar_init(drain_bar, 1);
+        for (int w = 0; w < C::EW; ++w) ptx::mbar_init(drain_bar + 8 + 8 * w, 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&maps.a[0][0]);
@@ -458,6 +469,7 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
         const int h = (warp - 2) >> 2;        // its share of the columns
         const uint32_t acce_leader0 = ptx::mapa_shared(acce0, 0u);
         DenseSlabs out{slabs + (warp - 2) * C::SLABS * C::SLAB_BYTES, 0, lane};
+        [[maybe_unused]] uint32_t kept_phase = 0;
         for (int j = 0, u; (u = dense_walk(p, pair, pairs, j)) < p.units; ++j) {
             const DenseUnit U = dense_unit<E>(p, u);
             const DenseProblem& q = p.q[U.q];
@@ -574,42 +586,45 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
                 }
                 release();
             } else if constexpr (E == DenseEnd::GATE_GRAD) {
-                // 16 columns at a time; what was kept of them is on its way while the 16 before are worked on
-                const __nv_bfloat16* gp = p.gate + static_cast<long long>(row) * p.ld_kept + col0;
-                const __nv_bfloat16* up = p.up + static_cast<long long>(row) * p.ld_kept + col0;
-                const int there = row < q.M ? q.N - col0 : 0;   // (the buffers' rows are whole pieces)
-                uint4 g4[2], u4[2];
-                auto fetch = [&](int c) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const bool in = c + 8 * i < there && c < C::CW;
-                        g4[i] = in ? *reinterpret_cast<const uint4*>(gp + c + 8 * i) : make_uint4(0, 0, 0, 0);
-                        u4[i] = in ? *reinterpret_cast<const uint4*>(up + c + 8 * i) : make_uint4(0, 0, 0, 0);
+                // What was kept of 64 columns comes into the two slabs (gate, up) and is replaced there by dgate and
+                // dup: a lane reads and writes its own row. The first 64 columns of a tile are fetched before
+                // its accumulator is complete, so that they arrive meanwhile.
+                uint8_t *sg = out.base, *su = out.base + C::SLAB_BYTES;
+                const uint32_t bar = drain_bar + 8 + 8 * (warp - 2);
+                auto fetch = [&](int col) {
+                    if (lane == 0) {
+                        ptx::bulk_wait_read<0>();   // the slabs' last results are copied out
+                        ptx::mbar_arrive_expect_tx(bar, 2 * C::SLAB_BYTES);
+                        ptx::tma_load_2d(ptx::smem_u32(sg), &maps.a[1][0], bar, col, row0);
+                        ptx::tma_load_2d(ptx::smem_u32(su), &maps.a[1][1], bar, col, row0);
                     }
+                    __syncwarp();
                 };
-                fetch(0);
-                if (!wait(accf0 + 8 * b, (j >> 1) & 1, DEV_TIMEOUT_EPILOGUE)) break;
+                fetch(col0);
+                const bool ready = wait(accf0 + 8 * b, (j >> 1) & 1, DEV_TIMEOUT_EPILOGUE);
                 ptx::tc_fence_after();
+                bool here = true;
                 dense_with_act(p.act, [&](auto act) {
 #pragma unroll 1
                     for (int c = 0; c < C::CW; c += 64) {
-                        uint8_t* sg = out.take();   // both slabs: this warp's copies have read them
-                        uint8_t* su = out.take_other();
+                        if (c) fetch(col0 + c);
+                        here = here && wait(bar, kept_phase, DEV_TIMEOUT_EPILOGUE);
+                        kept_phase ^= 1u;
+                        if (!here || !ready) break;
 #pragma unroll 1
                         for (int k = 0; k < 64; k += 16) {
                             uint32_t r[16], wg[8], wu[8];
                             ptx::tmem_ld_32x32b_x16(th + c + k, r);
-                            const uint32_t gw[8] = {g4[0].x, g4[0].y, g4[0].z, g4[0].w, g4[1].x, g4[1].y, g4[1].z, g4[1].w};
-                            const uint32_t uw[8] = {u4[0].x, u4[0].y, u4[0].z, u4[0].w, u4[1].x, u4[1].y, u4[1].z, u4[1].w};
-                            fetch(c + k + 16);
+                            out.get<2>(sg, k / 8, wg);
+                            out.get<2>(su, k / 8, wu);
                             ptx::tmem_ld_wait(r);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 float dg[2], du[2];
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    const float g = __uint_as_float(e ? gw[i] & 0xffff0000u : gw[i] << 16);
-                                    const float x = __uint_as_float(e ? uw[i] & 0xffff0000u : uw[i] << 16);
+                                    const float g = __uint_as_float(e ? wg[i] & 0xffff0000u : wg[i] << 16);
+                                    const float x = __uint_as_float(e ? wu[i] & 0xffff0000u : wu[i] << 16);
                                     const float d = __uint_as_float(r[2 * i + e]);
                                     float slope;
                                     const float a = dense_act<decltype(act)::value, true>(g, slope);
@@ -627,6 +642,11 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
                         out.out<__nv_bfloat16>(su, &maps.c[1], p.more[0], row0, col0 + c, 0, q.M, 0);
                     }
                 });
+                if (!here || !ready) {
+                    if (lane == 0) spin_ns(200000);   // copies issued before the abort land within microseconds
+                    __syncwarp();
+                    break;
+                }
             } else {
                 long long target = -1;
                 if (row < q.M)
