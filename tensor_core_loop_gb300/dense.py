@@ -227,16 +227,24 @@ def cross_entropy_grad(x, w, targets, grad, out_dtype=None, stream=None):
 
 
 def _tensors(tensors, name):
-    """(host arrays of addresses, lengths and types) of contiguous bf16 and fp32 tensors."""
-    n = len(tensors)
-    if n > _INT:
+    """(addresses, lengths, types) of contiguous bf16 and fp32 tensors. (A model has hundreds of them: maps over
+    the methods cost half of a loop.)"""
+    if len(tensors) > _INT:
         _too_large(name)
-    types = [_TYPES.get(t.dtype) for t in tensors]
+    T = torch.Tensor
+    types = list(map(_TYPES.get, map(T.dtype.__get__, tensors)))
     if None in types:
         raise TypeError(f"{name} must be bfloat16 or float32, not {tensors[types.index(None)].dtype}")
-    if not all([t.is_contiguous() for t in tensors]):
+    if not all(map(T.is_contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous")
-    return (array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]), array("i", types))
+    return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), types
+
+
+def _where(stream, tensors):
+    """The GPU that all of them are on; they are recorded on ``stream`` as ``_device`` does."""
+    if len(set(map(torch.Tensor.get_device, tensors))) != 1:
+        raise ValueError("all tensors must be on one GPU")
+    return _device(stream, "tensors", *(tensors if stream is not None else tensors[:1]))
 
 
 def _at(a):
@@ -251,15 +259,16 @@ def grad_norm(tensors, stream=None):
     if not tensors:
         raise ValueError("at least one tensor")
     ptr, length, types = _tensors(tensors, "tensors")
-    device = _device(stream, "tensors", *tensors)
+    device = _where(stream, tensors)
+    host = array("Q", ptr), array("q", length), array("i", types)
     with _on(stream):
         norm = torch.empty((), dtype=_F32, device=device)
-        _call(_lib().tcl_grad_norm, "grad_norm", device, stream, len(tensors), *map(_at, (ptr, length, types)), norm.data_ptr())
+        _call(_lib().tcl_grad_norm, "grad_norm", device, stream, len(tensors), *map(_at, host), norm.data_ptr())
     return norm
 
 
 def clip_grads(tensors, max_norm: float, out=None, stream=None):
-    """Scales the tensors, in place or into ``out`` (a list of the same shapes and types), by
+    """Scales the tensors, in place or into ``out`` (a list of tensors of the same lengths and types), by
     max_norm / norm where their ``grad_norm`` is larger than ``max_norm``; a norm that is infinite or
     NaN scales nothing. Returns the norm before, an fp32 scalar on the GPU."""
     tensors = list(tensors)
@@ -269,15 +278,15 @@ def clip_grads(tensors, max_norm: float, out=None, stream=None):
     if not max_norm >= 0:
         raise ValueError("max_norm must not be negative")
     ptr, length, types = _tensors(tensors, "tensors")
-    to = tensors if out is None else list(out)
-    if out is not None and ([t.shape for t in to] != [t.shape for t in tensors] or
-                            [t.dtype for t in to] != [t.dtype for t in tensors]):
-        raise ValueError("out must hold a tensor of the same shape and type for each one")
-    to_ptr = ptr if out is None else _tensors(to, "out")[0]
-    host = [_at(a) for a in (ptr, to_ptr, length, types)]
-    device = _device(stream, "tensors", *tensors, *(() if out is None else to))
+    to_ptr, everything = ptr, tensors
+    if out is not None:
+        everything = tensors + list(out)
+        to_ptr, to_length, to_types = _tensors(everything[len(tensors):], "out")
+        if to_length != length or to_types != types:
+            raise ValueError("out must hold a tensor of the same length and type for each one")
+    device = _where(stream, everything)
+    host = array("Q", ptr), array("Q", to_ptr), array("q", length), array("i", types)
     with _on(stream):
         norm = torch.empty((), dtype=_F32, device=device)
-        _call(_lib().tcl_clip_gradients, "clip_grads", device, stream, len(tensors), *host, max_norm,
-              norm.data_ptr())
+        _call(_lib().tcl_clip_gradients, "clip_grads", device, stream, len(tensors), *map(_at, host), max_norm, norm.data_ptr())
     return norm
