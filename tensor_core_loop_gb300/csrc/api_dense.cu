@@ -328,20 +328,33 @@ int launch_few(DenseEnd end, const Mat& x, const Mat& w0, const Mat* w1, DenseFe
     DenseFewLaunch l = {};
     l.end = end;
     l.bq = p.T <= 16 ? 16 : p.T <= 32 ? 32 : 64;
-    int st;
-    if ((st = tensor_map_bf16(x.p, x.cols, x.rows, x.ld * 2, l.bq, &l.x)) || (st = map_of(w0, false, 128, &l.w[0]))) return st;
-    if (w1 && (st = map_of(*w1, false, 128, &l.w[1]))) return st;
     p.N = w0.rows;
     p.num_kb = static_cast<int>(blocks64(w0.cols));
-    p.tiles = tiles_of(w0.rows, 128);
     p.timeout_ns = kTimeoutNs;
     p.status = g.status;
-    // share tiles while every CTA has a place and two k-blocks or more
-    const int places = g.sms * dense_few_per_sm(l.bq);
-    p.split = 1;
-    while (p.split < 8 && static_cast<long long>(p.tiles) * p.split * 2 <= places && p.num_kb >= p.split * 4) p.split *= 2;
+    // Rows of a tile and CTAs that share one: the least time of the CTA with the most to load. In units of a
+    // row's k-block (128 bytes): a tile's end counts as 400 of them, the exchange of a shared tile's sums as 1500.
+    long long least = 0;
+    for (int split = 1; split <= 8; split *= 2) {
+        if (split > 1 && p.num_kb < 2 * split) break;
+        const int places = dense_few_clusters(split, g.sms);
+        for (int rows = 128; rows >= 64; rows -= 8) {
+            const long long tiles = tiles_of(p.N, rows), waves = (tiles + places - 1) / places;
+            if (split > 1 && waves > 1) continue;   // (a shared tile is its CTAs' only one)
+            const long long cost = waves * (static_cast<long long>(rows) * ((p.num_kb + split - 1) / split) + 400) +
+                                   (split > 1 ? 1500 : 0);
+            if (least && cost >= least) continue;
+            least = cost;
+            p.split = split;
+            p.rows = rows;
+            p.tiles = static_cast<int>(tiles);
+        }
+    }
+    int st;
+    if ((st = tensor_map_bf16(x.p, x.cols, x.rows, x.ld * 2, l.bq, &l.x)) || (st = map_of(w0, false, p.rows, &l.w[0]))) return st;
+    if (w1 && (st = map_of(*w1, false, p.rows, &l.w[1]))) return st;
     l.p = p;
-    l.grid = std::min(places / p.split, p.tiles) * p.split;
+    l.grid = std::min(p.split > 1 ? p.tiles : g.sms, p.tiles) * p.split;
     l.stream = g.stream;
     if (ctas) *ctas = l.grid;
     return status_of(launch_dense_few(l));
@@ -631,7 +644,7 @@ int tcl_cross_entropy(int tokens, int hidden, int vocab, const void* X, int ldx,
     const Entropy n = {tokens, hidden, vocab, room.operand(X, ldx, tokens, hidden), room.operand(W, ldw, vocab, hidden), targets,
                        target_bytes, loss, lse};
     const bool few = tokens <= kMostFew;
-    int chunks = few ? 4 * 2 * g.sms : tiles_of(vocab, 64), chunk = 0;
+    int chunks = few ? 4 * g.sms : tiles_of(vocab, 64), chunk = 0;
     float2* parts = room.take<float2>(static_cast<long long>(chunks) * tokens);
     float* target_logit = room.take<float>(tokens);
     if ((st = enough(room, workspace_bytes))) return st;

@@ -3,9 +3,10 @@
 // What bounds them is the weights' way from HBM, once: 128 weight rows are the MMA's M side
 // (tensor-memory lanes), the tokens its N side, so that no shared memory and no MMA is spent on
 // tokens that do not exist and a thread holds one output column of every token. The loads run
-// through a ring of 64-value k-blocks that keeps some 100 KB in flight on each SM; where
-// tiles leave places on the GPU free, the CTAs of a cluster share a tile's k-blocks and one
-// after another's sums are added over distributed shared memory.
+// through a ring of 64-value k-blocks that keeps some 170 to 200 KB in flight on each SM. A tile has as many
+// weight rows (128 at most) as give all SMs the same share; where there are too few rows
+// for that, the CTAs of a cluster share a tile's k-blocks and one after another's sums are
+// added over distributed shared memory.
 //
 // The ends are those of dense_product.cuh, for the forward direction: STORE, GATE (two weight
 // tiles to a CTA: 128 rows of either matrix), ENTROPY (sums over all vocabulary rows that a warp saw).
@@ -17,6 +18,7 @@ namespace tcl {
 
 struct DenseFewParams {
     int T, N, num_kb, tiles, split;
+    int rows;              // weight rows of a tile, a multiple of 8: as many as deal them out evenly (128 at most)
     int act, f32;
     int early;             // the weights are not what the kernel before this one in the stream writes
     DenseOut out[3];
@@ -34,21 +36,20 @@ struct DenseFewCfg {
     static constexpr int MATS = E_ == DenseEnd::GATE ? 2 : 1;
     static constexpr int A_BYTES = 128 * 128, Q_BYTES = BQ * 128;
     static constexpr int STAGE_BYTES = MATS * A_BYTES + Q_BYTES;
-    static constexpr int PER_SM = BQ <= 32 ? 2 : 1;
-    static constexpr int STAGES = (PER_SM == 2 ? 112640 : 204800) / STAGE_BYTES;
+    static constexpr int STAGES = 212992 / STAGE_BYTES;
     static constexpr int COLS = MATS * BQ;               // tensor-memory columns of a tile
     static constexpr int TMEM_COLS = 2 * COLS < 32 ? 32 : 2 * COLS;
     static constexpr int THREADS = 64 + 128;
     static constexpr int NBARS = 2 * STAGES + 5;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + (NBARS + 2) * 8;
-    static_assert(PER_SM * (SMEM_BYTES + 1024) <= 233472 && PER_SM * TMEM_COLS <= 512, "CTAs of an SM");
+    static_assert(SMEM_BYTES <= 232448 && TMEM_COLS <= 512, "fits an SM");
     static_assert(COLS * 128 * 4 <= STAGES * STAGE_BYTES, "a shared tile's sums fit the ring");
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor-memory columns");
 };
 
 // k-blocks of 64 values: four MMAs each, one or two weight tiles.
 template <int BQ, DenseEnd E>
-__global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E>::PER_SM)
+__global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, 1)
     dense_few_kernel(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1,
                      const __grid_constant__ CUtensorMap tmX, const DenseFewParams p) {
     using C = DenseFewCfg<BQ, E>;
@@ -101,9 +102,9 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E
     const int ahead = p.early && u0 < p.tiles ? min(hi - lo, C::STAGES) : 0;
     auto load_weights = [&](uint32_t s, int kb, int tile) {
         const uint32_t sa = ptx::smem_u32(smem) + s * C::STAGE_BYTES, fb = full0 + 8 * s;
-        ptx::mbar_arrive_expect_tx_elected(fb, C::STAGE_BYTES);
-        ptx::tma_load_2d_elected(sa, &tmW0, fb, kb * 64, tile * 128);
-        if constexpr (C::MATS == 2) ptx::tma_load_2d_elected(sa + C::A_BYTES, &tmW1, fb, kb * 64, tile * 128);
+        ptx::mbar_arrive_expect_tx_elected(fb, C::MATS * p.rows * 128 + C::Q_BYTES);
+        ptx::tma_load_2d_elected(sa, &tmW0, fb, kb * 64, tile * p.rows);
+        if constexpr (C::MATS == 2) ptx::tma_load_2d_elected(sa + C::A_BYTES, &tmW1, fb, kb * 64, tile * p.rows);
     };
     if (warp == 0)
         for (int i = 0; i < ahead; ++i) load_weights(i, lo + i, u0);
@@ -121,10 +122,12 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E
     // ENTROPY: what this warp has summed up over its tiles; lane i % 32 holds token i's
     [[maybe_unused]] float run_ref[(BQ + 31) / 32] = {}, run_sum[(BQ + 31) / 32] = {};
     // D of weight row `row` and token i, as this lane's (GATE: gate and up)
-    auto finish = [&](int row0, int i, float v, float v1) {
-        const int row = row0 + lane;
+    auto finish = [&](int tile, int i, float v, float v1) {
+        // (the lanes behind the tile's rows hold what the ring held before)
+        const int in_tile = (warp & 3) * 32 + lane, row0 = tile * p.rows + (warp & 3) * 32;
+        const int row = in_tile < p.rows ? row0 + lane : p.N;
         if constexpr (E == DenseEnd::ENTROPY) {
-            if (i >= p.T || row0 >= p.N) return;   // (the same for all lanes)
+            if (i >= p.T || row0 >= p.N || (warp & 3) * 32 >= p.rows) return;   // (the same for all lanes)
             const long long target =
                 p.wide_targets ? static_cast<const long long*>(p.targets)[i] : static_cast<const int*>(p.targets)[i];
             if (row == target && row < p.N) p.target_logit[i] = v;
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E
                         sums[(c + i) * 128] = __uint_as_float(r[i]);
                         if constexpr (C::MATS == 2) sums[(BQ + c + i) * 128] = __uint_as_float(r1[i]);
                     } else {
-                        finish(u * 128 + quarter * 32, c + i, __uint_as_float(r[i]),
+                        finish(u, c + i, __uint_as_float(r[i]),
                                C::MATS == 2 ? __uint_as_float(r1[i]) : 0.0f);
                     }
                 }
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, DenseFewCfg<BQ, E
                     v += ptx::ld_cluster_f32(at + 4 * (i * 128));
                     if constexpr (C::MATS == 2) v1 += ptx::ld_cluster_f32(at + 4 * ((BQ + i) * 128));
                 }
-                finish(u0 * 128 + quarter * 32, i, v, v1);
+                finish(u0, i, v, v1);
             }
         }
         __syncwarp();

@@ -35,7 +35,9 @@ struct DenseFewLaunch {
     int grid;
     cudaStream_t stream;
 };
-int dense_few_per_sm(int bq);
+// Clusters of `split` (1, 2, 4 or 8) of its CTAs that the GPU holds at once: fewer than its SMs would do for, since
+// a cluster stays within a group of SMs.
+int dense_few_clusters(int split, int sms);
 cudaError_t launch_dense_few(const DenseFewLaunch& a);
 
 // ---- passes (k_dense_rows.cu)

@@ -5,33 +5,45 @@ namespace tcl {
 namespace {
 
 template <int BQ, DenseEnd E>
-cudaError_t launch(const DenseFewLaunch& a) {
-    using C = DenseFewCfg<BQ, E>;
-    auto kern = dense_few_kernel<BQ, E>;
+cudaError_t prepare(int* dev) {
+    // the shared-memory opt-in is per function and device: set once per device
     static bool attr_done[64] = {};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    cudaError_t err = cudaGetDevice(dev);
     if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-        if (err != cudaSuccess) return err;
-        if (dev >= 0 && dev < 64) attr_done[dev] = true;
+    if (*dev < 0 || *dev >= 64 || !attr_done[*dev]) {
+        err = cudaFuncSetAttribute(dense_few_kernel<BQ, E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   DenseFewCfg<BQ, E>::SMEM_BYTES);
+        if (err == cudaSuccess && *dev >= 0 && *dev < 64) attr_done[*dev] = true;
     }
+    return err;
+}
+
+template <int BQ, DenseEnd E>
+cudaLaunchConfig_t config(int grid, int split, cudaStream_t stream, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.grid);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM_BYTES;
-    cfg.stream = a.stream;
-    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(DenseFewCfg<BQ, E>::THREADS);
+    cfg.dynamicSmemBytes = DenseFewCfg<BQ, E>::SMEM_BYTES;
+    cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = a.p.split;
+    attr[1].val.clusterDim.x = split;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, a.w[0], a.w[1], a.x, a.p);
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    return cfg;
+}
+
+template <int BQ, DenseEnd E>
+cudaError_t launch(const DenseFewLaunch& a) {
+    int dev = 0;
+    const cudaError_t err = prepare<BQ, E>(&dev);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = config<BQ, E>(a.grid, a.p.split, a.stream, attr);
+    return cudaLaunchKernelEx(&cfg, dense_few_kernel<BQ, E>, a.w[0], a.w[1], a.x, a.p);
 }
 
 template <int BQ>
@@ -45,7 +57,22 @@ cudaError_t launch(const DenseFewLaunch& a) {
 
 }  // namespace
 
-int dense_few_per_sm(int bq) { return bq <= 32 ? 2 : 1; }
+int dense_few_clusters(int split, int sms) {
+    // (one CTA of any of these kernels fills an SM, so one of them answers for all; asked once per device)
+    if (split == 1) return sms;
+    static int known[64][4] = {};
+    int dev = 0, n = 0;
+    if (prepare<16, DenseEnd::STORE>(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms / split * 3 / 4;
+    const int k = split == 2 ? 1 : split == 4 ? 2 : 3;
+    if (known[dev][k]) return known[dev][k];
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = config<16, DenseEnd::STORE>(split, split, nullptr, attr);
+    if (cudaOccupancyMaxActiveClusters(&n, dense_few_kernel<16, DenseEnd::STORE>, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return sms / split * 3 / 4;
+    }
+    return known[dev][k] = n;
+}
 
 cudaError_t launch_dense_few(const DenseFewLaunch& a) {
     return a.bq == 16 ? launch<16>(a) : a.bq == 32 ? launch<32>(a) : launch<64>(a);
