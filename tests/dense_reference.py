@@ -121,7 +121,7 @@ def cross_entropy(x, w, targets, grad=None, dtype=torch.bfloat16):
         return out
     hot = torch.zeros_like(p).scatter_(1, at, 1.0)
     weight = torch.where(kept, grad.double(), 0.0)[:, None]
-    relative = (arg + e_lse[:, None] + 2 * ACT) * SLACK
+    relative = torch.expm1(arg + e_lse[:, None]) + 2 * ACT
     d = V((p - hot) * weight, weight.abs() * (p * relative + (p - hot).abs() * BF) * SLACK + TINY * (weight != 0))
     dx = rounded(matmul(d, exactly(w)))
     # the rows of x are rounded once more after their scaling

@@ -99,3 +99,401 @@ def test_entropy(tokens, hidden, vocab, ids):
     ref.within(got[1][kept], ref.V(want[1].v[kept], want[1].e[kept]), "lse")
     ref.within(got[2], want[2], "dx")
     ref.within(got[3], want[3], "dw")
+
+
+# ------------------------------------------------------------------------------ layouts
+
+@pytest.mark.parametrize("tokens", [5, 130])
+@pytest.mark.parametrize("extra,offset", [(0, 1), (1, 0), (3, 5), (8, 8), (64, 0)])
+def test_ffn_of_rows_at_any_distance_and_address(tokens, extra, offset):
+    hidden, inner = 136, 200
+    x, wg, wu, wd, grad = block(7, tokens, hidden, inner)
+    out, kept = tcl.gated_ffn(x, wg, wu, wd, keep=True)
+    want = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept)
+    for which in range(5):
+        ops = [laid_out(t, t.shape[1] + extra, offset) if i == which or which == 4 else t for i, t in enumerate((x, wg, wu, wd))]
+        g = laid_out(grad, hidden + extra, offset) if which == 4 else grad
+        got, k = tcl.gated_ffn(*ops, keep=True)
+        assert torch.equal(got, out) and all(torch.equal(a, b) for a, b in zip(k, kept))
+        for a, b in zip(tcl.gated_ffn_grad(g, *ops, k), want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("tokens", [5, 130])
+@pytest.mark.parametrize("extra,offset", [(0, 1), (1, 0), (3, 5), (8, 8), (64, 0)])
+def test_entropy_of_rows_at_any_distance_and_address(tokens, extra, offset):
+    x, w, y, grad = tokens_of(8, tokens, 136, 700)
+    want = tcl.cross_entropy_grad(x, w, y, grad)
+    loss = tcl.cross_entropy(x, w, y)
+    for which in range(3):
+        a = laid_out(x, 136 + extra, offset) if which != 1 else x
+        b = laid_out(w, 136 + extra, offset) if which != 0 else w
+        for got, r in zip(tcl.cross_entropy_grad(a, b, y, grad), want):
+            assert torch.equal(got, r)
+        for got, r in zip(tcl.cross_entropy(a, b, y), loss):
+            assert torch.equal(got, r)
+
+
+def test_kept_rows_at_another_distance():
+    x, wg, wu, wd, grad = block(9, 150, 64, 90)
+    _, kept = tcl.gated_ffn(x, wg, wu, wd, keep=True)
+    want = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept)
+    moved = []
+    for t in kept:
+        room = torch.full((150, 104), float("nan"), dtype=BF16, device=DEV)
+        room[:, :90] = t
+        moved.append(room[:, :90])
+    for a, b in zip(tcl.gated_ffn_grad(grad, x, wg, wu, wd, tcl.GatedFfnKept(*moved)), want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("tokens,hidden,inner", [(3, 64, 72), (200, 130, 257)])
+def test_ffn_weights_gradients_in_fp32(tokens, hidden, inner):
+    x, wg, wu, wd, grad = block(10, tokens, hidden, inner)
+    _, kept = tcl.gated_ffn(x, wg, wu, wd, keep=True)
+    got = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept, out_dtype=F32)
+    want = ref.gated_ffn_grad(grad, x, wg, wu, wd, "silu", F32)
+    assert [t.dtype for t in got] == [BF16, F32, F32, F32]
+    for g, w in zip(got, want):
+        ref.within(g, w, "gradient")
+    for g, h in zip(got[1:], tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept)[1:]):
+        assert torch.equal(g.to(BF16), h)
+
+
+@pytest.mark.parametrize("tokens,hidden,vocab", [(3, 64, 72), (200, 130, 1025)])
+def test_entropy_weights_gradient_in_fp32(tokens, hidden, vocab):
+    x, w, y, grad = tokens_of(11, tokens, hidden, vocab)
+    got = tcl.cross_entropy_grad(x, w, y, grad, out_dtype=F32)
+    assert got[3].dtype == F32
+    ref.within(got[3], ref.cross_entropy(x, w, y, grad, F32)[3], "dw")
+    assert torch.equal(got[3].to(BF16), tcl.cross_entropy_grad(x, w, y, grad)[3])
+
+
+# ------------------------------------------------------------------------------ no tokens, dropped tokens, values
+
+def test_no_tokens():
+    x, wg, wu, wd, grad = block(12, 0, 72, 130)
+    out, kept = tcl.gated_ffn(x, wg, wu, wd, keep=True)
+    assert out.shape == (0, 72) and all(t.shape == (0, 130) for t in kept)
+    for dtype in (BF16, F32):
+        dx, *dw = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept, out_dtype=dtype)
+        assert dx.shape == (0, 72) and not any(t.any() for t in dw)
+    y, g = torch.empty(0, dtype=torch.int64, device=DEV), torch.empty(0, device=DEV)
+    assert all(t.shape == (0,) for t in tcl.cross_entropy(x, wg, y))
+    loss, lse, dx, dw = tcl.cross_entropy_grad(x, wg, y, g)
+    assert dx.shape == (0, 72) and dw.shape == wg.shape and not dw.any()
+
+
+@pytest.mark.parametrize("tokens", [7, 64, 300])
+def test_dropped_tokens_may_hold_anything(tokens):
+    x, w, y, grad = tokens_of(13, tokens, 72, 1000, drop=0.0)
+    y[::3] = torch.tensor([-1, 1000, -2 ** 62, 2 ** 62, -100], device=DEV).repeat(tokens)[: y[::3].numel()]
+    x[::3] = torch.tensor([float("nan"), float("inf"), -float("inf"), 1e38], device=DEV).repeat(tokens)[: y[::3].numel(), None].to(BF16)
+    grad[::6] = float("nan")
+    loss, lse, dx, dw = tcl.cross_entropy_grad(x, w, y, grad)
+    want = ref.cross_entropy(x, w, y, grad)
+    kept = (y >= 0) & (y < 1000)
+    assert not loss[~kept].any() and not dx[~kept].any()
+    ref.within(loss, want[0], "loss")
+    ref.within(dx, want[2], "dx")
+    ref.within(dw, want[3], "dw")
+    assert torch.equal(tcl.cross_entropy(x, w, y)[0], loss) or tokens <= 64   # (few tokens: another order of the sums)
+    ref.within(tcl.cross_entropy(x, w, y)[0], want[0], "loss")
+
+
+@pytest.mark.parametrize("tokens", [7, 100])
+def test_every_token_dropped(tokens):
+    x, w, _, grad = tokens_of(14, tokens, 64, 300)
+    y = torch.full((tokens,), -100, device=DEV)
+    loss, _, dx, dw = tcl.cross_entropy_grad(x, w, y, grad)
+    assert not loss.any() and not dx.any() and not dw.any()
+
+
+def far_logits(seed, tokens, vocab, level, spread):
+    """x and w of which the first product of a row and a column sets the logits' level: rows at
+    +-level and 0 in turn, chunks of the vocabulary at different heights."""
+    g = torch.Generator().manual_seed(seed)
+    x, w = torch.randn(tokens, 64, generator=g), torch.randn(vocab, 64, generator=g) * spread / 8
+    x[:, 0] = torch.tensor([level, -level, 0.0, level / 2]).repeat(tokens)[:tokens]
+    w[:, 0] = 1.0
+    w[vocab // 3: vocab // 2, 0] = 0.25
+    y = torch.randint(0, vocab, (tokens,), generator=g)
+    return x.to(BF16).to(DEV), w.to(BF16).to(DEV), y.to(DEV), (torch.rand(tokens, generator=g) / tokens).to(DEV)
+
+
+@pytest.mark.parametrize("tokens", [9, 150])
+@pytest.mark.parametrize("level,spread", [(40.0, 1.0), (64.0, 8.0), (90.0, 1.0), (300.0, 20.0), (20000.0, 1.0)])
+def test_logits_far_from_zero(tokens, level, spread):
+    """Exponentials that leave fp32's range without their largest logit taken out, and chunks of one row that
+    do so while others do not."""
+    x, w, y, grad = far_logits(15, tokens, 1100, level, spread)
+    want = ref.cross_entropy(x, w, y, grad)
+    for got in (tcl.cross_entropy(x, w, y), tcl.cross_entropy_grad(x, w, y, grad)):
+        for g, r, what in zip(got, want, ("loss", "lse", "dx", "dw")):
+            ref.within(g, r, what)
+
+
+def test_masked_vocabulary():
+    """Columns at minus infinity (a masked part of the vocabulary) have no weight."""
+    x, w, y, _ = tokens_of(16, 200, 64, 900, drop=0.0)
+    x[:, 0], w[:, 0] = 1.0, 0.0
+    w[256:700, 0] = -float("inf")
+    y = torch.where((y >= 256) & (y < 700), y % 256, y)
+    keep = torch.cat([w[:256], w[700:]])
+    z = torch.where(y >= 700, y - 444, y)
+    for n in (10, 200):
+        got = tcl.cross_entropy(x[:n], w, y[:n])
+        want = ref.cross_entropy(x[:n], keep, z[:n])
+        for g, r in zip(got, want):
+            ref.within(g, r, "loss")
+
+
+def test_nan_stays_in_its_row():
+    x, w, y, _ = tokens_of(17, 100, 64, 500, drop=0.0)
+    wg, wu = w[:300], w[200:]
+    wd = w.t()[:, :300].contiguous()
+    out = tcl.gated_ffn(x, wg, wu, wd)
+    loss = tcl.cross_entropy(x, w, y)[0]
+    x[33] = float("nan")
+    rows = torch.arange(100, device=DEV) != 33
+    for n in (100, 50):
+        got = tcl.gated_ffn(x[:n], wg, wu, wd)
+        assert got[33].isnan().all()
+        full = torch.equal(got[rows[:n]], out[:n][rows[:n]])
+        assert full or n == 50
+        assert got[rows[:n]].isfinite().all()
+        got = tcl.cross_entropy(x[:n], w, y[:n])[0]
+        assert got[33].isnan() and got[rows[:n]].isfinite().all()
+    assert torch.equal(tcl.cross_entropy(x, w, y)[0][rows], loss[rows])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_over_their_whole_range(act):
+    """One hidden value and weights of one: gates of every size, up to where the results end."""
+    v = torch.cat([torch.linspace(-20, 20, 4001), torch.tensor([1e-30, -1e-30, 3e3, -3e3, 1e5, -1e5, 1e18, -1e18, 0.0, -0.0])])
+    x = torch.zeros(v.numel(), 8, dtype=BF16, device=DEV)
+    x[:, 0] = v.to(BF16).to(DEV)
+    x[:, 1] = 1.0
+    eye = torch.eye(8, dtype=BF16, device=DEV)
+    wg, wu, wd = eye[:1].contiguous(), eye[1:2].contiguous(), eye[:, :1].contiguous()
+    out, kept = tcl.gated_ffn(x, wg, wu, wd, activation=act, keep=True)
+    want = ref.gated_ffn(x, wg, wu, wd, act)
+    ref.within(out, want[0], "out")
+    grad = torch.zeros_like(x)
+    grad[:, 0] = 1.0
+    got = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept, activation=act)
+    ref.within(got[0], ref.gated_ffn_grad(grad, x, wg, wu, wd, act)[0], "dx")
+
+
+# ------------------------------------------------------------------------------ large sizes
+
+def test_exponentials_in_pieces():
+    """More than 2 GiB of exponentials: the pieces' gradients of w are added in fp32."""
+    tokens, vocab = 8192 + 300, 131072
+    x, w, y, grad = tokens_of(18, tokens, 64, vocab)
+    loss, lse, dx, dw = tcl.cross_entropy_grad(x, w, y, grad)
+    total = torch.zeros(vocab, 64, dtype=torch.float64, device=DEV)
+    bound = torch.zeros_like(total)
+    for i in range(0, tokens, 2048):
+        p = slice(i, i + 2048)
+        want = ref.cross_entropy(x[p], w, y[p], grad[p], F32)
+        ref.within(loss[p], want[0], "loss")
+        ref.within(dx[p], want[2], "dx")
+        total += want[3].v
+        bound += want[3].e + 2.0 ** -23 * want[3].v.abs()
+    ref.within(dw, ref.rounded(ref.V(total, bound)), "dw")
+
+
+def test_weights_past_32_bits_of_elements():
+    tokens, hidden, vocab = 70, 4096, 540_000
+    g = torch.Generator(device=DEV).manual_seed(19)
+    x = torch.randn(tokens, hidden, device=DEV, generator=g).to(BF16)
+    w = torch.empty(vocab, hidden, dtype=BF16, device=DEV)
+    for i in range(0, vocab, 60_000):
+        w[i:i + 60_000] = torch.randn(60_000, hidden, device=DEV, generator=g) * 0.02
+    y = torch.randint(vocab - 2000, vocab, (tokens,), device=DEV, generator=g)
+    grad = torch.rand(tokens, device=DEV, generator=g) / tokens
+    loss, lse, dx, dw = tcl.cross_entropy_grad(x, w, y, grad)
+    l = torch.cat([x.double() @ w[i:i + 60_000].double().t() for i in range(0, vocab, 60_000)], 1)
+    want = torch.logsumexp(l, 1)
+    error = float(ref.unit(hidden) * (x.double().abs() @ w[:1000].double().abs().t()).max()) * 1.5 + 1e-5
+    assert ((lse - want).abs() <= error).all()
+    assert ((loss - (want - l.gather(1, y[:, None])[:, 0])).abs() <= 2 * error).all()
+    rows = torch.cat([torch.arange(300, device=DEV), torch.arange(vocab - 2000, vocab, device=DEV)])
+    d = torch.exp(l[:, rows] - want[:, None])
+    d -= (rows == y[:, None]).double()
+    d *= grad.double()[:, None]
+    far = ref.rounded(ref.matmul(ref.V(d.t(), d.t().abs() * (ref.BF + 2 * error)), ref.V(x.double(), ref.BF * x.double().abs())))
+    ref.within(dw[rows], far, "dw")
+    few = tcl.cross_entropy(x[:5], w, y[:5])
+    assert ((few[1] - want[:5]).abs() <= error).all()
+
+
+def test_kept_past_32_bits_of_elements():
+    tokens, hidden, inner = 262_200, 64, 8320
+    g = torch.Generator(device=DEV).manual_seed(20)
+    x = torch.randn(tokens, hidden, device=DEV, generator=g).to(BF16)
+    wg, wu = ((torch.randn(inner, hidden, device=DEV, generator=g) / 8).to(BF16) for _ in range(2))
+    wd = (torch.randn(hidden, inner, device=DEV, generator=g) / 90).to(BF16)
+    grad = torch.randn(tokens, hidden, device=DEV, generator=g).to(BF16)
+    out, kept = tcl.gated_ffn(x, wg, wu, wd, keep=True)
+    dx, dwg, dwu, dwd = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept, out_dtype=F32)
+    for p in (slice(0, 200), slice(tokens - 200, tokens)):
+        for a, b in zip((out[p], *(k[p] for k in kept)), ref.gated_ffn(x[p], wg, wu, wd, "silu")):
+            ref.within(a, b, "forward")
+        ref.within(dx[p], ref.gated_ffn_grad(grad[p], x[p], wg, wu, wd, "silu")[0], "dx")
+    # Eight columns of h, summed over all tokens. An fp32 sum errs in each of its additions by 2^-23 of the partial
+    # sum at most (of one that starts anywhere, where K is cut into ranges): twice the largest one from the
+    # start on, and the 16 products that an MMA adds to it.
+    some = slice(inner - 8, inner)
+    r = ref.gated_ffn(x, wg[some], wu[some], wd[:, some], "silu")
+    gx, xx = ref.exactly(grad), ref.exactly(x)
+    dh = ref.matmul(gx, ref.exactly(wd[:, some]))
+    a, slope = ref.act("silu", r[1])
+    dg, du = ref.rounded(ref.times(ref.times(dh, r[2]), slope)), ref.rounded(ref.times(dh, a))
+    for got, left, right in ((dwg[some], dg, xx), (dwu[some], du, xx), (dwd[:, some].t(), r[3], gx)):
+        product = left.v[:, :, None] * right.v[:, None, :]
+        sums = product.cumsum(0)
+        bound = left.e.t() @ right.v.abs() + ref.unit(tokens) * 2 * (sums.abs().amax(0) + 16 * product.abs().amax(0))
+        ref.within(got, ref.V(sums[-1], bound), "weights' gradient")
+
+
+# ------------------------------------------------------------------------------ streams, graphs, threads
+
+def step(x, gate, up, down, table, targets, grad):
+    """A training step's dense part: block with a residual, loss, gradients, clipping."""
+    out, kept = tcl.gated_ffn(x, gate, up, down, keep=True)
+    y = x + out
+    loss, lse, dy, dtable = tcl.cross_entropy_grad(y, table, targets, grad)
+    dx, *dw = tcl.gated_ffn_grad(dy, x, gate, up, down, kept)
+    grads = [*dw, dtable]
+    before = [t.clone() for t in grads]
+    norm = tcl.clip_grads(grads, 0.01)
+    return dict(out=out, kept=kept, y=y, loss=loss, dy=dy, dx=dx, before=before, grads=grads, norm=norm)
+
+
+def operands(seed, tokens, hidden, inner, vocab):
+    x, gate, up, down, _ = block(seed, tokens, hidden, inner)
+    _, table, targets, grad = tokens_of(seed, tokens, hidden, vocab)
+    return x, gate, up, down, table, targets, grad
+
+
+def flat(r):
+    return [r["out"], *r["kept"], r["loss"], r["dy"], r["dx"], *r["before"], *r["grads"], r["norm"]]
+
+
+@pytest.mark.parametrize("tokens,hidden,inner,vocab", [(48, 64, 200, 333), (300, 136, 384, 2050)])
+def test_training_step(tokens, hidden, inner, vocab):
+    """The calls one after another, each against 64 bits of what it was given, eager and captured."""
+    ops = operands(21, tokens, hidden, inner, vocab)
+    x, gate, up, down, table, targets, grad = ops
+    r = step(*ops)
+    for a, b in zip((r["out"], *r["kept"]), ref.gated_ffn(x, gate, up, down, "silu")):
+        ref.within(a, b, "block")
+    loss, _, dy, dtable = ref.cross_entropy(r["y"], table, targets, grad)
+    ref.within(r["loss"], loss, "loss")
+    ref.within(r["dy"], dy, "dy")
+    ref.within(r["before"][3], dtable, "dtable")
+    for a, b in zip((r["dx"], *r["before"][:3]), ref.gated_ffn_grad(r["dy"], x, gate, up, down, "silu")):
+        ref.within(a, b, "gradient")
+    norm = float(sum((t.double() ** 2).sum() for t in r["before"])) ** 0.5
+    assert norm > 0.01 and abs(float(r["norm"]) - norm) <= 20 * 2.0 ** -24 * norm
+    for t, g in zip(r["before"], r["grads"]):
+        exact = t.double() * (0.01 / norm)
+        assert ((g.double() - exact).abs() <= (ref.BF + 2.0 ** -19) * exact.abs() + ref.TINY).all()
+
+    # captured, and replayed with other tokens in the same places
+    static = [t.clone() for t in ops]
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        held = step(*static)
+    for seed in (21, 22):
+        fresh = operands(seed, tokens, hidden, inner, vocab)
+        for s, t in zip(static, fresh):
+            s.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(flat(held), flat(step(*fresh))):
+            assert torch.equal(a, b)
+
+
+def test_same_bits_again():
+    ops = operands(23, 513, 320, 1000, 5003)
+    first = flat(step(*ops))
+    for _ in range(3):
+        for a, b in zip(first, flat(step(*ops))):
+            assert torch.equal(a, b)
+
+
+def test_streams_side_by_side():
+    """Steps of different sizes on two streams and the current one, without any order between them."""
+    jobs = [operands(24, 300, 136, 384, 2050), operands(25, 20, 1030, 515, 700), operands(26, 1000, 256, 1030, 9001)]
+    alone = [[t.clone() for t in flat(step(*ops))] for ops in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.current_stream()]
+    got = []
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, flat(step(*jobs[i]))))
+    torch.cuda.synchronize()
+    for i, r in got:
+        for a, b in zip(r, alone[i]):
+            assert torch.equal(a, b)
+
+
+def test_given_stream():
+    """Calls on a stream that is not the current one, whose operands are dropped right after."""
+    ops = operands(27, 200, 130, 300, 1500)
+    x, gate, up, down, table, targets, grad = ops
+    out, kept = tcl.gated_ffn(x, gate, up, down, keep=True)
+    want = [out, *tcl.cross_entropy(x, table, targets), *tcl.cross_entropy_grad(x, table, targets, grad),
+            *tcl.gated_ffn_grad(x, x, gate, up, down, kept), tcl.grad_norm([gate, up])]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    a = [t.clone() for t in ops]
+    s.wait_stream(torch.cuda.current_stream())
+    o, k = tcl.gated_ffn(*a[:4], keep=True, stream=s)
+    got = [o, *tcl.cross_entropy(a[0], a[4], a[5], stream=s), *tcl.cross_entropy_grad(a[0], a[4], a[5], a[6], stream=s),
+           *tcl.gated_ffn_grad(a[0], *a[:4], k, stream=s), tcl.grad_norm(a[1:3], stream=s)]
+    del a, k
+    junk = [torch.full_like(t, 3) for t in ops]   # (takes the memory if it was given back)
+    s.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+    del junk
+
+
+def test_two_threads():
+    import threading
+    jobs = [operands(28, 300, 136, 384, 2050), operands(29, 40, 1030, 515, 700)]
+    alone = [[t.clone() for t in flat(step(*ops))] for ops in jobs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(10):
+                r = flat(step(*jobs[i]))
+                s.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(r, alone[i])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_same_memory_for_gate_and_up():
+    """One matrix as both weights, one tensor as x and grad: nothing says that they may not be."""
+    x, wg, _, wd, _ = block(30, 130, 136, 200)
+    out, kept = tcl.gated_ffn(x, wg, wg, wd, keep=True)
+    ref.within(out, ref.gated_ffn(x, wg, wg, wd, "silu")[0], "out")
+    for a, b in zip(tcl.gated_ffn_grad(x, x, wg, wg, wd, kept), ref.gated_ffn_grad(x, x, wg, wg, wd, "silu")):
+        ref.within(a, b, "gradient")
