@@ -65,10 +65,25 @@ def _lib():
 
 
 class GatedFfnKept(NamedTuple):
-    """What ``gated_ffn`` keeps for its gradients; tokens × inner, bf16, rows on 16-byte pieces."""
-    gate: "torch.Tensor"     # x · w_gateᵀ  # noqa: F821
-    up: "torch.Tensor"       # x · w_upᵀ  # noqa: F821
-    hidden: "torch.Tensor"   # act(gate) · up  # noqa: F821
+    """What ``gated_ffn`` keeps for its gradients, bf16. (One buffer, of which views are made where they are asked
+    for: four views cost as much of the host's time as the call's launches.)"""
+    values: "torch.Tensor"   # 3 × tokens × a pitch of at least inner: hidden, gate, up  # noqa: F821
+    inner: int
+
+    @property
+    def hidden(self):
+        """act(gate) · up: tokens × inner."""
+        return self.values[0, :, :self.inner]
+
+    @property
+    def gate(self):
+        """x · w_gateᵀ: tokens × inner."""
+        return self.values[1, :, :self.inner]
+
+    @property
+    def up(self):
+        """x · w_upᵀ: tokens × inner."""
+        return self.values[2, :, :self.inner]
 
 
 def _call(fn, what, device, stream, *args):
@@ -145,10 +160,7 @@ def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", keep: bool = Fa
         _call(_lib().tcl_gated_ffn, "gated_ffn", device, stream, tokens, hidden, inner, x.data_ptr(), ldx, w_gate.data_ptr(),
               ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd, act, h + part if keep else None,
               h + 2 * part if keep else None, h, pitch, out.data_ptr(), hidden)
-        if not keep:
-            return out
-        mid = mid[..., :inner]
-        return out, GatedFfnKept(mid[1], mid[2], mid[0])
+        return (out, GatedFfnKept(mid, inner)) if keep else out
 
 
 def gated_ffn_grad(grad, x, w_gate, w_up, w_down, kept: GatedFfnKept, activation: str = "silu", out_dtype=None, stream=None):
@@ -159,21 +171,22 @@ def gated_ffn_grad(grad, x, w_gate, w_up, w_down, kept: GatedFfnKept, activation
     r, c, ld_grad = _bf16(grad, "grad")
     _shape(r, c, (tokens, hidden), "grad")
     dtype, code = _w_type(out_dtype)
-    ldk = None
-    for t, name in zip(kept, ("kept.gate", "kept.up", "kept.hidden")):
-        r, c, _ = _bf16(t, name)
-        _shape(r, c, (tokens, inner), name)
-        if ldk is None:
-            ldk = t.stride(0) if tokens > 1 else (inner + 7) & ~7
-        if (tokens > 1 and t.stride(0) != ldk) or ldk % 8 or t.data_ptr() % 16:
-            raise ValueError("kept must be as gated_ffn returned it: rows on 16-byte pieces, one distance between them")
-    device = _device(stream, "grad", grad, x, w_gate, w_up, w_down, *kept)
+    values, width = kept
+    if values.dtype != _BF16:
+        raise TypeError("kept.values must be bfloat16")
+    shape = values.shape
+    if len(shape) != 3 or shape[:2] != (3, tokens) or width != inner or shape[2] < inner or shape[2] % 8 or shape[2] > _INT or \
+            not values.is_contiguous() or values.data_ptr() % 16:
+        raise ValueError("kept must be as gated_ffn returned it for these operands")
+    pitch = shape[2]
+    device = _device(stream, "grad", grad, x, w_gate, w_up, w_down, values)
     with _on(stream):
         dx = torch.empty((tokens, hidden), dtype=_BF16, device=device)
         dw = [torch.empty(w.shape, dtype=dtype, device=device) for w in (w_gate, w_up, w_down)]
+        h, part = values.data_ptr(), 2 * tokens * pitch
         _call(_lib().tcl_gated_ffn_grad, "gated_ffn_grad", device, stream, tokens, hidden, inner, grad.data_ptr(), ld_grad,
               x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd, act,
-              *(t.data_ptr() for t in kept), ldk, dx.data_ptr(), hidden, dw[0].data_ptr(), hidden, dw[1].data_ptr(), hidden,
+              h + part, h + 2 * part, h, pitch, dx.data_ptr(), hidden, dw[0].data_ptr(), hidden, dw[1].data_ptr(), hidden,
               dw[2].data_ptr(), inner, code)
     return dx, *dw
 
@@ -198,7 +211,8 @@ def cross_entropy(x, w, targets, stream=None):
     tokens, hidden, vocab, ldx, ldw = _entropy(x, w, targets)
     device = _device(stream, "x", x, w, targets)
     with _on(stream):
-        loss, lse = torch.empty((2, tokens), dtype=_F32, device=device)
+        loss = torch.empty(tokens, dtype=_F32, device=device)
+        lse = torch.empty(tokens, dtype=_F32, device=device)
         _call(_lib().tcl_cross_entropy, "cross_entropy", device, stream, tokens, hidden, vocab, x.data_ptr(), ldx, w.data_ptr(),
               ldw, targets.data_ptr(), targets.element_size(), loss.data_ptr(), lse.data_ptr())
     return loss, lse
@@ -217,7 +231,8 @@ def cross_entropy_grad(x, w, targets, grad, out_dtype=None, stream=None):
     dtype, code = _w_type(out_dtype)
     device = _device(stream, "x", x, w, targets, grad)
     with _on(stream):
-        loss, lse = torch.empty((2, tokens), dtype=_F32, device=device)
+        loss = torch.empty(tokens, dtype=_F32, device=device)
+        lse = torch.empty(tokens, dtype=_F32, device=device)
         dx = torch.empty((tokens, hidden), dtype=_BF16, device=device)
         dw = torch.empty((vocab, hidden), dtype=dtype, device=device)
         _call(_lib().tcl_cross_entropy_grad, "cross_entropy_grad", device, stream, tokens, hidden, vocab, x.data_ptr(), ldx,

@@ -122,7 +122,9 @@ def cross_entropy(x, w, targets, grad=None, dtype=torch.bfloat16):
     hot = torch.zeros_like(p).scatter_(1, at, 1.0)
     weight = torch.where(kept, grad.double(), 0.0)[:, None]
     relative = torch.expm1(arg + e_lse[:, None]) + 2 * ACT
-    d = V((p - hot) * weight, weight.abs() * (p * relative + (p - hot).abs() * BF) * SLACK + TINY * (weight != 0))
+    # exponentials are held relative to a power of two within 2^64 of a row's sum, and below 2^-126 of that as zeros:
+    # a probability below 2^-126 · 2^64 may come out as none
+    d = V((p - hot) * weight, weight.abs() * (p * relative + (p - hot).abs() * BF + 2.0 ** -62) * SLACK + TINY * (weight != 0))
     dx = rounded(matmul(d, exactly(w)))
     # the rows of x are rounded once more after their scaling
     xs = V(x, BF * x.abs() * SLACK)

@@ -138,9 +138,7 @@ def test_clip_refuses_its_own(L, kw, status):
 def test_binding_refuses():
     x, wg, wd = torch.zeros(4, 64, dtype=BF16), torch.zeros(96, 64, dtype=BF16), torch.zeros(64, 96, dtype=BF16)
     table, y, grad = torch.zeros(100, 64, dtype=BF16), torch.zeros(4, dtype=torch.int64), torch.zeros(4)
-    k = torch.zeros(4, 96, dtype=BF16)
-    kept = tcl.GatedFfnKept(k, k, k)
-    odd = torch.zeros(4, 100, dtype=BF16)[:, :96]   # (rows 100 apart)
+    kept = tcl.GatedFfnKept(torch.zeros(3, 4, 96, dtype=BF16), 96)
     for err, call in [
         (ValueError, lambda: tcl.gated_ffn(x, wg, wg, wd)),                                   # not on a GPU
         (ValueError, lambda: tcl.gated_ffn(x, wg, wg, wd, activation="relu")),
@@ -158,10 +156,11 @@ def test_binding_refuses():
         (ValueError, lambda: tcl.gated_ffn_grad(x[:3], x, wg, wg, wd, kept)),
         (TypeError, lambda: tcl.gated_ffn_grad(x.float(), x, wg, wg, wd, kept)),
         (TypeError, lambda: tcl.gated_ffn_grad(x, x, wg, wg, wd, kept, out_dtype=torch.float16)),
-        (TypeError, lambda: tcl.gated_ffn_grad(x, x, wg, wg, wd, tcl.GatedFfnKept(k.float(), k, k))),
-        (ValueError, lambda: tcl.gated_ffn_grad(x, x, wg, wg, wd, tcl.GatedFfnKept(k, k, k[:3]))),
-        (ValueError, lambda: tcl.gated_ffn_grad(x, x, wg, wg, wd, tcl.GatedFfnKept(odd, odd, odd))),
-        (ValueError, lambda: tcl.gated_ffn_grad(x, x, wg, wg, wd, tcl.GatedFfnKept(k, k, torch.zeros(4, 104, dtype=BF16)[:, :96]))),
+        (TypeError, lambda: tcl.gated_ffn_grad(x, x, wg, wg, wd, kept._replace(values=kept.values.float()))),
+        *[(ValueError, lambda v=v: tcl.gated_ffn_grad(x, x, wg, wg, wd, kept._replace(**v))) for v in (
+            dict(inner=95), dict(values=kept.values[:, :3]), dict(values=kept.values[:2]), dict(values=kept.values[..., :88]),
+            dict(values=torch.zeros(3, 4, 100, dtype=BF16)), dict(values=torch.zeros(3, 4, 104, dtype=BF16)[..., :96]),
+            dict(values=torch.zeros(3 * 4 * 96 + 8, dtype=BF16)[1:1153].view(3, 4, 96)))],
         (ValueError, lambda: tcl.cross_entropy(x, table, y)),                                 # not on a GPU
         (TypeError, lambda: tcl.cross_entropy(x, table.float(), y)),
         (TypeError, lambda: tcl.cross_entropy(x, table, y.short())),
@@ -221,12 +220,12 @@ def test_operands_are_recorded_on_the_given_stream(monkeypatch):
     x, wg, wu = torch.zeros(4, 64, dtype=BF16), torch.zeros(96, 64, dtype=BF16), torch.ones(96, 64, dtype=BF16)
     wd, gr = torch.zeros(64, 96, dtype=BF16), torch.zeros(4, 64, dtype=BF16)
     y, w = torch.zeros(4, dtype=torch.int64), torch.zeros(4)
-    kept = tcl.GatedFfnKept(*(torch.zeros(4, 96, dtype=BF16) for _ in range(3)))
+    kept = tcl.GatedFfnKept(torch.zeros(3, 4, 96, dtype=BF16), 96)
     a, b, c, d = (torch.zeros(5) for _ in range(4))
     for call, tensors in (
         (lambda st: tcl.gated_ffn(x, wg, wu, wd, stream=st), [x, wg, wu, wd]),
         (lambda st: tcl.gated_ffn(x, wg, wu, wd, keep=True, stream=st), [x, wg, wu, wd]),
-        (lambda st: tcl.gated_ffn_grad(gr, x, wg, wu, wd, kept, stream=st), [gr, x, wg, wu, wd, *kept]),
+        (lambda st: tcl.gated_ffn_grad(gr, x, wg, wu, wd, kept, stream=st), [gr, x, wg, wu, wd, kept.values]),
         (lambda st: tcl.cross_entropy(x, wg, y, stream=st), [x, wg, y]),
         (lambda st: tcl.cross_entropy_grad(x, wg, y, w, stream=st), [x, wg, y, w]),
         (lambda st: tcl.grad_norm([a, b], stream=st), [a, b]),

@@ -57,7 +57,7 @@ def test_ffn(tokens, hidden, inner, act):
     x, wg, wu, wd, grad = block(tokens + hidden, tokens, hidden, inner)
     out, kept = tcl.gated_ffn(x, wg, wu, wd, activation=act, keep=True)
     want = ref.gated_ffn(x, wg, wu, wd, act)
-    for got, w, what in zip((out, *kept), want, ("out", "gate", "up", "hidden")):
+    for got, w, what in zip((out, kept.gate, kept.up, kept.hidden), want, ("out", "gate", "up", "hidden")):
         assert got.dtype == BF16
         ref.within(got, w, what)
     assert torch.equal(tcl.gated_ffn(x, wg, wu, wd, activation=act), out)
@@ -114,7 +114,7 @@ def test_ffn_of_rows_at_any_distance_and_address(tokens, extra, offset):
         ops = [laid_out(t, t.shape[1] + extra, offset) if i == which or which == 4 else t for i, t in enumerate((x, wg, wu, wd))]
         g = laid_out(grad, hidden + extra, offset) if which == 4 else grad
         got, k = tcl.gated_ffn(*ops, keep=True)
-        assert torch.equal(got, out) and all(torch.equal(a, b) for a, b in zip(k, kept))
+        assert torch.equal(got, out) and torch.equal(parts(k), parts(kept))
         for a, b in zip(tcl.gated_ffn_grad(g, *ops, k), want):
             assert torch.equal(a, b)
 
@@ -134,17 +134,20 @@ def test_entropy_of_rows_at_any_distance_and_address(tokens, extra, offset):
             assert torch.equal(got, r)
 
 
+def parts(kept):
+    """gate, up and hidden, without what lies between their rows."""
+    return torch.stack([kept.gate, kept.up, kept.hidden])
+
+
 def test_kept_rows_at_another_distance():
     x, wg, wu, wd, grad = block(9, 150, 64, 90)
     _, kept = tcl.gated_ffn(x, wg, wu, wd, keep=True)
     want = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept)
-    moved = []
-    for t in kept:
-        room = torch.full((150, 104), float("nan"), dtype=BF16, device=DEV)
-        room[:, :90] = t
-        moved.append(room[:, :90])
-    for a, b in zip(tcl.gated_ffn_grad(grad, x, wg, wu, wd, tcl.GatedFfnKept(*moved)), want):
-        assert torch.equal(a, b)
+    for pitch in (96, 104, 200):
+        room = torch.full((3, 150, pitch), float("nan"), dtype=BF16, device=DEV)
+        room[..., :90] = kept.values[..., :90]
+        for a, b in zip(tcl.gated_ffn_grad(grad, x, wg, wu, wd, tcl.GatedFfnKept(room, 90)), want):
+            assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("tokens,hidden,inner", [(3, 64, 72), (200, 130, 257)])
@@ -174,7 +177,7 @@ def test_entropy_weights_gradient_in_fp32(tokens, hidden, vocab):
 def test_no_tokens():
     x, wg, wu, wd, grad = block(12, 0, 72, 130)
     out, kept = tcl.gated_ffn(x, wg, wu, wd, keep=True)
-    assert out.shape == (0, 72) and all(t.shape == (0, 130) for t in kept)
+    assert out.shape == (0, 72) and parts(kept).shape == (3, 0, 130)
     for dtype in (BF16, F32):
         dx, *dw = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept, out_dtype=dtype)
         assert dx.shape == (0, 72) and not any(t.any() for t in dw)
@@ -339,7 +342,7 @@ def test_kept_past_32_bits_of_elements():
     out, kept = tcl.gated_ffn(x, wg, wu, wd, keep=True)
     dx, dwg, dwu, dwd = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept, out_dtype=F32)
     for p in (slice(0, 200), slice(tokens - 200, tokens)):
-        for a, b in zip((out[p], *(k[p] for k in kept)), ref.gated_ffn(x[p], wg, wu, wd, "silu")):
+        for a, b in zip((out[p], kept.gate[p], kept.up[p], kept.hidden[p]), ref.gated_ffn(x[p], wg, wu, wd, "silu")):
             ref.within(a, b, "forward")
         ref.within(dx[p], ref.gated_ffn_grad(grad[p], x[p], wg, wu, wd, "silu")[0], "dx")
     # Eight columns of h, summed over all tokens. An fp32 sum errs in each of its additions by 2^-23 of the partial
@@ -379,7 +382,7 @@ def operands(seed, tokens, hidden, inner, vocab):
 
 
 def flat(r):
-    return [r["out"], *r["kept"], r["loss"], r["dy"], r["dx"], *r["before"], *r["grads"], r["norm"]]
+    return [r["out"], parts(r["kept"]), r["loss"], r["dy"], r["dx"], *r["before"], *r["grads"], r["norm"]]
 
 
 @pytest.mark.parametrize("tokens,hidden,inner,vocab", [(48, 64, 200, 333), (300, 136, 384, 2050)])
@@ -388,7 +391,7 @@ def test_training_step(tokens, hidden, inner, vocab):
     ops = operands(21, tokens, hidden, inner, vocab)
     x, gate, up, down, table, targets, grad = ops
     r = step(*ops)
-    for a, b in zip((r["out"], *r["kept"]), ref.gated_ffn(x, gate, up, down, "silu")):
+    for a, b in zip((r["out"], *parts(r["kept"])), ref.gated_ffn(x, gate, up, down, "silu")):
         ref.within(a, b, "block")
     loss, _, dy, dtable = ref.cross_entropy(r["y"], table, targets, grad)
     ref.within(r["loss"], loss, "loss")
