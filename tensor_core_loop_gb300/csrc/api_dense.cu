@@ -109,9 +109,9 @@ long long blocks_of(const Product& q) {
 
 // What a launch costs, in microseconds, measured on a GB300: a k-block of a tile, a tile's end (where it does
 // not hide behind the next tile's k-blocks), a launch, and the joining of K ranges.
-// (A narrow tile has 2/3 of a wide one's operand bytes and half of its MMAs: the way from the L2, 64 bytes a cycle
-// and SM, bounds it.)
-double block_us(int bn) { return bn == 256 ? 0.27 : 0.23; }
+// (The way from the L2 bounds all but wide tiles with K contiguous in A: a narrow tile has 2/3 of a wide one's operand
+// bytes and half of its MMAs, and boxes of contiguous rows come in at two thirds of the rate of boxes of K.)
+double block_us(int bn, bool mn = false) { return mn ? (bn == 256 ? 0.32 : 0.30) : bn == 256 ? 0.27 : 0.22; }
 double tile_us(int bn) { return bn == 256 ? 3.0 : 2.0; }
 constexpr double kLaunchUs = 5.0;
 
@@ -130,7 +130,7 @@ double deal(Group& g, int sms) {
     for (int i = 0; i < g.n; ++i) {
         const Product& q = g.q[i];
         const long long n = static_cast<long long>(tiles_of(q.M, 256)) * tiles_of(q.N, g.bn) * q.splits;
-        const double us = block_us(g.bn) * std::ceil(static_cast<double>(blocks_of(q)) / q.splits) + 0.3;
+        const double us = block_us(g.bn, q.a_mn) * std::ceil(static_cast<double>(blocks_of(q)) / q.splits) + 0.3;
         units += n;
         work += us * static_cast<double>(n);
         if (i == 0) first = n;
