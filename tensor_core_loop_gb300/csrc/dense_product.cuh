@@ -19,10 +19,10 @@
 //              logit, and in training the exponentials themselves in bf16 (dense_entropy.cuh says
 //              what they are relative to)
 //
-// Roles of each CTA: warp 0 loads (TMA, 128-byte swizzle, a ring of 64-value k-blocks), warp 1 of
-// the pair's leader issues the MMAs into one of two accumulators in tensor memory, warps 2 to 9
-// read the other one (each 32 lanes × half of the columns) and store through slabs of 32 rows ×
-// 128 bytes, copied out by the tensor copy engine. A pair walks its tiles blockIdx/2, + pairs, ...
+// Roles of each CTA: warp 0 loads A, warp 10 B (TMA, 128-byte swizzle, a ring of 64-value k-blocks),
+// warp 1 of the pair's leader issues the MMAs into one of two accumulators in tensor memory, warps 2
+// to 9 read the other one (each 32 lanes × half of the columns) and store through slabs of 32
+// rows × 128 bytes, copied out by the tensor copy engine. A pair walks its tiles blockIdx/2, + pairs, ...
 //
 // Every wait is bounded; a role that gives up raises the pair's abort flag.
 #pragma once
@@ -143,7 +143,8 @@ struct DenseCfg {
     static constexpr int EW = 8;                    // epilogue warps
     static constexpr int SLABS = 2, SLAB_BYTES = 32 * 128;
     static constexpr int NBARS = 2 * STAGES + 5 + EW;   // (a warp's own: GATE_GRAD)
-    static constexpr int THREADS = 64 + 32 * EW;
+    static constexpr int B_WARP = 2 + EW;           // the warp that loads B
+    static constexpr int THREADS = 96 + 32 * EW;
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EW * SLABS * SLAB_BYTES + (NBARS + 2) * 8;
     static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB per-block shared memory limit");
@@ -368,51 +369,52 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
         return wait_warp_pair(bar, parity, abort_flag, net, p.timeout_ns, p.status, code);
     };
 
-    if (warp == 0) {
-        // ------------------------------------------------ operand loads
+    if (warp == 0 || warp == C::B_WARP) {
+        // ------------------------------------------------ operand loads: a warp for A, one for B
+        // (What a warp does for a k-block, waiting for its slot and issuing a copy or two, takes it some 400 cycles
+        // for both operands: with one warp, tiles whose operands both have contiguous rows took 640 cycles a
+        // k-block, 512 of them the MMAs'.)
+        const bool of_a = warp == 0;
         const uint32_t full_leader0 = ptx::mapa_shared(full0, 0u);
+        const uint32_t to0 = ptx::smem_u32(smem) + (of_a ? 0 : C::A_BYTES);
         uint32_t s = 0, ph = 0;
         bool ok = true;
         for (int j = 0, u; ok && (u = dense_walk(p, pair, pairs, j)) < p.units; ++j) {
             const DenseUnit U = dense_unit<E>(p, u);
             const DenseProblem& q = p.q[U.q];
-            const bool a_mn = E == DenseEnd::STORE && q.a_mn;
-            const bool b_mn = E == DenseEnd::GATE_GRAD || (E == DenseEnd::STORE && q.b_mn);
-            const int row = U.m0 + static_cast<int>(rank) * 128;
-            const int col = E == DenseEnd::GATE ? U.n * C::CW : U.n * BN + static_cast<int>(rank) * C::CW;
-            for (int kb = U.lo; kb < U.hi; ++kb) {
-                if (!wait(empty0 + 8 * s, ph ^ 1u, DEV_TIMEOUT_PRODUCER)) {
-                    ok = false;
-                    break;
+            const bool mn = of_a ? E == DenseEnd::STORE && q.a_mn
+                                 : E == DenseEnd::GATE_GRAD || (E == DenseEnd::STORE && q.b_mn);
+            const bool whole = of_a ? q.a_3d : q.b_3d, two = of_a || BN == 256;   // (boxes of 64 rows)
+            const int at = of_a ? U.m0 + static_cast<int>(rank) * 128
+                                : E == DenseEnd::GATE ? U.n * C::CW : U.n * BN + static_cast<int>(rank) * C::CW;
+            const CUtensorMap* map0 = of_a ? &maps.a[U.q][0] : &maps.b[U.q][E == DenseEnd::GATE ? static_cast<int>(rank) : 0];
+            const CUtensorMap* map1 = of_a ? &maps.a[U.q][1] : &maps.b[U.q][1];
+            const int kb0 = E == DenseEnd::STORE ? q.kb0 : U.hi;   // the k-block from which on the second pair counts
+            // a run of k-blocks through one of the loops below; `load` issues a k-block's copies
+            auto run = [&](auto load) {
+                for (int kb = U.lo; kb < U.hi; ++kb) {
+                    if (!wait(empty0 + 8 * s, ph ^ 1u, DEV_TIMEOUT_PRODUCER)) return false;
+                    const bool second = kb >= kb0;
+                    if (of_a && rank == 0) ptx::mbar_arrive_expect_tx_elected(full0 + 8 * s, 2 * C::STAGE_BYTES);
+                    load(to0 + s * C::STAGE_BYTES, second ? map1 : map0, full_leader0 + 8 * s, (second ? kb - kb0 : kb) * C::BK);
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
-                const int second = E == DenseEnd::STORE && kb >= q.kb0;
-                const int k = (second ? kb - q.kb0 : kb) * C::BK;
-                const CUtensorMap* ma = &maps.a[U.q][second];
-                const CUtensorMap* mb = &maps.b[U.q][E == DenseEnd::GATE ? static_cast<int>(rank) : second];
-                const uint32_t sa = ptx::smem_u32(smem) + s * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-                const uint32_t fb = full_leader0 + 8 * s;
-                if (rank == 0) ptx::mbar_arrive_expect_tx_elected(full0 + 8 * s, 2 * C::STAGE_BYTES);
-                if (a_mn && q.a_3d) {   // boxes of 64 rows of M × 64 of K
-                    ptx::tma_load_3d_pair_elected(sa, ma, fb, 0, k, row / 64);
-                } else if (a_mn) {
-                    ptx::tma_load_2d_pair_elected(sa, ma, fb, row, k);
-                    ptx::tma_load_2d_pair_elected(sa + 8192, ma, fb, row + 64, k);
-                } else {
-                    ptx::tma_load_2d_pair_elected(sa, ma, fb, k, row);
-                }
-                if (b_mn && q.b_3d) {
-                    ptx::tma_load_3d_pair_elected(sb, mb, fb, 0, k, col / 64);
-                } else if (b_mn) {
-                    ptx::tma_load_2d_pair_elected(sb, mb, fb, col, k);
-                    if constexpr (BN == 256) ptx::tma_load_2d_pair_elected(sb + 8192, mb, fb, col + 64, k);
-                } else {
-                    ptx::tma_load_2d_pair_elected(sb, mb, fb, k, col);
-                }
-                if (++s == C::STAGES) {
-                    s = 0;
-                    ph ^= 1u;
-                }
-            }
+                return true;
+            };
+            if (!mn)
+                ok = run([&](uint32_t to, const CUtensorMap* m, uint32_t bar, int k) { ptx::tma_load_2d_pair_elected(to, m, bar, k, at); });
+            else if (whole)
+                ok = run([&](uint32_t to, const CUtensorMap* m, uint32_t bar, int k) {
+                    ptx::tma_load_3d_pair_elected(to, m, bar, 0, k, at / 64);
+                });
+            else
+                ok = run([&](uint32_t to, const CUtensorMap* m, uint32_t bar, int k) {
+                    ptx::tma_load_2d_pair_elected(to, m, bar, at, k);
+                    if (two) ptx::tma_load_2d_pair_elected(to + 8192, m, bar, at + 64, k);
+                });
         }
         if (!ok && lane == 0) spin_ns(200000);   // copies issued before the abort land within microseconds
         __syncwarp();
