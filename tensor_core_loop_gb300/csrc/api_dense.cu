@@ -18,7 +18,7 @@ typedef __nv_bfloat16 bf16;
 
 constexpr unsigned long long kTimeoutNs = 1000000000ull;   // bound on every in-kernel wait: 1 s
 constexpr int kMostSize = 0x7ffeffff;                       // sizes are rounded up to whole tiles in 32 bits
-constexpr int kMostFew = 64;                                // tokens of the kernel for few of them
+constexpr int kMostFew = 128;                               // tokens of the kernel for few of them
 constexpr long long kExpBytes = 1ll << 31;                  // exponentials kept at a time
 
 bool width(int n) { return n >= 1 && n <= kMostSize; }
@@ -107,12 +107,20 @@ long long blocks_of(const Product& q) {
     return blocks64(k_of(q.a, q.a_mn)) + (q.two ? blocks64(k_of(q.a1, q.a_mn)) : 0);
 }
 
+// A result of the caller's.
+DenseOut result(void* p, long long ld, int cols, int rows, int f32) {
+    return {p, ld, cols, on(p, 16) && (rows == 1 || ld * (f32 ? 4 : 2) % 16 == 0)};
+}
+
 // What a launch costs, in microseconds, measured on a GB300: a k-block of a tile, a tile's end (where it does
 // not hide behind the next tile's k-blocks), a launch, and the joining of K ranges.
 // (The way from the L2 bounds all but wide tiles with K contiguous in A: a narrow tile has 2/3 of a wide one's operand
 // bytes and half of its MMAs, and boxes of contiguous rows come in at two thirds of the rate of boxes of K.)
 double block_us(int bn, bool mn = false) { return mn ? (bn == 256 ? 0.32 : 0.30) : bn == 256 ? 0.27 : 0.22; }
 double tile_us(int bn) { return bn == 256 ? 3.0 : 2.0; }
+// The least time between a pair's tiles: what their epilogue warps and the memory take for one (rows off the 16-byte
+// grid are stored by the warps themselves).
+double end_us(int bn, int f32, bool by_copy) { return (bn == 256 ? 0.9 : 0.5) * (f32 ? 1.6 : 1.0) * (by_copy ? 1.0 : 2.2); }
 constexpr double kLaunchUs = 5.0;
 
 // A launch of up to kDenseProblems products: the tiles' width, K ranges of the first one (the longest),
@@ -130,7 +138,9 @@ double deal(Group& g, int sms) {
     for (int i = 0; i < g.n; ++i) {
         const Product& q = g.q[i];
         const long long n = static_cast<long long>(tiles_of(q.M, 256)) * tiles_of(q.N, g.bn) * q.splits;
-        const double us = block_us(g.bn, q.a_mn) * std::ceil(static_cast<double>(blocks_of(q)) / q.splits) + 0.3;
+        const bool parts = q.splits > 1;
+        const double us = std::max(block_us(g.bn, q.a_mn) * std::ceil(static_cast<double>(blocks_of(q)) / q.splits) + 0.3,
+                                   end_us(g.bn, parts || q.f32, parts || result(q.out, q.ldo, q.N, q.M, q.f32).tma));
         units += n;
         work += us * static_cast<double>(n);
         if (i == 0) first = n;
@@ -195,10 +205,6 @@ int map_out(const DenseOut& o, int f32, int rows, int mats, CUtensorMap* out) {
     if (!o.tma) return TCL_OK;
     const long long row = up(o.ld * (f32 ? 4 : 2), 16);   // (a single row never steps to a second one)
     return tensor_map_result(o.p, !f32, o.cols, rows, mats, row, row * rows, out);
-}
-
-DenseOut result(void* p, long long ld, int cols, int rows, int f32) {
-    return {p, ld, cols, on(p, 16) && (rows == 1 || ld * (f32 ? 4 : 2) % 16 == 0)};
 }
 
 int launch_pairs(DenseLaunch& l, const Gpu& g) {
@@ -327,7 +333,7 @@ DenseLaunch ended(DenseEnd end, int M, int N, long long k, int cols256, const Gp
 int launch_few(DenseEnd end, const Mat& x, const Mat& w0, const Mat* w1, DenseFewParams p, const Gpu& g, int* ctas = nullptr) {
     DenseFewLaunch l = {};
     l.end = end;
-    l.bq = p.T <= 16 ? 16 : p.T <= 32 ? 32 : 64;
+    l.bq = p.T <= 16 ? 16 : p.T <= 32 ? 32 : p.T <= 64 ? 64 : 128;
     p.N = w0.rows;
     p.num_kb = static_cast<int>(blocks64(w0.cols));
     p.timeout_ns = kTimeoutNs;

@@ -1,4 +1,4 @@
-// Products of few rows of tokens with bf16 weight matrices: D = x·W^T, x T × K with T <= 64.
+// Products of few rows of tokens with bf16 weight matrices: D = x·W^T, x T × K with T <= 128.
 //
 // What bounds them is the weights' way from HBM, once: 128 weight rows are the MMA's M side
 // (tensor-memory lanes), the tokens its N side, so that no shared memory and no MMA is spent on
@@ -29,6 +29,15 @@ struct DenseFewParams {
     unsigned long long timeout_ns;
     unsigned int* status;
 };
+
+// f(0), f(1), ... f(N - 1) with the numbers as types.
+template <int N, class F>
+__device__ __forceinline__ void dense_each(F f) {
+    if constexpr (N > 0) {
+        dense_each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>());
+    }
+}
 
 template <int BQ_, DenseEnd E_>
 struct DenseFewCfg {
@@ -119,8 +128,89 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, 1)
                : p.act == DENSE_GELU ? dense_act<DENSE_GELU, false>(g, unused)
                                      : dense_act<DENSE_GELU_TANH, false>(g, unused);
     };
-    // ENTROPY: what this warp has summed up over its tiles; lane i % 32 holds token i's
-    [[maybe_unused]] float run_ref[(BQ + 31) / 32] = {}, run_sum[(BQ + 31) / 32] = {};
+    // ENTROPY: what this warp has summed up over its tiles, and the rows of W that are the tokens' targets (-1:
+    // none); lane 2j (and 2j + 1) holds those of the tokens j, 16 + j, 32 + j, ...
+    constexpr int SLOTS = E == DenseEnd::ENTROPY ? BQ / 16 : 1;
+    [[maybe_unused]] float run_ref[SLOTS] = {}, run_sum[SLOTS] = {};
+    [[maybe_unused]] int target[SLOTS];
+    if constexpr (E == DenseEnd::ENTROPY) {
+#pragma unroll
+        for (int k = 0; k < SLOTS; ++k) {
+            const int i = 16 * k + lane / 2;
+            const long long t = i >= p.T           ? -1
+                                : p.wide_targets ? static_cast<const long long*>(p.targets)[i]
+                                                 : static_cast<const int*>(p.targets)[i];
+            target[k] = t >= 0 && t < p.N ? static_cast<int>(t) : -1;
+        }
+    }
+    // One token's logits, a lane a row: the sum relative to the largest of them, if need be.
+    [[maybe_unused]] auto one_token = [&](bool in, float v, float& ref, float& sum) {
+        auto total = [](float x) {
+#pragma unroll
+            for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+            return x;
+        };
+        ref = 0.0f;
+        sum = total(in ? ptx::exp2_approx(v * 1.4426950408889634f) : 0.0f);
+        if (dense_plain_sum(sum)) return;
+        float top = in ? v : __int_as_float(0xff800000);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        ref = dense_exponent(top);
+        sum = total(in ? ptx::exp2_approx(fmaf(v, 1.4426950408889634f, -ref)) : 0.0f);
+    };
+    // Sixteen tokens' logits (16k ..) of this lane's row. Each step of the butterfly halves the tokens that a lane
+    // adds up: 16 shuffles for 16 sums over 32 lanes.
+    [[maybe_unused]] auto sixteen = [&](int tile, auto slot, const uint32_t (&r)[16]) {
+        constexpr int k = decltype(slot)::value;
+        const int in_tile = (warp & 3) * 32 + lane, row0 = tile * p.rows + (warp & 3) * 32, row = row0 + lane;
+        if (row0 >= p.N || (warp & 3) * 32 >= p.rows || 16 * k >= p.T) return;   // (the same for all lanes)
+        const bool in = in_tile < p.rows && row < p.N;
+        if (__any_sync(0xffffffffu, target[k] >= row0 && target[k] < row0 + 32)) {
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+                const int t = __shfl_sync(0xffffffffu, target[k], 2 * i);
+                if (in && row == t) {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j == i) v = __uint_as_float(r[j]);
+                    p.target_logit[16 * k + i] = v;
+                }
+            }
+        }
+        float e[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) e[i] = in ? ptx::exp2_approx(__uint_as_float(r[i]) * 1.4426950408889634f) : 0.0f;
+        auto halve = [&](auto half) {
+            constexpr int n = decltype(half)::value;
+            const bool upper = lane & (2 * n);
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float given = __shfl_xor_sync(0xffffffffu, upper ? e[i] : e[i + n], 2 * n);
+                e[i] = (upper ? e[i + n] : e[i]) + given;
+            }
+        };
+        halve(std::integral_constant<int, 8>());
+        halve(std::integral_constant<int, 4>());
+        halve(std::integral_constant<int, 2>());
+        halve(std::integral_constant<int, 1>());
+        e[0] += __shfl_xor_sync(0xffffffffu, e[0], 1);
+        const bool exists = 16 * k + lane / 2 < p.T;
+        if (!__any_sync(0xffffffffu, exists && !dense_plain_sum(e[0]))) {
+            dense_merge(run_ref[k], run_sum[k], 0.0f, e[0]);
+            return;
+        }
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+            float v = 0.0f, ref, sum;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (j == i) v = __uint_as_float(r[j]);
+            one_token(in, v, ref, sum);
+            if (lane / 2 == i) dense_merge(run_ref[k], run_sum[k], ref, sum);
+        }
+    };
     // D of weight row `row` and token i, as this lane's (GATE: gate and up)
     auto finish = [&](int tile, int i, float v, float v1) {
         // (the lanes behind the tile's rows hold what the ring held before)
@@ -128,26 +218,14 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, 1)
         const int row = in_tile < p.rows ? row0 + lane : p.N;
         if constexpr (E == DenseEnd::ENTROPY) {
             if (i >= p.T || row0 >= p.N || (warp & 3) * 32 >= p.rows) return;   // (the same for all lanes)
-            const long long target =
-                p.wide_targets ? static_cast<const long long*>(p.targets)[i] : static_cast<const int*>(p.targets)[i];
-            if (row == target && row < p.N) p.target_logit[i] = v;
-            const float l2 = row < p.N ? v * 1.4426950408889634f : __int_as_float(0xff800000);
-            auto total = [](float x) {
+            float ref, sum;
+            one_token(row < p.N, v, ref, sum);
 #pragma unroll
-                for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                return x;
-            };
-            float ref = 0.0f, sum = total(ptx::exp2_approx(l2));
-            if (!dense_plain_sum(sum)) {
-                float top = row < p.N ? v : __int_as_float(0xff800000);
-#pragma unroll
-                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                ref = dense_exponent(top);
-                sum = total(ptx::exp2_approx(row < p.N ? fmaf(v, 1.4426950408889634f, -ref) : __int_as_float(0xff800000)));
+            for (int k = 0; k < SLOTS; ++k) {
+                if (i >> 4 != k) continue;
+                if (row == __shfl_sync(0xffffffffu, target[k], 2 * (i & 15)) && row < p.N) p.target_logit[i] = v;
+                if (lane / 2 == (i & 15)) dense_merge(run_ref[k], run_sum[k], ref, sum);
             }
-#pragma unroll
-            for (int k = 0; k < (BQ + 31) / 32; ++k)
-                if (i == lane + 32 * k) dense_merge(run_ref[k], run_sum[k], ref, sum);
         } else {
             if (i >= p.T || row >= p.N) return;
             auto put = [&](const DenseOut& o, float x) {
@@ -242,26 +320,36 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, 1)
             const uint32_t t = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * C::COLS;
             // (the ring is free: a shared tile is this CTA's only one, and all its MMAs are done)
             float* sums = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
-#pragma unroll
+            auto release = [&]() {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_relaxed(acce0 + 8 * b);
+            };
+            if (E == DenseEnd::ENTROPY && share == 1) {
+                dense_each<BQ / 16>([&](auto k) {
+                    uint32_t r[16];
+                    ptx::tmem_ld_32x32b_x16(t + 16 * decltype(k)::value, r);
+                    ptx::tmem_ld_wait(r);
+                    if (decltype(k)::value == BQ / 16 - 1) release();
+                    if constexpr (E == DenseEnd::ENTROPY) sixteen(u, k, r);
+                });
+                continue;
+            }
+#pragma unroll 1
             for (int c = 0; c < BQ; c += 16) {
                 uint32_t r[16], r1[16];
                 ptx::tmem_ld_32x32b_x16(t + c, r);
                 if constexpr (C::MATS == 2) ptx::tmem_ld_32x32b_x16(t + BQ + c, r1);
                 ptx::tmem_ld_wait(r);
                 if constexpr (C::MATS == 2) ptx::tmem_ld_wait(r1);
-                if (c + 16 == BQ) {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_relaxed(acce0 + 8 * b);
-                }
+                if (c + 16 == BQ) release();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     if (share > 1) {
                         sums[(c + i) * 128] = __uint_as_float(r[i]);
                         if constexpr (C::MATS == 2) sums[(BQ + c + i) * 128] = __uint_as_float(r1[i]);
-                    } else {
-                        finish(u, c + i, __uint_as_float(r[i]),
-                               C::MATS == 2 ? __uint_as_float(r1[i]) : 0.0f);
+                    } else if (E != DenseEnd::ENTROPY) {
+                        finish(u, c + i, __uint_as_float(r[i]), C::MATS == 2 ? __uint_as_float(r1[i]) : 0.0f);
                     }
                 }
             }
@@ -290,11 +378,11 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, 1)
         ptx::cluster_sync();   // no part leaves while another may still read its sums
     }
 
-    if (E == DenseEnd::ENTROPY && warp >= 2) {
+    if (E == DenseEnd::ENTROPY && warp >= 2 && lane % 2 == 0) {
 #pragma unroll
-        for (int k = 0; k < (BQ + 31) / 32; ++k)
-            if (lane + 32 * k < p.T)
-                p.parts[static_cast<long long>(blockIdx.x * 4 + (warp & 3)) * p.T + lane + 32 * k] =
+        for (int k = 0; k < SLOTS; ++k)
+            if (16 * k + lane / 2 < p.T)
+                p.parts[static_cast<long long>(blockIdx.x * 4 + (warp & 3)) * p.T + 16 * k + lane / 2] =
                     make_float2(run_ref[k], run_sum[k]);
     }
     ptx::tc_fence_before();

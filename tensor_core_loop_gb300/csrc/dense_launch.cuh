@@ -29,7 +29,7 @@ cudaError_t launch_dense_pair(const DenseLaunch& a);
 
 struct DenseFewLaunch {
     DenseEnd end;
-    int bq;              // 16, 32 or 64
+    int bq;              // 16, 32, 64 or 128
     CUtensorMap w[2], x;
     DenseFewParams p;
     int grid;

@@ -75,7 +75,12 @@ int dense_few_clusters(int split, int sms) {
 }
 
 cudaError_t launch_dense_few(const DenseFewLaunch& a) {
-    return a.bq == 16 ? launch<16>(a) : a.bq == 32 ? launch<32>(a) : launch<64>(a);
+    switch (a.bq) {
+        case 16: return launch<16>(a);
+        case 32: return launch<32>(a);
+        case 64: return launch<64>(a);
+        default: return launch<128>(a);
+    }
 }
 
 }  // namespace tcl

@@ -47,7 +47,7 @@ def block(seed, tokens, hidden, inner):
 # ------------------------------------------------------------------------------ the feed-forward block
 
 SIZES = [(1, 1, 1), (1, 64, 128), (1, 8, 8), (2, 72, 56), (16, 256, 384), (17, 130, 70), (32, 512, 1000), (33, 1030, 515),
-         (64, 320, 4100), (65, 256, 384), (128, 64, 64), (256, 128, 256), (257, 1030, 777), (300, 776, 2056), (513, 65, 129),
+         (64, 320, 4100), (65, 256, 384), (100, 72, 2600), (128, 64, 64), (129, 64, 136), (256, 128, 256), (257, 1030, 777), (300, 776, 2056), (513, 65, 129),
          (700, 192, 1000)]
 
 
@@ -81,7 +81,7 @@ def tokens_of(seed, tokens, hidden, vocab, spread=1.5, drop=0.1):
 
 
 ENTROPY_SIZES = [(1, 1, 1), (1, 64, 1), (1, 64, 500), (3, 8, 31), (16, 256, 5000), (17, 130, 1001), (33, 72, 129), (64, 1030, 700),
-                 (65, 128, 64), (100, 64, 128), (256, 320, 4096), (257, 130, 3001), (300, 65, 20011), (1000, 512, 257)]
+                 (65, 128, 64), (100, 64, 128), (128, 72, 20011), (129, 64, 200), (256, 320, 4096), (257, 130, 3001), (300, 65, 20011), (1000, 512, 257)]
 
 
 @pytest.mark.parametrize("ids", [torch.int64, torch.int32])
@@ -103,7 +103,7 @@ def test_entropy(tokens, hidden, vocab, ids):
 
 # ------------------------------------------------------------------------------ layouts
 
-@pytest.mark.parametrize("tokens", [5, 130])
+@pytest.mark.parametrize("tokens", [5, 70, 130])
 @pytest.mark.parametrize("extra,offset", [(0, 1), (1, 0), (3, 5), (8, 8), (64, 0)])
 def test_ffn_of_rows_at_any_distance_and_address(tokens, extra, offset):
     hidden, inner = 136, 200
@@ -119,7 +119,7 @@ def test_ffn_of_rows_at_any_distance_and_address(tokens, extra, offset):
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("tokens", [5, 130])
+@pytest.mark.parametrize("tokens", [5, 70, 130])
 @pytest.mark.parametrize("extra,offset", [(0, 1), (1, 0), (3, 5), (8, 8), (64, 0)])
 def test_entropy_of_rows_at_any_distance_and_address(tokens, extra, offset):
     x, w, y, grad = tokens_of(8, tokens, 136, 700)
@@ -187,7 +187,7 @@ def test_no_tokens():
     assert dx.shape == (0, 72) and dw.shape == wg.shape and not dw.any()
 
 
-@pytest.mark.parametrize("tokens", [7, 64, 300])
+@pytest.mark.parametrize("tokens", [7, 64, 120, 300])
 def test_dropped_tokens_may_hold_anything(tokens):
     x, w, y, grad = tokens_of(13, tokens, 72, 1000, drop=0.0)
     y[::3] = torch.tensor([-1, 1000, -2 ** 62, 2 ** 62, -100], device=DEV).repeat(tokens)[: y[::3].numel()]
@@ -200,7 +200,7 @@ def test_dropped_tokens_may_hold_anything(tokens):
     ref.within(loss, want[0], "loss")
     ref.within(dx, want[2], "dx")
     ref.within(dw, want[3], "dw")
-    assert torch.equal(tcl.cross_entropy(x, w, y)[0], loss) or tokens <= 64   # (few tokens: another order of the sums)
+    assert torch.equal(tcl.cross_entropy(x, w, y)[0], loss) or tokens <= 128   # (few tokens: another order of the sums)
     ref.within(tcl.cross_entropy(x, w, y)[0], want[0], "loss")
 
 
@@ -224,7 +224,7 @@ def far_logits(seed, tokens, vocab, level, spread):
     return x.to(BF16).to(DEV), w.to(BF16).to(DEV), y.to(DEV), (torch.rand(tokens, generator=g) / tokens).to(DEV)
 
 
-@pytest.mark.parametrize("tokens", [9, 150])
+@pytest.mark.parametrize("tokens", [9, 90, 150])
 @pytest.mark.parametrize("level,spread", [(40.0, 1.0), (64.0, 8.0), (90.0, 1.0), (300.0, 20.0), (20000.0, 1.0)])
 def test_logits_far_from_zero(tokens, level, spread):
     """Exponentials that leave fp32's range without their largest logit taken out, and chunks of one row that
@@ -244,7 +244,7 @@ def test_masked_vocabulary():
     y = torch.where((y >= 256) & (y < 700), y % 256, y)
     keep = torch.cat([w[:256], w[700:]])
     z = torch.where(y >= 700, y - 444, y)
-    for n in (10, 200):
+    for n in (10, 100, 200):
         got = tcl.cross_entropy(x[:n], w, y[:n])
         want = ref.cross_entropy(x[:n], keep, z[:n])
         for g, r in zip(got, want):
@@ -252,18 +252,18 @@ def test_masked_vocabulary():
 
 
 def test_nan_stays_in_its_row():
-    x, w, y, _ = tokens_of(17, 100, 64, 500, drop=0.0)
+    x, w, y, _ = tokens_of(17, 200, 64, 500, drop=0.0)
     wg, wu = w[:300], w[200:]
     wd = w.t()[:, :300].contiguous()
     out = tcl.gated_ffn(x, wg, wu, wd)
     loss = tcl.cross_entropy(x, w, y)[0]
     x[33] = float("nan")
-    rows = torch.arange(100, device=DEV) != 33
-    for n in (100, 50):
+    rows = torch.arange(200, device=DEV) != 33
+    for n in (200, 100, 50):
         got = tcl.gated_ffn(x[:n], wg, wu, wd)
         assert got[33].isnan().all()
         full = torch.equal(got[rows[:n]], out[:n][rows[:n]])
-        assert full or n == 50
+        assert full or n <= 128   # (few tokens: another order of the sums)
         assert got[rows[:n]].isfinite().all()
         got = tcl.cross_entropy(x[:n], w, y[:n])[0]
         assert got[33].isnan() and got[rows[:n]].isfinite().all()
