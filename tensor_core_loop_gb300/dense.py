@@ -299,6 +299,8 @@ def clip_grads(tensors, max_norm: float, out=None, stream=None):
         to_ptr, to_length, to_types = _tensors(everything[len(tensors):], "out")
         if to_length != length or to_types != types:
             raise ValueError("out must hold a tensor of the same length and type for each one")
+    if len(set(to_ptr)) < len(to_ptr) and len({a for a, n in zip(to_ptr, length) if n}) < len(length) - length.count(0):
+        raise ValueError("a tensor is given twice")   # (it would be scaled twice)
     device = _where(stream, everything)
     host = array("Q", ptr), array("Q", to_ptr), array("q", length), array("i", types)
     with _on(stream):

@@ -182,6 +182,8 @@ def test_binding_refuses():
         (ValueError, lambda: tcl.clip_grads([grad], -1.0)),
         (ValueError, lambda: tcl.clip_grads([grad], float("nan"))),
         (ValueError, lambda: tcl.clip_grads([grad], 1.0)),                                    # not on a GPU
+        (ValueError, lambda: tcl.clip_grads([grad, table, grad], 1.0)),                       # twice the same
+        (ValueError, lambda: tcl.clip_grads([grad, grad[:0], grad + 1], 1.0, out=[grad, grad[:0], grad])),
         (ValueError, lambda: tcl.clip_grads([grad], 1.0, out=[])),
         (ValueError, lambda: tcl.clip_grads([grad], 1.0, out=[grad[:3]])),
         (ValueError, lambda: tcl.clip_grads([grad], 1.0, out=[x[0, :4]])),
