@@ -166,8 +166,11 @@ double choose(Group& g, int sms) {
     int bn = 0, splits = 1;
     const long long kb = blocks_of(g.q[0]);
     for (int i = 1; i < g.n; ++i) g.q[i].splits = 1;
+    static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
     for (g.bn = 256; g.bn >= 128; g.bn /= 2) {
-        for (int s = 1; s <= 64 && s * 4 <= std::max(kb, 4ll); s += s < 8 ? 1 : s / 4) {
+        const long long tiles = static_cast<long long>(tiles_of(g.q[0].M, 256)) * tiles_of(g.q[0].N, g.bn);
+        for (const int s : kSplits) {
+            if (s > 1 && (s * 4 > kb || tiles * s > 2 * sms)) break;   // (short ranges; more units than hide their ends)
             g.q[0].splits = s;
             double us = deal(g, sms);
             // the ranges' sums are written and read again, at 5 TB/s

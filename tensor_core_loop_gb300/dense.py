@@ -88,19 +88,15 @@ class GatedFfnKept(NamedTuple):
 
 def _call(fn, what, device, stream, *args):
     """Calls fn(*args, workspace, its size, stream), with a workspace where it asks for one."""
+    if device.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return _call(fn, what, device, stream, *args)
     raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
     size = ctypes.c_size_t(0)
-
-    def once(workspace):
-        if device.index == torch._C._cuda_getDevice():
-            return fn(*args, workspace, size, raw)
-        with torch.cuda.device(device):
-            return fn(*args, workspace, size, raw)
-
-    st = once(None)
+    st = fn(*args, None, size, raw)
     if st == _WORKSPACE:
         room = torch.empty(size.value, dtype=torch.uint8, device=device)   # (on the stream: the caller is inside _on)
-        st = once(room.data_ptr())
+        st = fn(*args, room.data_ptr(), size, raw)
     if st:
         raise TclError(st, what)
 
