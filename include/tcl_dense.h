@@ -20,7 +20,8 @@
  * Matrices are bf16, row-major, leading dimensions in elements; weights as a layer stores them,
  * outputs × inputs. Bases have to be aligned to their element (TCL_ERR_ALIGN). Operands whose
  * base is not 16-byte aligned or whose leading dimension is not a multiple of 8 are copied into the
- * workspace first. Results may have any leading dimension (whole 16-byte pieces are stored fastest).
+ * workspace first. Results may have any leading dimension (rows on 16-byte pieces are stored
+ * fastest); what lies between their rows is left as it was. They overlap neither operands nor one another.
  *
  * Products run on the tensor cores with fp32 sums. Every result is rounded once; what is rounded
  * to bf16 between two products of a call is named there.

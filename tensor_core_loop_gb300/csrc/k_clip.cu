@@ -33,6 +33,12 @@ __device__ __forceinline__ int tensor_of(const ClipTensors& a, long long piece) 
     return lo;
 }
 
+// Elements before the next 16-byte unit.
+template <typename T>
+__device__ __forceinline__ int to_unit(const T* p) {
+    return static_cast<int>(-reinterpret_cast<uintptr_t>(p) & 15) / static_cast<int>(sizeof(T));
+}
+
 template <typename T>
 __device__ __forceinline__ float value(T x);
 template <>
@@ -108,9 +114,16 @@ __global__ void __launch_bounds__(kThreads, 5) square_sums_kernel(const __grid_c
         const ClipTensor& t = a.t[tensor_of(a, piece)];
         const long long at = (piece - t.before) * a.piece;
         const T* x = static_cast<const T*>(t.from) + at;
-        const int n = static_cast<int>(t.n - at < a.piece ? t.n - at : a.piece);
+        int n = static_cast<int>(t.n - at < a.piece ? t.n - at : a.piece);
+        const int lead = min(n, to_unit(x));
+        if (threadIdx.x < lead) {
+            const double f = value(x[threadIdx.x]);
+            sum += f * f;
+        }
+        x += lead;
+        n -= lead;
         int done = 0;
-        if (reinterpret_cast<uintptr_t>(x) % 16 == 0) {
+        {
             constexpr int STEP = kThreads * 32;
             const uint4* x4 = reinterpret_cast<const uint4*>(x);
             for (; done + STEP <= n; done += STEP) {
@@ -165,9 +178,14 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
         const long long at = (piece - t.before) * a.piece;
         const T* x = static_cast<const T*>(t.from) + at;
         T* y = static_cast<T*>(t.to) + at;
-        const int n = static_cast<int>(t.n - at < a.piece ? t.n - at : a.piece);
+        int n = static_cast<int>(t.n - at < a.piece ? t.n - at : a.piece);
         int done = 0;
-        if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % 16 == 0) {
+        if ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) % 16 == 0) {
+            const int lead = min(n, to_unit(x));
+            if (threadIdx.x < lead) y[threadIdx.x] = scaled ? static_cast<T>(value(x[threadIdx.x]) * f) : x[threadIdx.x];
+            x += lead;
+            y += lead;
+            n -= lead;
             constexpr int STEP = kThreads * Q * U;
             const uint4* x4 = reinterpret_cast<const uint4*>(x);
             uint4* y4 = reinterpret_cast<uint4*>(y);

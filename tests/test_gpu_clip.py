@@ -95,6 +95,15 @@ def test_squares_past_the_range_of_fp32(dtype, scale):
     check(ts, norm, out, float(torch.tensor(bound, dtype=F32)))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shift", range(8))
+def test_results_at_another_alignment(dtype, shift):
+    ts = tensors(6, (70001, 8192, 3), (dtype,), offset=shift)
+    for other in (shift, 0, 3):
+        out = [torch.zeros(t.numel() + other, dtype=dtype, device=DEV)[other:] for t in ts]
+        check(ts, tcl.clip_grads(ts, 2.0, out=out), out, 2.0)
+
+
 def test_zeros_have_norm_zero():
     ts = [torch.zeros(100000, device=DEV), torch.zeros(3, dtype=BF16, device=DEV)]
     assert float(tcl.clip_grads(ts, 0.0)) == 0.0 and not any(t.any() for t in ts)

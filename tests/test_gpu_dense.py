@@ -172,6 +172,71 @@ def test_entropy_weights_gradient_in_fp32(tokens, hidden, vocab):
     assert torch.equal(got[3].to(BF16), tcl.cross_entropy_grad(x, w, y, grad)[3])
 
 
+class Rows:
+    """A result with rows `extra` apart, 7 around it."""
+
+    def __init__(self, rows, cols, extra, dtype=BF16):
+        self.pitch, self.cols = cols + extra, cols
+        self.room = torch.full((rows * self.pitch + 64,), 7.0, dtype=dtype, device=DEV)
+        self.view = self.room[: rows * self.pitch].view(rows, self.pitch)
+
+    def args(self):
+        return self.room.data_ptr(), self.pitch
+
+    def check(self, want):
+        assert torch.equal(self.view[:, : self.cols], want)
+        assert (self.view[:, self.cols:] == 7).all() and (self.room[self.view.numel():] == 7).all()
+
+
+def c_call(fn, *args):
+    """Through the C interface, with a workspace of exactly the size that it asks for, surrounded by a pattern."""
+    import ctypes
+    size = ctypes.c_size_t(0)
+    st = fn(*args, None, size, torch.cuda.current_stream().cuda_stream)
+    if st == 13:
+        room = torch.full((size.value + 512,), 0x5a, dtype=torch.uint8, device=DEV)
+        st = fn(*args, room.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+        assert (room[size.value:] == 0x5a).all()
+    assert st == 0
+
+
+@pytest.mark.parametrize("wtype", [0, 1])
+@pytest.mark.parametrize("tokens", [5, 100, 300])
+@pytest.mark.parametrize("hidden,inner,extra", [(130, 200, 0), (130, 200, 6), (130, 201, 7), (136, 200, 8), (64, 128, 1), (72, 321, 2)])
+def test_results_with_wider_rows(tokens, hidden, inner, extra, wtype):
+    """What lies between the rows of results stays as it was."""
+    from tensor_core_loop_gb300 import dense
+    L = dense._lib()
+    dtype = F32 if wtype == 0 else BF16
+    x, wg, wu, wd, grad = block(31, tokens, hidden, inner)
+    out, kept = tcl.gated_ffn(x, wg, wu, wd, keep=True)
+    to = Rows(tokens, hidden, extra)
+    pitch = kept.values.shape[2]
+    mid = torch.empty_like(kept.values)
+    h, part = mid.data_ptr(), 2 * tokens * pitch
+    ops = [a for t in (x, wg, wu, wd) for a in (t.data_ptr(), t.shape[1])]
+    c_call(L.tcl_gated_ffn, tokens, hidden, inner, *ops, 0, h + part, h + 2 * part, h, pitch, *to.args())
+    to.check(out)
+    assert torch.equal(mid[..., :inner], kept.values[..., :inner])
+    want = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept, out_dtype=dtype)
+    res = [Rows(tokens, hidden, extra), Rows(inner, hidden, extra, dtype), Rows(inner, hidden, extra, dtype), Rows(hidden, inner, extra, dtype)]
+    c_call(L.tcl_gated_ffn_grad, tokens, hidden, inner, grad.data_ptr(), hidden, *ops, 0, h + part, h + 2 * part, h, pitch,
+           *(a for r in res for a in r.args()), wtype)
+    for r, w in zip(res, want):
+        r.check(w)
+    y = torch.randint(0, inner, (tokens,), device=DEV)
+    weight = torch.rand(tokens, device=DEV)
+    want = tcl.cross_entropy_grad(x, wg, y, weight, out_dtype=dtype)
+    loss, lse = torch.empty(2, tokens, device=DEV)
+    res = [Rows(tokens, hidden, extra), Rows(inner, hidden, extra, dtype)]
+    c_call(L.tcl_cross_entropy_grad, tokens, hidden, inner, *ops[:4], y.data_ptr(), 8, weight.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+           *(a for r in res for a in r.args()), wtype)
+    for g, w in zip((loss, lse), want):
+        assert torch.equal(g, w)
+    for r, w in zip(res, want[2:]):
+        r.check(w)
+
+
 # ------------------------------------------------------------------------------ no tokens, dropped tokens, values
 
 def test_no_tokens():
@@ -500,3 +565,42 @@ def test_same_memory_for_gate_and_up():
     ref.within(out, ref.gated_ffn(x, wg, wg, wd, "silu")[0], "out")
     for a, b in zip(tcl.gated_ffn_grad(x, x, wg, wg, wd, kept), ref.gated_ffn_grad(x, x, wg, wg, wd, "silu")):
         ref.within(a, b, "gradient")
+
+
+FIRST = """
+import torch, tensor_core_loop_gb300 as tcl
+dev = torch.device("cuda:0")
+t = lambda *s: torch.full(s, 0.01, dtype=torch.bfloat16, device=dev)
+n = {tokens}
+x, wg, wd, table = t(n, 64), t(200, 64), t(64, 200), t(300, 64)
+y, grad = torch.zeros(n, dtype=torch.int64, device=dev), torch.ones(n, device=dev)
+tcl.lib()
+s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g, stream=s):
+    out, kept = tcl.gated_ffn(x, wg, wg, wd, keep=True)
+    grads = tcl.gated_ffn_grad(x, x, wg, wg, wd, kept)
+    loss = tcl.cross_entropy(out, table, y)
+    more = tcl.cross_entropy_grad(out, table, y, grad)
+    norm = tcl.clip_grads([*grads, more[3]], 1e-3)
+g.replay()
+torch.cuda.synchronize()
+held = [out, *loss, *more[:3], norm]
+out2, kept = tcl.gated_ffn(x, wg, wg, wd, keep=True)
+more2 = tcl.cross_entropy_grad(out2, table, y, grad)
+norm2 = tcl.clip_grads([*tcl.gated_ffn_grad(x, x, wg, wg, wd, kept), more2[3]], 1e-3)
+for a, b in zip(held, [out2, *tcl.cross_entropy(out2, table, y), *more2[:3], norm2]):
+    assert torch.equal(a, b)
+assert tcl.last_device_error() == (0, 0)
+"""
+
+
+@pytest.mark.parametrize("tokens", [5, 200])
+def test_first_calls_of_a_process_inside_a_capture(tokens):
+    """Nothing has to be set up by a call before: no scratch, no attribute, no measurement."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(tokens=tokens)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
