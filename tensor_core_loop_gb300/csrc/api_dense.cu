@@ -18,7 +18,6 @@ typedef __nv_bfloat16 bf16;
 
 constexpr unsigned long long kTimeoutNs = 1000000000ull;   // bound on every in-kernel wait: 1 s
 constexpr int kMostSize = 0x7ffeffff;                       // sizes are rounded up to whole tiles in 32 bits
-constexpr int kMostFew = 128;                               // tokens of the kernel for few of them
 constexpr long long kExpBytes = 1ll << 31;                  // exponentials kept at a time
 
 bool width(int n) { return n >= 1 && n <= kMostSize; }
@@ -333,6 +332,16 @@ DenseLaunch ended(DenseEnd end, int M, int N, long long k, int cols256, const Gp
 
 // ------------------------------------------------------------------ few tokens
 
+// Whether `values` weights are read by the kernel for few tokens. Measured in CUDA graphs on a GB300, the block,
+// microseconds, it against tiles on pairs of SMs:
+//   hidden × inner   tokens = 1         16          64          100
+//   4096 × 14336      59.4 | 99.6   60.5 | 79.5   65.6 | 82.0   71.5 | 83.9
+//   4096 × 8192       40.5 | 63.8   41.1 | 51.5   46.9 | 53.1   54.4 | 53.9
+//   2048 × 5632       20.5 | 35.3   20.5 | 28.7   24.7 | 28.7   30.7 | 28.7
+//   512 × 1408        12.3 | 16.6   12.3 | 16.4   16.4 | 16.4   20.5 | 16.4
+// (cross entropy over 131072 × 4096: 64 tokens 170 | 190, 128 tokens 185 | 193)
+bool is_few(int tokens, long long values) { return tokens <= 64 || (tokens <= 128 && values > 40000000ll); }
+
 int launch_few(DenseEnd end, const Mat& x, const Mat& w0, const Mat* w1, DenseFewParams p, const Gpu& g, int* ctas = nullptr) {
     DenseFewLaunch l = {};
     l.end = end;
@@ -548,7 +557,8 @@ int tcl_gated_ffn(int tokens, int hidden, int inner, const void* X, int ldx, con
     q.out = out;
     q.ldo = ldo;
     Group down = {&q, 1};
-    if (tokens > kMostFew) {
+    const bool few = is_few(tokens, static_cast<long long>(hidden) * inner);
+    if (!few) {
         choose(down, g.sms);
         reserve(room, down);
     }
@@ -556,7 +566,7 @@ int tcl_gated_ffn(int tokens, int hidden, int inner, const void* X, int ldx, con
     const auto lock = library_lock();
     int st;
     if (room.copies.n && (st = status_of(launch_dense_copies(room.copies, stream)))) return st;
-    if (tokens > kMostFew) {
+    if (!few) {
         if ((st = gate_pairs(f, static_cast<bf16*>(gate), static_cast<bf16*>(upp), static_cast<bf16*>(h), ld_kept, g))) return st;
         return run(down, g);
     }
@@ -652,7 +662,7 @@ int tcl_cross_entropy(int tokens, int hidden, int vocab, const void* X, int ldx,
     Room room{static_cast<uint8_t*>(workspace), *workspace_bytes};
     const Entropy n = {tokens, hidden, vocab, room.operand(X, ldx, tokens, hidden), room.operand(W, ldw, vocab, hidden), targets,
                        target_bytes, loss, lse};
-    const bool few = tokens <= kMostFew;
+    const bool few = is_few(tokens, static_cast<long long>(hidden) * vocab);
     int chunks = few ? 4 * g.sms : tiles_of(vocab, 64), chunk = 0;
     float2* parts = room.take<float2>(static_cast<long long>(chunks) * tokens);
     float* target_logit = room.take<float>(tokens);

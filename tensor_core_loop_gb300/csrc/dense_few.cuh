@@ -19,7 +19,7 @@ namespace tcl {
 struct DenseFewParams {
     int T, N, num_kb, tiles, split;
     int rows;              // weight rows of a tile, a multiple of 8: as many as deal them out evenly (128 at most)
-    int act, f32;
+    int act;
     int early;             // the weights are not what the kernel before this one in the stream writes
     DenseOut out[3];
     const void* targets;
@@ -122,12 +122,6 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, 1)
     auto wait = [&](uint32_t bar, uint32_t parity, unsigned int code) {
         return wait_warp(bar, parity, abort_flag, p.timeout_ns, p.status, code);
     };
-    auto act_of = [&](float g) {
-        float unused;
-        return p.act == DENSE_SILU   ? dense_act<DENSE_SILU, false>(g, unused)
-               : p.act == DENSE_GELU ? dense_act<DENSE_GELU, false>(g, unused)
-                                     : dense_act<DENSE_GELU_TANH, false>(g, unused);
-    };
     // ENTROPY: what this warp has summed up over its tiles, and the rows of W that are the tokens' targets (-1:
     // none); lane 2j (and 2j + 1) holds those of the tokens j, 16 + j, 32 + j, ...
     constexpr int SLOTS = E == DenseEnd::ENTROPY ? BQ / 16 : 1;
@@ -143,21 +137,28 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, 1)
             target[k] = t >= 0 && t < p.N ? static_cast<int>(t) : -1;
         }
     }
-    // One token's logits, a lane a row: the sum relative to the largest of them, if need be.
-    [[maybe_unused]] auto one_token = [&](bool in, float v, float& ref, float& sum) {
-        auto total = [](float x) {
+    // One token's logits, the first `there` of v in each lane: their exponentials' sum, relative to the largest of
+    // them if need be.
+    [[maybe_unused]] auto one_token = [&](const auto& v, int there, float& ref, float& sum) {
+        constexpr int N = sizeof(v) / sizeof(v[0]);
+        auto total = [&](float taken) {
+            float x = 0.0f;
+#pragma unroll
+            for (int k = 0; k < N; ++k) x += k < there ? ptx::exp2_approx(fmaf(v[k], 1.4426950408889634f, -taken)) : 0.0f;
 #pragma unroll
             for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
             return x;
         };
         ref = 0.0f;
-        sum = total(in ? ptx::exp2_approx(v * 1.4426950408889634f) : 0.0f);
+        sum = total(0.0f);
         if (dense_plain_sum(sum)) return;
-        float top = in ? v : __int_as_float(0xff800000);
+        float top = __int_as_float(0xff800000);
+#pragma unroll
+        for (int k = 0; k < N; ++k) top = k < there ? fmaxf(top, v[k]) : top;
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         ref = dense_exponent(top);
-        sum = total(in ? ptx::exp2_approx(fmaf(v, 1.4426950408889634f, -ref)) : 0.0f);
+        sum = total(ref);
     };
     // Sixteen tokens' logits (16k ..) of this lane's row. Each step of the butterfly halves the tokens that a lane
     // adds up: 16 shuffles for 16 sums over 32 lanes.
@@ -203,39 +204,73 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, 1)
         }
 #pragma unroll 1
         for (int i = 0; i < 16; ++i) {
-            float v = 0.0f, ref, sum;
+            float v[1] = {0.0f}, ref, sum;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                if (j == i) v = __uint_as_float(r[j]);
-            one_token(in, v, ref, sum);
+                if (j == i) v[0] = __uint_as_float(r[j]);
+            one_token(v, in ? 1 : 0, ref, sum);
             if (lane / 2 == i) dense_merge(run_ref[k], run_sum[k], ref, sum);
         }
     };
-    // D of weight row `row` and token i, as this lane's (GATE: gate and up)
-    auto finish = [&](int tile, int i, float v, float v1) {
+    // STORE, GATE: 16 tokens' results (from token c on) of this lane's row; consecutive lanes hold consecutive columns
+    [[maybe_unused]] auto column = [&](int tile, int c, const uint32_t (&r)[16], const uint32_t (&r1)[16]) {
         // (the lanes behind the tile's rows hold what the ring held before)
-        const int in_tile = (warp & 3) * 32 + lane, row0 = tile * p.rows + (warp & 3) * 32;
-        const int row = in_tile < p.rows ? row0 + lane : p.N;
+        const int in_tile = (warp & 3) * 32 + lane, row = tile * p.rows + in_tile, n = p.T - c;
+        if (in_tile >= p.rows || row >= p.N) return;
+        auto put = [&](const DenseOut& o, const auto& x) {
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(o.p) + c * o.ld + row;
+#pragma unroll
+            for (int i = 0; i < 16; ++i, to += o.ld)
+                if (i < n) *to = __float2bfloat16_rn(x(i));
+        };
+        if constexpr (E == DenseEnd::GATE) {
+            dense_with_act(p.act, [&](auto act) {
+                put(p.out[0], [&](int i) {
+                    float unused;
+                    return dense_act<decltype(act)::value, false>(__uint_as_float(r[i]), unused) * __uint_as_float(r1[i]);
+                });
+            });
+            if (p.out[1].p) {
+                put(p.out[1], [&](int i) { return __uint_as_float(r[i]); });
+                put(p.out[2], [&](int i) { return __uint_as_float(r1[i]); });
+            }
+        } else {
+            put(p.out[0], [&](int i) { return __uint_as_float(r[i]); });
+        }
+    };
+    // Token i's results of a whole tile, four rows to a lane
+    [[maybe_unused]] auto whole_row = [&](int tile, int i, const float (&v)[4], const float (&v1)[4]) {
+        const int row = tile * p.rows + 4 * lane, there = min(p.rows - 4 * lane, p.N - row);
         if constexpr (E == DenseEnd::ENTROPY) {
-            if (i >= p.T || row0 >= p.N || (warp & 3) * 32 >= p.rows) return;   // (the same for all lanes)
             float ref, sum;
-            one_token(row < p.N, v, ref, sum);
+            one_token(v, there, ref, sum);
 #pragma unroll
             for (int k = 0; k < SLOTS; ++k) {
-                if (i >> 4 != k) continue;
-                if (row == __shfl_sync(0xffffffffu, target[k], 2 * (i & 15)) && row < p.N) p.target_logit[i] = v;
+                if (i >> 4 != k) continue;   // (the same for all lanes)
+                const int at = __shfl_sync(0xffffffffu, target[k], 2 * (i & 15)) - row;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (at == j && j < there) p.target_logit[i] = v[j];
                 if (lane / 2 == (i & 15)) dense_merge(run_ref[k], run_sum[k], ref, sum);
             }
         } else {
-            if (i >= p.T || row >= p.N) return;
-            auto put = [&](const DenseOut& o, float x) {
-                if (E == DenseEnd::STORE && p.f32)
-                    static_cast<float*>(o.p)[i * o.ld + row] = x;
-                else
-                    static_cast<__nv_bfloat16*>(o.p)[i * o.ld + row] = __float2bfloat16_rn(x);
+            auto put = [&](const DenseOut& o, const float (&x)[4]) {
+                __nv_bfloat16* to = static_cast<__nv_bfloat16*>(o.p) + i * o.ld + row;
+                if (there >= 4 && reinterpret_cast<uintptr_t>(to) % 8 == 0) {
+                    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < there) to[j] = __float2bfloat16_rn(x[j]);
+                }
             };
             if constexpr (E == DenseEnd::GATE) {
-                put(p.out[0], act_of(v) * v1);
+                dense_with_act(p.act, [&](auto act) {
+                    float unused, h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[j] = dense_act<decltype(act)::value, false>(v[j], unused) * v1[j];
+                    put(p.out[0], h);
+                });
                 if (p.out[1].p) {
                     put(p.out[1], v);
                     put(p.out[2], v1);
@@ -343,14 +378,14 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, 1)
                 ptx::tmem_ld_wait(r);
                 if constexpr (C::MATS == 2) ptx::tmem_ld_wait(r1);
                 if (c + 16 == BQ) release();
+                if (share > 1) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (share > 1) {
+                    for (int i = 0; i < 16; ++i) {
                         sums[(c + i) * 128] = __uint_as_float(r[i]);
                         if constexpr (C::MATS == 2) sums[(BQ + c + i) * 128] = __uint_as_float(r1[i]);
-                    } else if (E != DenseEnd::ENTROPY) {
-                        finish(u, c + i, __uint_as_float(r[i]), C::MATS == 2 ? __uint_as_float(r1[i]) : 0.0f);
                     }
+                } else if constexpr (E != DenseEnd::ENTROPY) {
+                    if (c < p.T) column(u, c, r, r1);
                 }
             }
             __syncwarp();
@@ -362,16 +397,30 @@ __global__ void __launch_bounds__(DenseFewCfg<BQ, E>::THREADS, 1)
         __syncwarp();
         ptx::cluster_sync();   // every part's sums are in its shared memory
         if (warp >= 2 && u0 < p.tiles) {
-            const int quarter = warp & 3;
-            const uint32_t sums = ptx::smem_u32(smem) + 4 * (quarter * 32 + lane);
-            for (int i = part; i < min(BQ, p.T); i += share) {
-                float v = 0.0f, v1 = 0.0f;
-                for (int r = 0; r < share; ++r) {
+            // a warp a token: all parts' sums of four rows a lane are on their way together
+            const uint32_t sums = ptx::smem_u32(smem) + 16 * lane;
+            for (int i = part + share * (warp - 2); i < p.T; i += 4 * share) {
+                uint4 x[C::MATS][8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    if (r >= share) continue;
                     const uint32_t at = ptx::mapa_shared(sums, static_cast<uint32_t>(r));
-                    v += ptx::ld_cluster_f32(at + 4 * (i * 128));
-                    if constexpr (C::MATS == 2) v1 += ptx::ld_cluster_f32(at + 4 * ((BQ + i) * 128));
+#pragma unroll
+                    for (int m = 0; m < C::MATS; ++m) x[m][r] = ptx::ld_cluster_v4(at + 512 * (m * BQ + i));
                 }
-                finish(u0, i, v, v1);
+                float v[2][4] = {};
+#pragma unroll
+                for (int m = 0; m < C::MATS; ++m) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        if (r >= share) continue;
+                        v[m][0] += __uint_as_float(x[m][r].x);
+                        v[m][1] += __uint_as_float(x[m][r].y);
+                        v[m][2] += __uint_as_float(x[m][r].z);
+                        v[m][3] += __uint_as_float(x[m][r].w);
+                    }
+                }
+                whole_row(u0, i, v[0], v[1]);
             }
         }
         __syncwarp();

@@ -47,7 +47,7 @@ def block(seed, tokens, hidden, inner):
 # ------------------------------------------------------------------------------ the feed-forward block
 
 SIZES = [(1, 1, 1), (1, 64, 128), (1, 8, 8), (2, 72, 56), (16, 256, 384), (17, 130, 70), (32, 512, 1000), (33, 1030, 515),
-         (64, 320, 4100), (65, 256, 384), (100, 72, 2600), (128, 64, 64), (129, 64, 136), (256, 128, 256), (257, 1030, 777), (300, 776, 2056), (513, 65, 129),
+         (64, 320, 4100), (65, 256, 384), (100, 72, 2600), (65, 4096, 10240), (128, 4100, 10243), (128, 64, 64), (129, 64, 136), (256, 128, 256), (257, 1030, 777), (300, 776, 2056), (513, 65, 129),
          (700, 192, 1000)]
 
 
@@ -81,7 +81,7 @@ def tokens_of(seed, tokens, hidden, vocab, spread=1.5, drop=0.1):
 
 
 ENTROPY_SIZES = [(1, 1, 1), (1, 64, 1), (1, 64, 500), (3, 8, 31), (16, 256, 5000), (17, 130, 1001), (33, 72, 129), (64, 1030, 700),
-                 (65, 128, 64), (100, 64, 128), (128, 72, 20011), (129, 64, 200), (256, 320, 4096), (257, 130, 3001), (300, 65, 20011), (1000, 512, 257)]
+                 (65, 128, 64), (100, 64, 128), (128, 72, 20011), (120, 640, 70001), (129, 64, 200), (256, 320, 4096), (257, 130, 3001), (300, 65, 20011), (1000, 512, 257)]
 
 
 @pytest.mark.parametrize("ids", [torch.int64, torch.int32])
