@@ -25,6 +25,8 @@ bool on(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n 
 long long up(long long x, long long m) { return (x + m - 1) / m * m; }
 int tiles_of(int n, int tile) { return static_cast<int>((static_cast<long long>(n) + tile - 1) / tile); }
 long long blocks64(long long k) { return (k + 63) / 64; }
+// Whether the tiles of an M × N result, the narrow ones, can be counted in 32 bits.
+bool countable(int M, int N) { return static_cast<long long>(tiles_of(M, 256)) * tiles_of(N, 128) <= 0x3fffffffll; }
 
 int status_of(cudaError_t err) {
     if (err == cudaSuccess) return TCL_OK;
@@ -387,6 +389,10 @@ struct Ffn {
 
 int ffn_sizes(int tokens, int hidden, int inner, int act) {
     if (tokens < 0 || tokens > kMostSize || !width(hidden) || !width(inner)) return TCL_ERR_DIMS;
+    // (the gate's tiles are half as wide; the gradients' products share a launch)
+    if (!countable(tokens, 2 * std::min(inner, 0x3fffffff)) || !countable(tokens, hidden) || !countable(inner, hidden) ||
+        !countable(hidden, inner))
+        return TCL_ERR_DIMS;
     return act < 0 || act > 2 ? TCL_ERR_CONFIG : TCL_OK;
 }
 
@@ -439,6 +445,7 @@ struct Entropy {
 int entropy_checks(int tokens, int hidden, int vocab, const void* X, int ldx, const void* W, int ldw, const void* targets,
                    int target_bytes, const float* loss, const float* lse) {
     if (tokens < 0 || tokens > kMostSize || !width(hidden) || !width(vocab)) return TCL_ERR_DIMS;
+    if (!countable(tokens, vocab) || !countable(tokens, hidden) || !countable(vocab, hidden)) return TCL_ERR_DIMS;
     if (target_bytes != 4 && target_bytes != 8) return TCL_ERR_CONFIG;
     if (tokens && (!X || !W || !targets || !loss || !lse)) return TCL_ERR_NULL;
     if (ldx < hidden || ldw < hidden) return TCL_ERR_LD;

@@ -53,6 +53,7 @@ def ffn(L, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [
+    (dict(T=2 ** 30, F=2 ** 23, ldd=2 ** 23, ldk=2 ** 23), 2), (dict(T=2 ** 30, H=2 ** 23), 2),
     (dict(T=-1), 2), (dict(H=0), 2), (dict(F=0), 2), (dict(T=BIG), 2), (dict(F=BIG, ldd=BIG, ldk=BIG), 2), (dict(act=3), 8), (dict(act=-1), 8),
     (dict(X=None), 1), (dict(G=None), 1), (dict(U=None), 1), (dict(D=None), 1), (dict(h=None), 1), (dict(out=None), 1),
     (dict(gate=None), 1), (dict(up=None), 1), (dict(wsb=None), 1), (dict(wsb=size(256)), 1),
@@ -97,7 +98,7 @@ def entropy_grad(L, **kw):
 
 @pytest.mark.parametrize("call", [entropy, entropy_grad])
 @pytest.mark.parametrize("kw,status", [
-    (dict(T=-1), 2), (dict(H=0), 2), (dict(V=0), 2), (dict(T=MOST), 2), (dict(V=BIG), 2), (dict(yb=2), 8),
+    (dict(T=-1), 2), (dict(H=0), 2), (dict(V=0), 2), (dict(T=MOST), 2), (dict(V=BIG), 2), (dict(T=2 ** 29, V=2 ** 29), 2), (dict(yb=2), 8),
     *[(dict([(k, None)]), 1) for k in ("X", "W", "y", "loss", "lse", "wsb")], (dict(ldx=63), 3), (dict(ldw=63), 3),
     (dict(X=PO), 4), (dict(W=PO), 4), (dict(y=P4), 4), (dict(yb=4, y=P2), 4), (dict(loss=P2), 4), (dict(lse=P2), 4),
     (dict(ws=P8, wsb=size(512)), 4), (dict(wsb=size(512)), 1)])
