@@ -486,6 +486,11 @@ EntropyRows entropy_rows(const Entropy& n, int t0, int rows, int chunks, int chu
     r.wide_targets = n.target_bytes == 8;
     r.loss = n.loss + t0;
     r.lse = n.lse + t0;
+    r.x = n.x.p + t0 * n.x.ld;
+    r.ld_x = n.x.ld;
+    r.w = n.w.p;
+    r.ld_w = n.w.ld;
+    r.hidden = n.H;
     return r;
 }
 
@@ -772,11 +777,8 @@ int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int
         r.e = e;
         r.ld_e = lde;
         r.factor = factor;
-        r.x = n.x.p + t0 * n.x.ld;
-        r.ld_x = n.x.ld;
         r.scaled = scaled;
         r.ld_scaled = ldh;
-        r.hidden = hidden;
         if ((st = status_of(launch_entropy_rows(r, stream)))) return st;
         Product q[2];
         products(t0, rows, q);

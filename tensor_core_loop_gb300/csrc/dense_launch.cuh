@@ -74,16 +74,16 @@ struct EntropyRows {
     const void* targets;
     int wide_targets;
     float *loss, *lse;
+    const __nv_bfloat16 *x, *w;   // their rows, on 16-byte pieces
+    long long ld_x, ld_w;
+    int hidden;
     // in training:
     const float* grad;     // NULL: no gradients
     __nv_bfloat16* e;      // exponentials
     long long ld_e;
     float* factor;
-    const __nv_bfloat16* x;
-    long long ld_x;
     __nv_bfloat16* scaled;
     long long ld_scaled;
-    int hidden;
 };
 cudaError_t launch_entropy_rows(const EntropyRows& a, cudaStream_t stream);
 

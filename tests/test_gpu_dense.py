@@ -604,3 +604,18 @@ def test_first_calls_of_a_process_inside_a_capture(tokens):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST.format(tokens=tokens)], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("tokens", [16, 300])
+def test_losses_are_fp32_sums(tokens):
+    """The target's logit is an fp32 sum of 16 products to a thread (4096 of them) and five to eight more
+    additions: off by 26 roundings of 2^-24 of the products' magnitudes at most. lse is off by the other
+    logits' errors, which the softmax averages: here below 2^-21 of it."""
+    x, w, y, _ = tokens_of(32, tokens, 4096, 3000, spread=2.0, drop=0.0)
+    x[::2] += (12 * w[y[::2]].double() / (w[y[::2]].double() ** 2).sum(1, keepdim=True)).to(BF16)   # (near-certain ones)
+    l = x.double() @ w.double().t()
+    lse = torch.logsumexp(l, 1)
+    want = lse - l.gather(1, y[:, None])[:, 0]
+    size = (x.double().abs() * w[y].double().abs()).sum(1)
+    for got in (tcl.cross_entropy(x, w, y)[0], tcl.cross_entropy_grad(x, w, y, torch.ones(tokens, device=DEV))[0]):
+        assert ((got.double() - want).abs() <= 26 * 2.0 ** -24 * size + 2.0 ** -21 * lse).all()
