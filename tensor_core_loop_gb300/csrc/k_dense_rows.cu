@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(kRowThreads) entropy_rows_kernel(const Entropy
     __shared__ float factor[ROWS], dots[kRowThreads / 32];
     auto target_of = [&](long long t) -> long long {
         if (t >= a.rows) return -1;
-        const long long v =
-            a.wide_targets ? static_cast<const long long*>(a.targets)[t] : static_cast<const int*>(a.targets)[t];
+        const long long v = a.wide_targets ? __ldcg(static_cast<const long long*>(a.targets) + t)
+                                           : __ldcg(static_cast<const int*>(a.targets) + t);
         return v < a.vocab ? v : -1;
     };
     // the rows of x: a warp each, or the block its one
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kRowThreads) entropy_rows_kernel(const Entropy
         const __nv_bfloat16* w = a.w + t * a.ld_w;
 #pragma unroll 4
         for (int i = lane; i < pieces; i += XT) {
-            const uint4 p = reinterpret_cast<const uint4*>(x)[i], q = reinterpret_cast<const uint4*>(w)[i];
+            const uint4 p = __ldcg(reinterpret_cast<const uint4*>(x) + i), q = __ldcg(reinterpret_cast<const uint4*>(w) + i);
             const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -138,13 +138,17 @@ __global__ void __launch_bounds__(kRowThreads) entropy_rows_kernel(const Entropy
                 dot = fmaf(__uint_as_float(u[j] & 0xffff0000u), __uint_as_float(v[j] & 0xffff0000u), dot);
             }
         }
-        if (rest < a.hidden) dot = fmaf(__bfloat162float(x[rest]), __bfloat162float(w[rest]), dot);
+        auto one = [](const __nv_bfloat16* p) {
+            return __uint_as_float(static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short*>(p))) << 16);
+        };
+        if (rest < a.hidden) dot = fmaf(one(x + rest), one(w + rest), dot);
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
     if (threadIdx.x % 32 == 0) dots[threadIdx.x / 32] = dot;
     // (The kernel before this one in the stream is the logits' own: it writes none of what is read above, and
-    // what came before it had ended when it started to read.)
+    // what came before it had ended when it started to read. Read from the L2: what a first-level cache holds
+    // may be older until the wait.)
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
