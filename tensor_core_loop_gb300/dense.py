@@ -86,17 +86,19 @@ class GatedFfnKept(NamedTuple):
         return self.values[2, :, :self.inner]
 
 
-def _call(fn, what, device, stream, *args):
-    """Calls fn(*args, workspace, its size, stream), with a workspace where it asks for one."""
+def _call(fn, what, device, stream, room, *args):
+    """Calls fn(*args, workspace, its size, stream) with a workspace of ``room`` bytes, and once more with a
+    larger one where it asks for that."""
     if device.index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            return _call(fn, what, device, stream, *args)
+            return _call(fn, what, device, stream, room, *args)
     raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    size = ctypes.c_size_t(0)
-    st = fn(*args, None, size, raw)
+    size = ctypes.c_size_t(room)
+    space = torch.empty(room, dtype=torch.uint8, device=device) if room else None   # (on the stream: the caller is inside _on)
+    st = fn(*args, space.data_ptr() if room else None, size, raw)
     if st == _WORKSPACE:
-        room = torch.empty(size.value, dtype=torch.uint8, device=device)   # (on the stream: the caller is inside _on)
-        st = fn(*args, room.data_ptr(), size, raw)
+        space = torch.empty(size.value, dtype=torch.uint8, device=device)
+        st = fn(*args, space.data_ptr(), size, raw)
     if st:
         raise TclError(st, what)
 
@@ -153,7 +155,7 @@ def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", keep: bool = Fa
         out = torch.empty((tokens, hidden), dtype=_BF16, device=device)
         h = mid.data_ptr()
         part = 2 * tokens * pitch
-        _call(_lib().tcl_gated_ffn, "gated_ffn", device, stream, tokens, hidden, inner, x.data_ptr(), ldx, w_gate.data_ptr(),
+        _call(_lib().tcl_gated_ffn, "gated_ffn", device, stream, 0, tokens, hidden, inner, x.data_ptr(), ldx, w_gate.data_ptr(),
               ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd, act, h + part if keep else None,
               h + 2 * part if keep else None, h, pitch, out.data_ptr(), hidden)
         return (out, GatedFfnKept(mid, inner)) if keep else out
@@ -180,7 +182,8 @@ def gated_ffn_grad(grad, x, w_gate, w_up, w_down, kept: GatedFfnKept, activation
         dx = torch.empty((tokens, hidden), dtype=_BF16, device=device)
         dw = [torch.empty(w.shape, dtype=dtype, device=device) for w in (w_gate, w_up, w_down)]
         h, part = values.data_ptr(), 2 * tokens * pitch
-        _call(_lib().tcl_gated_ffn_grad, "gated_ffn_grad", device, stream, tokens, hidden, inner, grad.data_ptr(), ld_grad,
+        room = 2 * ((2 * tokens * ((inner + 63) & ~63) + 255) & ~255)   # (what most sizes take: dgate and dup)
+        _call(_lib().tcl_gated_ffn_grad, "gated_ffn_grad", device, stream, room, tokens, hidden, inner, grad.data_ptr(), ld_grad,
               x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd, act,
               h + part, h + 2 * part, h, pitch, dx.data_ptr(), hidden, dw[0].data_ptr(), hidden, dw[1].data_ptr(), hidden,
               dw[2].data_ptr(), inner, code)
@@ -209,7 +212,9 @@ def cross_entropy(x, w, targets, stream=None):
     with _on(stream):
         loss = torch.empty(tokens, dtype=_F32, device=device)
         lse = torch.empty(tokens, dtype=_F32, device=device)
-        _call(_lib().tcl_cross_entropy, "cross_entropy", device, stream, tokens, hidden, vocab, x.data_ptr(), ldx, w.data_ptr(),
+        # (what operands on 16-byte pieces take: sums for each token and 64 words, or each warp of the GPU)
+        room = tokens * max(8 * ((vocab + 63) // 64), 8192) + 1024
+        _call(_lib().tcl_cross_entropy, "cross_entropy", device, stream, room, tokens, hidden, vocab, x.data_ptr(), ldx, w.data_ptr(),
               ldw, targets.data_ptr(), targets.element_size(), loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
@@ -231,7 +236,7 @@ def cross_entropy_grad(x, w, targets, grad, out_dtype=None, stream=None):
         lse = torch.empty(tokens, dtype=_F32, device=device)
         dx = torch.empty((tokens, hidden), dtype=_BF16, device=device)
         dw = torch.empty((vocab, hidden), dtype=dtype, device=device)
-        _call(_lib().tcl_cross_entropy_grad, "cross_entropy_grad", device, stream, tokens, hidden, vocab, x.data_ptr(), ldx,
+        _call(_lib().tcl_cross_entropy_grad, "cross_entropy_grad", device, stream, 0, tokens, hidden, vocab, x.data_ptr(), ldx,
               w.data_ptr(), ldw, targets.data_ptr(), targets.element_size(), grad.data_ptr(), loss.data_ptr(), lse.data_ptr(),
               dx.data_ptr(), hidden, dw.data_ptr(), hidden, code)
     return loss, lse, dx, dw
@@ -258,6 +263,11 @@ def _where(stream, tensors):
     return _device(stream, "tensors", *(tensors if stream is not None else tensors[:1]))
 
 
+def _clip_room(tensors):
+    """A sum for each block of the launches that they take."""
+    return 16384 * (len(tensors) // 256 + 2)
+
+
 def _at(a):
     """The address of an array's first element."""
     return a.buffer_info()[0]
@@ -274,7 +284,7 @@ def grad_norm(tensors, stream=None):
     host = array("Q", ptr), array("q", length), array("i", types)
     with _on(stream):
         norm = torch.empty((), dtype=_F32, device=device)
-        _call(_lib().tcl_grad_norm, "grad_norm", device, stream, len(tensors), *map(_at, host), norm.data_ptr())
+        _call(_lib().tcl_grad_norm, "grad_norm", device, stream, _clip_room(tensors), len(tensors), *map(_at, host), norm.data_ptr())
     return norm
 
 
@@ -301,5 +311,5 @@ def clip_grads(tensors, max_norm: float, out=None, stream=None):
     host = array("Q", ptr), array("Q", to_ptr), array("q", length), array("i", types)
     with _on(stream):
         norm = torch.empty((), dtype=_F32, device=device)
-        _call(_lib().tcl_clip_gradients, "clip_grads", device, stream, len(tensors), *map(_at, host), max_norm, norm.data_ptr())
+        _call(_lib().tcl_clip_gradients, "clip_grads", device, stream, _clip_room(tensors), len(tensors), *map(_at, host), max_norm, norm.data_ptr())
     return norm
