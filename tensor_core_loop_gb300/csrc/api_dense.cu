@@ -768,8 +768,8 @@ int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int
     if ((st = enough(room, workspace_bytes))) return st;
     const auto lock = library_lock();
     if (room.copies.n && (st = status_of(launch_dense_copies(room.copies, stream)))) return st;
-    for (int t0 = 0; t0 < tokens; t0 += piece) {
-        const int rows = std::min(piece, tokens - t0);
+    for (long long from = 0; from < tokens; from += piece) {   // (the end of the last piece may pass 32 bits)
+        const int t0 = static_cast<int>(from), rows = std::min(piece, tokens - t0);
         int chunk;
         if ((st = entropy_pairs(n, t0, rows, e, lde, parts, target_logit, &chunk, g))) return st;
         EntropyRows r = entropy_rows(n, t0, rows, tiles_of(vocab, chunk), chunk, parts, target_logit);

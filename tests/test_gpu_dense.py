@@ -372,6 +372,26 @@ def test_exponentials_in_pieces():
     ref.within(dw, ref.rounded(ref.V(total, bound)), "dw")
 
 
+def test_as_many_tokens_as_there_may_be():
+    """The last piece's end passes 32 bits. Only some tokens, first, last and at the pieces' ends, have a
+    weight."""
+    tokens, vocab, piece = 2 ** 31 - 2 ** 16 - 1, 512, 2 ** 21
+    g = torch.Generator(device=DEV).manual_seed(28)
+    x = torch.zeros(tokens, 8, dtype=BF16, device=DEV)[:, :1]   # (rows of one value on 16-byte pieces)
+    w = (torch.randn(vocab, 1, device=DEV, generator=g)).to(BF16)
+    y = torch.full((tokens,), -1, dtype=torch.int32, device=DEV)
+    grad = torch.zeros(tokens, device=DEV)
+    some = torch.cat([torch.arange(i, i + 40, device=DEV) for i in (0, piece - 20, 512 * piece - 20, 1023 * piece - 20, tokens - 40)])
+    x[some] = torch.randn(some.numel(), 1, device=DEV, generator=g).to(BF16)
+    y[some] = torch.randint(0, vocab, (some.numel(),), device=DEV, generator=g).int()
+    grad[some] = torch.rand(some.numel(), device=DEV, generator=g)
+    loss, lse, dx, dw = tcl.cross_entropy_grad(x, w, y, grad)
+    want = ref.cross_entropy(x[some], w, y[some], grad[some])
+    for got, r, what in zip((loss[some], lse[some], dx[some], dw), want, ("loss", "lse", "dx", "dw")):
+        ref.within(got, r, what)
+    assert int((loss != 0).sum()) <= some.numel() and int((dx != 0).sum()) <= some.numel()
+
+
 def test_weights_past_32_bits_of_elements():
     tokens, hidden, vocab = 70, 4096, 540_000
     g = torch.Generator(device=DEV).manual_seed(19)
