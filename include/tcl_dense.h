@@ -7,7 +7,8 @@
  * too, with these differences.
  *   Sizes: tokens may be 0 (nothing is read; the gradients of weights are zeros); widths are at
  *     least 1; all are below 2^31 - 2^16, and a product has fewer than 2^30 tiles of 256 × 128 (the
- *     block's first one of 256 × 64; TCL_ERR_DIMS otherwise).
+ *     block's first one of 256 × 64; TCL_ERR_DIMS otherwise). What a sum runs over is at most 2^25:
+ *     hidden and inner; for the gradients also the vocabulary and the block's tokens.
  *   Memory: nothing is allocated and nothing kept between calls. A call that needs a workspace
  *     gets it from the caller: *workspace_bytes is the size of what `workspace` points to (256-byte
  *     aligned; 0 and NULL: none). Where a call needs more, it launches nothing, writes the size

@@ -19,6 +19,9 @@ typedef __nv_bfloat16 bf16;
 constexpr unsigned long long kTimeoutNs = 1000000000ull;   // bound on every in-kernel wait: 1 s
 constexpr int kMostSize = 0x7ffeffff;                       // sizes are rounded up to whole tiles in 32 bits
 constexpr long long kExpBytes = 1ll << 31;                  // exponentials kept at a time
+// A sum's terms: the warps that wait for a tile's whole sum (dX: over two pairs) would give up after kTimeoutNs.
+// 2^26 terms are 2^20 k-blocks of 0.3 us, 0.7 us where all of the operands come from HBM.
+constexpr int kMostTerms = 1 << 25;
 
 bool width(int n) { return n >= 1 && n <= kMostSize; }
 bool on(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -389,6 +392,7 @@ struct Ffn {
 
 int ffn_sizes(int tokens, int hidden, int inner, int act) {
     if (tokens < 0 || tokens > kMostSize || !width(hidden) || !width(inner)) return TCL_ERR_DIMS;
+    if (hidden > kMostTerms || inner > kMostTerms) return TCL_ERR_DIMS;
     // (the gate's tiles are half as wide; the gradients' products share a launch)
     if (!countable(tokens, 2 * std::min(inner, 0x3fffffff)) || !countable(tokens, hidden) || !countable(inner, hidden) ||
         !countable(hidden, inner))
@@ -444,7 +448,7 @@ struct Entropy {
 
 int entropy_checks(int tokens, int hidden, int vocab, const void* X, int ldx, const void* W, int ldw, const void* targets,
                    int target_bytes, const float* loss, const float* lse) {
-    if (tokens < 0 || tokens > kMostSize || !width(hidden) || !width(vocab)) return TCL_ERR_DIMS;
+    if (tokens < 0 || tokens > kMostSize || !width(hidden) || !width(vocab) || hidden > kMostTerms) return TCL_ERR_DIMS;
     if (!countable(tokens, vocab) || !countable(tokens, hidden) || !countable(vocab, hidden)) return TCL_ERR_DIMS;
     if (target_bytes != 4 && target_bytes != 8) return TCL_ERR_CONFIG;
     if (tokens && (!X || !W || !targets || !loss || !lse)) return TCL_ERR_NULL;
@@ -600,6 +604,7 @@ int tcl_gated_ffn_grad(int tokens, int hidden, int inner, const void* grad, int 
                        int ld_dgate, void* dWup, int ld_dup, void* dWdown, int ld_ddown, int w_type, void* workspace,
                        size_t* workspace_bytes, cudaStream_t stream) {
     if (const int st = ffn_sizes(tokens, hidden, inner, act)) return st;
+    if (tokens > kMostTerms) return TCL_ERR_DIMS;
     if (w_type != TCL_OUT_F32 && w_type != TCL_OUT_BF16) return TCL_ERR_CONFIG;
     if (!workspace_bytes || (*workspace_bytes && !workspace) || !dWgate || !dWup || !dWdown) return TCL_ERR_NULL;
     if (tokens && (!grad || !X || !Wgate || !Wup || !Wdown || !gate || !upp || !h || !dX)) return TCL_ERR_NULL;
@@ -704,6 +709,7 @@ int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void* X, int
                            int ld_dx, void* dW, int ld_dw, int w_type, void* workspace, size_t* workspace_bytes,
                            cudaStream_t stream) {
     if (const int st = entropy_checks(tokens, hidden, vocab, X, ldx, W, ldw, targets, target_bytes, loss, lse)) return st;
+    if (vocab > kMostTerms) return TCL_ERR_DIMS;   // (tokens come in pieces of 2^24 at most)
     if (w_type != TCL_OUT_F32 && w_type != TCL_OUT_BF16) return TCL_ERR_CONFIG;
     if (!workspace_bytes || (*workspace_bytes && !workspace) || !dW || (tokens && (!grad || !dX))) return TCL_ERR_NULL;
     if (ld_dx < hidden || ld_dw < hidden) return TCL_ERR_LD;

@@ -48,6 +48,8 @@ MOST = 2 ** 31 - 2 ** 16
 def ffn(L, **kw):
     d = dict(T=4, H=64, F=96, X=P, ldx=64, G=P, ldg=64, U=P, ldu=64, D=P, ldd=96, act=0, gate=P, up=P, h=P, ldk=96, out=P, ldo=64,
              ws=None, wsb=size())
+    if kw.pop("names", None):
+        return d
     d.update(kw)
     return L.tcl_gated_ffn(*d.values(), None)
 
@@ -64,9 +66,20 @@ def test_ffn_refuses(L, kw, status):
     assert ffn(L, **kw) == status
 
 
+@pytest.mark.parametrize("call,kw", [
+    ("ffn", dict(H=2 ** 25 + 1)), ("ffn", dict(F=2 ** 25 + 1)), ("ffn_grad", dict(T=2 ** 25 + 1)), ("ffn_grad", dict(F=2 ** 26)),
+    ("entropy", dict(H=2 ** 25 + 1)), ("entropy_grad", dict(H=2 ** 26)), ("entropy_grad", dict(V=2 ** 25 + 1))])
+def test_sums_too_long_for_a_bounded_wait_are_refused(L, call, kw):
+    far = dict.fromkeys([k for k in globals()[call](L, names=True) if k.startswith("ld")], 2 ** 27)
+    assert globals()[call](L, **far, **kw) == 2
+    assert globals()[call](L, **far, **{k: 2 ** 25 for k in kw}, **{"X": None}) == 1   # (as far as the next check)
+
+
 def ffn_grad(L, **kw):
     d = dict(T=4, H=64, F=96, grad=P, ldgr=64, X=P, ldx=64, G=P, ldg=64, U=P, ldu=64, D=P, ldd=96, act=0, gate=P, up=P, h=P, ldk=96,
              dX=P, lddx=64, dG=P, lddg=64, dU=P, lddu=64, dD=P, lddd=96, wt=1, ws=None, wsb=size())
+    if kw.pop("names", None):
+        return d
     d.update(kw)
     return L.tcl_gated_ffn_grad(*d.values(), None)
 
@@ -85,6 +98,8 @@ def test_ffn_grad_refuses(L, kw, status):
 
 def entropy(L, **kw):
     d = dict(T=4, H=64, V=100, X=P, ldx=64, W=P, ldw=64, y=P, yb=8, loss=P, lse=P, ws=None, wsb=size())
+    if kw.pop("names", None):
+        return d
     d.update(kw)
     return L.tcl_cross_entropy(*d.values(), None)
 
@@ -92,6 +107,8 @@ def entropy(L, **kw):
 def entropy_grad(L, **kw):
     d = dict(T=4, H=64, V=100, X=P, ldx=64, W=P, ldw=64, y=P, yb=8, grad=P, loss=P, lse=P, dX=P, lddx=64, dW=P, lddw=64, wt=1, ws=None,
              wsb=size())
+    if kw.pop("names", None):
+        return d
     d.update(kw)
     return L.tcl_cross_entropy_grad(*d.values(), None)
 
