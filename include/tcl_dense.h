@@ -72,7 +72,8 @@ TCL_API int tcl_cross_entropy(int tokens, int hidden, int vocab, const void* X, 
 
 /* The same and the gradients of sum over t of grad[t]·loss[t] (grad: fp32):
  *   d[t][v] = grad[t]·(exp(l[t][v] - lse[t]) - [v = target[t]]),  dX = d · W (bf16),  dW = d^T · X
- * (w_type). Dropped tokens add nothing, whatever their rows hold, and their rows of dX are zeros.
+ * (w_type). Dropped tokens add nothing, whatever their rows hold, and their rows of dX are zeros; one that is
+ * not dropped and has a logit that is infinity or NaN makes its row of dX and all of dW NaN.
  * The exponentials are computed once, kept in bf16 for a piece of the tokens at a time (at most
  * 2 GiB, or 256 tokens) and read by both products; the rows of X for dW are rounded to bf16 again
  * after their scaling by grad[t] / (sum of the exponentials). Pieces of dW are added in fp32. */

@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(kRowThreads) entropy_rows_kernel(const Entropy
         }
     }
     if (k == 0) {
-        const float f = kept ? weight / s : 0.0f;
+        // (an infinite sum, of an infinite logit, must not pass for a token without weight)
+        const float f = kept ? s < __int_as_float(0x7f800000) ? weight / s : __int_as_float(0x7fffffff) : 0.0f;
         factor[r] = f;
         if (in) a.factor[row] = f;
     }

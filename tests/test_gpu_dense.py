@@ -335,6 +335,21 @@ def test_nan_stays_in_its_row():
     assert torch.equal(tcl.cross_entropy(x, w, y)[0][rows], loss[rows])
 
 
+@pytest.mark.parametrize("tokens", [200, 2100])
+@pytest.mark.parametrize("target", [0, 7])
+def test_infinite_logit_is_not_lost(tokens, target):
+    """One token with one logit of infinity (minus infinity for the others): its gradients are no numbers."""
+    x, w, y, grad = tokens_of(27, tokens, 64, 500, drop=0.0)
+    x[:, 0], w[:, 0] = -1.0, 0.0
+    x[33, 0], w[7, 0], y[33] = 1.0, float("inf"), target
+    y = torch.where((y == 7) & (torch.arange(tokens, device=DEV) != 33), 8, y)
+    loss, lse, dx, dw = tcl.cross_entropy_grad(x, w, y, grad)
+    assert float(lse[33]) == float("inf") and not loss[33].isfinite()
+    assert dx[33].isnan().all() and dw.isnan().all()
+    others = torch.arange(tokens, device=DEV) != 33
+    assert loss[others].isfinite().all() and dx[others][:, 1:].isfinite().all()
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 def test_activations_over_their_whole_range(act):
     """One hidden value and weights of one: gates of every size, up to where the results end."""
