@@ -167,10 +167,15 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const double length = norm_of(parts, nparts);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(length);
-    // (a norm that is NaN or infinite scales nothing: the caller, who is told of it, drops the step)
-    const bool scaled = length > bound && length < __longlong_as_double(0x7ff0000000000000ll);
-    const float f = scaled ? static_cast<float>(static_cast<double>(bound) / length) : 1.0f;
+    const float told = static_cast<float>(length);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = told;
+    // (a norm that is NaN or infinite, in fp32, scales nothing: the caller, who is told of it, drops the step)
+    const bool scaled = length > bound && told < __int_as_float(0x7f800000);
+    // A factor below fp32's normal numbers keeps its digits: 2^-126 of it goes first. (What that takes from a small
+    // element is less than half of fp32's smallest number times f, and f < 1.)
+    const double factor = scaled ? static_cast<double>(bound) / length : 1.0;
+    const bool tiny = factor < 0x1p-126;
+    const float first = tiny ? 0x1p-126f : 1.0f, f = static_cast<float>(tiny ? factor * 0x1p126 : factor);
     for (long long back = blockIdx.x; back < a.pieces; back += gridDim.x) {
         const long long piece = a.pieces - 1 - back;
         const ClipTensor& t = a.t[tensor_of(a, piece)];
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
         int done = 0;
         if ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) % 16 == 0) {
             const int lead = min(n, to_unit(x));
-            if (threadIdx.x < lead) y[threadIdx.x] = scaled ? static_cast<T>(value(x[threadIdx.x]) * f) : x[threadIdx.x];
+            if (threadIdx.x < lead) y[threadIdx.x] = scaled ? static_cast<T>(value(x[threadIdx.x]) * first * f) : x[threadIdx.x];
             x += lead;
             y += lead;
             n -= lead;
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
                 float e[U];
                 unpack(v, e);
 #pragma unroll
-                for (int i = 0; i < U; ++i) e[i] *= f;
+                for (int i = 0; i < U; ++i) e[i] = e[i] * first * f;
                 return scaled ? pack(e) : v;
             };
             for (; done + STEP <= n; done += STEP) {
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
             for (int i = done / U + threadIdx.x; i < n / U; i += kThreads) y4[i] = times(x4[i]);
             done = n / U * U;
         }
-        for (int i = done + threadIdx.x; i < n; i += kThreads) y[i] = scaled ? static_cast<T>(value(x[i]) * f) : x[i];
+        for (int i = done + threadIdx.x; i < n; i += kThreads) y[i] = scaled ? static_cast<T>(value(x[i]) * first * f) : x[i];
     }
 }
 

@@ -96,6 +96,24 @@ def test_squares_past_the_range_of_fp32(dtype, scale):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_norm_past_the_range_of_fp32_scales_nothing(dtype):
+    """Finite in 64 bits, but told as infinity."""
+    ts = [torch.full((9000,), 2e38, dtype=dtype, device=DEV)]
+    out = [torch.zeros_like(ts[0])]
+    assert float(tcl.clip_grads(ts, 1.0, out=out)) == math.inf and torch.equal(out[0], ts[0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_factors_below_the_normal_numbers(dtype, offset):
+    """bound/norm of 1e-42 or so: results are normal numbers all the same."""
+    ts = tensors(7, (9000, 21), (dtype,), scale=3e35, offset=offset)
+    bound = float(torch.tensor(1e-5, dtype=F32))
+    out = [torch.zeros(t.numel() + 1, dtype=dtype, device=DEV)[1:] for t in ts]
+    check(ts, tcl.clip_grads(ts, bound, out=out), out, bound)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("shift", range(8))
 def test_results_at_another_alignment(dtype, shift):
     ts = tensors(6, (70001, 8192, 3), (dtype,), offset=shift)
