@@ -90,8 +90,8 @@ TCL_API int tcl_grad_norm(int count, const void* const* tensors, const long long
                           void* workspace, size_t* workspace_bytes, cudaStream_t stream);
 
 /* The same, and to[i] = from[i] · bound/norm, rounded once, where norm > bound; else, and where the
- * norm is infinite or NaN, to[i] = from[i]. to[i] may be from[i]; otherwise no two tensors overlap.
- * bound >= 0. */
+ * norm is infinite or NaN, to[i] = from[i]. to[i] may be from[i]; otherwise a
+ * result overlaps no other tensor (TCL_ERR_CONFIG). bound >= 0. */
 TCL_API int tcl_clip_gradients(int count, const void* const* from, void* const* to, const long long* lengths,
                                const int* types, float bound, float* norm, void* workspace, size_t* workspace_bytes,
                                cudaStream_t stream);

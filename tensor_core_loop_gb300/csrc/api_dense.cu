@@ -6,6 +6,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <memory>
+#include <new>
 
 #include "clip_launch.cuh"
 #include "dense_launch.cuh"
@@ -513,6 +515,34 @@ int clip_checks(int count, const void* const* from, const long long* lengths, co
     return TCL_OK;
 }
 
+// Whether a result shares memory with another one, or with an operand that is not its own: the blocks of one tensor
+// would read what those of the other may have scaled already.
+int overlap_checks(int count, const void* const* from, void* const* to, const long long* lengths, const int* types) {
+    struct Span {
+        uintptr_t lo, hi;
+        int i;
+    };
+    const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[count ? count : 1]);
+    if (!spans) return TCL_ERR_NO_MEMORY;
+    auto span = [&](const void* p, int i) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        return Span{lo, lo + static_cast<uintptr_t>(lengths[i]) * (types[i] == TCL_OUT_F32 ? 4 : 2), i};
+    };
+    Span* end = spans.get();
+    for (int i = 0; i < count; ++i)
+        if (lengths[i]) *end++ = span(to[i], i);
+    std::sort(spans.get(), end, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    for (Span* s = spans.get(); s + 1 < end; ++s)
+        if (s->hi > s[1].lo) return TCL_ERR_CONFIG;
+    for (int i = 0; i < count; ++i) {
+        if (!lengths[i] || from[i] == to[i]) continue;   // (its own span, and no two of those overlap)
+        const Span a = span(from[i], i);
+        const Span* s = std::upper_bound(spans.get(), end, a.lo, [](uintptr_t lo, const Span& b) { return lo < b.hi; });
+        if (s < end && s->lo < a.hi) return TCL_ERR_CONFIG;
+    }
+    return TCL_OK;
+}
+
 // Calls f with one launch's tensors after another's: those of one type, kClipTensors at most.
 template <class F>
 int each_launch(int count, const void* const* from, void* const* to, const long long* lengths, const int* types, F f) {
@@ -830,6 +860,7 @@ int tcl_clip_gradients(int count, const void* const* from, void* const* to, cons
         if (lengths[i] && !to[i]) return TCL_ERR_NULL;
         if (!on(to[i], types[i] == TCL_OUT_F32 ? 4 : 2)) return TCL_ERR_ALIGN;
     }
+    if (const int st = overlap_checks(count, from, to, lengths, types)) return st;
     Gpu g;
     if (const int st = gpu_of(stream, &g)) return st;
     int blocks = 0;

@@ -210,6 +210,26 @@ def test_binding_refuses():
             call()
 
 
+@pytest.mark.parametrize("ptrs,to,lengths,types", [
+    ((0, 4096), (8192, 8192), (4, 5), (0, 1)), ((0, 4096), (8192, 8204), (4, 5), (0, 1)), ((0, 16), (0, 14), (4, 5), (0, 1)),
+    ((0, 4096), (4, 8192), (4, 5), (0, 1)), ((0, 4096), (4096, 0), (4, 4), (0, 0)), ((0, 4096), (8192, 10), (4, 5), (0, 1)),
+    ((0, 64, 128), (0, 64, 78), (8, 8, 2), (0, 1, 1)), ((0, 64, 128), (256, 132, 512), (8, 8, 4), (0, 0, 1)),
+    ((0, 0, 0), (64, 256, 15 * 4), (8, 8, 8), (0, 0, 0))])
+def test_clip_refuses_results_in_other_tensors(L, ptrs, to, lengths, types):
+    assert clip(L, ptrs=tuple(P + a for a in ptrs), to=tuple(P + a for a in to), lengths=lengths, types=types) == 8
+
+
+@pytest.mark.parametrize("ptrs,to,lengths,types", [
+    ((0, 16), (0, 16), (4, 5), (0, 1)), ((0, 16), (64, 80), (4, 5), (0, 1)), ((0, 0), (64, 128), (4, 4), (0, 0)),
+    ((0, 0, 16), (0, 0, 16), (4, 0, 5), (0, 0, 1)), ((32, 0), (32, 48), (4, 4), (0, 0)),
+    ((0, 64, 128), (0, 64, 80), (8, 8, 2), (0, 1, 1))])   # (the second one ends where the third one begins)
+def test_clip_takes_results_beside_them(L, ptrs, to, lengths, types):
+    """(As far as the device: there is none here, or too small a workspace.)"""
+    if torch.cuda.is_available():
+        pytest.skip("addresses that are none")
+    assert clip(L, ptrs=tuple(P + a for a in ptrs), to=tuple(P + a for a in to), lengths=lengths, types=types) not in (0, 1, 2, 4, 8, 9)
+
+
 def meta(shape, strides, dtype=BF16):
     return torch.empty_strided(shape, strides, dtype=dtype, device="meta")
 
