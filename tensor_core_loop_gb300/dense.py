@@ -212,8 +212,8 @@ def cross_entropy(x, w, targets, stream=None):
     with _on(stream):
         loss = torch.empty(tokens, dtype=_F32, device=device)
         lse = torch.empty(tokens, dtype=_F32, device=device)
-        # (what operands on 16-byte pieces take: sums for each token and 64 words, or each warp of the GPU)
-        room = tokens * max(8 * ((vocab + 63) // 64), 8192) + 1024
+        # (what operands on 16-byte pieces take: sums for each token and 64 words, for few tokens each warp of the GPU)
+        room = tokens * (8 * max((vocab + 63) // 64, 1024 if tokens <= 128 else 0) + 4) + 512
         _call(_lib().tcl_cross_entropy, "cross_entropy", device, stream, room, tokens, hidden, vocab, x.data_ptr(), ldx, w.data_ptr(),
               ldw, targets.data_ptr(), targets.element_size(), loss.data_ptr(), lse.data_ptr())
     return loss, lse
@@ -291,7 +291,8 @@ def grad_norm(tensors, stream=None):
 def clip_grads(tensors, max_norm: float, out=None, stream=None):
     """Scales the tensors, in place or into ``out`` (a list of tensors of the same lengths and types), by
     max_norm / norm where their ``grad_norm`` is larger than ``max_norm``; a norm that is infinite or
-    NaN scales nothing. Returns the norm before, an fp32 scalar on the GPU."""
+    NaN scales nothing. Returns the norm before, an fp32 scalar on the GPU. A result may be its own tensor, but
+    shares no memory with another one."""
     tensors = list(tensors)
     if not tensors:
         raise ValueError("at least one tensor")

@@ -370,6 +370,17 @@ def test_activations_over_their_whole_range(act):
 
 # ------------------------------------------------------------------------------ large sizes
 
+def test_many_tokens_over_few_words_take_little_memory():
+    """A workspace of some values for each token, at the first call."""
+    tokens = 300_000
+    x, w, y, _ = tokens_of(29, tokens, 64, 100)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    tcl.cross_entropy(x, w, y)
+    assert torch.cuda.max_memory_allocated() - before <= tokens * (8 * 2 + 4 + 4 + 4) + 2 ** 22
+
+
 def test_exponentials_in_pieces():
     """More than 2 GiB of exponentials: the pieces' gradients of w are added in fp32."""
     tokens, vocab = 8192 + 300, 131072
