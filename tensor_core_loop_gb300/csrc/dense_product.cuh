@@ -16,7 +16,7 @@
 //              pass will want them
 //   GATE_GRAD  D = dh; dgate = dh·up·act'(gate), dup = dh·act(gate)
 //   ENTROPY    D = logits: for each row the sum of the exponentials over 128 columns, the target's
-//              logit, and in training the exponentials themselves in bf16 (dense_entropy.cuh says
+//              logit, and in training the exponentials themselves in bf16 (k_dense_rows.cu says
 //              what they are relative to)
 //
 // Roles of each CTA: warp 0 loads A, warp 10 B (TMA, 128-byte swizzle, a ring of 64-value k-blocks),
