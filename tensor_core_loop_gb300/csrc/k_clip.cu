@@ -174,8 +174,11 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
     // A factor below fp32's normal numbers keeps its digits: 2^-126 of it goes first. (What that takes from a small
     // element is less than half of fp32's smallest number times f, and f < 1.)
     const double factor = scaled ? static_cast<double>(bound) / length : 1.0;
-    const bool tiny = factor < 0x1p-126;
-    const float first = tiny ? 0x1p-126f : 1.0f, f = static_cast<float>(tiny ? factor * 0x1p126 : factor);
+    float first = 1.0f, f = static_cast<float>(factor);
+    if (f < 0x1p-126f) {
+        first = 0x1p-126f;
+        f = static_cast<float>(factor * 0x1p126);
+    }
     for (long long back = blockIdx.x; back < a.pieces; back += gridDim.x) {
         const long long piece = a.pieces - 1 - back;
         const ClipTensor& t = a.t[tensor_of(a, piece)];
