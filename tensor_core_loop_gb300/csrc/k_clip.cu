@@ -67,17 +67,19 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
 }
 
-// The sum over a block of 256, the same for all of its threads; its order is fixed.
+// The sum over a block of 256, in its first warp alone; its order is fixed. (An SM has two fp64 lanes: an instruction
+// of eight warps takes 128 cycles.)
 __device__ __forceinline__ double block_sum(double v) {
-    __shared__ double sh[kThreads / 32];
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
+    __shared__ double sh[kThreads];
+    sh[threadIdx.x] = v;
     __syncthreads();
     double s = 0.0;
+    if (threadIdx.x < 32) {
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) s += sh[i];
+        for (int i = 0; i < kThreads / 32; ++i) s += sh[32 * i + threadIdx.x];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    }
     return s;
 }
 
@@ -147,10 +149,12 @@ __global__ void __launch_bounds__(kThreads, 5) square_sums_kernel(const __grid_c
     if (threadIdx.x == 0) parts[blockIdx.x] = sum;
 }
 
+// The norm, in the block's first warp alone.
 __device__ __forceinline__ double norm_of(const double* parts, int n) {
     double s = 0.0;
     for (int i = threadIdx.x; i < n; i += kThreads) s += parts[i];
-    return sqrt(block_sum(s));
+    s = block_sum(s);
+    return threadIdx.x < 32 ? sqrt(s) : 0.0;
 }
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const double* parts, int n, float* norm) {
@@ -166,19 +170,24 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
     constexpr int U = 16 / sizeof(T), Q = 8;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    __shared__ float sh[3];
     const double length = norm_of(parts, nparts);
-    const float told = static_cast<float>(length);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = told;
-    // (a norm that is NaN or infinite, in fp32, scales nothing: the caller, who is told of it, drops the step)
-    const bool scaled = length > bound && told < __int_as_float(0x7f800000);
-    // A factor below fp32's normal numbers keeps its digits: 2^-126 of it goes first. (What that takes from a small
-    // element is less than half of fp32's smallest number times f, and f < 1.)
-    const double factor = scaled ? static_cast<double>(bound) / length : 1.0;
-    float first = 1.0f, f = static_cast<float>(factor);
-    if (f < 0x1p-126f) {
-        first = 0x1p-126f;
-        f = static_cast<float>(factor * 0x1p126);
+    if (threadIdx.x == 0) {
+        const float told = static_cast<float>(length);
+        if (norm && blockIdx.x == 0) *norm = told;
+        // (a norm that is NaN or infinite, in fp32, scales nothing: the caller, who is told of it, drops the step)
+        const bool larger = length > bound && told < __int_as_float(0x7f800000);
+        // A factor below fp32's normal numbers keeps its digits: 2^-126 of it goes first. (What that takes from a
+        // small element is less than half of fp32's smallest number times the rest, and that is below 1.)
+        const double factor = larger ? static_cast<double>(bound) / length : 1.0;
+        const bool tiny = factor < 0x1p-126;
+        sh[0] = larger ? 1.0f : 0.0f;
+        sh[1] = tiny ? 0x1p-126f : 1.0f;
+        sh[2] = static_cast<float>(tiny ? factor * 0x1p126 : factor);
     }
+    __syncthreads();
+    const bool scaled = sh[0] != 0.0f;
+    const float first = sh[1], f = sh[2];
     for (long long back = blockIdx.x; back < a.pieces; back += gridDim.x) {
         const long long piece = a.pieces - 1 - back;
         const ClipTensor& t = a.t[tensor_of(a, piece)];
