@@ -248,12 +248,17 @@ def _tensors(tensors, name):
     if len(tensors) > _INT:
         _too_large(name)
     T = torch.Tensor
-    types = list(map(_TYPES.get, map(T.dtype.__get__, tensors)))
-    if None in types:
-        raise TypeError(f"{name} must be bfloat16 or float32, not {tensors[types.index(None)].dtype}")
+    types = list(map(T.dtype.__get__, tensors))
+    for other in set(types) - _TYPES.keys():
+        raise TypeError(f"{name} must be bfloat16 or float32, not {other}")
     if not all(map(T.is_contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous")
     return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), types
+
+
+def _codes(types):
+    one = types[0]
+    return array("i", (_TYPES[one],)) * len(types) if types.count(one) == len(types) else array("i", map(_TYPES.get, types))
 
 
 def _where(stream, tensors):
@@ -281,7 +286,7 @@ def grad_norm(tensors, stream=None):
         raise ValueError("at least one tensor")
     ptr, length, types = _tensors(tensors, "tensors")
     device = _where(stream, tensors)
-    host = array("Q", ptr), array("q", length), array("i", types)
+    host = array("Q", ptr), array("q", length), _codes(types)
     with _on(stream):
         norm = torch.empty((), dtype=_F32, device=device)
         _call(_lib().tcl_grad_norm, "grad_norm", device, stream, _clip_room(tensors), len(tensors), *map(_at, host), norm.data_ptr())
@@ -309,7 +314,7 @@ def clip_grads(tensors, max_norm: float, out=None, stream=None):
     if len(set(to_ptr)) < len(to_ptr) and len({a for a, n in zip(to_ptr, length) if n}) < len(length) - length.count(0):
         raise ValueError("a tensor is given twice")   # (it would be scaled twice)
     device = _where(stream, everything)
-    host = array("Q", ptr), array("Q", to_ptr), array("q", length), array("i", types)
+    host = array("Q", ptr), array("Q", to_ptr), array("q", length), _codes(types)
     with _on(stream):
         norm = torch.empty((), dtype=_F32, device=device)
         _call(_lib().tcl_clip_gradients, "clip_grads", device, stream, _clip_room(tensors), len(tensors), *map(_at, host), max_norm, norm.data_ptr())
