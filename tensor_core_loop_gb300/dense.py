@@ -236,7 +236,10 @@ def cross_entropy_grad(x, w, targets, grad, out_dtype=None, stream=None):
         lse = torch.empty(tokens, dtype=_F32, device=device)
         dx = torch.empty((tokens, hidden), dtype=_BF16, device=device)
         dw = torch.empty((vocab, hidden), dtype=dtype, device=device)
-        _call(_lib().tcl_cross_entropy_grad, "cross_entropy_grad", device, stream, 0, tokens, hidden, vocab, x.data_ptr(), ldx,
+        # (what most sizes take: exponentials, scaled rows of x, sums for each 64 words and two more values a token)
+        words = (vocab + 63) // 64
+        room = tokens * (136 * words + 128 * ((hidden + 63) // 64) + 8) + 1280 if tokens * words <= 1 << 24 else 0
+        _call(_lib().tcl_cross_entropy_grad, "cross_entropy_grad", device, stream, room, tokens, hidden, vocab, x.data_ptr(), ldx,
               w.data_ptr(), ldw, targets.data_ptr(), targets.element_size(), grad.data_ptr(), loss.data_ptr(), lse.data_ptr(),
               dx.data_ptr(), hidden, dw.data_ptr(), hidden, code)
     return loss, lse, dx, dw
