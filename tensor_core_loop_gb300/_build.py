@@ -1,4 +1,5 @@
-"""Builds the in-tree shared library ``libtcl_gb300.so`` from ``csrc/*.cu`` with nvcc.
+"""Builds the in-tree shared library ``libtcl_gb300.so`` from ``csrc/*.cu`` with nvcc, and where
+PyTorch is installed the binding's own module ``_tensors.so`` from ``csrc/tensors.cpp``.
 
 Every translation unit is compiled for sm_103a only
 (``-gencode arch=compute_103a,code=sm_103a``), in parallel, into
@@ -12,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB_NAME = "libtcl_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+TENSORS_PATH = os.path.join(PKG, "_tensors.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -45,6 +48,30 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_tensors(force: bool) -> str:
+    """The module that asks PyTorch's tensors for their addresses (the library itself needs no PyTorch)."""
+    try:
+        import torch
+    except ImportError:
+        return ""
+    src = os.path.join(CSRC, "tensors.cpp")
+    if not force and not _stale(TENSORS_PATH, [src, __file__, torch.__file__]):
+        return ""
+    tmp = TENSORS_PATH + f".tmp{os.getpid()}"
+    home = os.path.dirname(torch.__file__)
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           "-I", sysconfig.get_path("include"), src, "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(src)}:\n{r.stderr}")
+    os.replace(tmp, TENSORS_PATH)
+    return r.stderr
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -66,11 +93,12 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")
         return r.stderr
 
-    if todo:
-        with ThreadPoolExecutor(max_workers=jobs or min(len(todo), os.cpu_count() or 4)) as ex:
-            for log in ex.map(compile_one, todo):
-                if verbose and log:
-                    print(log)
+    with ThreadPoolExecutor(max_workers=jobs or min(len(todo) + 1, os.cpu_count() or 4)) as ex:
+        tensors = ex.submit(_build_tensors, force)
+        for log in ex.map(compile_one, todo):
+            if verbose and log:
+                print(log)
+        tensors.result()
     if force or todo or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]

@@ -24,7 +24,6 @@ gradients are calls of their own.
 from __future__ import annotations
 
 import ctypes
-from array import array
 from typing import NamedTuple
 
 try:
@@ -41,10 +40,10 @@ __all__ = ["gated_ffn", "gated_ffn_grad", "GatedFfnKept", "cross_entropy", "cros
 EXPORTED_SYMBOLS_DENSE = ("tcl_gated_ffn", "tcl_gated_ffn_grad", "tcl_cross_entropy", "tcl_cross_entropy_grad",
                           "tcl_grad_norm", "tcl_clip_gradients")
 _ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
-_WORKSPACE = 13   # TCL_ERR_WORKSPACE
+_CONFIG, _WORKSPACE = 8, 13   # TCL_ERR_CONFIG, TCL_ERR_WORKSPACE
 if torch is not None:
     _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-    _TYPES = {_BF16: OUT_BF16, _F32: OUT_F32}
+    _TYPES = {_BF16: OUT_BF16, _F32: OUT_F32}   # (as tensors.cpp has them)
 
 _bound = None
 
@@ -245,28 +244,25 @@ def cross_entropy_grad(x, w, targets, grad, out_dtype=None, stream=None):
     return loss, lse, dx, dw
 
 
-def _tensors(tensors, name):
-    """(addresses, lengths, types) of contiguous bf16 and fp32 tensors. (A model has hundreds of them: maps over
-    the methods cost half of a loop.)"""
+_native = None
+
+
+def _look(tensors, name):
+    """(addresses, lengths, types, GPU) of contiguous bf16 and fp32 tensors, the first three as bytes."""
+    global _native
+    if _native is None:
+        try:
+            from . import _tensors as _native
+        except ImportError as e:
+            raise RuntimeError("_tensors.so is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`") from e
     if len(tensors) > _INT:
         _too_large(name)
-    T = torch.Tensor
-    types = list(map(T.dtype.__get__, tensors))
-    for other in set(types) - _TYPES.keys():
-        raise TypeError(f"{name} must be bfloat16 or float32, not {other}")
-    if not all(map(T.is_contiguous, tensors)):
-        raise ValueError(f"{name} must be contiguous")
-    return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), types
+    return _native.look(tensors, name)
 
 
-def _codes(types):
-    one = types[0]
-    return array("i", (_TYPES[one],)) * len(types) if types.count(one) == len(types) else array("i", map(_TYPES.get, types))
-
-
-def _where(stream, tensors):
+def _where(stream, tensors, *gpus):
     """The GPU that all of them are on; they are recorded on ``stream`` as ``_device`` does."""
-    if len(set(map(torch.Tensor.get_device, tensors))) != 1:
+    if gpus[0] == -2 or gpus.count(gpus[0]) < len(gpus):
         raise ValueError("all tensors must be on one GPU")
     return _device(stream, "tensors", *(tensors if stream is not None else tensors[:1]))
 
@@ -276,23 +272,17 @@ def _clip_room(tensors):
     return 16384 * (len(tensors) // 256 + 2)
 
 
-def _at(a):
-    """The address of an array's first element."""
-    return a.buffer_info()[0]
-
-
 def grad_norm(tensors, stream=None):
     """The square root of the sum of all elements' squares over bf16 and fp32 tensors: an fp32 scalar
     on the GPU. The same tensors give the same bits."""
     tensors = list(tensors)
     if not tensors:
         raise ValueError("at least one tensor")
-    ptr, length, types = _tensors(tensors, "tensors")
-    device = _where(stream, tensors)
-    host = array("Q", ptr), array("q", length), _codes(types)
+    *host, gpu = _look(tensors, "tensors")
+    device = _where(stream, tensors, gpu)
     with _on(stream):
         norm = torch.empty((), dtype=_F32, device=device)
-        _call(_lib().tcl_grad_norm, "grad_norm", device, stream, _clip_room(tensors), len(tensors), *map(_at, host), norm.data_ptr())
+        _call(_lib().tcl_grad_norm, "grad_norm", device, stream, _clip_room(tensors), len(tensors), *host, norm.data_ptr())
     return norm
 
 
@@ -307,18 +297,22 @@ def clip_grads(tensors, max_norm: float, out=None, stream=None):
     max_norm = float(max_norm)
     if not max_norm >= 0:
         raise ValueError("max_norm must not be negative")
-    ptr, length, types = _tensors(tensors, "tensors")
-    to_ptr, everything = ptr, tensors
+    ptr, length, types, gpu = _look(tensors, "tensors")
+    to, gpus, everything = ptr, (gpu,), tensors
     if out is not None:
-        everything = tensors + list(out)
-        to_ptr, to_length, to_types = _tensors(everything[len(tensors):], "out")
+        out = list(out)
+        to, to_length, to_types, to_gpu = _look(out, "out")
         if to_length != length or to_types != types:
             raise ValueError("out must hold a tensor of the same length and type for each one")
-    if len(set(to_ptr)) < len(to_ptr) and len({a for a, n in zip(to_ptr, length) if n}) < len(length) - length.count(0):
-        raise ValueError("a tensor is given twice")   # (it would be scaled twice)
-    device = _where(stream, everything)
-    host = array("Q", ptr), array("Q", to_ptr), array("q", length), _codes(types)
+        gpus, everything = (gpu, to_gpu), tensors + out
+    device = _where(stream, everything, *gpus)
     with _on(stream):
         norm = torch.empty((), dtype=_F32, device=device)
-        _call(_lib().tcl_clip_gradients, "clip_grads", device, stream, _clip_room(tensors), len(tensors), *map(_at, host), max_norm, norm.data_ptr())
+        try:
+            _call(_lib().tcl_clip_gradients, "clip_grads", device, stream, _clip_room(tensors), len(tensors), ptr, to, length, types,
+                  max_norm, norm.data_ptr())
+        except TclError as e:
+            if e.status != _CONFIG:
+                raise
+            raise ValueError("a result shares memory with another tensor") from None
     return norm

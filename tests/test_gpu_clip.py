@@ -125,3 +125,16 @@ def test_results_at_another_alignment(dtype, shift):
 def test_zeros_have_norm_zero():
     ts = [torch.zeros(100000, device=DEV), torch.zeros(3, dtype=BF16, device=DEV)]
     assert float(tcl.clip_grads(ts, 0.0)) == 0.0 and not any(t.any() for t in ts)
+
+
+def test_results_that_share_memory_are_refused():
+    a, b = tensors(8, (4096, 50), (F32,))
+    before = a.clone()
+    for call in (lambda: tcl.clip_grads([a, b, a], 0.1), lambda: tcl.clip_grads([a, a[4000:]], 0.1),
+                 lambda: tcl.clip_grads([b, a[:50]], 0.1, out=[a[10:60], b]), lambda: tcl.clip_grads([b, b + 1], 0.1, out=[a[:50], a[49:99]])):
+        with pytest.raises(ValueError, match="shares memory"):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(a, before)
+    norm = tcl.grad_norm([a, a])   # (reads alone may)
+    assert abs(float(norm) - math.sqrt(2) * norm_of([a])) <= 20 * 2.0 ** -24 * float(norm)
