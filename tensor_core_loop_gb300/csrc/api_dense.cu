@@ -135,18 +135,24 @@ struct Group {
     Product* q;
     int n, bn;
     int units, long_units, extra, pairs;
+    bool deep;   // six k-blocks and a slab
 };
 
 // Deals the units out; the time that takes.
 double deal(Group& g, int sms) {
     long long units = 0, first = 0;
     double each[2] = {0.0, 0.0}, work = 0.0;   // a unit of the first product, the longest of the others
+    double two_slabs = 0.0, one_slab = 0.0, last = 0.0;
     for (int i = 0; i < g.n; ++i) {
         const Product& q = g.q[i];
         const long long n = static_cast<long long>(tiles_of(q.M, 256)) * tiles_of(q.N, g.bn) * q.splits;
         const bool parts = q.splits > 1;
-        const double us = std::max(block_us(g.bn, q.a_mn) * std::ceil(static_cast<double>(blocks_of(q)) / q.splits) + 0.3,
-                                   end_us(g.bn, parts || q.f32, parts || result(q.out, q.ldo, q.N, q.M, q.f32).tma));
+        const double loop = block_us(g.bn, q.a_mn) * std::ceil(static_cast<double>(blocks_of(q)) / q.splits) + 0.3;
+        const double end = end_us(g.bn, parts || q.f32, parts || result(q.out, q.ldo, q.N, q.M, q.f32).tma);
+        const double us = std::max(loop, end);
+        two_slabs += us * static_cast<double>(n);
+        one_slab += std::max(0.97 * loop, 1.4 * end) * static_cast<double>(n);
+        last = std::max(last, end);
         units += n;
         work += us * static_cast<double>(n);
         if (i == 0) first = n;
@@ -154,6 +160,7 @@ double deal(Group& g, int sms) {
     }
     g.units = static_cast<int>(std::min(units, 0x40000000ll));
     g.pairs = static_cast<int>(std::min<long long>(sms / 2, units));
+    g.deep = one_slab + 0.25 * last * g.pairs < two_slabs;   // (each pair's last end shows)
     g.long_units = static_cast<int>(std::min(first, 0x40000000ll));
     const int r0 = g.long_units % g.pairs;
     g.extra = g.n > 1 && r0 ? static_cast<int>(each[0] / each[1] + 0.5) : 0;
@@ -234,6 +241,7 @@ int run(const Group& g, const Gpu& gpu) {
     p.units = g.units;
     p.long_units = g.long_units;
     p.extra = g.extra;
+    p.deep = g.deep;
     int st, first = 0;
     for (int i = 0; i < g.n; ++i) {
         const Product& q = g.q[i];
@@ -408,6 +416,7 @@ int gate_pairs(const Ffn& f, bf16* gate, bf16* upp, bf16* h, long long ldk, cons
     if ((st = map_of(f.x, false, 128, &l.maps.a[0][0])) || (st = map_of(f.wg, false, l.bn / 2, &l.maps.b[0][0])) ||
         (st = map_of(f.wu, false, l.bn / 2, &l.maps.b[0][1])))
         return st;
+    l.p.deep = l.p.q[0].kb0 >= 12;   // (12 k-blocks: a tile's ends, gate and up kept, do not show beside them)
     l.p.act = f.act;
     void* const to[3] = {h, gate, upp};
     for (int i = 0; i < (gate ? 3 : 1); ++i) {

@@ -72,6 +72,7 @@ struct DenseParams {
     // longest K ranges) in turn; `extra` units of the rest to each pair that got one fewer; then
     // the others in turn. Everyone ends within about one unit of the others.
     int long_units, extra;
+    int deep;              // STORE, GATE, wide tiles: a ring of six k-blocks and one staging slab a warp (else five and two)
     int act;
     DenseOut more[2];      // GATE: gate, up (no address: not asked for); GATE_GRAD: dup
     const void* targets;   // ENTROPY: M of them, int32 or int64
@@ -137,16 +138,22 @@ template <int BN_>
 struct DenseCfg {
     static constexpr int BM = 256, BN = BN_, BK = 64;
     static constexpr int CW = BN / 2;               // columns of an epilogue warp
+    // Wide tiles have room for five k-blocks and two staging slabs a warp, or for six and one: the sixth where K is
+    // long (hidden 4096, inner 14336, gate and up kept: 512 tokens 123 us to 118, 2048 tokens 411 to 400;
+    // gradients of 300 tokens 213 to 201, of 1023 tokens 413 to 405), the second slab where k-blocks are few and the
+    // ends show (gradients of 100 tokens 153 us, 169 with one slab).
     static constexpr int STAGES = BN == 256 ? 5 : 6;
+    static constexpr int MOST_STAGES = 6;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128;   // a CTA's share of a k-block
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EW = 8;                    // epilogue warps
     static constexpr int SLABS = 2, SLAB_BYTES = 32 * 128;
-    static constexpr int NBARS = 2 * STAGES + 5 + EW;   // (a warp's own: GATE_GRAD)
+    static constexpr int NBARS = 2 * MOST_STAGES + 5 + EW;   // (a warp's own: GATE_GRAD)
     static constexpr int B_WARP = 2 + EW;           // the warp that loads B
     static constexpr int THREADS = 96 + 32 * EW;
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EW * SLABS * SLAB_BYTES + (NBARS + 2) * 8;
+    static_assert(BN != 256 || STAGE_BYTES == EW * SLAB_BYTES, "a k-block for a slab of each warp");
     static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB per-block shared memory limit");
 };
 
@@ -191,10 +198,16 @@ __device__ __forceinline__ DenseUnit dense_unit(const DenseParams& p, int u) {
 struct DenseSlabs {
     uint8_t* base;
     int used, lane;
+    bool one;
     __device__ __forceinline__ uint8_t* take() {
         uint8_t* s = base + used * DenseCfg<256>::SLAB_BYTES;
-        used ^= 1;
-        if (lane == 0) ptx::bulk_wait_read<DenseCfg<256>::SLABS - 1>();   // the copy that last used this slab has read it
+        if (!one) used ^= 1;
+        if (lane == 0) {   // the copy that last used this slab has read it
+            if (one)
+                ptx::bulk_wait_read<0>();
+            else
+                ptx::bulk_wait_read<1>();
+        }
         __syncwarp();
         return s;
     }
@@ -319,14 +332,16 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
-    uint8_t* slabs = smem + C::STAGES * C::STAGE_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(slabs + C::EW * C::SLABS * C::SLAB_BYTES);
+    const bool deep = BN == 256 && (E == DenseEnd::STORE || E == DenseEnd::GATE) && p.deep;
+    const uint32_t stages = C::STAGES + deep;
+    uint8_t* slabs = smem + stages * C::STAGE_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::EW * C::SLABS * C::SLAB_BYTES);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::NBARS);
     volatile uint32_t* abort_flag = tmem_holder + 1;
 
     const uint32_t full0 = ptx::smem_u32(bars);
-    const uint32_t empty0 = full0 + 8 * C::STAGES;
-    const uint32_t accf0 = empty0 + 8 * C::STAGES;
+    const uint32_t empty0 = full0 + 8 * C::MOST_STAGES;
+    const uint32_t accf0 = empty0 + 8 * C::MOST_STAGES;
     const uint32_t acce0 = accf0 + 16;
     const uint32_t drain_bar = acce0 + 16;
 
@@ -335,7 +350,7 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
     const uint32_t rank = ptx::cluster_ctarank();
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
+        for (int s = 0; s < C::MOST_STAGES; ++s) {
             ptx::mbar_init(full0 + 8 * s, 1);    // the leader's producer and both CTAs' bytes
             ptx::mbar_init(empty0 + 8 * s, 1);   // the MMAs' commit
         }
@@ -397,7 +412,7 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
                     const bool second = kb >= kb0;
                     if (of_a && rank == 0) ptx::mbar_arrive_expect_tx_elected(full0 + 8 * s, 2 * C::STAGE_BYTES);
                     load(to0 + s * C::STAGE_BYTES, second ? map1 : map0, full_leader0 + 8 * s, (second ? kb - kb0 : kb) * C::BK);
-                    if (++s == C::STAGES) {
+                    if (++s == stages) {
                         s = 0;
                         ph ^= 1u;
                     }
@@ -452,7 +467,7 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
                     ptx::mma_f16_pair_x4_elected(tmem_base + b * BN, ad, bd, ad + as, bd + bs, ad + 2 * as, bd + 2 * bs,
                                                  ad + 3 * as, bd + 3 * bs, idesc, kb > U.lo ? 1u : 0u);
                     ptx::mma_commit_pair_multicast_elected(empty0 + 8 * s, 0x3);
-                    if (++s == C::STAGES) {
+                    if (++s == stages) {
                         s = 0;
                         ph ^= 1u;
                     }
@@ -470,7 +485,7 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
         const int quarter = warp & 3;         // the tensor-memory lanes this warp may read
         const int h = (warp - 2) >> 2;        // its share of the columns
         const uint32_t acce_leader0 = ptx::mapa_shared(acce0, 0u);
-        DenseSlabs out{slabs + (warp - 2) * C::SLABS * C::SLAB_BYTES, 0, lane};
+        DenseSlabs out{slabs + (warp - 2) * (deep ? 1 : C::SLABS) * C::SLAB_BYTES, 0, lane, deep};
         [[maybe_unused]] uint32_t kept_phase = 0;
         for (int j = 0, u; (u = dense_walk(p, pair, pairs, j)) < p.units; ++j) {
             const DenseUnit U = dense_unit<E>(p, u);
