@@ -481,6 +481,7 @@ int entropy_pairs(const Entropy& n, int t0, int rows, bf16* e, long long lde, fl
     p.parts = parts;
     p.target_logit = target_logit;
     p.exps = e != nullptr;
+    p.deep = e ? 0 : 2;
     if (e) {
         p.q[0].out = {e, lde, static_cast<int>(up(n.V, 8)), 1};
         if ((st = map_out(p.q[0].out, 0, rows, 1, &l.maps.c[0]))) return st;

@@ -72,7 +72,8 @@ struct DenseParams {
     // longest K ranges) in turn; `extra` units of the rest to each pair that got one fewer; then
     // the others in turn. Everyone ends within about one unit of the others.
     int long_units, extra;
-    int deep;              // STORE, GATE, wide tiles: a ring of six k-blocks and one staging slab a warp (else five and two)
+    int deep;              // STORE, GATE, wide tiles: a ring of six k-blocks and one staging slab a warp (else five and two);
+                           // ENTROPY, wide tiles that store nothing: 2, a ring of seven
     int act;
     DenseOut more[2];      // GATE: gate, up (no address: not asked for); GATE_GRAD: dup
     const void* targets;   // ENTROPY: M of them, int32 or int64
@@ -143,7 +144,7 @@ struct DenseCfg {
     // gradients of 300 tokens 213 to 201, of 1023 tokens 413 to 405), the second slab where k-blocks are few and the
     // ends show (gradients of 100 tokens 153 us, 169 with one slab).
     static constexpr int STAGES = BN == 256 ? 5 : 6;
-    static constexpr int MOST_STAGES = 6;
+    static constexpr int MOST_STAGES = 7;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128;   // a CTA's share of a k-block
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EW = 8;                    // epilogue warps
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
     const uint32_t raw_addr = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
     const bool deep = BN == 256 && (E == DenseEnd::STORE || E == DenseEnd::GATE) && p.deep;
-    const uint32_t stages = C::STAGES + deep;
+    const uint32_t stages = C::STAGES + (BN == 256 && E != DenseEnd::GATE_GRAD ? p.deep : 0);
     uint8_t* slabs = smem + stages * C::STAGE_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::EW * C::SLABS * C::SLAB_BYTES);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::NBARS);
