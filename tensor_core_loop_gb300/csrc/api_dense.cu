@@ -433,6 +433,9 @@ int gate_grad(const Ffn& f, const Mat& grad, const bf16* gate, const bf16* upp, 
     int st;
     if ((st = map_of(grad, false, 128, &l.maps.a[0][0])) || (st = map_of(f.wd, true, l.bn / 2, &l.maps.b[0][0], f.wd.chunks()))) return st;
     l.p.q[0].b_3d = f.wd.chunks();
+    // four warps end a tile in some 25,000 cycles: behind 56 k-blocks of the next tile, where there is one (4096 × 14336,
+    // all gradients of 1024 tokens 402 us to 392, of 512 tokens 241 to 239; of 130, a tile a pair, 158.5 to 159.2)
+    l.p.deep = l.p.q[0].kb0 >= 56 && l.p.units > l.pairs;
     l.p.act = f.act;
     for (int i = 0; i < 2; ++i)   // 64 columns × 32 rows at a time
         if ((st = tensor_map_bf16(i ? upp : gate, f.F, f.T, ldk * 2, 32, &l.maps.a[1][i]))) return st;

@@ -73,7 +73,8 @@ struct DenseParams {
     // the others in turn. Everyone ends within about one unit of the others.
     int long_units, extra;
     int deep;              // STORE, GATE, wide tiles: a ring of six k-blocks and one staging slab a warp (else five and two);
-                           // ENTROPY, wide tiles that store nothing: 2, a ring of seven
+                           // ENTROPY, wide tiles that store nothing: 2, a ring of seven; GATE_GRAD, wide tiles: a ring of six,
+                           // the tile's end by four warps (else five and eight)
     int act;
     DenseOut more[2];      // GATE: gate, up (no address: not asked for); GATE_GRAD: dup
     const void* targets;   // ENTROPY: M of them, int32 or int64
@@ -333,8 +334,8 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
-    const bool deep = BN == 256 && (E == DenseEnd::STORE || E == DenseEnd::GATE) && p.deep;
-    const uint32_t stages = C::STAGES + (BN == 256 && E != DenseEnd::GATE_GRAD ? p.deep : 0);
+    const bool deep = BN == 256 && E != DenseEnd::ENTROPY && p.deep;
+    const uint32_t stages = C::STAGES + (BN == 256 ? p.deep : 0);
     uint8_t* slabs = smem + stages * C::STAGE_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::EW * C::SLABS * C::SLAB_BYTES);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::NBARS);
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
         const int quarter = warp & 3;         // the tensor-memory lanes this warp may read
         const int h = (warp - 2) >> 2;        // its share of the columns
         const uint32_t acce_leader0 = ptx::mapa_shared(acce0, 0u);
-        DenseSlabs out{slabs + (warp - 2) * (deep ? 1 : C::SLABS) * C::SLAB_BYTES, 0, lane, deep};
+        DenseSlabs out{slabs + (warp - 2) * (deep && E != DenseEnd::GATE_GRAD ? 1 : C::SLABS) * C::SLAB_BYTES, 0, lane, deep};
         [[maybe_unused]] uint32_t kept_phase = 0;
         for (int j = 0, u; (u = dense_walk(p, pair, pairs, j)) < p.units; ++j) {
             const DenseUnit U = dense_unit<E>(p, u);
@@ -618,13 +619,17 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
                     }
                     __syncwarp();
                 };
-                fetch(col0);
+                const bool mine = !deep || h == 0;   // (a ring of six: half of the warps, all columns each)
+                const int cw = deep ? BN : C::CW;
+                if (mine) fetch(col0);
                 const bool ready = wait(accf0 + 8 * b, (j >> 1) & 1, DEV_TIMEOUT_EPILOGUE);
                 ptx::tc_fence_after();
                 bool here = true;
-                dense_with_act(p.act, [&](auto act) {
+                if (!mine)
+                    release();
+                else dense_with_act(p.act, [&](auto act) {
 #pragma unroll 1
-                    for (int c = 0; c < C::CW; c += 64) {
+                    for (int c = 0; c < cw; c += 64) {
                         if (c) fetch(col0 + c);
                         here = here && wait(bar, kept_phase, DEV_TIMEOUT_EPILOGUE);
                         kept_phase ^= 1u;
@@ -655,7 +660,7 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
                             out.put<2>(sg, k / 8, wg);
                             out.put<2>(su, k / 8, wu);
                         }
-                        if (c + 64 == C::CW) release();
+                        if (c + 64 == cw) release();
                         out.out<__nv_bfloat16>(sg, &maps.c[0], q.out, row0, col0 + c, 0, q.M, 0);
                         out.out<__nv_bfloat16>(su, &maps.c[1], p.more[0], row0, col0 + c, 0, q.M, 0);
                     }

@@ -101,6 +101,25 @@ def test_entropy(tokens, hidden, vocab, ids):
     ref.within(got[3], want[3], "dw")
 
 
+@pytest.mark.parametrize("tokens,hidden,inner,act,dtype", [(300, 3600, 10001, "silu", BF16), (777, 3590, 5000, "gelu", BF16),
+                                                            (600, 4100, 7000, "gelu_tanh", F32)])
+def test_ffn_of_long_sums(tokens, hidden, inner, act, dtype):
+    """More than 56 k-blocks and more tiles than pairs of SMs: tiles of several rounds, longer rings, ends by fewer
+    warps."""
+    x, wg, wu, wd, grad = block(30, tokens, hidden, inner)
+    out, kept = tcl.gated_ffn(x, wg, wu, wd, activation=act, keep=True)
+    for got, w, what in zip((out, kept.gate, kept.up, kept.hidden), ref.gated_ffn(x, wg, wu, wd, act), ("out", "gate", "up", "hidden")):
+        ref.within(got, w, what)
+    got = tcl.gated_ffn_grad(grad, x, wg, wu, wd, kept, activation=act, out_dtype=dtype)
+    for g, w, what in zip(got, ref.gated_ffn_grad(grad, x, wg, wu, wd, act, dtype), ("dx", "dw_gate", "dw_up", "dw_down")):
+        ref.within(g, w, what)
+
+
+@pytest.mark.parametrize("tokens,hidden,vocab", [(500, 1030, 20011), (300, 2048, 40000)])
+def test_entropy_of_long_sums(tokens, hidden, vocab):
+    test_entropy(tokens, hidden, vocab, torch.int64)
+
+
 # ------------------------------------------------------------------------------ layouts
 
 @pytest.mark.parametrize("tokens", [5, 70, 130])
