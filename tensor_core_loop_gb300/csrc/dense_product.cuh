@@ -21,8 +21,8 @@
 //
 // Roles of each CTA: warp 0 loads A, warp 10 B (TMA, 128-byte swizzle, a ring of 64-value k-blocks),
 // warp 1 of the pair's leader issues the MMAs into one of two accumulators in tensor memory, warps 2
-// to 9 read the other one (each 32 lanes × half of the columns) and store through slabs of 32
-// rows × 128 bytes, copied out by the tensor copy engine. A pair walks its tiles blockIdx/2, + pairs, ...
+// to 9 read the other one (each 32 lanes × half of the columns, or four of them all columns) and store through
+// slabs of 32 rows × 128 bytes, copied out by the tensor copy engine. A pair walks its tiles blockIdx/2, + pairs, ...
 //
 // Every wait is bounded; a role that gives up raises the pair's abort flag.
 #pragma once
