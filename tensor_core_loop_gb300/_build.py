@@ -55,7 +55,7 @@ def _build_tensors(force: bool) -> str:
     except ImportError:
         return ""
     src = os.path.join(CSRC, "tensors.cpp")
-    if not force and not _stale(TENSORS_PATH, [src, __file__, torch.__file__]):
+    if not force and not _stale(TENSORS_PATH, [src, __file__, torch.__file__, *glob.glob(os.path.join(INCLUDE, "*.h"))]):
         return ""
     tmp = TENSORS_PATH + f".tmp{os.getpid()}"
     home = os.path.dirname(torch.__file__)
@@ -63,8 +63,8 @@ def _build_tensors(force: bool) -> str:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", os.path.join(home, "include"),
            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
-           "-I", sysconfig.get_path("include"), src, "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu",
-           "-lc10"]
+           "-I", sysconfig.get_path("include"), "-I", INCLUDE, src, "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(src)}:\n{r.stderr}")

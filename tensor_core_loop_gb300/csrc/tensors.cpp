@@ -1,14 +1,27 @@
-// Python module `_tensors`: what a call over many PyTorch tensors needs of them, read in one call.
+// Python module `_tensors`: the binding's short ways to PyTorch's tensors.
 //
-// A model's gradients are dozens to hundreds of tensors. From Python each question to one of them (type, contiguous,
-// address, length, device) costs some 75 ns: 62 gradients and as many results took 50 us of a call whose kernels
-// take 12. Here the five cost some 10 ns together.
+// look() reads what a call over many tensors needs of them. A model's gradients are dozens to hundreds; from Python each
+// question to one of them (type, contiguous, address, length, device) costs some 75 ns: 62 gradients and as many
+// results took 50 us of a call whose kernels take 12. Here the five cost some 10 ns together.
+//
+// The calls on matrices do what dense.py does with a call on the current stream whose operands are all in order: check
+// them, allocate the results and a workspace, call the library. Anything else gets None, and dense.py does it or says what is
+// wrong. Small ones take 7 to 8 us of the host's time instead of 20 (Python's checks and allocations and the driver's launches
+// push one another out of its caches).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <climits>
 #include <cstdint>
 #include <exception>
+
+#include "tcl_dense.h"
 
 namespace {
 
@@ -59,7 +72,147 @@ PyObject* look(PyObject*, PyObject* args) {
     return nullptr;
 }
 
-PyMethodDef methods[] = {{"look", look, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
+// The library's entries, by bind(gated_ffn, gated_ffn_grad, cross_entropy, cross_entropy_grad).
+struct {
+    decltype(&tcl_gated_ffn) ffn;
+    decltype(&tcl_gated_ffn_grad) ffn_grad;
+    decltype(&tcl_cross_entropy) entropy;
+    decltype(&tcl_cross_entropy_grad) entropy_grad;
+} lib;
+
+PyObject* bind(PyObject*, PyObject* args) {
+    unsigned long long a[4];
+    if (!PyArg_ParseTuple(args, "KKKK", &a[0], &a[1], &a[2], &a[3])) return nullptr;
+    lib = {reinterpret_cast<decltype(lib.ffn)>(a[0]), reinterpret_cast<decltype(lib.ffn_grad)>(a[1]),
+           reinterpret_cast<decltype(lib.entropy)>(a[2]), reinterpret_cast<decltype(lib.entropy_grad)>(a[3])};
+    Py_RETURN_NONE;
+}
+
+// A bf16 matrix with contiguous rows on the current GPU.
+struct Mat {
+    const at::Tensor* t;
+    void* p;
+    int rows, cols, ld;
+};
+
+struct Call {
+    int device = -1;
+    bool ok = true;
+
+    const at::Tensor* tensor(PyObject* o) {
+        if (!ok || !THPVariable_Check(o)) return fail();
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (!t.is_cuda()) return fail();
+        if (device < 0) device = c10::cuda::current_device();
+        return t.get_device() == device ? &t : fail();
+    }
+    Mat mat(PyObject* o) {
+        Mat m = {};
+        const at::Tensor* t = tensor(o);
+        if (!t || t->scalar_type() != at::kBFloat16 || t->dim() != 2) {
+            ok = false;
+            return m;
+        }
+        const int64_t rows = t->size(0), cols = t->size(1), ld = rows > 1 ? t->stride(0) : (cols + 15) / 16 * 16;
+        ok = cols >= 1 && (cols == 1 || t->stride(1) == 1) && ld >= cols && ld <= INT_MAX && rows <= INT_MAX;
+        if (ok) m = {t, t->data_ptr(), static_cast<int>(rows), static_cast<int>(cols), static_cast<int>(ld)};
+        return m;
+    }
+    // A contiguous vector of n values of a type (or of another one).
+    const at::Tensor* vector(PyObject* o, int64_t n, at::ScalarType type, at::ScalarType other) {
+        const at::Tensor* t = tensor(o);
+        if (!t || (t->scalar_type() != type && t->scalar_type() != other) || t->dim() != 1 || t->size(0) != n || !t->is_contiguous())
+            return fail();
+        return t;
+    }
+    cudaStream_t stream() const { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream(); }
+
+  private:
+    const at::Tensor* fail() {
+        ok = false;
+        return nullptr;
+    }
+};
+
+at::Tensor empty(at::IntArrayRef size, const at::Tensor& like, at::ScalarType type) { return at::empty(size, like.options().dtype(type)); }
+
+// f(workspace, its size) with `room` bytes, and once more with a larger one where it asks for that: its status.
+template <class F>
+int with_room(size_t room, const at::Tensor& like, F f) {
+    at::Tensor space;
+    size_t size = room;
+    for (int again = 0;; ++again) {
+        if (size) space = empty({static_cast<int64_t>(size)}, like, at::kByte);
+        void* const p = size ? space.data_ptr() : nullptr;
+        int st;
+        Py_BEGIN_ALLOW_THREADS
+        st = f(p, &size);
+        Py_END_ALLOW_THREADS
+        if (st != TCL_ERR_WORKSPACE || again) return st;
+    }
+}
+
+// gated_ffn(x, w_gate, w_up, w_down, act, keep): (out, kept values or None), a status, or None
+PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 6) Py_RETURN_NONE;
+    Call c;
+    const Mat x = c.mat(a[0]), g = c.mat(a[1]), u = c.mat(a[2]), d = c.mat(a[3]);
+    const long act = PyLong_AsLong(a[4]);
+    const bool keep = a[5] == Py_True;
+    if (act < 0 && PyErr_Occurred()) return nullptr;
+    if (!c.ok || act < 0 || (!keep && a[5] != Py_False) || g.cols != x.cols || u.cols != x.cols || u.rows != g.rows || d.rows != x.cols ||
+        d.cols != g.rows)
+        Py_RETURN_NONE;
+    const int64_t pitch = (static_cast<int64_t>(g.rows) + 63) / 64 * 64;   // (rows on whole lines of 128 bytes)
+    if (pitch > INT_MAX) Py_RETURN_NONE;
+    const at::Tensor mid = empty({keep ? 3 : 1, x.rows, pitch}, *x.t, at::kBFloat16);
+    const at::Tensor out = empty({x.rows, x.cols}, *x.t, at::kBFloat16);
+    char* const h = static_cast<char*>(mid.data_ptr());
+    const int64_t part = 2 * x.rows * pitch;
+    const cudaStream_t stream = c.stream();
+    const int st = with_room(0, out, [&](void* space, size_t* size) {
+        return lib.ffn(x.rows, x.cols, g.rows, x.p, x.ld, g.p, g.ld, u.p, u.ld, d.p, d.ld, static_cast<int>(act), keep ? h + part : nullptr,
+                       keep ? h + 2 * part : nullptr, h, static_cast<int>(pitch), out.data_ptr(), x.cols, space, size, stream);
+    });
+    if (st) return PyLong_FromLong(st);
+    if (!keep) return THPVariable_Wrap(out);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(mid));
+    END_HANDLE_TH_ERRORS
+}
+
+// cross_entropy(x, w, targets): (loss, lse), a status, or None
+PyObject* cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 3) Py_RETURN_NONE;
+    Call c;
+    const Mat x = c.mat(a[0]), w = c.mat(a[1]);
+    const at::Tensor* y = c.vector(a[2], x.rows, at::kLong, at::kInt);
+    if (!c.ok || w.cols != x.cols || w.rows < 1) Py_RETURN_NONE;
+    const at::Tensor loss = empty({x.rows}, *x.t, at::kFloat), lse = empty({x.rows}, *x.t, at::kFloat);
+    // (what operands on 16-byte pieces take: sums for each token and 64 words, for few tokens each warp of the GPU)
+    const size_t words = (static_cast<size_t>(w.rows) + 63) / 64;
+    const size_t room = x.rows * (8 * std::max<size_t>(words, x.rows <= 128 ? 1024 : 0) + 4) + 512;
+    const cudaStream_t stream = c.stream();
+    const int st = with_room(room, loss, [&](void* space, size_t* size) {
+        return lib.entropy(x.rows, x.cols, w.rows, x.p, x.ld, w.p, w.ld, y->data_ptr(), static_cast<int>(y->element_size()),
+                           static_cast<float*>(loss.data_ptr()), static_cast<float*>(lse.data_ptr()), space, size, stream);
+    });
+    if (st) return PyLong_FromLong(st);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(loss), THPVariable_Wrap(lse));
+    END_HANDLE_TH_ERRORS
+}
+
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyMethodDef fast(const char* name) {
+    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
+}
+
+PyMethodDef methods[] = {{"look", look, METH_VARARGS, nullptr},
+                         {"bind", bind, METH_VARARGS, nullptr},
+                         fast<gated_ffn>("gated_ffn"),
+                         fast<cross_entropy>("cross_entropy"),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -63,6 +63,22 @@ def _lib():
     return _bound
 
 
+_native = None   # _tensors, once it is loaded
+
+
+def _load():
+    global _native
+    try:
+        from . import _tensors
+    except ImportError as e:
+        raise RuntimeError("_tensors.so is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`") from e
+    L = _lib()
+    _tensors.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                    for f in (L.tcl_gated_ffn, L.tcl_gated_ffn_grad, L.tcl_cross_entropy, L.tcl_cross_entropy_grad)))
+    _native = _tensors
+    return _native
+
+
 class GatedFfnKept(NamedTuple):
     """What ``gated_ffn`` keeps for its gradients, bf16. (One buffer, of which views are made where they are asked
     for: four views cost as much of the host's time as the call's launches.)"""
@@ -146,6 +162,12 @@ def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", keep: bool = Fa
     normal distribution) or "gelu_tanh". The product in the middle is rounded to bf16.
 
     ``keep=True``: (out, kept) with what ``gated_ffn_grad`` needs."""
+    if stream is None:
+        done = (_native or _load()).gated_ffn(x, w_gate, w_up, w_down, _ACTIVATIONS.get(activation, -1), keep)
+        if done is not None:   # (else: something to refuse, or another GPU than the current one)
+            if done.__class__ is int:
+                raise TclError(done, "gated_ffn")
+            return (done[0], GatedFfnKept(done[1], w_gate.shape[0])) if keep else done
     (tokens, hidden, inner, act), (ldx, ldg, ldu, ldd) = _ffn(x, w_gate, w_up, w_down, activation)
     device = _device(stream, "x", x, w_gate, w_up, w_down)
     with _on(stream):
@@ -206,6 +228,12 @@ def cross_entropy(x, w, targets, stream=None):
     """(loss, lse) of the logits l = x · wᵀ (tokens × vocabulary), which are never stored: for each
     token lse = log Σ exp(l) and loss = lse - l[target], fp32. ``targets`` (int32 or int64) outside the
     vocabulary drop their token: its loss is 0."""
+    if stream is None:
+        done = (_native or _load()).cross_entropy(x, w, targets)
+        if done is not None:
+            if done.__class__ is int:
+                raise TclError(done, "cross_entropy")
+            return done
     tokens, hidden, vocab, ldx, ldw = _entropy(x, w, targets)
     device = _device(stream, "x", x, w, targets)
     with _on(stream):
@@ -244,20 +272,11 @@ def cross_entropy_grad(x, w, targets, grad, out_dtype=None, stream=None):
     return loss, lse, dx, dw
 
 
-_native = None
-
-
 def _look(tensors, name):
     """(addresses, lengths, types, GPU) of contiguous bf16 and fp32 tensors, the first three as bytes."""
-    global _native
-    if _native is None:
-        try:
-            from . import _tensors as _native
-        except ImportError as e:
-            raise RuntimeError("_tensors.so is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`") from e
     if len(tensors) > _INT:
         _too_large(name)
-    return _native.look(tensors, name)
+    return (_native or _load()).look(tensors, name)
 
 
 def _where(stream, tensors, *gpus):
