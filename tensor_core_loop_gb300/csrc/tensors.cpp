@@ -6,7 +6,7 @@
 //
 // The calls on matrices do what dense.py does with a call on the current stream whose operands are all in order: check
 // them, allocate the results and a workspace, call the library. Anything else gets None, and dense.py does it or says what is
-// wrong. Small ones take 7 to 8 us of the host's time instead of 20 (Python's checks and allocations and the driver's launches
+// wrong. Small ones take 7 to 8 us of the host's time instead of 20, gradients 15 instead of 30 (Python's checks and allocations and the driver's launches
 // push one another out of its caches).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -203,6 +203,78 @@ PyObject* cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// The weights' gradients' type: TCL_OUT_F32, TCL_OUT_BF16, or another number.
+bool w_type(PyObject* o, int* code, at::ScalarType* type) {
+    const long v = PyLong_AsLong(o);
+    *code = static_cast<int>(v);
+    *type = v == TCL_OUT_F32 ? at::kFloat : at::kBFloat16;
+    return v == TCL_OUT_F32 || v == TCL_OUT_BF16;
+}
+
+// gated_ffn_grad(grad, x, w_gate, w_up, w_down, kept values, inner, act, w_type): (dx, dw_gate, dw_up, dw_down), a status, or None
+PyObject* gated_ffn_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 9) Py_RETURN_NONE;
+    Call c;
+    const Mat gr = c.mat(a[0]), x = c.mat(a[1]), g = c.mat(a[2]), u = c.mat(a[3]), d = c.mat(a[4]);
+    const at::Tensor* kept = c.tensor(a[5]);
+    if (!c.ok || !PyLong_Check(a[6])) Py_RETURN_NONE;
+    const long inner = PyLong_AsLong(a[6]), act = PyLong_AsLong(a[7]);
+    int code;
+    at::ScalarType type;
+    const bool typed = w_type(a[8], &code, &type);
+    if (PyErr_Occurred()) return nullptr;
+    if (!typed || act < 0 || inner != g.rows || g.cols != x.cols || u.cols != x.cols || u.rows != g.rows || d.rows != x.cols ||
+        d.cols != g.rows || gr.rows != x.rows || gr.cols != x.cols || kept->scalar_type() != at::kBFloat16 || kept->dim() != 3 ||
+        kept->size(0) != 3 || kept->size(1) != x.rows || kept->size(2) < g.rows || kept->size(2) % 8 || kept->size(2) > INT_MAX ||
+        !kept->is_contiguous() || reinterpret_cast<uintptr_t>(kept->data_ptr()) % 16)
+        Py_RETURN_NONE;
+    const int64_t pitch = kept->size(2), part = 2 * x.rows * pitch;
+    const at::Tensor dx = empty({x.rows, x.cols}, *x.t, at::kBFloat16), dg = empty({g.rows, g.cols}, *x.t, type),
+                     du = empty({g.rows, g.cols}, *x.t, type), dd = empty({d.rows, d.cols}, *x.t, type);
+    const char* const h = static_cast<const char*>(kept->data_ptr());
+    const size_t room = 2 * ((2 * static_cast<size_t>(x.rows) * ((g.rows + 63) / 64 * 64) + 255) / 256 * 256);   // (what most sizes take)
+    const cudaStream_t stream = c.stream();
+    const int st = with_room(room, dx, [&](void* space, size_t* size) {
+        return lib.ffn_grad(x.rows, x.cols, g.rows, gr.p, gr.ld, x.p, x.ld, g.p, g.ld, u.p, u.ld, d.p, d.ld, static_cast<int>(act),
+                            h + part, h + 2 * part, h, static_cast<int>(pitch), dx.data_ptr(), x.cols, dg.data_ptr(), x.cols,
+                            du.data_ptr(), x.cols, dd.data_ptr(), g.rows, code, space, size, stream);
+    });
+    if (st) return PyLong_FromLong(st);
+    return Py_BuildValue("(NNNN)", THPVariable_Wrap(dx), THPVariable_Wrap(dg), THPVariable_Wrap(du), THPVariable_Wrap(dd));
+    END_HANDLE_TH_ERRORS
+}
+
+// cross_entropy_grad(x, w, targets, grad, w_type): (loss, lse, dx, dw), a status, or None
+PyObject* cross_entropy_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 5) Py_RETURN_NONE;
+    Call c;
+    const Mat x = c.mat(a[0]), w = c.mat(a[1]);
+    const at::Tensor* y = c.vector(a[2], x.rows, at::kLong, at::kInt);
+    const at::Tensor* gr = c.vector(a[3], x.rows, at::kFloat, at::kFloat);
+    int code;
+    at::ScalarType type;
+    const bool typed = w_type(a[4], &code, &type);
+    if (PyErr_Occurred()) return nullptr;
+    if (!c.ok || !typed || w.cols != x.cols || w.rows < 1) Py_RETURN_NONE;
+    const at::Tensor loss = empty({x.rows}, *x.t, at::kFloat), lse = empty({x.rows}, *x.t, at::kFloat),
+                     dx = empty({x.rows, x.cols}, *x.t, at::kBFloat16), dw = empty({w.rows, w.cols}, *x.t, type);
+    // (what most sizes take: exponentials, scaled rows of x, sums for each 64 words and two more values a token)
+    const size_t words = (static_cast<size_t>(w.rows) + 63) / 64, tokens = x.rows;
+    const size_t room = tokens && tokens * words <= 1u << 24 ? tokens * (136 * words + 128 * ((static_cast<size_t>(x.cols) + 63) / 64) + 8) + 1280 : 0;
+    const cudaStream_t stream = c.stream();
+    const int st = with_room(room, loss, [&](void* space, size_t* size) {
+        return lib.entropy_grad(x.rows, x.cols, w.rows, x.p, x.ld, w.p, w.ld, y->data_ptr(), static_cast<int>(y->element_size()),
+                                static_cast<const float*>(gr->data_ptr()), static_cast<float*>(loss.data_ptr()),
+                                static_cast<float*>(lse.data_ptr()), dx.data_ptr(), x.cols, dw.data_ptr(), x.cols, code, space, size,
+                                stream);
+    });
+    if (st) return PyLong_FromLong(st);
+    return Py_BuildValue("(NNNN)", THPVariable_Wrap(loss), THPVariable_Wrap(lse), THPVariable_Wrap(dx), THPVariable_Wrap(dw));
+    END_HANDLE_TH_ERRORS
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef fast(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
@@ -212,6 +284,8 @@ PyMethodDef methods[] = {{"look", look, METH_VARARGS, nullptr},
                          {"bind", bind, METH_VARARGS, nullptr},
                          fast<gated_ffn>("gated_ffn"),
                          fast<cross_entropy>("cross_entropy"),
+                         fast<gated_ffn_grad>("gated_ffn_grad"),
+                         fast<cross_entropy_grad>("cross_entropy_grad"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

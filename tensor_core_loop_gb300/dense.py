@@ -186,6 +186,13 @@ def gated_ffn_grad(grad, x, w_gate, w_up, w_down, kept: GatedFfnKept, activation
     """(dx, dw_gate, dw_up, dw_down) of ``gated_ffn`` from the gradient of its result and what it
     kept. ``dx`` is bf16, the weights' gradients are bf16 or ``out_dtype=torch.float32``. The gradients
     of the two products in the middle are rounded to bf16."""
+    if stream is None:
+        done = (_native or _load()).gated_ffn_grad(grad, x, w_gate, w_up, w_down, *kept, _ACTIVATIONS.get(activation, -1),
+                                                   _TYPES.get(out_dtype or _BF16, -1))
+        if done is not None:
+            if done.__class__ is int:
+                raise TclError(done, "gated_ffn_grad")
+            return done
     (tokens, hidden, inner, act), (ldx, ldg, ldu, ldd) = _ffn(x, w_gate, w_up, w_down, activation)
     r, c, ld_grad = _bf16(grad, "grad")
     _shape(r, c, (tokens, hidden), "grad")
@@ -251,6 +258,12 @@ def cross_entropy_grad(x, w, targets, grad, out_dtype=None, stream=None):
     weight for each token (1/tokens for a mean). Dropped tokens add nothing and get zeros. ``dx`` is
     bf16, ``dw`` bf16 or ``out_dtype=torch.float32``. The exponentials of the logits, computed once for
     both, are kept in bf16 for 2 GiB of them at a time."""
+    if stream is None:
+        done = (_native or _load()).cross_entropy_grad(x, w, targets, grad, _TYPES.get(out_dtype or _BF16, -1))
+        if done is not None:
+            if done.__class__ is int:
+                raise TclError(done, "cross_entropy_grad")
+            return done
     tokens, hidden, vocab, ldx, ldw = _entropy(x, w, targets)
     if grad.dtype != _F32:
         raise TypeError("grad must be float32")
