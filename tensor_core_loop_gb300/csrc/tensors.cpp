@@ -5,9 +5,10 @@
 // results took 50 us of a call whose kernels take 12. Here the five cost some 10 ns together.
 //
 // The calls on matrices do what dense.py does with a call on the current stream whose operands are all in order: check
-// them, allocate the results and a workspace, call the library. Anything else gets None, and dense.py does it or says what is
-// wrong. Small ones take 7 to 8 us of the host's time instead of 20, gradients 15 instead of 30 (Python's checks and allocations and the driver's launches
-// push one another out of its caches).
+// them, allocate the results and a workspace, call the library. Anything else gets None, and dense.py does it or says
+// what is wrong. Small ones take 7 to 8 us of the host's time instead of 20, gradients 15 instead of 30, 62 tensors
+// clipped 14 instead of 27 (Python's checks and allocations and the driver's launches push one another out of the
+// host's caches).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <ATen/ops/empty.h>
@@ -20,6 +21,7 @@
 #include <climits>
 #include <cstdint>
 #include <exception>
+#include <vector>
 
 #include "tcl_dense.h"
 
@@ -72,19 +74,21 @@ PyObject* look(PyObject*, PyObject* args) {
     return nullptr;
 }
 
-// The library's entries, by bind(gated_ffn, gated_ffn_grad, cross_entropy, cross_entropy_grad).
+// The library's entries, by bind(gated_ffn, gated_ffn_grad, cross_entropy, cross_entropy_grad, clip_gradients).
 struct {
     decltype(&tcl_gated_ffn) ffn;
     decltype(&tcl_gated_ffn_grad) ffn_grad;
     decltype(&tcl_cross_entropy) entropy;
     decltype(&tcl_cross_entropy_grad) entropy_grad;
+    decltype(&tcl_clip_gradients) clip;
 } lib;
 
 PyObject* bind(PyObject*, PyObject* args) {
-    unsigned long long a[4];
-    if (!PyArg_ParseTuple(args, "KKKK", &a[0], &a[1], &a[2], &a[3])) return nullptr;
+    unsigned long long a[5];
+    if (!PyArg_ParseTuple(args, "KKKKK", &a[0], &a[1], &a[2], &a[3], &a[4])) return nullptr;
     lib = {reinterpret_cast<decltype(lib.ffn)>(a[0]), reinterpret_cast<decltype(lib.ffn_grad)>(a[1]),
-           reinterpret_cast<decltype(lib.entropy)>(a[2]), reinterpret_cast<decltype(lib.entropy_grad)>(a[3])};
+           reinterpret_cast<decltype(lib.entropy)>(a[2]), reinterpret_cast<decltype(lib.entropy_grad)>(a[3]),
+           reinterpret_cast<decltype(lib.clip)>(a[4])};
     Py_RETURN_NONE;
 }
 
@@ -275,6 +279,43 @@ PyObject* cross_entropy_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// clip_grads(tensors, out or None, bound): the norm, a status, or None
+PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 3 || !PyList_Check(a[0]) || (a[1] != Py_None && !PyList_Check(a[1])) || !PyFloat_Check(a[2])) Py_RETURN_NONE;
+    const Py_ssize_t count = PyList_GET_SIZE(a[0]);
+    if (count < 1 || count > INT_MAX || (a[1] != Py_None && PyList_GET_SIZE(a[1]) != count)) Py_RETURN_NONE;
+    Call c;
+    const at::Tensor* first = nullptr;
+    std::vector<const void*> from(count);
+    std::vector<void*> to(count);
+    std::vector<long long> lengths(count);
+    std::vector<int> types(count);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        const at::Tensor* t = c.tensor(PyList_GET_ITEM(a[0], i));
+        if (!t || (t->scalar_type() != at::kFloat && t->scalar_type() != at::kBFloat16) || !t->is_contiguous()) Py_RETURN_NONE;
+        first = t;
+        from[i] = to[i] = t->data_ptr();
+        lengths[i] = t->numel();
+        types[i] = t->scalar_type() == at::kBFloat16 ? TCL_OUT_BF16 : TCL_OUT_F32;
+        if (a[1] == Py_None) continue;
+        const at::Tensor* o = c.tensor(PyList_GET_ITEM(a[1], i));
+        if (!o || o->scalar_type() != t->scalar_type() || o->numel() != t->numel() || !o->is_contiguous()) Py_RETURN_NONE;
+        to[i] = o->data_ptr();
+    }
+    const at::Tensor norm = empty({}, *first, at::kFloat);
+    const float bound = static_cast<float>(PyFloat_AS_DOUBLE(a[2]));
+    const cudaStream_t stream = c.stream();
+    const size_t room = 16384 * (count / 256 + 2);   // (a sum for each block of the launches that they take)
+    const int st = with_room(room, norm, [&](void* space, size_t* size) {
+        return lib.clip(static_cast<int>(count), from.data(), to.data(), lengths.data(), types.data(), bound,
+                        static_cast<float*>(norm.data_ptr()), space, size, stream);
+    });
+    if (st) return PyLong_FromLong(st);
+    return THPVariable_Wrap(norm);
+    END_HANDLE_TH_ERRORS
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef fast(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
@@ -286,6 +327,7 @@ PyMethodDef methods[] = {{"look", look, METH_VARARGS, nullptr},
                          fast<cross_entropy>("cross_entropy"),
                          fast<gated_ffn_grad>("gated_ffn_grad"),
                          fast<cross_entropy_grad>("cross_entropy_grad"),
+                         fast<clip_grads>("clip_grads"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

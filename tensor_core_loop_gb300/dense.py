@@ -74,7 +74,8 @@ def _load():
         raise RuntimeError("_tensors.so is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`") from e
     L = _lib()
     _tensors.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                    for f in (L.tcl_gated_ffn, L.tcl_gated_ffn_grad, L.tcl_cross_entropy, L.tcl_cross_entropy_grad)))
+                    for f in (L.tcl_gated_ffn, L.tcl_gated_ffn_grad, L.tcl_cross_entropy, L.tcl_cross_entropy_grad,
+                              L.tcl_clip_gradients)))
     _native = _tensors
     return _native
 
@@ -299,6 +300,9 @@ def _where(stream, tensors, *gpus):
     return _device(stream, "tensors", *(tensors if stream is not None else tensors[:1]))
 
 
+_SHARED = "a result shares memory with another tensor"
+
+
 def _clip_room(tensors):
     """A sum for each block of the launches that they take."""
     return 16384 * (len(tensors) // 256 + 2)
@@ -329,10 +333,17 @@ def clip_grads(tensors, max_norm: float, out=None, stream=None):
     max_norm = float(max_norm)
     if not max_norm >= 0:
         raise ValueError("max_norm must not be negative")
+    if out is not None:
+        out = list(out)
+    if stream is None:
+        done = (_native or _load()).clip_grads(tensors, out, max_norm)
+        if done is not None:
+            if done.__class__ is not int:
+                return done
+            raise ValueError(_SHARED) if done == _CONFIG else TclError(done, "clip_grads")
     ptr, length, types, gpu = _look(tensors, "tensors")
     to, gpus, everything = ptr, (gpu,), tensors
     if out is not None:
-        out = list(out)
         to, to_length, to_types, to_gpu = _look(out, "out")
         if to_length != length or to_types != types:
             raise ValueError("out must hold a tensor of the same length and type for each one")
@@ -346,5 +357,5 @@ def clip_grads(tensors, max_norm: float, out=None, stream=None):
         except TclError as e:
             if e.status != _CONFIG:
                 raise
-            raise ValueError("a result shares memory with another tensor") from None
+            raise ValueError(_SHARED) from None
     return norm

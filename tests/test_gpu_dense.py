@@ -599,6 +599,28 @@ def test_given_stream():
     del junk
 
 
+@pytest.mark.parametrize("tokens", [5, 300])
+def test_given_stream_and_current_one_give_the_same_bits(tokens):
+    """Two ways through the binding."""
+    x, wg, wu, wd, grad = block(31, tokens, 72, 200)
+    xe, w, y, ge = tokens_of(31, tokens, 72, 500)
+    st = torch.cuda.current_stream()
+    for dtype in (None, BF16, F32):
+        out, kept = tcl.gated_ffn(x, wg, wu, wd, activation="gelu", keep=True)
+        again, kept_again = tcl.gated_ffn(x, wg, wu, wd, activation="gelu", keep=True, stream=st)
+        pairs = [(out, again), (kept.hidden, kept_again.hidden), (kept.gate, kept_again.gate), (kept.up, kept_again.up)]
+        pairs += [(out, tcl.gated_ffn(x, wg, wu, wd, activation="gelu"))]
+        args = (grad, x, wg, wu, wd, kept, "gelu", dtype)
+        pairs += zip(tcl.gated_ffn_grad(*args), tcl.gated_ffn_grad(*args, stream=st))
+        pairs += zip(tcl.cross_entropy(xe, w, y), tcl.cross_entropy(xe, w, y, stream=st))
+        pairs += zip(tcl.cross_entropy_grad(xe, w, y, ge, dtype), tcl.cross_entropy_grad(xe, w, y, ge, dtype, stream=st))
+        grads = [a.clone() for a, _ in pairs]
+        outs = [[torch.empty_like(a) for a in grads] for _ in range(2)]
+        pairs += [(tcl.clip_grads(grads, 1, out=outs[0]), tcl.clip_grads(grads, 1, out=outs[1], stream=st)), *zip(*outs)]
+        for a, b in pairs:
+            assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a, b)
+
+
 def test_two_threads():
     import threading
     jobs = [operands(28, 300, 136, 384, 2050), operands(29, 40, 1030, 515, 700)]
