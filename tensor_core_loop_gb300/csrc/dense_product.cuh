@@ -315,10 +315,13 @@ __device__ __forceinline__ float dense_exponent(float top) {
 
 // Adds a chunk's sum, relative to 2^ref, to a row's.
 __device__ __forceinline__ void dense_merge(float& to_ref, float& to_sum, float ref, float sum) {
+    constexpr float INF = __builtin_huge_valf();
     if (sum == 0.0f) return;
     if (to_sum == 0.0f) {
         to_ref = ref;
         to_sum = sum;
+    } else if (sum == INF || to_sum == INF) {   // (of an infinite logit: times a power of two that is zero it would be NaN)
+        to_sum += sum;
     } else if (ref <= to_ref) {
         to_sum += ref == to_ref ? sum : sum * exp2f(ref - to_ref);
     } else {

@@ -1,0 +1,47 @@
+"""The cross entropy of logits that are far from zero, large or infinite, against 64 bits."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import tensor_core_loop_gb300 as tcl
+from test_gpu_dense import tokens_of
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    tcl.lib()
+    yield
+    assert tcl.last_device_error() == (0, 0)
+
+
+def losses(x, w, y):
+    """By the call without gradients and by the one with them."""
+    return tcl.cross_entropy(x, w, y), tcl.cross_entropy_grad(x, w, y, torch.ones(x.shape[0], device=DEV))
+
+
+@pytest.mark.parametrize("tokens", [7, 100, 200, 2100])
+@pytest.mark.parametrize("level", [100.0, 300.0, -300.0])
+def test_infinite_logit_beside_far_ones(tokens, level):
+    """One token with one logit of infinity, the other words' logits so far from zero that their exponentials are
+    taken relative to another power of two than the infinite one."""
+    x, w, y, _ = tokens_of(41, tokens, 64, 500, drop=0.0)
+    x[:, :2], w[:, :2] = 0.0, 0.0
+    x[:, 0] = -1.0
+    x[3, 0], w[7, 0] = 1.0, INF
+    x[3, 1], w[8:, 1] = level, 1.0
+    y = torch.where(y == 7, 8, y)
+    others = torch.arange(tokens, device=DEV) != 3
+    for loss, lse, *grads in losses(x, w, y):
+        assert float(lse[3]) == INF and float(loss[3]) == INF
+        assert lse[others].isfinite().all() and loss[others].isfinite().all()
+        if grads:
+            assert grads[0][3].isnan().all() and grads[1].isnan().all()
+            assert grads[0][others][:, 1:].isfinite().all()
