@@ -65,7 +65,8 @@ TCL_API int tcl_gated_ffn_grad(int tokens, int hidden, int inner, const void* gr
 /* With logits l = X · W^T (tokens × vocab, never stored) and for each token t
  *   lse[t] = log sum over v of exp(l[t][v]),  loss[t] = lse[t] - l[t][target[t]],
  * both fp32. Targets are int32 or int64 (target_bytes 4 or 8); one outside 0 .. vocab-1 drops its
- * token: its loss is 0. X: tokens × hidden, W: vocab × hidden. */
+ * token: its loss is 0. A logit beyond ±2^30 counts as infinite: above it lse is infinity, below it the word has
+ * no weight. X: tokens × hidden, W: vocab × hidden. */
 TCL_API int tcl_cross_entropy(int tokens, int hidden, int vocab, const void* X, int ldx, const void* W, int ldw,
                               const void* targets, int target_bytes, float* loss, float* lse, void* workspace,
                               size_t* workspace_bytes, cudaStream_t stream);
@@ -73,7 +74,7 @@ TCL_API int tcl_cross_entropy(int tokens, int hidden, int vocab, const void* X, 
 /* The same and the gradients of sum over t of grad[t]·loss[t] (grad: fp32):
  *   d[t][v] = grad[t]·(exp(l[t][v] - lse[t]) - [v = target[t]]),  dX = d · W (bf16),  dW = d^T · X
  * (w_type). Dropped tokens add nothing, whatever their rows hold, and their rows of dX are zeros; one that is
- * not dropped and has a logit that is infinity or NaN makes its row of dX and all of dW NaN.
+ * not dropped and has a logit that is infinity, beyond 2^30 or NaN makes its row of dX and all of dW NaN.
  * The exponentials are computed once, kept in bf16 for a piece of the tokens at a time (at most
  * 2 GiB, or 256 tokens) and read by both products; the rows of X for dW are rounded to bf16 again
  * after their scaling by grad[t] / (sum of the exponentials). Pieces of dW are added in fp32. */

@@ -307,10 +307,13 @@ __device__ __forceinline__ float dense_exps(uint32_t (&r)[32], float ref, int co
 // matter is near the ends of bf16's (or fp32's) range.
 __device__ __forceinline__ bool dense_plain_sum(float s) { return s > 5.4e-20f && s < 1.8e19f; }
 
-// The power of two to take out of exponentials whose largest logit is `top`: none where that is
-// infinite (the exponentials are zeros or infinities then, and stay so).
+// The power of two to take out of exponentials whose largest logit is `top`: none where that is beyond 2^30,
+// infinities among them (the exponentials are zeros or infinities then, and stay so). There fp32's numbers are 128
+// apart, and the product with log2(e), rounded, misses the exponent by so much that the exponentials would come
+// out as either all the same: a large logit as if it were not there. Up to 2^30 it misses it by 64 at most, which the
+// sums have room for.
 __device__ __forceinline__ float dense_exponent(float top) {
-    return fabsf(top) < __int_as_float(0x7f800000) ? ceilf(top * 1.4426950408889634f) : 0.0f;
+    return fabsf(top) <= 0x1p30f ? ceilf(top * 1.4426950408889634f) : 0.0f;
 }
 
 // Adds a chunk's sum, relative to 2^ref, to a row's.

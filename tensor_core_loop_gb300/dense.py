@@ -235,7 +235,7 @@ def _entropy(x, w, targets):
 def cross_entropy(x, w, targets, stream=None):
     """(loss, lse) of the logits l = x · wᵀ (tokens × vocabulary), which are never stored: for each
     token lse = log Σ exp(l) and loss = lse - l[target], fp32. ``targets`` (int32 or int64) outside the
-    vocabulary drop their token: its loss is 0."""
+    vocabulary drop their token: its loss is 0. Logits beyond ±2^30 count as infinite."""
     if stream is None:
         done = (_native or _load()).cross_entropy(x, w, targets)
         if done is not None:

@@ -10,6 +10,7 @@ from test_gpu_dense import tokens_of
 pytestmark = pytest.mark.gpu
 
 DEV = torch.device("cuda:0")
+BF16 = torch.bfloat16
 INF = float("inf")
 
 
@@ -45,3 +46,25 @@ def test_infinite_logit_beside_far_ones(tokens, level):
         if grads:
             assert grads[0][3].isnan().all() and grads[1].isnan().all()
             assert grads[0][others][:, 1:].isfinite().all()
+
+
+@pytest.mark.parametrize("tokens", [7, 100, 200, 2100])
+def test_logits_beyond_2_30_are_infinite(tokens):
+    """Finite ones as well: two fp32 numbers there differ by more than any exponential tells, and their multiples of
+    log2(e) by whole powers of two. Tokens of one large logit each, positive and negative ones in turn."""
+    x = torch.zeros(tokens, 64, dtype=BF16, device=DEV)
+    w = torch.zeros(300, 64, dtype=BF16, device=DEV)
+    w[7, 0] = 2.0 ** 20
+    w[:, 1] = (torch.arange(300, device=DEV) % 16).to(BF16)
+    x[:, 1] = 1.0
+    large = 2.0 ** torch.linspace(10.01, 100, tokens, device=DEV)
+    x[:, 0] = (large * torch.where(torch.arange(tokens, device=DEV) % 2 == 0, 1.0, -1.0)).to(BF16)
+    y = torch.full((tokens,), 20, device=DEV)
+    up = x[:, 0] > 0
+    keep = torch.arange(300, device=DEV) != 7
+    want = torch.logsumexp(w[keep, 1].double(), 0)
+    for loss, lse, *grads in losses(x, w, y):
+        assert (lse[up] == INF).all() and (loss[up] == INF).all()
+        assert ((lse[~up] - want).abs() <= 2.0 ** -20 * want).all() and loss[~up].isfinite().all()
+        if grads:
+            assert grads[0][up].isnan().all()
