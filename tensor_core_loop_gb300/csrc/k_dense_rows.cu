@@ -187,9 +187,12 @@ __global__ void __launch_bounds__(kRowThreads) entropy_rows_kernel(const Entropy
 #pragma unroll
             for (int i = 1; i < kRowThreads / 32; ++i) exact += dots[i];
         }
-        // (not where the logit is infinite: the difference is no number)
-        const float more = exp2f(fmaf(logit, 1.4426950408889634f, -c)) * expm1f(exact - logit);
-        if (fabsf(more) < __int_as_float(0x7f800000)) {
+        // (Not where the sum is infinite, and not where the two differ by more than one: one of them is infinite, or
+        // logits are beyond 10^5 or so, where the other words' are off by as much; from 16 on the sum less what
+        // the target loses would be zero or below.)
+        const float off = exact - logit;
+        const float more = exp2f(fmaf(logit, 1.4426950408889634f, -c)) * expm1f(off);
+        if (fabsf(off) <= 1.0f && fabsf(more) < __int_as_float(0x7f800000)) {
             s += more;
             logit = exact;
         }

@@ -4,6 +4,7 @@ from __future__ import annotations
 import pytest
 import torch
 
+import dense_reference as ref
 import tensor_core_loop_gb300 as tcl
 from test_gpu_dense import tokens_of
 
@@ -68,3 +69,23 @@ def test_logits_beyond_2_30_are_infinite(tokens):
         assert ((lse[~up] - want).abs() <= 2.0 ** -20 * want).all() and loss[~up].isfinite().all()
         if grads:
             assert grads[0][up].isnan().all()
+
+
+@pytest.mark.parametrize("tokens", [16, 300, 2100])
+@pytest.mark.parametrize("level", [-1e5, -1e7, -1e8, -5e8, 1e7, 5e8])
+def test_targets_far_above_the_rest_at_any_level(tokens, level):
+    """The target's logit, summed a second time, is off from the tensor core's by more than one: what that takes from
+    the sum of exponentials may not be more than there is."""
+    g = torch.Generator().manual_seed(42)
+    x = torch.rand(tokens, 4096, generator=g) + 0.5
+    w = (torch.rand(300, 1, generator=g) * 0.5 + 1.0) * (1 + 0.01 * torch.rand(300, 4096, generator=g))
+    x = x.to(BF16).to(DEV)
+    w = (w * (level / 4096)).to(BF16).to(DEV)
+    l = x.double() @ w.double().t()
+    y = l.argmax(1)
+    want = ref.cross_entropy(x, w, y)
+    for loss, lse, *grads in losses(x, w, y):
+        ref.within(lse, want[1], "lse")
+        ref.within(loss, want[0], "loss")
+        assert (loss >= -2.0 ** -22 * lse.abs()).all()
+        assert all(t.isfinite().all() for t in grads)
