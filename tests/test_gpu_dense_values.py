@@ -6,7 +6,7 @@ import torch
 
 import dense_reference as ref
 import tensor_core_loop_gb300 as tcl
-from test_gpu_dense import tokens_of
+from test_gpu_dense import far_logits, tokens_of
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,13 @@ def test_targets_far_above_the_rest_at_any_level(tokens, level):
         ref.within(loss, want[0], "loss")
         assert (loss >= -2.0 ** -22 * lse.abs()).all()
         assert all(t.isfinite().all() for t in grads)
+
+
+@pytest.mark.parametrize("level,spread", [(40.0, 1.0), (64.0, 8.0), (90.0, 1.0), (300.0, 20.0), (20000.0, 1.0)])
+def test_logits_far_from_zero_of_many_tokens(level, spread):
+    """More than 2048 tokens: eight rows to a block of the pass that brings a row's exponentials to one power of two."""
+    x, w, y, grad = far_logits(43, 2100, 1100, level, spread)
+    want = ref.cross_entropy(x, w, y, grad)
+    for got in (tcl.cross_entropy(x, w, y), tcl.cross_entropy_grad(x, w, y, grad)):
+        for g, r, what in zip(got, want, ("loss", "lse", "dx", "dw")):
+            ref.within(g, r, what)
