@@ -63,16 +63,24 @@ def _lib():
     return _bound
 
 
-_native = None   # _tensors, once it is loaded
+_native = None   # _tensors, once it is loaded; False where there is none
 
 
 def _load():
+    """The binding's own module, or False where it is missing or cannot be loaded (a warning says why): the calls then
+    go the way of those on a given stream, in some 15 us more of the host's time."""
     global _native
+    if _native is not None:
+        return _native
+    L = _lib()
     try:
         from . import _tensors
     except ImportError as e:
-        raise RuntimeError("_tensors.so is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`") from e
-    L = _lib()
+        import warnings
+        warnings.warn(f"dense calls take more of the host's time without the binding's module: {e} (it is built by "
+                      "`python -c 'import __graft_entry__ as g; g.build()'`)", RuntimeWarning, stacklevel=3)
+        _native = False
+        return _native
     _tensors.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                     for f in (L.tcl_gated_ffn, L.tcl_gated_ffn_grad, L.tcl_cross_entropy, L.tcl_cross_entropy_grad,
                               L.tcl_clip_gradients)))
@@ -163,8 +171,8 @@ def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", keep: bool = Fa
     normal distribution) or "gelu_tanh". The product in the middle is rounded to bf16.
 
     ``keep=True``: (out, kept) with what ``gated_ffn_grad`` needs."""
-    if stream is None:
-        done = (_native or _load()).gated_ffn(x, w_gate, w_up, w_down, _ACTIVATIONS.get(activation, -1), keep)
+    if stream is None and (native := _native or _load()):
+        done = native.gated_ffn(x, w_gate, w_up, w_down, _ACTIVATIONS.get(activation, -1), keep)
         if done is not None:   # (else: something to refuse, or another GPU than the current one)
             if done.__class__ is int:
                 raise TclError(done, "gated_ffn")
@@ -187,9 +195,9 @@ def gated_ffn_grad(grad, x, w_gate, w_up, w_down, kept: GatedFfnKept, activation
     """(dx, dw_gate, dw_up, dw_down) of ``gated_ffn`` from the gradient of its result and what it
     kept. ``dx`` is bf16, the weights' gradients are bf16 or ``out_dtype=torch.float32``. The gradients
     of the two products in the middle are rounded to bf16."""
-    if stream is None:
-        done = (_native or _load()).gated_ffn_grad(grad, x, w_gate, w_up, w_down, *kept, _ACTIVATIONS.get(activation, -1),
-                                                   _TYPES.get(out_dtype or _BF16, -1))
+    if stream is None and (native := _native or _load()):
+        done = native.gated_ffn_grad(grad, x, w_gate, w_up, w_down, *kept, _ACTIVATIONS.get(activation, -1),
+                                     _TYPES.get(out_dtype or _BF16, -1))
         if done is not None:
             if done.__class__ is int:
                 raise TclError(done, "gated_ffn_grad")
@@ -236,8 +244,8 @@ def cross_entropy(x, w, targets, stream=None):
     """(loss, lse) of the logits l = x · wᵀ (tokens × vocabulary), which are never stored: for each
     token lse = log Σ exp(l) and loss = lse - l[target], fp32. ``targets`` (int32 or int64) outside the
     vocabulary drop their token: its loss is 0. Logits beyond ±2^30 count as infinite."""
-    if stream is None:
-        done = (_native or _load()).cross_entropy(x, w, targets)
+    if stream is None and (native := _native or _load()):
+        done = native.cross_entropy(x, w, targets)
         if done is not None:
             if done.__class__ is int:
                 raise TclError(done, "cross_entropy")
@@ -259,8 +267,8 @@ def cross_entropy_grad(x, w, targets, grad, out_dtype=None, stream=None):
     weight for each token (1/tokens for a mean). Dropped tokens add nothing and get zeros. ``dx`` is
     bf16, ``dw`` bf16 or ``out_dtype=torch.float32``. The exponentials of the logits, computed once for
     both, are kept in bf16 for 2 GiB of them at a time."""
-    if stream is None:
-        done = (_native or _load()).cross_entropy_grad(x, w, targets, grad, _TYPES.get(out_dtype or _BF16, -1))
+    if stream is None and (native := _native or _load()):
+        done = native.cross_entropy_grad(x, w, targets, grad, _TYPES.get(out_dtype or _BF16, -1))
         if done is not None:
             if done.__class__ is int:
                 raise TclError(done, "cross_entropy_grad")
@@ -290,7 +298,19 @@ def _look(tensors, name):
     """(addresses, lengths, types, GPU) of contiguous bf16 and fp32 tensors, the first three as bytes."""
     if len(tensors) > _INT:
         _too_large(name)
-    return (_native or _load()).look(tensors, name)
+    if native := _native or _load():
+        return native.look(tensors, name)
+    for t in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be tensors, not {type(t).__name__}")
+        if t.dtype not in _TYPES:
+            raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+        if t.layout != torch.strided or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    n = len(tensors)
+    gpus = {t.device.index if t.is_cuda else -1 for t in tensors}
+    return (bytes((ctypes.c_uint64 * n)(*[t.data_ptr() for t in tensors])), bytes((ctypes.c_int64 * n)(*[t.numel() for t in tensors])),
+            bytes((ctypes.c_int32 * n)(*[_TYPES[t.dtype] for t in tensors])), -1 if n == 0 else gpus.pop() if len(gpus) == 1 else -2)
 
 
 def _where(stream, tensors, *gpus):
@@ -335,8 +355,8 @@ def clip_grads(tensors, max_norm: float, out=None, stream=None):
         raise ValueError("max_norm must not be negative")
     if out is not None:
         out = list(out)
-    if stream is None:
-        done = (_native or _load()).clip_grads(tensors, out, max_norm)
+    if stream is None and (native := _native or _load()):
+        done = native.clip_grads(tensors, out, max_norm)
         if done is not None:
             if done.__class__ is not int:
                 return done
