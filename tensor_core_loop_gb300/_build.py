@@ -1,5 +1,5 @@
 """Builds the in-tree shared library ``libtcl_gb300.so`` from ``csrc/*.cu`` with nvcc, and where
-PyTorch is installed the binding's own module ``_tensors.so`` from ``csrc/tensors.cpp``. Where that module
+PyTorch is installed the binding's own module (``tensors_path``) from ``csrc/tensors.cpp``. Where that module
 cannot be compiled, a warning says why: the library needs neither PyTorch nor Python, and the binding's
 calls go without it, in more of the host's time.
 
@@ -12,6 +12,7 @@ older than its sources or any header.
 from __future__ import annotations
 
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -51,8 +52,12 @@ def _stale(target: str, deps) -> bool:
 
 
 def tensors_path() -> str:
-    """Where the binding's own module is."""
-    return os.path.join(PKG, "_tensors.so")
+    """Where the binding's own module for this Python and this PyTorch is. It is compiled against their classes'
+    layouts, so that one compiled against others must never be loaded: each has a file of its own."""
+    import torch
+    of = (sysconfig.get_config_var("EXT_SUFFIX"), torch.__version__, torch.version.git_version, torch.version.cuda,
+          int(torch._C._GLIBCXX_USE_CXX11_ABI))
+    return os.path.join(PKG, f"_tensors-{hashlib.sha256(repr(of).encode()).hexdigest()[:12]}.so")
 
 
 def _build_tensors(force: bool) -> str:
@@ -65,7 +70,7 @@ def _build_tensors(force: bool) -> str:
         return ""
     path = tensors_path()
     src = os.path.join(CSRC, "tensors.cpp")
-    if not force and not _stale(path, [src, __file__, torch.__file__, *glob.glob(os.path.join(INCLUDE, "*.h"))]):
+    if not force and not _stale(path, [src, __file__, *glob.glob(os.path.join(INCLUDE, "*.h"))]):
         return ""
     tmp = path + f".tmp{os.getpid()}"
     home = os.path.dirname(torch.__file__)

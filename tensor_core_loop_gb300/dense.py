@@ -24,6 +24,8 @@ gradients are calls of their own.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import warnings
 from typing import NamedTuple
 
 try:
@@ -31,7 +33,7 @@ try:
 except ImportError:   # (the library itself needs no PyTorch; the calls below take its tensors)
     torch = None
 
-from . import OUT_BF16, OUT_F32, TclError, lib
+from . import OUT_BF16, OUT_F32, TclError, _build, lib
 from .fp8 import _INT, _device, _mat, _on, _too_large
 
 __all__ = ["gated_ffn", "gated_ffn_grad", "GatedFfnKept", "cross_entropy", "cross_entropy_grad", "grad_norm", "clip_grads",
@@ -63,20 +65,22 @@ def _lib():
     return _bound
 
 
-_native = None   # _tensors, once it is loaded; False where there is none
+_native = None   # the binding's own module, once it is loaded; False where there is none
 
 
 def _load():
-    """The binding's own module, or False where it is missing or cannot be loaded (a warning says why): the calls then
+    """The binding's own module for this Python and PyTorch, or False where there is none (a warning says why): the calls then
     go the way of those on a given stream, in some 15 us more of the host's time."""
     global _native
     if _native is not None:
         return _native
     L = _lib()
+    path = _build.tensors_path()
+    spec = importlib.util.spec_from_file_location(f"{__package__}._tensors", path)
     try:
-        from . import _tensors
+        _tensors = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_tensors)
     except ImportError as e:
-        import warnings
         warnings.warn(f"dense calls take more of the host's time without the binding's module: {e} (it is built by "
                       "`python -c 'import __graft_entry__ as g; g.build()'`)", RuntimeWarning, stacklevel=3)
         _native = False

@@ -53,20 +53,32 @@ def test_module_is_not_asked_of_a_pytorch_without_gpus(monkeypatch, tmp_path, re
     assert not recwarn and os.listdir(tmp_path) == ["g++"]
 
 
-def test_a_module_that_does_not_load_is_named_once(monkeypatch, recwarn):
-    import builtins
-    load = builtins.__import__
-
-    def broken(name, *args, **kw):
-        if "_tensors" in (name, *(args[2] or () if len(args) > 2 else ())):
-            raise ImportError("undefined symbol: THPVariableClass")
-        return load(name, *args, **kw)
-
-    monkeypatch.setattr(builtins, "__import__", broken)
+def test_a_module_that_does_not_load_is_named_once(monkeypatch, tmp_path, recwarn):
+    (tmp_path / "_tensors.so").write_bytes(b"not a library")
+    monkeypatch.setattr(_build, "tensors_path", lambda: str(tmp_path / "_tensors.so"))
     for _ in range(3):
         with pytest.raises(ValueError, match="CUDA"):
             tcl.grad_norm([torch.zeros(4)])
-    assert len([w for w in recwarn if "undefined symbol" in str(w.message)]) == 1
+    assert len([w for w in recwarn if str(tmp_path) in str(w.message)]) == 1
+
+
+@pytest.mark.parametrize("where,name,value", [(torch, "__version__", "2.0.1"), (torch.version, "git_version", "0" * 40), (torch.version, "cuda", "12.9"),
+                                              (torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)])
+def test_a_module_of_another_pytorch_is_not_loaded(monkeypatch, where, name, value):
+    """Exchanged for one with older file times or not."""
+    there = _build.tensors_path()
+    monkeypatch.setattr(where, name, value)
+    assert _build.tensors_path() != there
+    with pytest.warns(RuntimeWarning, match="without the binding's module"):
+        assert dense._load() is False
+
+
+def test_a_module_of_another_python_is_not_loaded(monkeypatch):
+    there, var = _build.tensors_path(), _build.sysconfig.get_config_var
+    monkeypatch.setattr(_build.sysconfig, "get_config_var", lambda n: ".cpython-399.so" if n == "EXT_SUFFIX" else var(n))
+    assert _build.tensors_path() != there
+    with pytest.warns(RuntimeWarning, match="without the binding's module"):
+        assert dense._load() is False
 
 
 def test_binding_without_the_module_refuses(monkeypatch):
