@@ -24,8 +24,8 @@
  * workspace first. Results may have any leading dimension (rows on 16-byte pieces are stored
  * fastest); what lies between their rows is left as it was. They overlap neither operands nor one another.
  *
- * Products run on the tensor cores with fp32 sums. Every result is rounded once; what is rounded
- * to bf16 between two products of a call is named there.
+ * Products run on the tensor cores with fp32 sums, of which every result is rounded once; what is
+ * rounded to bf16 between two products of a call, and what clipping rounds, is named there.
  */
 #ifndef TCL_DENSE_H
 #define TCL_DENSE_H
@@ -90,8 +90,9 @@ TCL_API int tcl_cross_entropy_grad(int tokens, int hidden, int vocab, const void
 TCL_API int tcl_grad_norm(int count, const void* const* tensors, const long long* lengths, const int* types, float* norm,
                           void* workspace, size_t* workspace_bytes, cudaStream_t stream);
 
-/* The same, and to[i] = from[i] · bound/norm, rounded once, where norm > bound; else, and where the
- * norm is infinite or NaN, to[i] = from[i]. to[i] may be from[i]; otherwise a
+/* The same, and to[i] = from[i] · f with f = bound/norm where norm > bound; else, and where the
+ * norm is infinite or NaN, to[i] = from[i]. f is worked out in fp64 and rounded to fp32, the product to fp32
+ * and from there to bf16 where that is the type. to[i] may be from[i]; otherwise a
  * result overlaps no other tensor (TCL_ERR_CONFIG). bound >= 0. */
 TCL_API int tcl_clip_gradients(int count, const void* const* from, void* const* to, const long long* lengths,
                                const int* types, float bound, float* norm, void* workspace, size_t* workspace_bytes,

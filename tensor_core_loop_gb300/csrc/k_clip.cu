@@ -9,8 +9,13 @@
 // 5.5 with 64 bytes and half of the blocks).
 //
 // Squares are added in fp32 within a thread's 32 elements and in fp64 from there on, in an order
-// that depends on the sizes alone, so that equal gradients give equal norms. Where 32 squares leave
+// that depends on the lengths and on the addresses modulo 16 (which elements make up a thread's 32): the same
+// tensors give the same norm, equal values at another alignment may give its neighbour. Where 32 squares leave
 // fp32's range (elements beyond 2^63 or all below 2^-50), they are added again in fp64.
+//
+// The factor is rounded to fp32, its product with a value to fp32 and then to the type: an fp32 result is off by two half
+// steps instead of one, a bf16 one by 2^-15 of a step more than a half. A factor in two parts, and a second
+// multiplication for each value, would spare that.
 #include <cuda_bf16.h>
 
 #include "clip_launch.cuh"

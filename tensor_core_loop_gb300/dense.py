@@ -349,7 +349,8 @@ def grad_norm(tensors, stream=None):
 def clip_grads(tensors, max_norm: float, out=None, stream=None):
     """Scales the tensors, in place or into ``out`` (a list of tensors of the same lengths and types), by
     max_norm / norm where their ``grad_norm`` is larger than ``max_norm``; a norm that is infinite or
-    NaN scales nothing. Returns the norm before, an fp32 scalar on the GPU. A result may be its own tensor, but
+    NaN scales nothing. The factor is rounded to float32, its product with a value to float32 and then to the value's
+    type. Returns the norm before, an fp32 scalar on the GPU. A result may be its own tensor, but
     shares no memory with another one."""
     tensors = list(tensors)
     if not tensors:
