@@ -3,12 +3,13 @@
 // What bounds them is the weights' way from HBM, once: 128 weight rows are the MMA's M side
 // (tensor-memory lanes), the tokens its N side, so that no shared memory and no MMA is spent on
 // tokens that do not exist and a thread holds one output column of every token. The loads run
-// through a ring of 64-value k-blocks that keeps some 170 to 200 KB in flight on each SM. A tile has as many
+// through a ring of 64-value k-blocks, whose slots have room for 128 weight rows: 184 to 209 KB are in flight on
+// each SM where a tile has as many, 102 to 147 KB with 64 rows. A tile has as many
 // weight rows (128 at most) as give all SMs the same share; where there are too few rows
 // for that, the CTAs of a cluster share a tile's k-blocks and one after another's sums are
 // added over distributed shared memory.
 //
-// The ends are those of dense_product.cuh, for the forward direction: STORE, GATE (two weight
+// The ends are those of dense_product.cuh (what they round to bf16, and why, stands there), for the forward direction: STORE, GATE (two weight
 // tiles to a CTA: 128 rows of either matrix), ENTROPY (sums over all vocabulary rows that a warp saw).
 #pragma once
 

@@ -19,6 +19,20 @@
 //              logit, and in training the exponentials themselves in bf16 (k_dense_rows.cu says
 //              what they are relative to)
 //
+// What is rounded to bf16 on the way from one product to the next, and why. The tensor core multiplies bf16 by bf16;
+// an fp32 operand would be read as TF32 (half of the rate, twice the bytes) or in two bf16 parts (twice the MMAs).
+// Errors by norm against 64 bits; the last rounding of a bf16 result alone makes 1.65e-3 of it.
+//   h                     the down product's operand: out 2.3e-3
+//   gate, up              kept for the gradients: 4 bytes a token and inner column, fp32 8. The block's gradients are
+//                         off by 2.9e-3 to 3.1e-3; with fp32 copies 2.4e-3
+//   dgate, dup            operands of three products
+//   the exponentials      operands of both of the entropy's gradients, 2 bytes a token and word; the sums that divide
+//                         them are of the unrounded ones (dx 2.2e-3)
+//   x·grad/S              the rows of x for dW: the tokens are what that product sums over, so their factors cannot
+//                         wait for its end; they go into the smaller operand (dW 2.7e-3)
+// Sums are the tensor core's fp32 ones, which are cut off, not rounded: by 2^-23 of a partial sum at most for each 16
+// terms, 5e-6 of the result in all where 4096 of them have one sign (k_dense_rows.cu says what becomes of that in a loss).
+//
 // Roles of each CTA: warp 0 loads A, warp 10 B (TMA, 128-byte swizzle, a ring of 64-value k-blocks),
 // warp 1 of the pair's leader issues the MMAs into one of two accumulators in tensor memory, warps 2
 // to 9 read the other one (each 32 lanes × half of the columns, or four of them all columns) and store through
@@ -581,7 +595,7 @@ __global__ void __launch_bounds__(DenseCfg<BN>::THREADS, 1)
                             ptx::tmem_ld_wait(x);
                             float unused;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
+                            for (int i = 0; i < 8; ++i)   // (h's one rounding)
                                 w[i] = pack_bf16(
                                     dense_act<decltype(a)::value, false>(__uint_as_float(g[2 * i]), unused) *
                                         __uint_as_float(x[2 * i]),

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kRowThreads) entropy_rows_kernel(const Entropy
         for (int i = k; i < a.chunks; i += KT) {
             const float ref = a.parts[static_cast<long long>(i) * a.rows + row].x;
             if (ref == c) continue;
-            const float f = exp2f(ref - c);
+            const float f = exp2f(ref - c);   // (a power of two: nothing is rounded again but what falls below 2^-126)
             for (int v = i * a.chunk; v < min(i * a.chunk + a.chunk, a.vocab); ++v) {
                 __nv_bfloat16* e = a.e + row * a.ld_e + v;
                 *e = __float2bfloat16_rn(__bfloat162float(*e) * f);
