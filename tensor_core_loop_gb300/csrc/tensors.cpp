@@ -173,7 +173,7 @@ PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor mid = empty({keep ? 3 : 1, x.rows, pitch}, *x.t, at::kBFloat16);
     const at::Tensor out = empty({x.rows, x.cols}, *x.t, at::kBFloat16);
     char* const h = static_cast<char*>(mid.data_ptr());
-    const int64_t part = 2 * x.rows * pitch;
+    const int64_t part = 2 * pitch * x.rows;
     const cudaStream_t stream = c.stream();
     const int st = with_room(0, out, [&](void* space, size_t* size) {
         return lib.ffn(x.rows, x.cols, g.rows, x.p, x.ld, g.p, g.ld, u.p, u.ld, d.p, d.ld, static_cast<int>(act), keep ? h + part : nullptr,
@@ -233,7 +233,7 @@ PyObject* gated_ffn_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
         kept->size(0) != 3 || kept->size(1) != x.rows || kept->size(2) < g.rows || kept->size(2) % 8 || kept->size(2) > INT_MAX ||
         !kept->is_contiguous() || reinterpret_cast<uintptr_t>(kept->data_ptr()) % 16)
         Py_RETURN_NONE;
-    const int64_t pitch = kept->size(2), part = 2 * x.rows * pitch;
+    const int64_t pitch = kept->size(2), part = 2 * pitch * x.rows;
     const at::Tensor dx = empty({x.rows, x.cols}, *x.t, at::kBFloat16), dg = empty({g.rows, g.cols}, *x.t, type),
                      du = empty({g.rows, g.cols}, *x.t, type), dd = empty({d.rows, d.cols}, *x.t, type);
     const char* const h = static_cast<const char*>(kept->data_ptr());
